@@ -15,19 +15,21 @@ import os
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libmoe_gb300.so")
 
-# Symbols declared in include/moe.h, include/gqa_attention.h, include/deltanet_scan.h and
-# include/moe_probe.h.
+# Symbols declared in include/moe.h, include/gqa_attention.h, include/gqa_paged.h,
+# include/deltanet_scan.h and include/moe_probe.h.
 EXPORTED = ("moe_status_string", "moe_max_tiles", "moe_workspace_bytes", "moe_route",
             "moe_expert_forward", "moe_layer_forward", "moe_layer_forward_opts", "moe_rmsnorm_router",
             "moe_clear_error_flags",
             "moe_read_error_flags", "moe_layer_forward_decode_noalloc", "moe_workspace_bytes_host",
             "moe_layer_forward_host", "moe_decode_stream_probe", "gqa_decode_workspace_bytes",
             "gqa_decode_attention", "gdn_scan_workspace_bytes", "gdn_scan", "gdn_scan_opts",
-            "moe_wait_timeout_probe", "moe_layer_forward_host_opts")
+            "moe_wait_timeout_probe", "moe_layer_forward_host_opts", "gqa_paged_workspace_bytes",
+            "gqa_paged_plan", "gqa_paged_append", "gqa_paged_attention")
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_MISALIGNED",
           4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_CUDA"}
 ERR_WAIT_TIMEOUT, ERR_FP16_RANGE, ERR_BAD_ROUTING, ERR_NON_FINITE = 1, 2, 4, 8
+ERR_BAD_PAGES = 16
 OPT_BF16_OPERANDS = 1
 OPT_HOST_INPUTS_READY = 1
 _OPERAND_OPTS = {"fp16": 0, "bf16": OPT_BF16_OPERANDS}
@@ -55,6 +57,13 @@ class ExpertsC(ctypes.Structure):
 class GqaDims(ctypes.Structure):
     _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("n_ctx", ctypes.c_int32), ("capacity", ctypes.c_int32)]
+
+
+class GqaPagedDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_heads", "n_kv_heads", "head_dim", "page_size", "num_pages", "max_pages", "n_seqs", "n_tokens", "max_new",
+        "window", "sinks", "dtype")] + [(n, ctypes.c_int64) for n in (
+            "q_stride", "o_stride", "k_stride", "v_stride", "page_stride", "head_stride", "row_stride")]
 
 
 class GdnDims(ctypes.Structure):
@@ -117,6 +126,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gqa_decode_workspace_bytes.argtypes = [P(GqaDims)]
     lib.gqa_decode_attention.restype = ctypes.c_int
     lib.gqa_decode_attention.argtypes = [P(GqaDims), VP, VP, VP, VP, VP, S, VP]
+    lib.gqa_paged_workspace_bytes.restype = S
+    lib.gqa_paged_workspace_bytes.argtypes = [P(GqaPagedDims)]
+    lib.gqa_paged_plan.restype = ctypes.c_int
+    lib.gqa_paged_plan.argtypes = [P(GqaPagedDims), VP, VP, VP, I32] + [VP] * 8 + [S, VP]
+    lib.gqa_paged_append.restype = ctypes.c_int
+    lib.gqa_paged_append.argtypes = [P(GqaPagedDims)] + [VP] * 7 + [S, VP]
+    lib.gqa_paged_attention.restype = ctypes.c_int
+    lib.gqa_paged_attention.argtypes = [P(GqaPagedDims)] + [VP] * 8 + [S, VP]
     lib.gdn_scan_workspace_bytes.restype = S
     lib.gdn_scan_workspace_bytes.argtypes = [P(GdnDims)]
     lib.gdn_scan.restype = ctypes.c_int
@@ -320,6 +337,99 @@ def gqa_decode_attention(gd: GqaDims, q, k_cache, v_cache, o, workspace, stream=
     _check(load_library().gqa_decode_attention(ctypes.byref(gd), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),
                                                _ptr(workspace), workspace.numel(), _stream(stream)),
            "gqa_decode_attention")
+
+
+_PAGED_DTYPES = {"bf16": 0, "fp16": 1}
+
+
+def gqa_paged_dims(n_heads, n_kv_heads, head_dim, page_size, num_pages, max_pages, n_seqs, n_tokens, max_new=0,
+                   window=0, sinks=0, dtype="bf16", q_stride=0, o_stride=0, k_stride=0, v_stride=0,
+                   cache_strides=(0, 0, 0)) -> GqaPagedDims:
+    """Shapes of the paged calls (include/gqa_paged.h).  max_new: bound on the new tokens of one sequence
+    (0: n_tokens; 1: the single-token form of the attention).  dtype: "bf16" or "fp16".  Strides in
+    elements, 0 for packed; cache_strides: (page, head, row) of both caches, as .stride()[:3] of a cache
+    indexed [page, head, offset, D]."""
+    pg, hd, row = cache_strides
+    return GqaPagedDims(n_heads, n_kv_heads, head_dim, page_size, num_pages, max_pages, n_seqs, n_tokens, max_new, window,
+                        sinks, _PAGED_DTYPES[dtype], q_stride, o_stride, k_stride, v_stride, pg, hd, row)
+
+
+def gqa_paged_workspace_bytes(pd: GqaPagedDims) -> int:
+    n = load_library().gqa_paged_workspace_bytes(ctypes.byref(pd))
+    if n == 0:
+        raise MoeError(1, "gqa_paged_workspace_bytes")
+    return n
+
+
+def alloc_gqa_paged_workspace(pd: GqaPagedDims, device="cuda"):
+    """Workspace of the paged calls for these dims, its error word cleared."""
+    import torch
+    ws = torch.empty(gqa_paged_workspace_bytes(pd), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _paged_ints(t, n: int, name: str) -> int:
+    """Pointer of a contiguous int32 tensor of at least n entries."""
+    if not t.is_cuda or t.element_size() != 4 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of at least {n} entries")
+    return t.data_ptr()
+
+
+def _paged_rows(t, rows: int, heads: int, D: int, stride: int, name: str) -> int:
+    """Pointer of a 16-bit [rows, heads, D] tensor whose token stride is that of the dims (0: packed)."""
+    if (not t.is_cuda or t.element_size() != 2 or t.shape != (rows, heads, D) or t.stride(2) != 1
+            or (heads > 1 and t.stride(1) != D) or (rows > 1 and t.stride(0) != (stride or heads * D))):
+        raise ValueError(f"{name}: expected a 16-bit CUDA tensor [{rows}, {heads}, {D}] of token stride "
+                         f"{stride or heads * D}")
+    return t.data_ptr()
+
+
+def _paged_cache(t, pd: GqaPagedDims, name: str) -> int:
+    """Pointer of a 16-bit cache indexed [page, head, offset, D] whose strides are those of the dims."""
+    P, H, S, D = pd.num_pages, pd.n_kv_heads, pd.page_size, pd.head_dim
+    st = t.stride()
+    if (not t.is_cuda or t.element_size() != 2 or t.shape != (P, H, S, D) or st[3] != 1
+            or (P > 1 and st[0] != (pd.page_stride or H * S * D)) or (H > 1 and st[1] != (pd.head_stride or S * D))
+            or st[2] != (pd.row_stride or D)):
+        raise ValueError(f"{name}: expected a 16-bit CUDA tensor [{P}, {H}, {S}, {D}] with the strides of the dims")
+    return t.data_ptr()
+
+
+def gqa_paged_plan(pd: GqaPagedDims, ctx_len, new_len, free_pages, n_free, block_table, q_start, kv_len, positions,
+                   slots, n_free_out, workspace, stream=None):
+    """Tables of one step from the sequences' lengths, on the GPU: q_start [B + 1], kv_len [B], positions
+    [T] (or None) and slots [T] are written, block_table [B, max_pages] gets fresh pages from the end of
+    free_pages[:n_free], n_free_out (may be n_free) what is left.  All int32."""
+    B, T = pd.n_seqs, pd.n_tokens
+    _check(load_library().gqa_paged_plan(
+        ctypes.byref(pd), _paged_ints(ctx_len, B, "ctx_len"), _paged_ints(new_len, B, "new_len"),
+        _paged_ints(free_pages, 0, "free_pages"), free_pages.numel(), _paged_ints(n_free, 1, "n_free"),
+        _paged_ints(block_table, B * pd.max_pages, "block_table"), _paged_ints(q_start, B + 1, "q_start"),
+        _paged_ints(kv_len, B, "kv_len"), None if positions is None else _paged_ints(positions, T, "positions"),
+        _paged_ints(slots, T, "slots"), _paged_ints(n_free_out, 1, "n_free_out"), _ptr(workspace), workspace.numel(),
+        _stream(stream)), "gqa_paged_plan")
+
+
+def gqa_paged_append(pd: GqaPagedDims, k, v, slots, q_start, k_cache, v_cache, workspace, stream=None):
+    """k, v [T, Hkv, D] into the slots of the caches (rows at or past q_start[B] are skipped)."""
+    T, H, D = pd.n_tokens, pd.n_kv_heads, pd.head_dim
+    _check(load_library().gqa_paged_append(
+        ctypes.byref(pd), _paged_rows(k, T, H, D, pd.k_stride, "k"), _paged_rows(v, T, H, D, pd.v_stride, "v"),
+        _paged_ints(slots, T, "slots"), _paged_ints(q_start, pd.n_seqs + 1, "q_start"), _paged_cache(k_cache, pd, "k_cache"),
+        _paged_cache(v_cache, pd, "v_cache"), _ptr(workspace), workspace.numel(), _stream(stream)), "gqa_paged_append")
+
+
+def gqa_paged_attention(pd: GqaPagedDims, q, k_cache, v_cache, block_table, q_start, kv_len, o, workspace, stream=None):
+    """Causal grouped-query attention of each sequence's new tokens (the last rows of its kv_len positions)
+    over its pages, with pd's window and sinks.  q, o [T, Hq, D] of pd's type."""
+    T, H, D, B = pd.n_tokens, pd.n_heads, pd.head_dim, pd.n_seqs
+    _check(load_library().gqa_paged_attention(
+        ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, "q"), _paged_cache(k_cache, pd, "k_cache"),
+        _paged_cache(v_cache, pd, "v_cache"), _paged_ints(block_table, B * pd.max_pages, "block_table"),
+        _paged_ints(q_start, B + 1, "q_start"), _paged_ints(kv_len, B, "kv_len"),
+        _paged_rows(o, T, H, D, pd.o_stride, "o"), _ptr(workspace), workspace.numel(), _stream(stream)),
+        "gqa_paged_attention")
 
 
 def gdn_dims(T, H, d_k=128, d_v=128) -> GdnDims:

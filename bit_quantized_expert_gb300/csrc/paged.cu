@@ -1,0 +1,477 @@
+// Paged key/value cache: the plan (block tables and slot maps), the append, and the C ABI of the three
+// calls (contracts in include/gqa_paged.h).
+//
+//   plan_kernel    one cluster of one to eight CTAs.  Every CTA scans the sequences' new and fresh-page
+//                  counts into shared memory (at most 4096 of each), then the cluster writes the table
+//                  entries (one warp a sequence) and the token rows (one thread a row, its sequence by
+//                  binary search) together.
+//   append_kernel  16 bytes a thread, head rows contiguous on both sides.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <utility>
+
+#include "paged.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxSeqs = 4096;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqsPerThread = kMaxSeqs / kPlanThreads;
+
+struct PlanArgs {
+  const int32_t *ctx_len, *new_len, *free_pages, *n_free;
+  int32_t *table, *q_start, *kv_len, *positions, *slots, *n_free_out;
+  uint32_t* err;
+  int B, T, page_shift, num_pages, max_pages, free_capacity;
+};
+
+// Lengths of one sequence, cut to the block-table row.
+struct PlanSeq {
+  int ctx, n;        // cached and new positions (as given, negatives as 0)
+  int old, held;     // pages before and after
+  int kv;            // length after the step
+};
+
+__device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int ctx, int n, bool& bad) {
+  PlanSeq s;
+  const long long cap = (long long)a.max_pages << a.page_shift;
+  const int round = (1 << a.page_shift) - 1;
+  if (ctx < 0 || n < 0 || (long long)max(ctx, 0) + max(n, 0) > cap) bad = true;
+  s.ctx = (int)min((long long)max(ctx, 0), cap);
+  s.n = max(n, 0);
+  s.kv = (int)min((long long)s.ctx + s.n, cap);
+  s.old = (int)(((long long)s.ctx + round) >> a.page_shift);
+  s.held = (int)(((long long)s.kv + round) >> a.page_shift);
+  return s;
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a) {
+  extern __shared__ long long plan_smem[];
+  long long* start_s = plan_smem;            // [B + 1] rows before each sequence
+  long long* base_s = plan_smem + a.B + 1;   // [B + 1] fresh pages before each sequence
+  __shared__ long long warp_s[2][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = (int)blockIdx.x, ctas = (int)gridDim.x;
+  bool bad = false;
+
+  // Exclusive sums over the sequences, four consecutive ones a thread, in 64 bits: the lengths are
+  // unchecked, so their sum may pass 32.
+  long long rows = 0, fresh = 0;
+  int nr[kPlanSeqsPerThread], fr[kPlanSeqsPerThread];
+#pragma unroll
+  for (int i = 0; i < kPlanSeqsPerThread; ++i) {
+    const int b = tid * kPlanSeqsPerThread + i;
+    nr[i] = fr[i] = 0;
+    if (b < a.B) {
+      const PlanSeq s = plan_seq(a, __ldg(a.ctx_len + b), __ldg(a.new_len + b), bad);
+      nr[i] = s.n;
+      fr[i] = s.held - s.old;
+    }
+    rows += nr[i];
+    fresh += fr[i];
+  }
+  long long ir = rows, jf = fresh;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long r = __shfl_up_sync(0xFFFFFFFFu, ir, off), f = __shfl_up_sync(0xFFFFFFFFu, jf, off);
+    if (lane >= off) {
+      ir += r;
+      jf += f;
+    }
+  }
+  if (lane == 31) {
+    warp_s[0][warp] = ir;
+    warp_s[1][warp] = jf;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long r = warp_s[0][lane], f = warp_s[1][lane];
+    const long long r0 = r, f0 = f;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long x = __shfl_up_sync(0xFFFFFFFFu, r, off), y = __shfl_up_sync(0xFFFFFFFFu, f, off);
+      if (lane >= off) {
+        r += x;
+        f += y;
+      }
+    }
+    warp_s[0][lane] = r - r0;
+    warp_s[1][lane] = f - f0;
+  }
+  __syncthreads();
+  {
+    long long r = warp_s[0][warp] + ir - rows, f = warp_s[1][warp] + jf - fresh;
+#pragma unroll
+    for (int i = 0; i < kPlanSeqsPerThread; ++i) {
+      const int b = tid * kPlanSeqsPerThread + i;
+      if (b <= a.B) {
+        start_s[b] = r;
+        base_s[b] = f;
+      }
+      r += nr[i];
+      f += fr[i];
+    }
+    if (a.B == kMaxSeqs && tid == kPlanThreads - 1) {
+      start_s[a.B] = r;
+      base_s[a.B] = f;
+    }
+  }
+  const int n_free_raw = __ldcg(a.n_free);
+  const int n_free = min(max(n_free_raw, 0), a.free_capacity);
+  if (n_free != n_free_raw) bad = true;
+  // Every CTA has read n_free (which n_free_out may be) before one of them writes n_free_out.
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  __syncthreads();
+
+  const long long total = start_s[a.B], taken = base_s[a.B];
+  if (total > a.T || taken > n_free) bad = true;
+  if (cta == 0 && tid == 0) *a.n_free_out = (int)max(0ll, n_free - taken);
+
+  // The m-th fresh page, or -1.
+  auto fresh_page = [&](long long m) {
+    if (m >= n_free) return -1;
+    const int p = __ldg(a.free_pages + (n_free - 1 - m));
+    if (p >= 0 && p < a.num_pages) return p;
+    bad = true;
+    return -1;
+  };
+
+  for (int b = tid + cta * kPlanThreads; b <= a.B; b += ctas * kPlanThreads) {
+    a.q_start[b] = (int)min(start_s[b], (long long)a.T);
+    if (b < a.B) {
+      const PlanSeq s = plan_seq(a, __ldg(a.ctx_len + b), __ldg(a.new_len + b), bad);
+      a.kv_len[b] = s.kv;
+    }
+  }
+  const int warps = kPlanThreads / 32;
+  for (int b = cta * warps + warp; b < a.B; b += ctas * warps) {
+    const long long m0 = base_s[b];
+    const int cnt = (int)(base_s[b + 1] - m0);
+    if (cnt == 0) continue;
+    const PlanSeq s = plan_seq(a, __ldg(a.ctx_len + b), __ldg(a.new_len + b), bad);
+    int32_t* row = a.table + (size_t)b * a.max_pages + s.old;
+    for (int i = lane; i < cnt; i += 32) row[i] = fresh_page(m0 + i);
+  }
+  const int rows_used = (int)min(total, (long long)a.T);
+  for (int t = cta * kPlanThreads + tid; t < rows_used; t += ctas * kPlanThreads) {
+    int lo = 0, hi = a.B - 1;   // the last sequence whose first row is at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (start_s[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    const int b = lo;
+    const PlanSeq s = plan_seq(a, __ldg(a.ctx_len + b), __ldg(a.new_len + b), bad);
+    const long long pos = (long long)s.ctx + (t - start_s[b]);
+    if (a.positions != nullptr) a.positions[t] = (int)min(pos, (long long)INT_MAX);
+    int page = -1;
+    if (pos < s.kv) {
+      const int ip = (int)(pos >> a.page_shift);
+      if (ip >= s.old) {
+        page = fresh_page(base_s[b] + (ip - s.old));
+      } else {
+        page = __ldcg(a.table + (size_t)b * a.max_pages + ip);   // a held page: no CTA writes its entry
+        if (page < 0 || page >= a.num_pages) {
+          bad = true;
+          page = -1;
+        }
+      }
+    }
+    a.slots[t] = page < 0 ? -1 : (page << a.page_shift) + (int)(pos & ((1 << a.page_shift) - 1));
+  }
+  if (bad) raise_flag(a.err, kErrBadPages);
+}
+
+struct AppendArgs {
+  const uint16_t *k, *v;
+  const int32_t *slots, *q_start;
+  uint16_t *kc, *vc;
+  uint32_t* err;
+  int Hkv, B, T, page_shift, num_pages;
+  int units;   // 16-byte units of a head row (8 or 16)
+  long long k_stride, v_stride, page_stride, head_stride, row_stride;
+};
+
+constexpr int kAppendThreads = 256;
+
+// Grid-stride over (token, head, 16-byte unit) of the keys and of the values (blockIdx.y).
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  const int rows = min(max(__ldg(a.q_start + a.B), 0), a.T);
+  const uint16_t* src = blockIdx.y == 0 ? a.k : a.v;
+  uint16_t* dst = blockIdx.y == 0 ? a.kc : a.vc;
+  const long long stride = blockIdx.y == 0 ? a.k_stride : a.v_stride;
+  const int per = a.Hkv * a.units;
+  const long long n = (long long)rows * per;
+  for (long long i = (long long)blockIdx.x * kAppendThreads + threadIdx.x; i < n;
+       i += (long long)gridDim.x * kAppendThreads) {
+    const int t = (int)(i / per), r = (int)(i % per), h = r / a.units, u = r % a.units;
+    const int slot = __ldg(a.slots + t), page = slot >> a.page_shift;
+    if (slot < 0 || page >= a.num_pages) {
+      if (slot != -1) raise_flag(a.err, kErrBadPages);
+      continue;
+    }
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + t * stride) + r);
+    const int off = slot & ((1 << a.page_shift) - 1);
+    *(reinterpret_cast<uint4*>(dst + page * a.page_stride + h * a.head_stride + off * a.row_stride) + u) = x;
+  }
+}
+
+bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+// The dims rules, and the dims with every default filled in.
+int check_paged_dims(const gqa_paged_dims* in, gqa_paged_dims* out) {
+  if (in == nullptr) return MOE_ERR_INVALID_ARG;
+  gqa_paged_dims d = *in;
+  if (d.n_heads < 1 || d.n_kv_heads < 1 || d.n_heads % d.n_kv_heads != 0) return MOE_ERR_INVALID_ARG;
+  if (d.page_size < 1 || d.num_pages < 1 || d.max_pages < 1 || d.n_seqs < 0 || d.n_tokens < 0 || d.max_new < 0 ||
+      d.window < 0 || d.sinks < 0 || (d.dtype != GQA_PAGED_BF16 && d.dtype != GQA_PAGED_FP16))
+    return MOE_ERR_INVALID_ARG;
+  if ((d.head_dim != 64 && d.head_dim != 128) || d.n_heads / d.n_kv_heads > 8 || d.n_seqs > kMaxSeqs)
+    return MOE_ERR_UNSUPPORTED;
+  if (d.page_size != 16 && d.page_size != 32 && d.page_size != 64 && d.page_size != 128) return MOE_ERR_UNSUPPORTED;
+  const long long lim = 1ll << 31;
+  if ((long long)d.num_pages * d.page_size >= lim || (long long)d.num_pages * d.page_size * d.n_kv_heads >= lim ||
+      (long long)d.max_pages * d.page_size >= lim || (long long)d.n_tokens * d.n_heads >= lim ||
+      (long long)d.n_seqs * d.n_kv_heads >= lim)
+    return MOE_ERR_UNSUPPORTED;
+  const long long D = d.head_dim;
+  if (d.max_new == 0) d.max_new = d.n_tokens;
+  if (d.q_stride == 0) d.q_stride = d.n_heads * D;
+  if (d.o_stride == 0) d.o_stride = d.n_heads * D;
+  if (d.k_stride == 0) d.k_stride = d.n_kv_heads * D;
+  if (d.v_stride == 0) d.v_stride = d.n_kv_heads * D;
+  if (d.page_stride == 0) d.page_stride = (long long)d.n_kv_heads * d.page_size * D;
+  if (d.head_stride == 0) d.head_stride = d.page_size * D;
+  if (d.row_stride == 0) d.row_stride = D;
+  // A stride over an extent of one is never stepped: any legal value serves.
+  if (d.n_tokens <= 1) d.q_stride = d.o_stride = d.n_heads * D, d.k_stride = d.v_stride = d.n_kv_heads * D;
+  if (d.n_kv_heads == 1) d.head_stride = D;
+  if (d.num_pages == 1) d.page_stride = std::max(d.page_size * d.row_stride, d.n_kv_heads * d.head_stride);
+  const long long s[7] = {d.q_stride, d.o_stride, d.k_stride, d.v_stride, d.page_stride, d.head_stride, d.row_stride};
+  const long long least[7] = {d.n_heads * D, d.n_heads * D, d.n_kv_heads * D, d.n_kv_heads * D, D, D, D};
+  for (int i = 0; i < 7; ++i) {
+    if (s[i] < least[i]) return MOE_ERR_INVALID_ARG;
+    if (s[i] >= (1ll << 39)) return MOE_ERR_UNSUPPORTED;
+  }
+  for (int i = 0; i < 7; ++i)
+    if (s[i] % 8 != 0) return MOE_ERR_MISALIGNED;
+  // No two elements of a cache at one address: in order of stride, each axis steps over the one below.
+  std::pair<long long, long long> ax[3] = {
+      {d.page_stride, d.num_pages}, {d.head_stride, d.n_kv_heads}, {d.row_stride, d.page_size}};
+  std::sort(ax, ax + 3);
+  long long span = D;   // elements from the first to past the last of the axes below
+  for (const auto& x : ax) {
+    if (x.second == 1) continue;
+    if (x.first < span) return MOE_ERR_INVALID_ARG;
+    span += x.first * (x.second - 1);
+  }
+  *out = d;
+  return MOE_OK;
+}
+
+PagedArgs paged_args(const gqa_paged_dims& d) {
+  PagedArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.Hq = d.n_heads;
+  a.Hkv = d.n_kv_heads;
+  a.G = d.n_heads / d.n_kv_heads;
+  a.page_shift = log2_of(d.page_size);
+  a.num_pages = d.num_pages;
+  a.max_pages = d.max_pages;
+  a.B = d.n_seqs;
+  a.T = d.n_tokens;
+  a.max_new = std::min(d.max_new, d.n_tokens);
+  // A window that no position can pass is none (and keeps p - window within 32 bits).
+  a.window = d.window >= (d.max_pages << a.page_shift) ? 0 : d.window;
+  a.sinks = d.sinks;
+  a.fp16 = d.dtype == GQA_PAGED_FP16;
+  a.q_stride = d.q_stride;
+  a.o_stride = d.o_stride;
+  a.page_stride = d.page_stride;
+  a.head_stride = d.head_stride;
+  a.row_stride = d.row_stride;
+  a.qk_scale = (float)(1.4426950408889634 / std::sqrt((double)d.head_dim));
+  return a;
+}
+
+int device_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
+// ---------------------------------------------------------------- attention, one warp per row and head
+__device__ __forceinline__ float to_f32(uint16_t b, int fp16) {
+  return fp16 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_f32(b);
+}
+
+__device__ __forceinline__ uint16_t from_f32(float v, int fp16) {
+  return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) attend_kernel(const PagedArgs a) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int t = (int)(id / a.Hq), h = (int)(id % a.Hq), g = h / a.G;
+  if (t >= a.T) return;
+  bool bad = false;
+  for (int b = 0; b < a.B; ++b) {
+    const SeqRows s = load_seq(a, b, bad);
+    if (t < s.row0 || t >= s.row0 + s.n) continue;
+    const int p = s.p0 + (t - s.row0);
+    float q[E], o[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      q[i] = to_f32(a.q[t * a.q_stride + (long long)h * D + lane + 32 * i], a.fp16);
+      o[i] = 0.f;
+    }
+    for (int j = 0; j <= p; ++j) {
+      if (!paged_sees(a, p, j)) continue;
+      const int page = __ldg(a.table + (size_t)b * a.max_pages + (j >> a.page_shift));
+      const bool ok = page >= 0 && page < a.num_pages;
+      bad |= !ok;
+      const long long at = ok ? page * a.page_stride + g * a.head_stride +
+                                    (j & ((1 << a.page_shift) - 1)) * a.row_stride + lane
+                              : 0;
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) x = fmaf(q[i], ok ? to_f32(a.kc[at + 32 * i], a.fp16) : 0.f, x);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+      x *= a.qk_scale;
+      const float mn = fmaxf(m, x), al = exp2f(m - mn), e = exp2f(x - mn);
+      m = mn;
+      l = l * al + e;
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] = fmaf(e, ok ? to_f32(a.vc[at + 32 * i], a.fp16) : 0.f, o[i] * al);
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float v = p < 0 ? 0.f : o[i] / l;
+      if (!isfinite(v)) raise_flag(a.err, kErrNonFinite);
+      a.o[t * a.o_stride + (long long)h * D + lane + 32 * i] = from_f32(v, a.fp16);
+    }
+  }
+  if (bad) raise_flag(a.err, kErrBadPages);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t gqa_paged_workspace_bytes(const gqa_paged_dims* dims) {
+  gqa_paged_dims d;
+  if (check_paged_dims(dims, &d) != MOE_OK) return 0;
+  return kWsHeadBytes;
+}
+
+extern "C" moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* ctx_len, const int32_t* new_len,
+                                     const int32_t* free_pages, int32_t free_capacity, const int32_t* n_free,
+                                     int32_t* block_table, int32_t* q_start, int32_t* kv_len, int32_t* positions,
+                                     int32_t* slots, int32_t* n_free_out, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  gqa_paged_dims d;
+  const int st = check_paged_dims(dims, &d);
+  if (st != MOE_OK) return (moe_status)st;
+  if (d.n_seqs == 0) return MOE_OK;
+  if (free_capacity < 0 || (free_capacity > 0 && free_pages == nullptr)) return MOE_ERR_INVALID_ARG;
+  const void* need[] = {ctx_len, new_len, n_free, block_table, q_start, kv_len, slots, n_free_out, workspace};
+  for (const void* p : need)
+    if (p == nullptr) return MOE_ERR_INVALID_ARG;
+  for (const void* p : need)
+    if (misaligned16(p)) return MOE_ERR_MISALIGNED;
+  if (misaligned16(positions) || misaligned16(free_pages)) return MOE_ERR_MISALIGNED;
+  if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
+  PlanArgs a = {ctx_len,    new_len, free_pages, n_free,     block_table,
+                q_start,    kv_len,  positions,  slots,      n_free_out,
+                static_cast<uint32_t*>(workspace), d.n_seqs, d.n_tokens, log2_of(d.page_size), d.num_pages, d.max_pages,
+                free_capacity};
+  // One CTA per 2048 rows or 256 sequences, up to the portable cluster size.
+  const long long want = std::max(((long long)d.n_tokens + 2047) / 2048, ((long long)d.n_seqs + 255) / 256);
+  const int ctas = want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
+  const size_t smem = 2 * ((size_t)d.n_seqs + 1) * sizeof(long long);
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               2 * (kMaxSeqs + 1) * (int)sizeof(long long)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, plan_kernel, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status gqa_paged_append(const gqa_paged_dims* dims, const uint16_t* k, const uint16_t* v,
+                                       const int32_t* slots, const int32_t* q_start, uint16_t* k_cache,
+                                       uint16_t* v_cache, void* workspace, size_t workspace_bytes, void* stream) {
+  gqa_paged_dims d;
+  const int st = check_paged_dims(dims, &d);
+  if (st != MOE_OK) return (moe_status)st;
+  if (d.n_seqs == 0 || d.n_tokens == 0) return MOE_OK;
+  const void* need[] = {k, v, slots, q_start, k_cache, v_cache, workspace};
+  for (const void* p : need)
+    if (p == nullptr) return MOE_ERR_INVALID_ARG;
+  for (const void* p : need)
+    if (misaligned16(p)) return MOE_ERR_MISALIGNED;
+  if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
+  int sms = 0;
+  if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
+  AppendArgs a = {k, v, slots, q_start, k_cache, v_cache, static_cast<uint32_t*>(workspace), d.n_kv_heads, d.n_seqs,
+                  d.n_tokens, log2_of(d.page_size), d.num_pages, d.head_dim / 8, d.k_stride, d.v_stride, d.page_stride,
+                  d.head_stride, d.row_stride};
+  const long long units = (long long)d.n_tokens * d.n_kv_heads * a.units;
+  const int grid = (int)std::min((units + kAppendThreads - 1) / kAppendThreads, (long long)sms * 8);
+  append_kernel<<<dim3(grid, 2), kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status gqa_paged_attention(const gqa_paged_dims* dims, const uint16_t* q, const uint16_t* k_cache,
+                                          const uint16_t* v_cache, const int32_t* block_table, const int32_t* q_start,
+                                          const int32_t* kv_len, uint16_t* o, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  gqa_paged_dims d;
+  const int st = check_paged_dims(dims, &d);
+  if (st != MOE_OK) return (moe_status)st;
+  if (d.n_seqs == 0 || d.n_tokens == 0) return MOE_OK;
+  const void* need[] = {q, k_cache, v_cache, block_table, q_start, kv_len, o, workspace};
+  for (const void* p : need)
+    if (p == nullptr) return MOE_ERR_INVALID_ARG;
+  for (const void* p : need)
+    if (misaligned16(p)) return MOE_ERR_MISALIGNED;
+  if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
+  PagedArgs a = paged_args(d);
+  a.q = q;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.table = block_table;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.o = o;
+  a.err = static_cast<uint32_t*>(workspace);
+  const long long warps = (long long)d.n_tokens * d.n_heads;
+  const unsigned grid = (unsigned)((warps + 3) / 4);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d.head_dim == 128) attend_kernel<128><<<grid, 128, 0, s>>>(a);
+  else attend_kernel<64><<<grid, 128, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

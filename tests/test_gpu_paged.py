@@ -1,0 +1,608 @@
+"""The paged key/value cache on the GPU against the oracle: plan and append exactly, attention within a
+bar that follows from its arithmetic.
+
+Bar per output element, with u = 2^-8 (bf16) or 2^-11 (fp16), half a step of the type:
+  u * |ref|                      the one rounding of the output;
+  u_p * mag                      rounding of the softmax numerators before the product with V: u in the
+                                 chunk form, 2^-17 in the single-token form, which keeps the remainders
+                                 (fp16 pairs hold at least as much);
+  2 * smax * (D/16 + 2) * 2^-23 * mag   the scores: D/16 tensor-core steps and two fp32 roundings, each
+                                 within 2^-23 (an accumulator that truncates) of sum_i |q_i k_i| / sqrt(D)
+                                 <= smax, moving a numerator by that fraction (the factor 2 also covers
+                                 its denominator; log2(e) and ln 2 cancel);
+  2^-19 * mag                    exp2 (2 ulp), the running sums and rescales in fp32, the merge: a few
+                                 dozen steps of 2^-24;
+  fp16 only, 2^-25 * (1 + N max|V|)   subnormal outputs, and numerators below 2^-14, held to 2^-25.
+mag is the same attention over |V|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_expert_gb300 as moe
+from oracle import paged_oracle as P
+
+pytestmark = pytest.mark.gpu
+
+U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+TORCH = {"bf16": torch.bfloat16, "fp16": torch.float16}
+NAN = {"bf16": 0x7FC1, "fp16": 0x7E01}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from bit_quantized_expert_gb300 import build
+    build.build()
+    moe.load_library()
+
+
+def bits(x, dtype):
+    """float32 array -> 16-bit patterns, rounded to nearest."""
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(TORCH[dtype]).view(torch.int16).numpy().view(np.uint16)
+
+
+def dev(a, dtype=None):
+    a = np.ascontiguousarray(a)
+    if a.dtype == np.uint16:
+        t = torch.from_numpy(a.view(np.int16)).cuda()
+        return t if dtype is None else t.view(TORCH[dtype])
+    return torch.from_numpy(a.astype(np.int32)).cuda()
+
+
+def host(t):
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+class Batch:
+    """Sequences with (cached, new) positions in shuffled pages.  Whatever no sequence wrote is NaN."""
+
+    def __init__(self, seqs, Hq=16, Hkv=2, D=128, page=64, dtype="bf16", layout="head", fused=False, pad=0, window=0,
+                 sinks=0, seed=0, q_scale=1.0, max_new=None, extra_pages=3):
+        r = np.random.default_rng(seed)
+        self.seqs, self.Hq, self.Hkv, self.D, self.page, self.dtype = seqs, Hq, Hkv, D, page, dtype
+        self.window, self.sinks, self.layout = window, sinks, layout
+        B, rows = len(seqs), sum(n for _, n in seqs)
+        T = rows + pad
+        kv = [c + n for c, n in seqs]
+        need = [-(-x // page) for x in kv]
+        self.P, self.M = sum(need) + extra_pages, max(need + [1]) + 1
+        order = r.permutation(self.P)
+        self.table = np.full((B, self.M), -1, np.int32)
+        at = 0
+        kc = np.full((self.P, Hkv, page, D), NAN[dtype], np.uint16)
+        vc = kc.copy()
+        for b in range(B):
+            self.table[b, :need[b]] = order[at:at + need[b]]
+            at += need[b]
+            k = bits(r.standard_normal((need[b], Hkv, page, D)), dtype)
+            v = bits(r.standard_normal((need[b], Hkv, page, D)), dtype)
+            live = (np.arange(need[b] * page) < kv[b]).reshape(-1, 1, page, 1)
+            kc[self.table[b, :need[b]]] = np.where(live, k, NAN[dtype])
+            vc[self.table[b, :need[b]]] = np.where(live, v, NAN[dtype])
+        self.kc, self.vc = kc, vc
+        self.q = bits(r.standard_normal((T, Hq, D)) * q_scale, dtype)
+        self.k, self.v = (bits(r.standard_normal((T, Hkv, D)), dtype) for _ in range(2))
+        self.q_start = np.cumsum([0] + [n for _, n in seqs]).astype(np.int32)
+        self.kv_len = np.array(kv, np.int32)
+        self.T, self.rows, self.fused = T, rows, fused
+        self.max_new = max([n for _, n in seqs] + [1]) if max_new is None else max_new
+
+    def upload(self):
+        d = self.dtype
+        kc, vc = dev(self.kc, d), dev(self.vc, d)
+        if self.layout == "position":
+            kc, vc = (c.transpose(1, 2).contiguous().transpose(1, 2) for c in (kc, vc))
+        elif self.layout == "interleaved":
+            both = torch.stack([kc, vc], 1)
+            kc, vc = both[:, 0], both[:, 1]
+        q, k, v = dev(self.q, d), dev(self.k, d), dev(self.v, d)
+        if self.fused:
+            x = torch.cat([t.reshape(self.T, -1) for t in (q, k, v)], 1)
+            q, k, v = (t.view(self.T, -1, self.D) for t in x.split([t.shape[1] * self.D for t in (q, k, v)], 1))
+        o_wide = torch.full((self.T, self.Hq * self.D + (64 if self.fused else 0)), 7.0, dtype=TORCH[d], device="cuda")
+        o = o_wide[:, :self.Hq * self.D].view(self.T, self.Hq, self.D)
+        self.dims = moe.gqa_paged_dims(self.Hq, self.Hkv, self.D, self.page, self.P, self.M, len(self.seqs), self.T,
+                                       max_new=self.max_new, window=self.window, sinks=self.sinks, dtype=d,
+                                       q_stride=q.stride(0), k_stride=k.stride(0), v_stride=v.stride(0),
+                                       o_stride=o.stride(0), cache_strides=kc.stride()[:3])
+        self.dev = dict(q=q, k=k, v=v, kc=kc, vc=vc, o=o, o_wide=o_wide, table=dev(self.table), q_start=dev(self.q_start),
+                        kv_len=dev(self.kv_len), ws=moe.alloc_gqa_paged_workspace(self.dims))
+        return self.dev
+
+    def attend(self, stream=None):
+        x = self.dev
+        moe.gqa_paged_attention(self.dims, x["q"], x["kc"], x["vc"], x["table"], x["q_start"], x["kv_len"], x["o"], x["ws"],
+                                stream=stream)
+
+    def run(self):
+        self.upload()
+        self.attend()
+        return P.to_f64(host(self.dev["o"]), self.dtype), moe.read_error_flags(self.dev["ws"])
+
+    def oracle(self, kc=None, vc=None):
+        return P.attention(self.q, self.kc if kc is None else kc, self.vc if vc is None else vc, self.table, self.q_start,
+                           self.kv_len, self.window, self.sinks, self.dtype)
+
+    def check(self, o, ref=None, rows=None, label=""):
+        ref, mag, smax = self.oracle() if ref is None else ref
+        rows = np.arange(self.rows) if rows is None else rows
+        u, n = U[self.dtype], int(self.kv_len.max())
+        u_p = 2.0 ** -17 if self.max_new == 1 else u
+        tol = u * np.abs(ref) + mag * (u_p + 2.0 ** -19 + 2 * smax[..., None] * (self.D // 16 + 2) * 2.0 ** -23)
+        if self.dtype == "fp16":
+            vmax = np.abs(np.nan_to_num(P.to_f64(self.vc, "fp16"), nan=0.0, posinf=0.0, neginf=0.0)).max()
+            tol = tol + 2.0 ** -25 * (1 + n * vmax)
+        ratio = (np.abs(o - ref)[rows] / np.maximum(tol[rows], 1e-30)).max() if len(rows) else 0.0
+        print(f"{label}: max |o - ref| / bar = {ratio:.3f}")
+        assert ratio <= 1.0, (label, ratio)
+        # rows behind the last sequence, and what lies between the rows of a wider buffer
+        assert (o[self.rows:] == 7.0).all()
+        assert (self.dev["o_wide"][:, self.Hq * self.D:].float() == 7.0).all()
+
+
+def _ok(batch, label=""):
+    o, flags = batch.run()
+    assert flags == 0, flags
+    batch.check(o, label=label)
+    return o
+
+
+# ---------------------------------------------------------------- attention: single tokens
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_single_tokens_ragged(dtype, page):
+    ctx = [0, 1, 14, 15, 16, 62, 63, 64, 65, 127, 128, 200, 511, 1000, 2049]
+    _ok(Batch([(c, 1) for c in ctx], page=page, dtype=dtype, seed=page), f"{dtype} page {page}")
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 8, 128), (6, 2, 128), (5, 1, 64), (32, 4, 128), (7, 7, 64), (14, 2, 64), (1, 1, 128),
+                                      (24, 3, 64)])
+def test_single_tokens_head_layouts(Hq, Hkv, D):
+    _ok(Batch([(c, 1) for c in (0, 77, 300, 640)], Hq=Hq, Hkv=Hkv, D=D, page=32, seed=Hq), f"{Hq}/{Hkv} D {D}")
+
+
+@pytest.mark.parametrize("layout", ["position", "interleaved"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_single_tokens_strides(layout, D):
+    _ok(Batch([(c, 1) for c in (3, 90, 257)], D=D, layout=layout, fused=True, pad=5, dtype="fp16", page=16, seed=9), layout)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 0), (100, 4), (100, 70), (129, 300), (4000, 4)])
+def test_single_tokens_window(window, sinks):
+    _ok(Batch([(c, 1) for c in (0, 1, 63, 99, 100, 163, 500, 1500)], window=window, sinks=sinks, page=16, seed=3),
+        f"window {window} sinks {sinks}")
+
+
+def test_single_tokens_idle_sequences_and_padding():
+    """Sequences without a new token between others; rows behind the last one stay as they were."""
+    _ok(Batch([(70, 0), (5, 1), (0, 0), (130, 1), (64, 0)], max_new=1, pad=3, seed=4))
+
+
+def test_single_tokens_long_and_short_together():
+    _ok(Batch([(20000, 1)] + [(c, 1) for c in range(0, 90, 3)] + [(9000, 1)], Hq=8, Hkv=2, seed=5))
+
+
+def test_single_tokens_many_sequences():
+    _ok(Batch([(c % 23, 1) for c in range(1500)], Hq=2, Hkv=1, D=64, page=16, dtype="fp16", seed=6))
+
+
+@pytest.mark.parametrize("q_scale", [8.0, 0.01])
+def test_single_tokens_peaked_and_flat(q_scale):
+    _ok(Batch([(3000, 1), (100, 1)], q_scale=q_scale, seed=7))
+
+
+# ---------------------------------------------------------------- attention: chunks
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_chunks_ragged(dtype, page):
+    seqs = [(0, 2), (0, 1), (0, 17), (5, 33), (127, 1), (128, 2), (100, 64), (300, 31), (0, 130), (513, 5)]
+    _ok(Batch(seqs, Hq=8, Hkv=1, page=page, dtype=dtype, seed=page), f"{dtype} page {page}")
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 4, 128), (6, 2, 128), (5, 1, 64), (16, 4, 64), (3, 3, 64), (14, 2, 128), (1, 1, 128),
+                                      (12, 2, 64)])
+def test_chunks_head_layouts(Hq, Hkv, D):
+    _ok(Batch([(0, 70), (200, 45), (37, 1)], Hq=Hq, Hkv=Hkv, D=D, page=32, seed=Hq), f"{Hq}/{Hkv} D {D}")
+
+
+@pytest.mark.parametrize("layout", ["position", "interleaved"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_chunks_strides(layout, D):
+    _ok(Batch([(3, 40), (90, 3), (140, 20)], Hq=8, D=D, layout=layout, fused=True, pad=5, dtype="fp16", page=16, seed=9), layout)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (100, 4), (100, 200), (128, 0), (300, 130), (4000, 4)])
+def test_chunks_window(window, sinks):
+    _ok(Batch([(0, 150), (400, 70), (1000, 9)], Hq=8, Hkv=2, window=window, sinks=sinks, page=16, seed=3),
+        f"window {window} sinks {sinks}")
+
+
+def test_chunks_idle_sequences_and_padding():
+    _ok(Batch([(70, 0), (5, 20), (0, 0), (130, 1), (64, 0)], pad=130, seed=4))
+
+
+def test_chunk_over_a_long_cache():
+    _ok(Batch([(6000, 9), (0, 3), (3000, 20)], Hq=4, Hkv=2, seed=5))
+
+
+@pytest.mark.parametrize("q_scale", [8.0, 0.01])
+def test_chunks_peaked_and_flat(q_scale):
+    _ok(Batch([(1000, 40), (100, 30)], Hq=8, q_scale=q_scale, seed=7))
+
+
+def test_scores_that_grow_along_the_cache():
+    """Every key is a larger multiple of the query than the one before it: the running maximum moves at
+    every tile, so everything summed before is scaled down again and again."""
+    for new, hq in ((1, 8), (30, 2)):
+        b = Batch([(900, new)], Hq=hq, Hkv=1, seed=8, q_scale=0.5)
+        q = P.to_f64(b.q[0, 0], "bf16")
+        flat = np.arange(900 + new)
+        k = bits(np.outer((flat + 1) / 60.0, q), "bf16")
+        for j in flat:
+            b.kc[b.table[0, j // 64], 0, j % 64] = k[j]
+        b.q[:] = b.q[0, 0]
+        _ok(b, f"new {new}")
+
+
+# ---------------------------------------------------------------- what a row does not see
+def _slot(b, s, p):
+    return b.table[s, p // b.page], p % b.page
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", [0x7F80, 0xFF80, 0x7FC0], ids=["inf", "-inf", "nan"])
+def test_non_finite_values_reach_only_rows_that_see_them(value, D):
+    """One value and one key of a chunk's own new positions: earlier rows do not see them."""
+    b = Batch([(50, 40), (0, 12)], Hq=8, D=D, page=16, seed=11)
+    clean = b.oracle()
+    pv, pk = _slot(b, 0, 50 + 25), _slot(b, 0, 50 + 33)
+    b.vc[pv[0], 1, pv[1], 17] = value
+    b.kc[pk[0], 0, pk[1], 5] = value
+    o, flags = b.run()
+    assert flags == moe.ERR_NON_FINITE
+    heads = b.Hq // 2
+    for row in range(40):
+        if row < 33:
+            b.check(o[:, :heads], tuple(x[:, :heads] for x in clean), [row])
+        if row < 25:
+            b.check(o[:, heads:], tuple(x[:, heads:] for x in clean), [row])
+        else:
+            assert not np.isfinite(o[row, heads:, 17]).any()
+            if value == 0x7F80:
+                assert (o[row, heads:, 17] == np.inf).all()
+            other = np.arange(D) != 17
+            b.check(o[:, heads:][:, :, other], tuple(x[:, heads:][:, :, other] if x.ndim == 3 else x[:, heads:] for x in clean),
+                    [row])
+    b.check(o, clean, np.arange(40, 52))
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_passed_window_pages_hold_anything(new):
+    """Positions behind the window are NaN and their wholly passed pages are gone from the table."""
+    b = Batch([(500, new), (90, new)], window=100, sinks=5, page=16, Hq=8, seed=12)
+    clean = b.oracle()
+    for s, (c, n) in enumerate(b.seqs):
+        lo = max(c - 99, 0)
+        for p in range(5, lo):
+            at = _slot(b, s, p)
+            b.kc[at[0], :, at[1]] = b.vc[at[0], :, at[1]] = NAN["bf16"]
+        for i in range(1, lo // 16):
+            b.table[s, i] = 1 << 30
+    o, flags = b.run()
+    assert flags == 0
+    b.check(o, clean)
+
+
+def test_rows_that_see_nothing_are_zero():
+    """More new tokens than positions: the rows before position 0 are zeros."""
+    b = Batch([(0, 30), (9, 1)], Hq=8, seed=13)
+    b.kv_len[0] = 12
+    o, flags = b.run()
+    assert flags == 0 and (o[:18] == 0).all()
+    b.check(o)
+    b = Batch([(0, 30)], Hq=8, seed=13)
+    b.kv_len[0] = 0
+    o, flags = b.run()
+    assert flags == 0 and (o == 0).all()
+    b = Batch([(0, 1), (9, 1)], seed=13)
+    b.kv_len[0] = 0
+    o, flags = b.run()
+    assert flags == 0 and (o[0] == 0).all()
+    b.check(o)
+
+
+# ---------------------------------------------------------------- out of range, without a fault
+@pytest.mark.parametrize("new", [1, 20])
+@pytest.mark.parametrize("page_no", [-1, -5, 10**6, 2**31 - 1, -2**31])
+def test_bad_pages_count_as_zeros(new, page_no):
+    b = Batch([(150, new), (90, new)], Hq=8, page=32, seed=14)
+    b.table[0, 2] = page_no
+    o, flags = b.run()
+    assert flags == moe.ERR_BAD_PAGES
+    b.check(o)
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_lengths_out_of_range(new):
+    """kv_len above the block-table row or negative, q_start that falls or passes T: bit 16, the other
+    sequences as they are."""
+    for change in ("long", "negative", "falls", "passes"):
+        b = Batch([(150, new), (90, new), (30, new)], Hq=8, page=32, seed=15)
+        clean = b.oracle()
+        rows = np.arange(new, 2 * new) if change in ("long", "negative") else np.arange(new)
+        if change == "long":
+            b.kv_len[0] = 10**9
+        elif change == "negative":
+            b.kv_len[0] = -4
+        elif change == "falls":
+            b.q_start[2] = -7
+        else:
+            b.q_start[2:] = 10**8
+        o, flags = b.run()
+        assert flags & moe.ERR_BAD_PAGES, change
+        b.check(o, clean, rows, change)
+
+
+def test_more_rows_than_max_new():
+    """The first max_new rows of the sequence are computed, the rest left as they were."""
+    for limit in (1, 5):
+        b = Batch([(20, 8), (30, 1)], Hq=8, seed=16, max_new=limit)
+        o, flags = b.run()
+        assert flags == moe.ERR_BAD_PAGES
+        b.check(o, rows=np.r_[0:limit, 8])
+        assert (o[limit:8] == 7.0).all()
+
+
+def test_offsets_beyond_32_bits():
+    """Pages whose elements lie past 2^31 and past 2^32 of a cache of 9 GB a tensor."""
+    page, H, D = 128, 2, 128
+    num = (1 << 32) // (page * H * D) + 5000
+    kc = torch.empty((num, H, page, D), dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    pages = [num - 1, 65536, 65535, num - 4000, 131071, 131072]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for p in pages:
+        for c in (kc, vc):
+            c[p].copy_(torch.randn((H, page, D), device="cuda", generator=gen))
+    small = [host(torch.stack([c[p] for p in pages])) for c in (kc, vc)]
+    table = torch.tensor([pages + [-1]], dtype=torch.int32, device="cuda")
+    for new in (1, 20):
+        b = Batch([(700 - new, new)], Hq=8, Hkv=H, page=page, seed=17)
+        b.upload()
+        b.kc, b.vc, b.table = small[0], small[1], np.arange(6, dtype=np.int32)[None]
+        d = moe.gqa_paged_dims(8, H, D, page, num, 7, 1, new, max_new=new)
+        ws = moe.alloc_gqa_paged_workspace(d)
+        moe.gqa_paged_attention(d, b.dev["q"], kc, vc, table, b.dev["q_start"], b.dev["kv_len"], b.dev["o"], ws)
+        assert moe.read_error_flags(ws) == 0
+        b.check(P.to_f64(host(b.dev["o"]), "bf16"), label=f"new {new}")
+        slots = torch.tensor([pages[0] * page + 5 + i for i in range(new)], dtype=torch.int32, device="cuda")
+        moe.gqa_paged_append(d, b.dev["k"], b.dev["v"], slots, b.dev["q_start"], kc, vc, ws)
+        assert (host(kc[pages[0]])[:, 5:5 + new] == b.k.transpose(1, 0, 2)).all()
+        kc[pages[0]].copy_(dev(small[0][0], "bf16"))
+        vc[pages[0]].copy_(dev(small[1][0], "bf16"))
+
+
+# ---------------------------------------------------------------- calls in company
+@pytest.mark.parametrize("new", [1, 150])
+def test_identical_across_calls(new):
+    b = Batch([(5000, new), (10, new), (777, new)], Hq=8, seed=18)
+    first, _ = b.run()
+    for _ in range(5):
+        b.dev["o"].fill_(7.0)
+        b.attend()
+        assert np.array_equal(P.to_f64(host(b.dev["o"]), "bf16"), first)
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Chunks on one stream beside single tokens on another, each with its own workspace."""
+    a, b = Batch([(900, 200), (50, 30)], Hq=8, seed=19), Batch([(4000, 1), (3, 1)], Hq=8, seed=20)
+    ra, rb = a.run()[0], b.run()[0]
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (sa, sb):
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        a.attend(stream=sa)
+        b.attend(stream=sb.cuda_stream)
+    torch.cuda.synchronize()
+    assert np.array_equal(P.to_f64(host(a.dev["o"]), "bf16"), ra) and np.array_equal(P.to_f64(host(b.dev["o"]), "bf16"), rb)
+
+
+# ---------------------------------------------------------------- plan
+def _plan_case(ctx, new, page, num_pages, M, pad, seed, n_free=None, table=None):
+    r = np.random.default_rng(seed)
+    order = r.permutation(num_pages).astype(np.int32)
+    tab = np.full((len(ctx), M), -9, np.int32)
+    at = 0
+    for b, c in enumerate(ctx):
+        n = -(-max(0, min(c, M * page)) // page)
+        tab[b, :n] = order[at:at + n]
+        at += n
+    free = order[at:]
+    T = sum(max(0, n) for n in new) + pad
+    return dict(ctx=ctx, new=new, free=free, n_free=len(free) if n_free is None else n_free, table=tab, page=page,
+                num_pages=num_pages, T=T)
+
+
+def _plan_run(c, in_place=True, positions=True, T=None):
+    T = c["T"] if T is None else T
+    B, M = c["table"].shape
+    d = moe.gqa_paged_dims(16, 2, 128, c["page"], c["num_pages"], M, B, T)
+    ws = moe.alloc_gqa_paged_workspace(d)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    t = dict(table=dev(c["table"]), q_start=torch.full((B + 3,), -7, **i32), kv_len=torch.full((B + 3,), -7, **i32),
+             positions=torch.full((T + 3,), -7, **i32), slots=torch.full((T + 3,), -7, **i32), n_free=dev(np.array([c["n_free"]])))
+    out = t["n_free"] if in_place else torch.zeros(1, **i32)
+    free = dev(c["free"]) if len(c["free"]) else torch.zeros(1, **i32)[:0]
+    moe.gqa_paged_plan(d, dev(np.array(c["ctx"])), dev(np.array(c["new"])), free, t["n_free"], t["table"], t["q_start"],
+                       t["kv_len"], t["positions"] if positions else None, t["slots"], out, ws)
+    flags = moe.read_error_flags(ws)
+    got = {k: v.cpu().numpy() for k, v in t.items()}
+    got["n_free"] = int(out[0])
+    keep = np.full(T, -7, np.int32)
+    want = P.plan(c["ctx"], c["new"], c["free"], c["n_free"], c["table"], c["page"], c["num_pages"], T, keep, keep)
+    assert flags == want["flags"]
+    assert np.array_equal(got["table"], want["table"])
+    assert got["n_free"] == want["n_free"]
+    assert np.array_equal(got["q_start"][:B + 1], want["q_start"]) and (got["q_start"][B + 1:] == -7).all()
+    assert np.array_equal(got["kv_len"][:B], want["kv_len"]) and (got["kv_len"][B:] == -7).all()
+    assert np.array_equal(got["slots"][:T], want["slots"]) and (got["slots"][T:] == -7).all()
+    if positions:
+        assert np.array_equal(got["positions"][:T], want["positions"]) and (got["positions"][T:] == -7).all()
+    return want
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("B", [1, 2, 33, 300, 1025, 4096])
+def test_plan(B, page):
+    r = np.random.default_rng(B + page)
+    ctx = [int(x) for x in r.integers(0, 5 * page, B)]
+    new = [int(x) for x in r.choice([0, 1, 1, 1, 2, page, page + 1, 3 * page], B)]
+    num = sum(-(-(c + n) // page) for c, n in zip(ctx, new)) + 5
+    want = _plan_run(_plan_case(ctx, new, page, num, 9, 7, B), in_place=bool(B % 2))
+    assert want["flags"] == 0
+
+
+def test_plan_sizes_at_the_ends():
+    _plan_run(_plan_case([0], [0], 16, 4, 3, 5, 1))                              # nothing new at all
+    _plan_run(_plan_case([0, 3], [0, 0], 16, 4, 3, 0, 1))                        # T = 0
+    _plan_run(_plan_case([0], [70000], 64, 1200, 1100, 0, 1), positions=False)   # one long prompt
+    _plan_run(_plan_case([15, 16, 17] * 50, [1, 1, 1] * 50, 16, 400, 3, 0, 1))   # decode across page ends
+    _plan_run(_plan_case([48] * 4, [0] * 4, 16, 12, 3, 0, 1))                    # full rows, no free page
+
+
+@pytest.mark.parametrize("what", ["exhausted", "empty", "over_row", "over_T", "negative", "bad_free", "bad_held", "n_free_high",
+                                  "n_free_negative", "huge"])
+def test_plan_out_of_range(what):
+    ctx, new, page, M, T = [10, 40, 0, 31, 16], [30, 1, 17, 2, 0], 16, 5, None
+    c = _plan_case(ctx, new, page, 30, M, 3, 5)
+    if what == "exhausted":
+        c["n_free"] = 2
+    elif what == "empty":
+        c["free"], c["n_free"] = c["free"][:0], 0
+    elif what == "over_row":
+        c["new"] = [30, 60, 17, 2, 0]
+        c["T"] += 59
+    elif what == "over_T":
+        T = 40
+    elif what == "negative":
+        c["ctx"], c["new"] = [10, -40, 0, 31, 16], [30, 1, 17, -2, 0]
+    elif what == "bad_free":
+        c["free"][-2], c["free"][-4] = 30, -1
+    elif what == "bad_held":
+        c["table"][0, 0], c["table"][3, 1] = 77, -3
+    elif what == "n_free_high":
+        c["n_free"] = len(c["free"]) + 1
+    elif what == "n_free_negative":
+        c["n_free"] = -3
+    else:
+        c["ctx"], c["new"] = [2**31 - 1, 0, 0, 0, 2**31 - 1], [2**31 - 1] * 5
+        T = 50
+        # (the oracle walks every new token: keep its rows short)
+        c["new"] = [2**31 - 1, 3, 2, 2, 1]
+    want = _plan_run(c, T=T)
+    assert want["flags"] == 16
+
+
+# ---------------------------------------------------------------- append
+@pytest.mark.parametrize("layout", ["head", "position", "interleaved"])
+@pytest.mark.parametrize("D,H,dtype,page", [(128, 2, "bf16", 64), (64, 3, "fp16", 16), (128, 1, "fp16", 128), (64, 8, "bf16", 32)])
+def test_append(layout, D, H, dtype, page):
+    """Every element of both caches: the rows in their slots, all else as it was.  Some rows have no
+    slot, some lie behind the last sequence with slots of anything."""
+    for seqs, pad in (([(0, 1)], 0), ([(3, 70), (0, 0), (40, 1), (200, 129)], 9)):
+        b = Batch(seqs, Hq=H, Hkv=H, D=D, dtype=dtype, page=page, layout=layout, fused=True, pad=pad, seed=D + H)
+        x = b.upload()
+        slots = np.full(b.T, 123456789, np.int32)
+        slots[:b.rows] = np.random.default_rng(1).permutation(b.P * page)[:b.rows]
+        slots[1:b.rows:7] = -1
+        moe.gqa_paged_append(b.dims, x["k"], x["v"], dev(slots), x["q_start"], x["kc"], x["vc"], x["ws"])
+        assert moe.read_error_flags(x["ws"]) == 0
+        kc, vc, _ = P.append(b.k, b.v, slots, b.rows, b.kc, b.vc)
+        assert np.array_equal(host(x["kc"]), kc) and np.array_equal(host(x["vc"]), vc)
+
+
+def test_append_out_of_range():
+    b = Batch([(3, 40)], seed=2)
+    x = b.upload()
+    for bad in (-2, b.P * b.page, 2**31 - 1, -2**31):
+        slots = np.arange(40, dtype=np.int32)
+        slots[7] = bad
+        before = host(x["kc"])
+        moe.gqa_paged_append(b.dims, x["k"], x["v"], dev(slots), x["q_start"], x["kc"], x["vc"], x["ws"])
+        assert moe.read_error_flags(x["ws"]) == 16
+        assert np.array_equal(host(x["kc"]), P.append(b.k, b.v, slots, 40, before, before)[0])
+
+
+# ---------------------------------------------------------------- the three together
+def _serve(page, window, sinks, dtype, graph):
+    """Five steps of a served batch whose sequences grow at different paces, two layers, the free list
+    counted down in place; every row against the oracle over the sequence's whole history."""
+    r = np.random.default_rng(page + window)
+    steps = [[40, 0, 7, 129], [1, 65, 1, 1], [1, 1, 0, 30], [16, 1, 1, 1], [1, 1, 1, 1]]
+    B, Hq, H, D, T, num, M = 4, 8, 2, 64, 180, 60, 20
+    d = moe.gqa_paged_dims(Hq, H, D, page, num, M, B, T, window=window, sinks=sinks, dtype=dtype)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ctx, new = torch.zeros(B, **i32), torch.zeros(B, **i32)
+    free, n_free, table = dev(r.permutation(num)), torch.full((1,), num, **i32), torch.full((B, M), -1, **i32)
+    q_start, kv_len = torch.zeros(B + 1, **i32), torch.zeros(B, **i32)
+    positions, slots = torch.zeros(T, **i32), torch.zeros(T, **i32)
+    half = dict(dtype=TORCH[dtype], device="cuda")
+    caches = [[torch.full((num, H, page, D), float("nan"), **half) for _ in range(2)] for _ in range(2)]
+    q, k, v, o = ([torch.zeros((T, h, D), **half) for _ in range(2)] for h in (Hq, H, H, Hq))
+    ws = moe.alloc_gqa_paged_workspace(d)
+
+    def step():
+        moe.gqa_paged_plan(d, ctx, new, free, n_free, table, q_start, kv_len, positions, slots, n_free, ws)
+        for l in range(2):
+            moe.gqa_paged_append(d, k[l], v[l], slots, q_start, *caches[l], ws)
+            moe.gqa_paged_attention(d, q[l], *caches[l], table, q_start, kv_len, o[l], ws)
+
+    g = None
+    if graph:
+        step()                       # nothing new: no page taken, no row written
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+    history = [[[np.zeros((0, H, D), np.uint16)] * 2 for _ in range(B)] for _ in range(2)]
+    for i, lens in enumerate(steps):
+        rows = sum(lens)
+        new.copy_(dev(np.array(lens)))
+        fresh = [[bits(r.standard_normal((T, h, D)), dtype) for h in (Hq, H, H)] for _ in range(2)]
+        for l in range(2):
+            for t, x in zip((q[l], k[l], v[l]), fresh[l]):
+                t.copy_(dev(x, dtype))
+            o[l].fill_(7.0)
+        g.replay() if graph else step()
+        assert moe.read_error_flags(ws) == 0
+        at = np.cumsum([0] + lens)
+        assert q_start.tolist() == at.tolist()
+        assert int(n_free[0]) == num - sum(-(-int(x) // page) for x in kv_len.tolist())
+        for l in range(2):
+            got = P.to_f64(host(o[l]), dtype)
+            assert (got[rows:] == 7.0).all()
+            for b in range(B):
+                kk, vv = history[l][b] = [np.concatenate([h, x[at[b]:at[b + 1]]]) for h, x in
+                                          zip(history[l][b], fresh[l][1:])]
+                L = len(kk)
+                if L == 0 or lens[b] == 0:
+                    continue
+                # the history as one page of L positions
+                ref, mag, smax = P.attention(fresh[l][0][at[b]:at[b + 1]], kk.transpose(1, 0, 2)[None],
+                                             vv.transpose(1, 0, 2)[None], np.array([[0]]), [0, lens[b]], [L], window, sinks,
+                                             dtype)
+                u = U[dtype]
+                tol = u * np.abs(ref) + mag * (u + 2.0 ** -19 + 2 * smax[..., None] * (D // 16 + 2) * 2.0 ** -23)
+                if dtype == "fp16":
+                    tol = tol + 2.0 ** -25 * (1 + L * 6.0)
+                assert (np.abs(got[at[b]:at[b + 1]] - ref) <= tol).all(), (i, l, b)
+        ctx.copy_(kv_len)
+    return [host(x) for x in o]
+
+
+@pytest.mark.parametrize("page,window,sinks,dtype", [(16, 0, 0, "bf16"), (32, 50, 4, "fp16"), (128, 0, 0, "fp16"), (64, 20, 0, "bf16")])
+def test_serving_steps(page, window, sinks, dtype):
+    eager = _serve(page, window, sinks, dtype, graph=False)
+    replayed = _serve(page, window, sinks, dtype, graph=True)      # the same step captured once and replayed
+    for a, b in zip(eager, replayed):
+        assert np.array_equal(a, b)

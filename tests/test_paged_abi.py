@@ -1,0 +1,134 @@
+"""Host-side refusals of the paged calls (include/gqa_paged.h): every call below returns from the argument
+checks before any CUDA work is enqueued, so no GPU is needed."""
+import ctypes
+import os
+
+import pytest
+
+import bit_quantized_expert_gb300 as moe
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(moe.LIB_PATH):
+        from bit_quantized_expert_gb300 import build
+        build.build()
+    return moe.load_library()
+
+
+GOOD = dict(n_heads=16, n_kv_heads=2, head_dim=128, page_size=64, num_pages=100, max_pages=20, n_seqs=4, n_tokens=37)
+
+
+def _calls(lib):
+    """The three calls with every pointer given by name (all good by default)."""
+    def nb(d):
+        return lib.gqa_paged_workspace_bytes(ctypes.byref(moe.gqa_paged_dims(**GOOD)))
+
+    def plan(d, **kw):
+        g = lambda n: kw.get(n, 256)
+        return lib.gqa_paged_plan(ctypes.byref(d), g("ctx"), g("new"), g("free"), kw.get("cap", 100), g("n_free"),
+                                  g("table"), g("q_start"), g("kv_len"), g("positions"), g("slots"), g("n_out"), g("ws"),
+                                  kw.get("nb", nb(d)), None)
+
+    def append(d, **kw):
+        g = lambda n: kw.get(n, 256)
+        return lib.gqa_paged_append(ctypes.byref(d), g("k"), g("v"), g("slots"), g("q_start"), g("kc"), g("vc"), g("ws"),
+                                    kw.get("nb", nb(d)), None)
+
+    def attention(d, **kw):
+        g = lambda n: kw.get(n, 256)
+        return lib.gqa_paged_attention(ctypes.byref(d), g("q"), g("kc"), g("vc"), g("table"), g("q_start"), g("kv_len"),
+                                       g("o"), g("ws"), kw.get("nb", nb(d)), None)
+
+    return {"plan": (plan, ("ctx", "new", "free", "n_free", "table", "q_start", "kv_len", "slots", "n_out", "ws")),
+            "append": (append, ("k", "v", "slots", "q_start", "kc", "vc", "ws")),
+            "attention": (attention, ("q", "kc", "vc", "table", "q_start", "kv_len", "o", "ws"))}
+
+
+@pytest.mark.parametrize("name", ["plan", "append", "attention"])
+def test_pointers_and_workspace(lib, name):
+    """1 for a null pointer, 3 for one off the 16-byte grid, 4 for a short workspace."""
+    call, pointers = _calls(lib)[name]
+    d = moe.gqa_paged_dims(**GOOD)
+    for p in pointers:
+        assert call(d, **{p: None}) == 1, p
+        assert call(d, **{p: 264}) == 3, p
+    assert call(d, nb=lib.gqa_paged_workspace_bytes(ctypes.byref(d)) - 1) == 4
+    if name == "plan":
+        assert call(d, positions=264) == 3 and call(d, cap=-1) == 1
+
+
+INVALID, UNSUPPORTED, MISALIGNED = 1, 2, 3
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n_heads=0), INVALID), (dict(n_kv_heads=0), INVALID), (dict(n_heads=15), INVALID), (dict(page_size=0), INVALID),
+    (dict(num_pages=0), INVALID), (dict(max_pages=0), INVALID), (dict(n_seqs=-1), INVALID), (dict(n_tokens=-1), INVALID),
+    (dict(max_new=-1), INVALID), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID),
+    (dict(head_dim=96), UNSUPPORTED), (dict(head_dim=256), UNSUPPORTED), (dict(n_heads=18), UNSUPPORTED),
+    (dict(page_size=48), UNSUPPORTED), (dict(page_size=256), UNSUPPORTED), (dict(n_seqs=4097), UNSUPPORTED),
+    (dict(num_pages=1 << 24, page_size=128), UNSUPPORTED), (dict(num_pages=1 << 24), UNSUPPORTED),
+    (dict(max_pages=1 << 25), UNSUPPORTED), (dict(n_tokens=1 << 27), UNSUPPORTED),
+    (dict(q_stride=2047), INVALID), (dict(q_stride=2052), MISALIGNED), (dict(k_stride=248), INVALID),
+    (dict(v_stride=260), MISALIGNED), (dict(o_stride=1 << 39), UNSUPPORTED), (dict(q_stride=-2048), INVALID),
+    (dict(cache_strides=(16384, 8192, 132)), MISALIGNED), (dict(cache_strides=(16384, 8192, 64)), INVALID),
+    (dict(cache_strides=(16384, 8064, 128)), INVALID),      # heads overlap
+    (dict(cache_strides=(16256, 8192, 128)), INVALID),      # pages overlap
+    (dict(cache_strides=(16384, 128, 128)), INVALID)])      # heads and positions at one address
+def test_dims_refused(lib, bad, status):
+    if "n_heads" in bad and bad["n_heads"] == 18:
+        bad = dict(n_heads=18, n_kv_heads=2)
+    d = moe.gqa_paged_dims(**{**GOOD, **bad})
+    assert lib.gqa_paged_workspace_bytes(ctypes.byref(d)) == 0
+    for call, _ in _calls(lib).values():
+        assert call(d) == status
+        # the dims are looked at first
+        assert call(d, ws=None) == status
+    with pytest.raises(moe.MoeError):
+        moe.alloc_gqa_paged_workspace(d)
+
+
+def test_unknown_type_refused(lib):
+    d = moe.gqa_paged_dims(**GOOD)
+    d.dtype = 2
+    assert lib.gqa_paged_workspace_bytes(ctypes.byref(d)) == 0
+    with pytest.raises(KeyError):
+        moe.gqa_paged_dims(**GOOD, dtype="fp8")
+
+
+def test_null_dims(lib):
+    assert lib.gqa_paged_workspace_bytes(None) == 0
+    assert lib.gqa_paged_attention(None, *[256] * 8, 1 << 30, None) == 1
+
+
+@pytest.mark.parametrize("extra", [
+    {}, dict(page_size=16), dict(page_size=128), dict(head_dim=64), dict(n_heads=2), dict(dtype="fp16"), dict(max_new=1),
+    dict(window=100, sinks=4), dict(window=2**31 - 1, sinks=2**31 - 1), dict(q_stride=2560, k_stride=2560, v_stride=2560),
+    dict(cache_strides=(16384, 128, 256)),              # position-major pages
+    dict(cache_strides=(32768, 8192, 128)),             # keys and values interleaved page by page
+    dict(cache_strides=(128, 12800, 25600))])           # pages innermost
+def test_dims_accepted(lib, extra):
+    d = moe.gqa_paged_dims(**{**GOOD, **extra})
+    assert lib.gqa_paged_workspace_bytes(ctypes.byref(d)) >= 256
+
+
+@pytest.mark.parametrize("name", ["plan", "append", "attention"])
+def test_nothing_to_do(lib, name):
+    """No sequences, and (but for the plan, which still writes the starts and lengths) no tokens."""
+    call, pointers = _calls(lib)[name]
+    none = {p: None for p in pointers}
+    assert call(moe.gqa_paged_dims(**{**GOOD, "n_seqs": 0}), **none) == 0
+    assert call(moe.gqa_paged_dims(**{**GOOD, "n_tokens": 0}), **none) == (1 if name == "plan" else 0)
+
+
+def test_binding_refuses_tensors_that_do_not_fit():
+    """The binding raises before it calls the library: host tensors, and shapes that are not the dims'."""
+    import torch
+    d = moe.gqa_paged_dims(**GOOD)
+    x = torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        moe._paged_ints(x, 4, "x")
+    with pytest.raises(ValueError):
+        moe._paged_rows(torch.zeros(37, 16, 128, dtype=torch.bfloat16), 37, 16, 128, 0, "q")
+    with pytest.raises(ValueError):
+        moe._paged_cache(torch.zeros(100, 2, 64, 128, dtype=torch.bfloat16), d, "k_cache")
