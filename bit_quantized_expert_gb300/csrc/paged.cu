@@ -17,9 +17,8 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxSeqs = 4096;
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanSeqsPerThread = kMaxSeqs / kPlanThreads;
+constexpr int kPlanSeqsPerThread = kPagedMaxSeqs / kPlanThreads;
 
 struct PlanArgs {
   const int32_t *ctx_len, *new_len, *free_pages, *n_free;
@@ -114,7 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
       r += nr[i];
       f += fr[i];
     }
-    if (a.B == kMaxSeqs && tid == kPlanThreads - 1) {
+    if (a.B == kPagedMaxSeqs && tid == kPlanThreads - 1) {
       start_s[a.B] = r;
       base_s[a.B] = f;
     }
@@ -219,7 +218,21 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   }
 }
 
-bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+// 1 for a null pointer, then 3 for one off its grid: 4 bytes for the int32 tables, 16 for all else.
+template <size_t N, size_t M>
+int check_pointers(const void* const (&tables)[N], const void* const (&wide)[M]) {
+  for (const void* p : tables)
+    if (p == nullptr) return MOE_ERR_INVALID_ARG;
+  for (const void* p : wide)
+    if (p == nullptr) return MOE_ERR_INVALID_ARG;
+  for (const void* p : tables)
+    if (misaligned(p, 4)) return MOE_ERR_MISALIGNED;
+  for (const void* p : wide)
+    if (misaligned(p, 16)) return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
 
 int log2_of(int v) {
   int s = 0;
@@ -235,7 +248,7 @@ int check_paged_dims(const gqa_paged_dims* in, gqa_paged_dims* out) {
   if (d.page_size < 1 || d.num_pages < 1 || d.max_pages < 1 || d.n_seqs < 0 || d.n_tokens < 0 || d.max_new < 0 ||
       d.window < 0 || d.sinks < 0 || (d.dtype != GQA_PAGED_BF16 && d.dtype != GQA_PAGED_FP16))
     return MOE_ERR_INVALID_ARG;
-  if ((d.head_dim != 64 && d.head_dim != 128) || d.n_heads / d.n_kv_heads > 8 || d.n_seqs > kMaxSeqs)
+  if ((d.head_dim != 64 && d.head_dim != 128) || d.n_heads / d.n_kv_heads > 8 || d.n_seqs > kPagedMaxSeqs)
     return MOE_ERR_UNSUPPORTED;
   if (d.page_size != 16 && d.page_size != 32 && d.page_size != 64 && d.page_size != 128) return MOE_ERR_UNSUPPORTED;
   const long long lim = 1ll << 31;
@@ -311,6 +324,22 @@ int device_sms(int* sms) {
   return MOE_OK;
 }
 
+// One cache as the tensor maps see it; boxes of `rows` positions of one page and head.
+bool encode_pages(CUtensorMap* m, const uint16_t* cache, const gqa_paged_dims& d, int rows) {
+  EncodeTiledFn f = encode_fn();
+  if (f == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.page_size, (cuuint64_t)d.n_kv_heads,
+                              (cuuint64_t)d.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)d.row_stride * 2, (cuuint64_t)d.head_stride * 2,
+                                 (cuuint64_t)d.page_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(rows, d.page_size), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return f(m, d.dtype == GQA_PAGED_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+           const_cast<uint16_t*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------------- attention, one warp per row and head
 __device__ __forceinline__ float to_f32(uint16_t b, int fp16) {
   return fp16 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_f32(b);
@@ -376,7 +405,7 @@ using namespace moe;
 extern "C" size_t gqa_paged_workspace_bytes(const gqa_paged_dims* dims) {
   gqa_paged_dims d;
   if (check_paged_dims(dims, &d) != MOE_OK) return 0;
-  return kWsHeadBytes;
+  return kWsHeadBytes + (d.max_new == 1 ? paged_decode_scratch(d.head_dim, kPagedMaxCtas) : 0);
 }
 
 extern "C" moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* ctx_len, const int32_t* new_len,
@@ -385,16 +414,13 @@ extern "C" moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* 
                                      int32_t* slots, int32_t* n_free_out, void* workspace, size_t workspace_bytes,
                                      void* stream) {
   gqa_paged_dims d;
-  const int st = check_paged_dims(dims, &d);
+  int st = check_paged_dims(dims, &d);
   if (st != MOE_OK) return (moe_status)st;
   if (d.n_seqs == 0) return MOE_OK;
   if (free_capacity < 0 || (free_capacity > 0 && free_pages == nullptr)) return MOE_ERR_INVALID_ARG;
-  const void* need[] = {ctx_len, new_len, n_free, block_table, q_start, kv_len, slots, n_free_out, workspace};
-  for (const void* p : need)
-    if (p == nullptr) return MOE_ERR_INVALID_ARG;
-  for (const void* p : need)
-    if (misaligned16(p)) return MOE_ERR_MISALIGNED;
-  if (misaligned16(positions) || misaligned16(free_pages)) return MOE_ERR_MISALIGNED;
+  if ((st = check_pointers({ctx_len, new_len, n_free, block_table, q_start, kv_len, slots, n_free_out}, {workspace})) != MOE_OK)
+    return (moe_status)st;
+  if (misaligned(positions, 4) || misaligned(free_pages, 4)) return MOE_ERR_MISALIGNED;
   if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
   PlanArgs a = {ctx_len,    new_len, free_pages, n_free,     block_table,
                 q_start,    kv_len,  positions,  slots,      n_free_out,
@@ -405,7 +431,7 @@ extern "C" moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* 
   const int ctas = want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
   const size_t smem = 2 * ((size_t)d.n_seqs + 1) * sizeof(long long);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               2 * (kMaxSeqs + 1) * (int)sizeof(long long)) != cudaSuccess)
+                                               2 * (kPagedMaxSeqs + 1) * (int)sizeof(long long)) != cudaSuccess)
     return MOE_ERR_CUDA;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -425,14 +451,10 @@ extern "C" moe_status gqa_paged_append(const gqa_paged_dims* dims, const uint16_
                                        const int32_t* slots, const int32_t* q_start, uint16_t* k_cache,
                                        uint16_t* v_cache, void* workspace, size_t workspace_bytes, void* stream) {
   gqa_paged_dims d;
-  const int st = check_paged_dims(dims, &d);
+  int st = check_paged_dims(dims, &d);
   if (st != MOE_OK) return (moe_status)st;
   if (d.n_seqs == 0 || d.n_tokens == 0) return MOE_OK;
-  const void* need[] = {k, v, slots, q_start, k_cache, v_cache, workspace};
-  for (const void* p : need)
-    if (p == nullptr) return MOE_ERR_INVALID_ARG;
-  for (const void* p : need)
-    if (misaligned16(p)) return MOE_ERR_MISALIGNED;
+  if ((st = check_pointers({slots, q_start}, {k, v, k_cache, v_cache, workspace})) != MOE_OK) return (moe_status)st;
   if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
   int sms = 0;
   if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
@@ -450,14 +472,11 @@ extern "C" moe_status gqa_paged_attention(const gqa_paged_dims* dims, const uint
                                           const int32_t* kv_len, uint16_t* o, void* workspace, size_t workspace_bytes,
                                           void* stream) {
   gqa_paged_dims d;
-  const int st = check_paged_dims(dims, &d);
+  int st = check_paged_dims(dims, &d);
   if (st != MOE_OK) return (moe_status)st;
   if (d.n_seqs == 0 || d.n_tokens == 0) return MOE_OK;
-  const void* need[] = {q, k_cache, v_cache, block_table, q_start, kv_len, o, workspace};
-  for (const void* p : need)
-    if (p == nullptr) return MOE_ERR_INVALID_ARG;
-  for (const void* p : need)
-    if (misaligned16(p)) return MOE_ERR_MISALIGNED;
+  if ((st = check_pointers({block_table, q_start, kv_len}, {q, k_cache, v_cache, o, workspace})) != MOE_OK)
+    return (moe_status)st;
   if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
   PagedArgs a = paged_args(d);
   a.q = q;
@@ -468,9 +487,19 @@ extern "C" moe_status gqa_paged_attention(const gqa_paged_dims* dims, const uint
   a.kv_len = kv_len;
   a.o = o;
   a.err = static_cast<uint32_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d.max_new == 1) {
+    int sms = 0;
+    PagedMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (device_sms(&sms) != MOE_OK || !encode_pages(&maps.k, k_cache, d, 64) || !encode_pages(&maps.v, v_cache, d, 64))
+      return MOE_ERR_CUDA;
+    void* scratch = static_cast<uint8_t*>(workspace) + kWsHeadBytes;
+    return launch_paged_decode(maps, a, d.head_dim, scratch, std::min(sms, kPagedMaxCtas), s) == cudaSuccess ? MOE_OK
+                                                                                                            : MOE_ERR_CUDA;
+  }
   const long long warps = (long long)d.n_tokens * d.n_heads;
   const unsigned grid = (unsigned)((warps + 3) / 4);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d.head_dim == 128) attend_kernel<128><<<grid, 128, 0, s>>>(a);
   else attend_kernel<64><<<grid, 128, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -10,6 +10,8 @@ namespace moe {
 
 constexpr uint32_t kErrBadPages = 16u;   // a length, page or slot out of range
 
+constexpr int kPagedMaxSeqs = 4096;
+
 struct PagedArgs {
   const uint16_t* q;        // [T, Hq, D]
   const uint16_t* kc;       // [num_pages, Hkv, page_size, D]
@@ -53,5 +55,140 @@ __device__ __forceinline__ SeqRows load_seq(const PagedArgs& a, int b, bool& bad
 __device__ __forceinline__ bool paged_sees(const PagedArgs& a, int p, int j) {
   return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
 }
+
+// The cache tiles of TN positions that rows at positions p_lo .. p_hi see: tiles 0 .. head - 1 hold the
+// leading positions that stay visible, the others follow `skip` tiles later.  At least one tile, so
+// that rows that see nothing are still written.
+struct TileRange {
+  int count, head, skip;
+  __device__ __forceinline__ int tile(int i) const { return i < head ? i : i + skip; }
+};
+
+template <int TN>
+__device__ __forceinline__ TileRange visible_tiles(const PagedArgs& a, int p_lo, int p_hi) {
+  TileRange r;
+  r.head = r.skip = 0;
+  r.count = p_hi < 0 ? 1 : p_hi / TN + 1;
+  if (a.window > 0 && p_hi >= 0) {
+    const int first = max(0, p_lo - a.window + 1) / TN;              // first tile of the window
+    const int head = (min(a.sinks, p_hi + 1) + TN - 1) / TN;
+    if (head < first) {
+      r.head = head;
+      r.skip = first - head;
+      r.count -= r.skip;
+    }
+  }
+  return r;
+}
+
+// Whether rows at positions p_lo .. p_hi see any position of page `ip`.
+__device__ __forceinline__ bool page_needed(const PagedArgs& a, int ip, int p_lo, int p_hi) {
+  const int j0 = ip << a.page_shift, j1 = j0 + (1 << a.page_shift) - 1;
+  return j0 <= p_hi && (a.window == 0 || j1 > p_lo - a.window || j0 < a.sinks);
+}
+
+// Whether every row at positions p_lo .. p_hi sees every position j0 .. j0 + TN - 1.
+template <int TN>
+__device__ __forceinline__ bool tile_open(const PagedArgs& a, int j0, int p_lo, int p_hi) {
+  return j0 + TN - 1 <= p_lo && (a.window == 0 || j0 > p_hi - a.window || j0 + TN <= a.sinks);
+}
+
+// ------------------------------------------------------------------------------------------
+// Split of the work over the CTAs.  The cache tiles of all items (an item is a block of query rows of
+// one key/value head), in order, are cut into equal consecutive shares, one a CTA.  An item that lies in
+// several shares leaves one partial result (unnormalised O, max and sum per row) in each, joined by a
+// second launch in order.  A CTA has at most two partials: slot 0 of an item that began before it, slot
+// 1 of one that goes on after it.
+// ------------------------------------------------------------------------------------------
+constexpr int kPagedMaxCtas = 256;
+
+// What the joining launch needs of a CTA whose last item goes on in later CTAs (until < 0: none).
+struct SplitRecord {
+  int32_t row, g, rows, until;   // first row of o, head group, rows of the item, last CTA with a part
+};
+
+// Exclusive sums of cost(b) over b = 0 .. B - 1 into pre_s[0 .. B], by a whole block of NT threads.
+template <int NT, class Cost>
+__device__ __forceinline__ void scan_sequences(int B, unsigned long long* pre_s, unsigned long long* warp_s, Cost cost) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (B + NT - 1) / NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  unsigned long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const unsigned long long c = cost(b);
+    pre_s[b] = mine;
+    mine += c;
+  }
+  unsigned long long inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+    if (lane >= off) inc += x;
+  }
+  if (lane == 31) warp_s[warp] = inc;
+  __syncthreads();
+  unsigned long long before = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) before += w < warp ? warp_s[w] : 0;
+  before += inc - mine;
+  for (int b = b0; b < b1; ++b) pre_s[b] += before;
+  if (tid == NT - 1) pre_s[B] = before + mine;
+  __syncthreads();
+}
+
+// The sequence that holds unit `pos` of the order (pre_s[b] <= pos < pre_s[b + 1]), by binary search.
+__device__ __forceinline__ int find_sequence(const unsigned long long* pre_s, int B, unsigned long long pos) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre_s[mid] <= pos) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The CTA whose share [c * total / n, (c + 1) * total / n) holds unit `pos`.
+__device__ __forceinline__ int share_of(unsigned long long pos, unsigned long long total, int n) {
+  int c = (int)((pos * n) / total);
+  while ((unsigned long long)(c + 1) * total / n <= pos) ++c;
+  while (c > 0 && (unsigned long long)c * total / n > pos) --c;
+  return c;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+      "%5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+struct PagedMaps {
+  CUtensorMap k, v;   // {D, page_size, Hkv, num_pages}, box {64, min(page_size, rows of a tile), 1, 1}, 128-byte swizzle
+  CUtensorMap q;      // chunk form: {D, Hq, T}, box {64, G, tokens of a tile}
+};
+
+// Two fp32 values rounded to a pair of the 16-bit type (lo in the low half), and back.
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if (FP16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <bool FP16>
+__device__ __forceinline__ float2 unpack16(uint32_t x) {
+  if (FP16) return __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+}
+
+// ------------------------------------------------------------------------------------------
+// The two forms and their joining launch
+// ------------------------------------------------------------------------------------------
+size_t paged_decode_scratch(int D, int ctas);      // bytes of partials and records
+cudaError_t launch_paged_decode(const PagedMaps& maps, const PagedArgs& a, int D, void* scratch, int ctas, cudaStream_t st);
 
 }  // namespace moe

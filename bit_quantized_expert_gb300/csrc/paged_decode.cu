@@ -1,0 +1,477 @@
+// Single-token attention over the paged cache (contract in include/gqa_paged.h): every sequence has at most
+// one new token, so the work is one pass over the visible cache, bound by HBM.
+//
+//   * the cache is walked in tiles of 64 positions; an item is one key/value head of one sequence, and all
+//     its query heads (up to eight) share the tile, so a cached byte is read once;
+//   * the tiles of all items, in order, are cut into equal shares, one per CTA and one CTA per SM: one long
+//     sequence is spread over every SM and a batch of very different lengths is balanced by construction
+//     (see paged.cuh); a share may hold the end of one item, several whole ones and the start of another;
+//   * one producer warp copies the tile's pages by tensor map into a ring (a page of the table is a box of
+//     16 to 64 rows), 32 page numbers at a time read ahead by its lanes; eight consumer warps take tiles
+//     in turn (four warps a tile, 16 positions a warp) with m16n8k16 products: S = Q K^T with the heads as
+//     the 16-row operand (rows 8..15 zero), then O += P V with rows 0..7 the rounded numerators and rows
+//     8..15 their rounding remainders, so P keeps about twice the type's bits;
+//   * all rows stand at one position and see the same set, so positions that they do not see are cut out
+//     of the value operand itself: whatever lies there, non-finite values included, has no effect;
+//   * running max, sum and O stay in registers; at an item's end the eight warps are joined in shared
+//     memory in a fixed order, and the result goes to o, or, for an item that other CTAs share, to a
+//     partial that a second launch joins in order.
+#include <cmath>
+
+#include "paged.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTN = 64;                        // positions per tile
+constexpr int kWarps = 8;                      // consumer warps: two groups of four, alternate tiles
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kRows = 8;                       // query heads per key/value head, at most
+constexpr float kNegBig = -1e30f;              // running max before any position is seen
+
+template <int D>
+struct Dec {
+  static constexpr int kBoxes = D / 64;                  // 64-dim boxes of a row
+  static constexpr int kBoxBytes = kTN * 128;
+  static constexpr int kStageBytes = 2 * kBoxes * kBoxBytes;
+  static constexpr int kStages = 128 * 1024 / kStageBytes;
+  static constexpr int kOStride = D + 8;                 // padded row of the joining buffer (floats)
+  static constexpr int kJoinBytes = kWarps * kRows * kOStride * 4;
+  static constexpr int kPartFloats = kRows * D + 2 * kRows;
+  static size_t smem(int B) { return 1024 + (size_t)kStages * kStageBytes + kJoinBytes + ((size_t)B + 1) * 8; }
+};
+
+struct DecodeSplit {
+  float* part;         // [ctas][2][kPartFloats]
+  SplitRecord* rec;    // [ctas]
+};
+
+template <bool FP16>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if (FP16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
+}
+
+// Byte offset of 16-byte chunk `chunk` (8 dims) of row `pos` in a tile of 64-dim boxes written by the
+// tensor map's 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz(int pos, int chunk) {
+  return (uint32_t)((chunk >> 3) * (kTN * 128) + pos * 128 + (((chunk & 7) ^ (pos & 7)) << 4));
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a, const DecodeSplit split) {
+  using C = Dec<D>;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages];
+  __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows], wt_s[kWarps][kRows];
+  __shared__ unsigned long long warp_s[kThreads / 32];
+  __shared__ int abort_s;
+  const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
+  float* join_s = reinterpret_cast<float*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes);
+  unsigned long long* pre_s =
+      reinterpret_cast<unsigned long long*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes + C::kJoinBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = (int)blockIdx.x;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 4);
+    }
+    abort_s = 0;
+    mbar_fence_init();
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- this CTA's share: units lo .. hi - 1 of (sequence, head, tile)
+  bool bad = false;
+  scan_sequences<kThreads>(a.B, pre_s, warp_s, [&](int b) {
+    const SeqRows s = load_seq(a, b, bad);
+    return s.n == 0 ? 0ull : (unsigned long long)visible_tiles<kTN>(a, s.p0, s.p0).count * a.Hkv;
+  });
+  if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
+  const unsigned long long total = pre_s[a.B];
+  const int ctas = (int)min((unsigned long long)gridDim.x, total);   // every share holds a tile
+  if (tid == 0) split.rec[cta].until = -1;
+  if (cta >= ctas) return;
+  const unsigned long long lo = total * cta / ctas, hi = total * (cta + 1) / ctas;
+  const int b_first = find_sequence(pre_s, a.B, lo);
+
+  if (warp == kWarps) {
+    // ---- producer warp
+    const int ppt = max(1, kTN >> a.page_shift);               // pages of a tile
+    const int box_rows = min(kTN, 1 << a.page_shift);
+    int b = b_first, issued = 0;
+    bool stop = false;
+    bad = false;
+    for (unsigned long long u = lo; u < hi && !stop; ++b) {
+      if (pre_s[b + 1] <= u) continue;
+      const SeqRows s = load_seq(a, b, bad);
+      const TileRange r = visible_tiles<kTN>(a, s.p0, s.p0);
+      const int32_t* row = a.table + (size_t)b * a.max_pages;
+      const unsigned long long end = min(pre_s[b + 1], hi);
+      while (u < end && !stop) {
+        const int g = (int)((u - pre_s[b]) / r.count), i0 = (int)((u - pre_s[b]) % r.count);
+        const int n = (int)min((unsigned long long)(r.count - i0), end - u);
+        int pg = 0;                                            // this lane's page of the batch of tiles
+        const int batch = 32 / ppt;
+        for (int i = 0; i < n && !stop; ++i) {
+          const int in = i % batch;
+          if (in == 0) {
+            const int t = i0 + i + lane / ppt;
+            pg = a.num_pages;                                  // out of the map's range: zeros
+            if (t < r.count && lane / ppt < n - i) {
+              const int ip = ((r.tile(t) * kTN) >> a.page_shift) + lane % ppt;
+              if (ip < a.max_pages && page_needed(a, ip, s.p0, s.p0)) {
+                const int p = __ldg(row + ip);
+                if (p >= 0 && p < a.num_pages) pg = p;
+                else bad = true;
+              }
+            }
+          }
+          const int st = issued % C::kStages;
+          if (issued >= C::kStages &&
+              !mbar_wait_warp(smem_u32(&empty[st]), ((issued / C::kStages) - 1) & 1, &abort_s, a.err)) {
+            stop = true;
+            break;
+          }
+          const uint32_t dst = base + st * C::kStageBytes, bar = smem_u32(&full[st]);
+          const int off = (r.tile(i0 + i) * kTN) & ((1 << a.page_shift) - 1);   // 64 in the second half of a page of 128
+          if (lane == 0) mbar_arrive_expect_tx(bar, C::kStageBytes);
+          __syncwarp();
+          // one copy a lane: (page of the tile, keys or values, 64-dim box)
+          const int copies = ppt * 2 * C::kBoxes, sub = lane / (2 * C::kBoxes), kv = (lane / C::kBoxes) & 1,
+                    box = lane % C::kBoxes;
+          const int p = __shfl_sync(0xFFFFFFFFu, pg, (in * ppt + sub) & 31);
+          if (lane < copies)
+            tma_load_4d(dst + (kv * C::kBoxes + box) * C::kBoxBytes + sub * box_rows * 128, kv ? &maps.v : &maps.k, bar,
+                        box * 64, off, g, p);
+          ++issued;
+        }
+        u += n;
+      }
+    }
+    if (bad) raise_flag(a.err, kErrBadPages);
+    // After a timeout, copies still in flight land before the CTA exits.
+    if (stop && lane == 0)
+      for (int i = max(0, issued - C::kStages); i < issued; ++i) {
+        const long long c0 = clock64();
+        while (!mbar_try_wait(smem_u32(&full[i % C::kStages]), (i / C::kStages) & 1) && clock64() - c0 < 4000000ll) {
+        }
+      }
+    return;
+  }
+
+  // ---- consumers.  Every warp walks every segment; after a timeout the waits fail at once and the walk
+  // goes on without data, so that the barriers still match.
+  const int wg = warp >> 2, wq = warp & 3;
+  const int r = lane >> 2, c2 = (lane & 3) * 2;
+  const int lrow = lane & 7, lmat = lane >> 3;
+  const int kpos = wq * 16 + 8 * (lmat >> 1) + lrow;   // key row this lane addresses
+  const int vpos = wq * 16 + 8 * (lmat & 1) + lrow;    // value row this lane addresses
+  int it = 0;                                          // tiles of the share so far
+  int b = b_first;
+  for (unsigned long long u = lo; u < hi; ++b) {
+    if (pre_s[b + 1] <= u) continue;
+    const SeqRows s = load_seq(a, b, bad);
+    const TileRange tr = visible_tiles<kTN>(a, s.p0, s.p0);
+    const unsigned long long end = min(pre_s[b + 1], hi);
+    while (u < end) {
+      const int g = (int)((u - pre_s[b]) / tr.count), i0 = (int)((u - pre_s[b]) % tr.count);
+      const int n = (int)min((unsigned long long)(tr.count - i0), end - u);
+      uint32_t qa[D / 16][2];   // the heads as the 16-row operand: rows r < G
+      {
+        const bool live = r < a.G;
+        const uint32_t* qh =
+            reinterpret_cast<const uint32_t*>(a.q + s.row0 * a.q_stride + (long long)(g * a.G + (live ? r : 0)) * D + c2);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          qa[kk][0] = live ? __ldg(qh + 8 * kk) : 0u;
+          qa[kk][1] = live ? __ldg(qh + 8 * kk + 4) : 0u;
+        }
+      }
+      float o[D / 8][4];
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      float m_run = kNegBig, l_run = 0.f;
+      for (int i = (it ^ wg) & 1; i < n; i += 2) {   // tile it + i of the share goes to group (it + i) & 1
+        const int st = (it + i) % C::kStages;
+        const bool ok = mbar_wait_warp(smem_u32(&full[st]), ((it + i) / C::kStages) & 1, &abort_s, a.err);
+        if (ok) {
+          const uint32_t sk = base + st * C::kStageBytes, sv = sk + C::kBoxes * C::kBoxBytes;
+          float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t b0, b1, b2, b3;
+            ldsm4(sk + swz(kpos, 2 * kk + (lmat & 1)), b0, b1, b2, b3);
+            mma16<FP16>(sc[0], qa[kk][0], 0u, qa[kk][1], 0u, b0, b1);
+            mma16<FP16>(sc[1], qa[kk][0], 0u, qa[kk][1], 0u, b2, b3);
+          }
+          const int j0 = tr.tile(i0 + i) * kTN;
+          uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;   // value pairs that the token sees
+          float x[2][2] = {{sc[0][0] * a.qk_scale, sc[0][1] * a.qk_scale}, {sc[1][0] * a.qk_scale, sc[1][1] * a.qk_scale}};
+          const bool open = tile_open<kTN>(a, j0, s.p0, s.p0);
+          if (!open) {
+            const int j = j0 + wq * 16 + c2;
+            const bool v00 = paged_sees(a, s.p0, j), v01 = paged_sees(a, s.p0, j + 1);
+            const bool v10 = paged_sees(a, s.p0, j + 8), v11 = paged_sees(a, s.p0, j + 9);
+            x[0][0] = v00 ? x[0][0] : -INFINITY;
+            x[0][1] = v01 ? x[0][1] : -INFINITY;
+            x[1][0] = v10 ? x[1][0] : -INFINITY;
+            x[1][1] = v11 ? x[1][1] : -INFINITY;
+            keep0 = (v00 ? 0xFFFFu : 0u) | (v01 ? 0xFFFF0000u : 0u);
+            keep1 = (v10 ? 0xFFFFu : 0u) | (v11 ? 0xFFFF0000u : 0u);
+          }
+          float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+          const float m_new = fmaxf(m_run, mx);
+          const float alpha = exp2f(m_run - m_new);
+          m_run = m_new;
+          float p[2][2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p[j][e] = exp2f(x[j][e] - m_new);
+          l_run = l_run * alpha + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            o[j][0] *= alpha;
+            o[j][1] *= alpha;
+            o[j][2] *= alpha;
+            o[j][3] *= alpha;
+          }
+          const uint32_t a0 = pack16<FP16>(p[0][0], p[0][1]), a2 = pack16<FP16>(p[1][0], p[1][1]);
+          const float2 t0 = unpack16<FP16>(a0), t2 = unpack16<FP16>(a2);
+          const uint32_t a1 = pack16<FP16>(p[0][0] - t0.x, p[0][1] - t0.y);
+          const uint32_t a3 = pack16<FP16>(p[1][0] - t2.x, p[1][1] - t2.y);
+#pragma unroll
+          for (int jj = 0; jj < D / 16; ++jj) {
+            uint32_t b0, b1, b2, b3;
+            ldsm4_t(sv + swz(vpos, 2 * jj + (lmat >> 1)), b0, b1, b2, b3);
+            if (!open) {
+              b0 &= keep0;
+              b1 &= keep1;
+              b2 &= keep0;
+              b3 &= keep1;
+            }
+            mma16<FP16>(o[2 * jj], a0, a1, a2, a3, b0, b1);
+            mma16<FP16>(o[2 * jj + 1], a0, a1, a2, a3, b2, b3);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+      }
+      it += n;
+
+      // ---- join the eight warps in order
+      l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
+      l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 2);
+      if ((lane & 3) == 0) {
+        m_s[warp][r] = m_run;
+        l_s[warp][r] = l_run;
+      }
+      float* ow = join_s + (warp * kRows + r) * C::kOStride + c2;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j)
+        *reinterpret_cast<float2*>(ow + 8 * j) = make_float2(o[j][0] + o[j][2], o[j][1] + o[j][3]);
+      consumers_sync();
+      if (tid < kWarps * kRows) {
+        const int rr = tid & (kRows - 1), w = tid / kRows;
+        float M = m_s[0][rr];
+#pragma unroll
+        for (int v = 1; v < kWarps; ++v) M = fmaxf(M, m_s[v][rr]);
+        wt_s[w][rr] = exp2f(m_s[w][rr] - M);
+      }
+      consumers_sync();
+      const bool whole = i0 == 0 && n == tr.count;
+      float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats;
+      for (int e = tid; e < a.G * (D / 4); e += kWarps * 32) {
+        const int row = e / (D / 4), dim = (e % (D / 4)) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(join_s + (w * kRows + row) * C::kOStride + dim);
+          const float sw = wt_s[w][row];
+          acc.x += v.x * sw;
+          acc.y += v.y * sw;
+          acc.z += v.z * sw;
+          acc.w += v.w * sw;
+          L += l_s[w][row] * sw;
+        }
+        if (whole) {
+          const float inv = s.p0 < 0 ? 0.f : 1.f / L;
+          const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          if (!isfinite(v.x) || !isfinite(v.y) || !isfinite(v.z) || !isfinite(v.w)) raise_flag(a.err, kErrNonFinite);
+          *reinterpret_cast<uint2*>(a.o + s.row0 * a.o_stride + (long long)(g * a.G + row) * D + dim) =
+              make_uint2(pack16<FP16>(v.x, v.y), pack16<FP16>(v.z, v.w));
+        } else {
+          *reinterpret_cast<float4*>(part + row * D + dim) = acc;
+          if (dim == 0) {
+            float M = m_s[0][row];
+#pragma unroll
+            for (int v = 1; v < kWarps; ++v) M = fmaxf(M, m_s[v][row]);
+            part[kRows * D + row] = M;
+            part[kRows * D + kRows + row] = L;
+          }
+        }
+      }
+      if (i0 == 0 && !whole && tid == 0) {
+        const unsigned long long last = pre_s[b] + (unsigned long long)(g + 1) * tr.count - 1;
+        split.rec[cta] = SplitRecord{s.row0, g, a.G, share_of(last, total, ctas)};
+      }
+      u += n;
+      consumers_sync();   // the joining buffer is free again
+    }
+  }
+}
+
+// Joins the parts of one split item (blockIdx.x: the CTA that began it) for one query head (blockIdx.y).
+// Warp w takes parts w, w + 4, ...; the four warps are then joined in order.
+constexpr int kJoinWarps = 4;
+constexpr int kJoinBatch = 8;
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const PagedArgs a, const DecodeSplit split) {
+  using C = Dec<D>;
+  constexpr int E = D / 32;
+  __shared__ float mw_s[kJoinWarps], lw_s[kJoinWarps];
+  __shared__ float red[kJoinWarps][D];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int first = (int)blockIdx.x, row = (int)blockIdx.y;
+  const SplitRecord rec = split.rec[first];
+  if (rec.until < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int parts = rec.until - first + 1;
+  float m = kNegBig, l = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int i0 = warp; i0 < parts; i0 += kJoinWarps * kJoinBatch) {
+    float mb[kJoinBatch], lb[kJoinBatch], ob[kJoinBatch][E];
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) {
+      const int c = i0 + i * kJoinWarps;
+      mb[i] = kNegBig;
+      lb[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) ob[i][e] = 0.f;
+      if (c < parts) {
+        const float* p = split.part + ((size_t)(first + c) * 2 + (c == 0 ? 1 : 0)) * C::kPartFloats;
+        mb[i] = __ldcg(p + kRows * D + row);
+        lb[i] = __ldcg(p + kRows * D + kRows + row);
+#pragma unroll
+        for (int e = 0; e < E; ++e) ob[i][e] = __ldcg(p + row * D + e * 32 + lane);
+      }
+    }
+    float mx = m;
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) mx = fmaxf(mx, mb[i]);
+    const float sc = exp2f(m - mx);
+    l *= sc;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= sc;
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) {
+      const float w = exp2f(mb[i] - mx);
+      l += lb[i] * w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += ob[i][e] * w;
+    }
+    m = mx;
+  }
+  if (lane == 0) {
+    mw_s[warp] = m;
+    lw_s[warp] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) red[warp][e * 32 + lane] = acc[e];
+  __syncthreads();
+  for (int d = threadIdx.x * 2; d < D; d += kJoinWarps * 64) {
+    float M = mw_s[0], L = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, mw_s[w]);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float sw = exp2f(mw_s[w] - M);
+      L += lw_s[w] * sw;
+      x += red[w][d] * sw;
+      y += red[w][d + 1] * sw;
+    }
+    x /= L;
+    y /= L;
+    if (!isfinite(x) || !isfinite(y)) raise_flag(a.err, kErrNonFinite);
+    *reinterpret_cast<uint32_t*>(a.o + rec.row * a.o_stride + (long long)(rec.g * a.G + row) * D + d) = pack16<FP16>(x, y);
+  }
+}
+
+template <int D, bool FP16>
+cudaError_t launch(const PagedMaps& maps, const PagedArgs& a, const DecodeSplit& split, int ctas, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)Dec<D>::smem(kPagedMaxSeqs));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Dec<D>::smem(a.B);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, decode_kernel<D, FP16>, maps, a, split);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(ctas, a.G);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, FP16>, a, split);
+}
+
+}  // namespace
+
+size_t paged_decode_scratch(int D, int ctas) {
+  return (size_t)ctas * (2 * (kRows * D + 2 * kRows) * sizeof(float) + sizeof(SplitRecord));
+}
+
+cudaError_t launch_paged_decode(const PagedMaps& maps, const PagedArgs& a, int D, void* scratch, int ctas, cudaStream_t st) {
+  DecodeSplit split;
+  split.part = static_cast<float*>(scratch);
+  split.rec = reinterpret_cast<SplitRecord*>(split.part + (size_t)ctas * 2 * (kRows * D + 2 * kRows));
+  if (D == 128) return a.fp16 ? launch<128, true>(maps, a, split, ctas, st) : launch<128, false>(maps, a, split, ctas, st);
+  return a.fp16 ? launch<64, true>(maps, a, split, ctas, st) : launch<64, false>(maps, a, split, ctas, st);
+}
+
+}  // namespace moe

@@ -32,7 +32,8 @@
  * operand type: at most half a step each, relative to the numerator); the single-token form keeps their
  * rounding remainders.  Results are identical from run to run.
  *
- * Conventions are those of moe.h: device pointers owned by the caller, 16-byte aligned; work is
+ * Conventions are those of moe.h: device pointers owned by the caller, 16-byte aligned (the int32 arrays
+ * 4-byte aligned, so they may be slices); work is
  * enqueued on `stream` (a cudaStream_t, NULL = legacy default stream) of the current device; argument
  * checks on the host before any launch; inputs never written, except that gqa_paged_plan's block
  * table is updated in place and n_free_out may be n_free.  Scratch and the error word live in the
@@ -140,8 +141,8 @@ moe_status gqa_paged_append(const gqa_paged_dims* dims, const uint16_t* k, const
  * (cut), more than max_new rows of a sequence (the first max_new are computed), a page number outside
  * 0 .. num_pages - 1 (its keys and values count as zeros).
  * Returns MOE_ERR_INVALID_ARG for a null pointer or a value of dims outside its meaning;
- * MOE_ERR_UNSUPPORTED for values outside the limits of dims; MOE_ERR_MISALIGNED for a pointer that is
- * not 16-byte aligned or a stride that is not a multiple of 8; MOE_ERR_WORKSPACE; MOE_ERR_CUDA as in
+ * MOE_ERR_UNSUPPORTED for values outside the limits of dims; MOE_ERR_MISALIGNED for a pointer off
+ * its alignment or a stride that is not a multiple of 8; MOE_ERR_WORKSPACE; MOE_ERR_CUDA as in
  * moe.h.  n_tokens == 0 or n_seqs == 0 is a no-op. */
 moe_status gqa_paged_attention(const gqa_paged_dims* dims, const uint16_t* q, const uint16_t* k_cache,
                                const uint16_t* v_cache, const int32_t* block_table, const int32_t* q_start,

@@ -47,15 +47,17 @@ def _calls(lib):
 
 @pytest.mark.parametrize("name", ["plan", "append", "attention"])
 def test_pointers_and_workspace(lib, name):
-    """1 for a null pointer, 3 for one off the 16-byte grid, 4 for a short workspace."""
+    """1 for a null pointer, 3 for one off its alignment (4 bytes for the int32 tables, 16 for all else),
+    4 for a short workspace."""
     call, pointers = _calls(lib)[name]
     d = moe.gqa_paged_dims(**GOOD)
     for p in pointers:
         assert call(d, **{p: None}) == 1, p
-        assert call(d, **{p: 264}) == 3, p
+        assert call(d, **{p: 264 if p in ("q", "k", "v", "kc", "vc", "o", "ws") else 258}) == 3, p
     assert call(d, nb=lib.gqa_paged_workspace_bytes(ctypes.byref(d)) - 1) == 4
     if name == "plan":
-        assert call(d, positions=264) == 3 and call(d, cap=-1) == 1
+        assert call(d, positions=258) == 3 and call(d, cap=-1) == 1
+        assert call(d, free=None, cap=0, ws=None) == 1 and call(d, free=None, cap=0, nb=0) == 4
 
 
 INVALID, UNSUPPORTED, MISALIGNED = 1, 2, 3
