@@ -340,61 +340,19 @@ bool encode_pages(CUtensorMap* m, const uint16_t* cache, const gqa_paged_dims& d
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// ---------------------------------------------------------------- attention, one warp per row and head
-__device__ __forceinline__ float to_f32(uint16_t b, int fp16) {
-  return fp16 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_f32(b);
-}
-
-__device__ __forceinline__ uint16_t from_f32(float v, int fp16) {
-  return fp16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
-
-template <int D>
-__global__ void __launch_bounds__(128) attend_kernel(const PagedArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(id / a.Hq), h = (int)(id % a.Hq), g = h / a.G;
-  if (t >= a.T) return;
-  bool bad = false;
-  for (int b = 0; b < a.B; ++b) {
-    const SeqRows s = load_seq(a, b, bad);
-    if (t < s.row0 || t >= s.row0 + s.n) continue;
-    const int p = s.p0 + (t - s.row0);
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      q[i] = to_f32(a.q[t * a.q_stride + (long long)h * D + lane + 32 * i], a.fp16);
-      o[i] = 0.f;
-    }
-    for (int j = 0; j <= p; ++j) {
-      if (!paged_sees(a, p, j)) continue;
-      const int page = __ldg(a.table + (size_t)b * a.max_pages + (j >> a.page_shift));
-      const bool ok = page >= 0 && page < a.num_pages;
-      bad |= !ok;
-      const long long at = ok ? page * a.page_stride + g * a.head_stride +
-                                    (j & ((1 << a.page_shift) - 1)) * a.row_stride + lane
-                              : 0;
-      float x = 0.f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) x = fmaf(q[i], ok ? to_f32(a.kc[at + 32 * i], a.fp16) : 0.f, x);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
-      x *= a.qk_scale;
-      const float mn = fmaxf(m, x), al = exp2f(m - mn), e = exp2f(x - mn);
-      m = mn;
-      l = l * al + e;
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = fmaf(e, ok ? to_f32(a.vc[at + 32 * i], a.fp16) : 0.f, o[i] * al);
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float v = p < 0 ? 0.f : o[i] / l;
-      if (!isfinite(v)) raise_flag(a.err, kErrNonFinite);
-      a.o[t * a.o_stride + (long long)h * D + lane + 32 * i] = from_f32(v, a.fp16);
-    }
-  }
-  if (bad) raise_flag(a.err, kErrBadPages);
+// The queries in boxes of one row tile: the G heads of a group for floor(128 / G) tokens.
+bool encode_queries(CUtensorMap* m, const uint16_t* q, const gqa_paged_dims& d) {
+  EncodeTiledFn f = encode_fn();
+  if (f == nullptr) return false;
+  const int G = d.n_heads / d.n_kv_heads;
+  const cuuint64_t dims[3] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.n_heads, (cuuint64_t)d.n_tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)d.head_dim * 2, (cuuint64_t)d.q_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return f(m, d.dtype == GQA_PAGED_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+           const_cast<uint16_t*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -405,7 +363,8 @@ using namespace moe;
 extern "C" size_t gqa_paged_workspace_bytes(const gqa_paged_dims* dims) {
   gqa_paged_dims d;
   if (check_paged_dims(dims, &d) != MOE_OK) return 0;
-  return kWsHeadBytes + (d.max_new == 1 ? paged_decode_scratch(d.head_dim, kPagedMaxCtas) : 0);
+  return kWsHeadBytes + (d.max_new == 1 ? paged_decode_scratch(d.head_dim, kPagedMaxCtas)
+                                        : paged_chunk_scratch(d.head_dim, kPagedMaxCtas));
 }
 
 extern "C" moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* ctx_len, const int32_t* new_len,
@@ -487,20 +446,17 @@ extern "C" moe_status gqa_paged_attention(const gqa_paged_dims* dims, const uint
   a.kv_len = kv_len;
   a.o = o;
   a.err = static_cast<uint32_t*>(workspace);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d.max_new == 1) {
-    int sms = 0;
-    PagedMaps maps;
-    std::memset(&maps, 0, sizeof(maps));
-    if (device_sms(&sms) != MOE_OK || !encode_pages(&maps.k, k_cache, d, 64) || !encode_pages(&maps.v, v_cache, d, 64))
-      return MOE_ERR_CUDA;
-    void* scratch = static_cast<uint8_t*>(workspace) + kWsHeadBytes;
-    return launch_paged_decode(maps, a, d.head_dim, scratch, std::min(sms, kPagedMaxCtas), s) == cudaSuccess ? MOE_OK
-                                                                                                            : MOE_ERR_CUDA;
-  }
-  const long long warps = (long long)d.n_tokens * d.n_heads;
-  const unsigned grid = (unsigned)((warps + 3) / 4);
-  if (d.head_dim == 128) attend_kernel<128><<<grid, 128, 0, s>>>(a);
-  else attend_kernel<64><<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const bool single = d.max_new == 1;
+  const int tile = single ? 64 : 128;   // positions of a cache tile
+  int sms = 0;
+  PagedMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  if (device_sms(&sms) != MOE_OK || !encode_pages(&maps.k, k_cache, d, tile) || !encode_pages(&maps.v, v_cache, d, tile) ||
+      (!single && !encode_queries(&maps.q, q, d)))
+    return MOE_ERR_CUDA;
+  void* scratch = static_cast<uint8_t*>(workspace) + kWsHeadBytes;
+  const int ctas = std::min(sms, kPagedMaxCtas);
+  const auto launch = single ? launch_paged_decode : launch_paged_chunk;
+  return launch(maps, a, d.head_dim, scratch, ctas, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK
+                                                                                                     : MOE_ERR_CUDA;
 }

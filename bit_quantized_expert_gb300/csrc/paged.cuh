@@ -100,11 +100,12 @@ __device__ __forceinline__ bool tile_open(const PagedArgs& a, int j0, int p_lo, 
 // second launch in order.  A CTA has at most two partials: slot 0 of an item that began before it, slot
 // 1 of one that goes on after it.
 // ------------------------------------------------------------------------------------------
-constexpr int kPagedMaxCtas = 256;
+constexpr int kPagedMaxCtas = 160;   // one CTA per SM, of 152
 
 // What the joining launch needs of a CTA whose last item goes on in later CTAs (until < 0: none).
 struct SplitRecord {
-  int32_t row, g, rows, until;   // first row of o, head group, rows of the item, last CTA with a part
+  int32_t row, g, rows, until;   // first row of o, head group, tokens of the item, last CTA with a part
+  int32_t p_lo;                  // position of the item's first token
 };
 
 // Exclusive sums of cost(b) over b = 0 .. B - 1 into pre_s[0 .. B], by a whole block of NT threads.
@@ -189,6 +190,8 @@ __device__ __forceinline__ float2 unpack16(uint32_t x) {
 // The two forms and their joining launch
 // ------------------------------------------------------------------------------------------
 size_t paged_decode_scratch(int D, int ctas);      // bytes of partials and records
+size_t paged_chunk_scratch(int D, int ctas);
+cudaError_t launch_paged_chunk(const PagedMaps& maps, const PagedArgs& a, int D, void* scratch, int ctas, cudaStream_t st);
 cudaError_t launch_paged_decode(const PagedMaps& maps, const PagedArgs& a, int D, void* scratch, int ctas, cudaStream_t st);
 
 }  // namespace moe

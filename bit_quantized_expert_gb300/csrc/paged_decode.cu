@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (i0 == 0 && !whole && tid == 0) {
         const unsigned long long last = pre_s[b] + (unsigned long long)(g + 1) * tr.count - 1;
-        split.rec[cta] = SplitRecord{s.row0, g, a.G, share_of(last, total, ctas)};
+        split.rec[cta] = SplitRecord{s.row0, g, 1, share_of(last, total, ctas), s.p0};
       }
       u += n;
       consumers_sync();   // the joining buffer is free again
