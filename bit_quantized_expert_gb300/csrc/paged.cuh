@@ -66,12 +66,14 @@ struct TileRange {
 
 template <int TN>
 __device__ __forceinline__ TileRange visible_tiles(const PagedArgs& a, int p_lo, int p_hi) {
+  constexpr int kShift = TN == 64 ? 6 : 7;
+  static_assert(TN == 1 << kShift, "tile");
   TileRange r;
   r.head = r.skip = 0;
-  r.count = p_hi < 0 ? 1 : p_hi / TN + 1;
+  r.count = p_hi < 0 ? 1 : (p_hi >> kShift) + 1;
   if (a.window > 0 && p_hi >= 0) {
-    const int first = max(0, p_lo - a.window + 1) / TN;              // first tile of the window
-    const int head = (min(a.sinks, p_hi + 1) + TN - 1) / TN;
+    const int first = max(0, p_lo - a.window + 1) >> kShift;         // first tile of the window
+    const int head = (min(a.sinks, p_hi + 1) + TN - 1) >> kShift;
     if (head < first) {
       r.head = head;
       r.skip = first - head;

@@ -27,7 +27,8 @@ namespace moe {
 namespace {
 
 constexpr int kTN = 128;                    // positions per cache tile
-constexpr int kThreads = 384;              // two softmax warpgroups, one for copies and products
+constexpr int kThreads = 384;               // two softmax warpgroups, one for copies and products
+constexpr int kSoftmaxWarps = 8;
 // Registers a thread: 168 at launch; 2 * 208 + 88 = 3 * 168 after the split.
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr int kItemRows = 256;              // two row tiles
@@ -41,7 +42,7 @@ struct Chunk {
   static constexpr int kTileBytes = kBoxes * kBoxBytes;        // a row tile of q, a tile of keys or of values
   static constexpr int kSlots = 4 * 32768 / kTileBytes;        // ring of key and value tiles
   static constexpr int kPartFloats = kItemRows * (D + 2);      // O by columns, then max, then sum
-  static size_t smem(int B) { return 1024 + (size_t)(2 + kSlots) * kTileBytes + ((size_t)B + 1) * 8; }
+  static size_t smem(int B) { return 1024 + (size_t)(2 + kSlots) * kTileBytes + ((size_t)B + 1) * 4; }
 };
 
 struct ChunkSplit {
@@ -49,7 +50,8 @@ struct ChunkSplit {
   SplitRecord* rec;    // [ctas]
 };
 
-// One item: tokens t0 .. t0 + n - 1 of a sequence, at positions p_lo .. p_hi.
+// One row block: tokens t0 .. t0 + n - 1 of a sequence, at positions p_lo .. p_hi; it is an item for each
+// key/value head.
 struct Item {
   int t0, n, p_lo, p_hi;
   TileRange r;
@@ -65,12 +67,171 @@ __device__ __forceinline__ Item item_of(const PagedArgs& a, const SeqRows& s, in
   return x;
 }
 
-// D[tmem] (+)= A[tmem] B[smem]: A K-major 16-bit pairs in tensor memory.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// A CTA's share: units lo .. hi - 1 of (sequence, row block, head, cache tile), and the row block that holds
+// unit lo (or ends just before it), which begins at unit `at`.
+struct Share {
+  unsigned long long lo, hi, at, total;
+  int b, qt, ctas;
+  unsigned long long slack;
+};
+
+// A cut of the order within the item of units s .. e - 1, moved to the item's nearer end if that is within
+// `slack`: what a part costs (a partial result written, read and joined) is more than that many tiles of
+// imbalance.
+__device__ __forceinline__ unsigned long long snap(unsigned long long x, unsigned long long s, unsigned long long e,
+                                                   unsigned long long slack) {
+  const unsigned long long down = x - s, up = e - x;
+  if (down <= slack && down <= up) return s;
+  return up <= slack ? e : x;
+}
+
+// x / d, in 32 bits where x allows.
+__device__ __forceinline__ unsigned long long quotient(unsigned long long x, uint32_t d) {
+  return (x >> 32) == 0 ? (uint32_t)x / d : x / d;
+}
+
+// Where the c-th of n equal shares of `total` units begins.
+__device__ __forceinline__ unsigned long long share_start(unsigned long long total, int c, int n) {
+  const unsigned long long q = quotient(total, (uint32_t)n);
+  return q * c + (uint32_t)(total - q * n) * (uint32_t)c / (uint32_t)n;
+}
+
+// Finds this CTA's share, the whole block together: row blocks per sequence are scanned into pre_s[0 .. B],
+// then their costs (tiles times heads), a run of consecutive row blocks a thread; the threads whose runs
+// hold the two cuts walk theirs once more.
+__device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint32_t* pre_s, unsigned long long* warp_s,
+                                           Share* share_s, bool& bad) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
+  uint32_t* warp32_s = reinterpret_cast<uint32_t*>(warp_s + kWarps);
+  unsigned long long blocks = 0, total = 0;
+  {
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    uint32_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      pre_s[b] = mine;
+      mine += (uint32_t)(load_seq(a, b, bad).n + tokens - 1) / (uint32_t)tokens;
+    }
+    uint32_t inc = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+      if (lane >= off) inc += x;
+    }
+    if (lane == 31) warp32_s[warp] = inc;
+    __syncthreads();
+    uint32_t before = inc - mine, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const uint32_t x = warp32_s[w];
+      before += w < warp ? x : 0u;
+      all += x;
+    }
+    for (int b = b0; b < b1; ++b) pre_s[b] += before;
+    if (tid == 0) pre_s[a.B] = all;
+    blocks = all;
+    __syncthreads();
+  }
+  const uint32_t per = (uint32_t)(blocks + kThreads - 1) / kThreads;
+  const uint32_t i0 = (uint32_t)min((unsigned long long)tid * per, blocks);
+  const uint32_t i1 = (uint32_t)min((unsigned long long)i0 + per, blocks);
+  int b_mine = 0;
+  if (i0 < i1) {
+    int lo = 0, hi = a.B - 1;   // the sequence that holds row block i0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre_s[mid] <= i0) lo = mid;
+      else hi = mid - 1;
+    }
+    b_mine = lo;
+  }
+  // body(b, qt, tiles) for this thread's row blocks
+  auto each = [&](auto&& body) {
+    int b = b_mine;
+    for (uint32_t i = i0; i < i1; ++b) {
+      const SeqRows s = load_seq(a, b, bad);
+      for (; i < i1 && i < pre_s[b + 1]; ++i) {
+        const int qt = (int)(i - pre_s[b]);
+        body(b, qt, (uint32_t)item_of(a, s, qt, tokens).r.count);
+      }
+    }
+  };
+  unsigned long long mine = 0;
+  each([&](int, int, uint32_t c) { mine += c; });
+  unsigned long long inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+    if (lane >= off) inc += x;
+  }
+  if (lane == 31) warp_s[warp] = inc;
+  __syncthreads();
+  unsigned long long before = inc - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const unsigned long long x = warp_s[w];
+    before += w < warp ? x : 0ull;
+    total += x;
+  }
+  before *= a.Hkv;
+  mine *= a.Hkv;
+  total *= a.Hkv;
+  const int ctas = (int)min((unsigned long long)gridDim.x, total), cta = (int)blockIdx.x;   // no more shares than tiles
+  if (cta >= ctas) return;
+  const unsigned long long slack = max(2ull, quotient(total, (uint32_t)ctas) / 32);
+  const unsigned long long lo = share_start(total, cta, ctas), hi = share_start(total, cta + 1, ctas);
+  if ((lo >= before && lo < before + mine) || (hi >= before && hi < before + mine)) {
+    unsigned long long at = before;
+    each([&](int b, int qt, uint32_t c) {
+      const unsigned long long end = at + (unsigned long long)c * a.Hkv;
+      auto cut = [&](unsigned long long x) {
+        const unsigned long long s = at + quotient(x - at, c) * c;
+        return x == s ? x : snap(x, s, s + c, slack);
+      };
+      if (lo >= at && lo < end) {
+        share_s->lo = cut(lo);
+        share_s->at = at;
+        share_s->b = b;
+        share_s->qt = qt;
+      }
+      if (hi >= at && hi < end) share_s->hi = cut(hi);
+      at = end;
+    });
+  }
+  if (tid == 0) {
+    if (hi == total) share_s->hi = total;
+    share_s->total = total;
+    share_s->ctas = ctas;
+    share_s->slack = slack;
+  }
+}
+
+// Four products of one 64-wide piece of the inner axis, in one statement: every descriptor is in a register
+// before the first, so that the issuing warp, which shares its scheduler with softmax warps, waits for one
+// slot a product and not for its descriptor arithmetic.
+// D[tmem] (+)= A[smem] B[smem]^T, both K-major in the 128-byte swizzle: 32 bytes a step.
+__device__ __forceinline__ void tc_mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, t;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.ne.b32 t, %11, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, t;\n\t}" ::"r"(d),
+      "l"(a), "l"(a + 2u), "l"(a + 4u), "l"(a + 6u), "l"(b), "l"(b + 2u), "l"(b + 4u), "l"(b + 6u), "r"(idesc), "r"(acc),
+      "r"(1u)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]: A 16-bit pairs in tensor memory (8 columns a step), B as desc_values (2048
+// bytes a step).
+__device__ __forceinline__ void tc_mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.ne.b32 t, %11, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, t;\n\t}" ::"r"(d),
+      "r"(a), "r"(a + 8u), "r"(a + 16u), "r"(a + 24u), "l"(b), "l"(b + 128u), "l"(b + 256u), "l"(b + 384u), "r"(idesc),
+      "r"(acc), "r"(1u)
       : "memory");
 }
 
@@ -92,7 +253,7 @@ __device__ __forceinline__ uint64_t desc_values(uint32_t saddr, uint32_t box_byt
       "=r"(v[o + 7]), "=r"(v[o + 8]), "=r"(v[o + 9]), "=r"(v[o + 10]), "=r"(v[o + 11]), "=r"(v[o + 12]),           \
       "=r"(v[o + 13]), "=r"(v[o + 14]), "=r"(v[o + 15])
 
-// 32 consecutive columns of this thread's row; valid only after tmem_wait_ld, which ties them.
+// 32 consecutive columns of this thread's row, load and wait in one statement.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "{\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -148,6 +309,36 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Pairs of fp32 values in one register pair.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpair2(uint64_t v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// The lowest n bits (n any integer).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
 // 0xFFFF in each half of w that holds a non-finite value.
 template <bool FP16>
 __device__ __forceinline__ uint32_t non_finite16(uint32_t w) {
@@ -183,26 +374,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a, const ChunkSplit split) {
   using C = Chunk<D>;
   extern __shared__ uint8_t sm_raw[];
-  // barriers: key/value slots (full, empty), q (full, empty), per row tile S full, P full, O full, O empty; second
-  // half of the values clean
-  __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 2 + 8 + 1];
-  __shared__ unsigned long long warp_s[kThreads / 32];
+  // barriers: key/value slots (full, empty), q (full, empty), per row tile S full, P
+  // full (its first and its second half), O full, O empty; second half of the values clean
+  __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 2 + 8 + 3];
+  __shared__ unsigned long long warp_s[kThreads / 32 * 2];
+  __shared__ Share share_s;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   __shared__ int bad_s[4];   // segment + 1 whose values had non-finite ones that a row sees
   const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t sQ = base, sKV = base + 2 * C::kTileBytes;
-  unsigned long long* pre_s =
-      reinterpret_cast<unsigned long long*>(sm_raw + (base - raw) + (2 + C::kSlots) * C::kTileBytes);
+  uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (base - raw) + (2 + C::kSlots) * C::kTileBytes);
   const uint32_t bar0 = smem_u32(bars);
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (C::kSlots + s); };
   constexpr int kB = 2 * C::kSlots;
-  const uint32_t QFULL = bar0 + 8u * kB, QEMPTY = QFULL + 8u, CLEAN = bar0 + 8u * (kB + 10);
+  const uint32_t QFULL = bar0 + 8u * kB, QEMPTY = QFULL + 8u, CLEAN = bar0 + 8u * (kB + 12);
   auto SFULL = [&](int t) { return bar0 + 8u * (kB + 2 + t); };
-  auto PFULL = [&](int t) { return bar0 + 8u * (kB + 4 + t); };
-  auto OFULL = [&](int t) { return bar0 + 8u * (kB + 6 + t); };
-  auto OEMPTY = [&](int t) { return bar0 + 8u * (kB + 8 + t); };
+  auto PFULL = [&](int t, int part) { return bar0 + 8u * (kB + 4 + 2 * t + part); };
+  auto OFULL = [&](int t) { return bar0 + 8u * (kB + 8 + t); };
+  auto OEMPTY = [&](int t) { return bar0 + 8u * (kB + 10 + t); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = (int)blockIdx.x;
   const int tpt = 128 / a.G, tokens = 2 * tpt;
@@ -216,74 +407,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(QEMPTY, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(SFULL(t), 1);
-      mbar_init(PFULL(t), 4);
+      mbar_init(PFULL(t, 0), 4);
+      mbar_init(PFULL(t, 1), 4);
       mbar_init(OFULL(t), 1);
       mbar_init(OEMPTY(t), 4);
     }
     mbar_init(CLEAN, 4);
     abort_s = 0;
     for (int i = 0; i < 4; ++i) bad_s[i] = 0;
+    share_s.lo = share_s.hi = 0;
     mbar_fence_init();
     prefetch_tmap(&maps.q);
     prefetch_tmap(&maps.k);
     prefetch_tmap(&maps.v);
   }
-  if (warp == 9) {
+  if (warp == kSoftmaxWarps + 1) {
     tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_relinquish();
   }
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- this CTA's share: units lo .. hi - 1 of (sequence, head, row block, cache tile)
   bool bad = false;
-  scan_sequences<kThreads>(a.B, pre_s, warp_s, [&](int b) {
-    const SeqRows s = load_seq(a, b, bad);
-    unsigned long long sum = 0;
-    for (int qt = 0; qt * tokens < s.n; ++qt) sum += item_of(a, s, qt, tokens).r.count;
-    return sum * a.Hkv;
-  });
+  find_share(a, tokens, pre_s, warp_s, &share_s, bad);
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
+  if (tid == 0) split.rec[cta].until = -1;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const unsigned long long total = pre_s[a.B];
-  const int ctas = (int)min((unsigned long long)gridDim.x, total);   // every share holds a tile
-  if (tid == 0) split.rec[cta].until = -1;
-  const bool active = cta < ctas;
-  const unsigned long long lo = active ? total * cta / ctas : 0, hi = active ? total * (cta + 1) / ctas : 0;
 
   // Walks the segments of the share: body(b, s, g, item, i0, n, u) for tiles i0 .. i0 + n - 1 of an item,
   // the first of them unit u; stops when the body returns false.
   auto walk = [&](auto&& body) {
-    unsigned long long u = lo;
-    for (int b = active ? find_sequence(pre_s, a.B, lo) : 0; u < hi; ++b) {
-      if (pre_s[b + 1] <= u) continue;
+    unsigned long long u = share_s.lo, at = share_s.at;
+    const unsigned long long hi = share_s.hi;
+    int b = share_s.b, qt = share_s.qt;
+    while (u < hi) {
       const SeqRows s = load_seq(a, b, bad);
-      const unsigned long long per_head = (pre_s[b + 1] - pre_s[b]) / a.Hkv;
-      int g = (int)((u - pre_s[b]) / per_head);
-      unsigned long long at = pre_s[b] + g * per_head;   // first unit of the item being looked at
-      int qt = 0;
-      while (u < hi && g < a.Hkv) {
+      for (; u < hi && qt * tokens < s.n; ++qt) {
         const Item x = item_of(a, s, qt, tokens);
-        if (at + x.r.count > u) {
+        for (int g = 0; g < a.Hkv && u < hi; ++g, at += x.r.count) {
+          if (at + x.r.count <= u) continue;
           const int i0 = (int)(u - at), n = (int)min((unsigned long long)(x.r.count - i0), hi - u);
           if (!body(b, s, g, x, i0, n, u)) return;
           u += n;
         }
-        at += x.r.count;
-        if (++qt * tokens >= s.n) {
-          qt = 0;
-          ++g;
-        }
       }
+      qt = 0;
+      ++b;
     }
   };
 
-  if (warp >= 8) {
+  if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 8) {
+    if (warp == kSoftmaxWarps) {
     // ---- copies
     const int ppt = max(1, kTN >> a.page_shift), box_rows = min(kTN, 1 << a.page_shift);
     const int batch = 32 / ppt;                              // tiles whose page numbers the lanes hold
@@ -340,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     });
     if (bad) raise_flag(a.err, kErrBadPages);
     (void)stop;
-    } else if (warp == 9) {
+    } else if (warp == kSoftmaxWarps + 1) {
     // ---- tensor-core instructions
     if (lane == 0) {
       const uint32_t fmt = FP16 ? 0u : ((1u << 7) | (1u << 10));
@@ -351,11 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto scores = [&](int t, int tile) {   // S_t = Q_t K^T
         const int sl = (2 * tile) % C::kSlots;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::kBoxBytes + (kk & 3) * 32;
-          tc_mma_f16(tmem + t * 128, smem_desc_sw128(sQ + t * C::kTileBytes + off),
-                     smem_desc_sw128(sKV + sl * C::kTileBytes + off), id_s, kk != 0);
-        }
+        for (int box = 0; box < C::kBoxes; ++box)
+          tc_mma4_ss(tmem + t * 128, smem_desc_sw128(sQ + t * C::kTileBytes + box * C::kBoxBytes),
+                     smem_desc_sw128(sKV + sl * C::kTileBytes + box * C::kBoxBytes), id_s, box != 0);
         tc_commit(SFULL(t));
       };
       walk([&](int, const SeqRows&, int, const Item& x, int i0, int n, unsigned long long) {
@@ -375,13 +551,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             return false;
           for (int t = 0; t < nt; ++t) {
             if (i == 0 && outs[t] > 0 && !wait(OEMPTY(t), outs[t] - 1)) return false;
-            if (!wait(PFULL(t), done[t])) return false;
+            for (int part = 0; part < 2; ++part) {
+              if (!wait(PFULL(t, part), done[t])) return false;
+              tc_fence_after();
+              tc_mma4_ts(tmem + kTmemO + t * 128, tmem + t * 128 + part * 32,
+                         desc_values(sKV + sv * C::kTileBytes + part * 8192, C::kBoxBytes), id_o, (i | part) != 0);
+            }
             ++done[t];
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kTN / 16; ++kk)
-              tc_mma_ts(tmem + kTmemO + t * 128, tmem + t * 128 + kk * 8,
-                        desc_values(sKV + sv * C::kTileBytes + kk * 2048, C::kBoxBytes), id_o, (i | kk) != 0);
             if (t == nt - 1) tc_commit(EMPTY(sv));
             if (more) {
               scores(t, it + 1);
@@ -403,20 +579,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---- softmax: row `r` of row tile `t`
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G, head = r % a.G;
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + t * 128 + lanes, tO = tmem + kTmemO + t * 128 + lanes;
     int it = 0, seg = 0, done = 0, outs = 0;
     walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, unsigned long long u) {
-      const bool mine = t == 0 || x.n > tpt;
-      const bool live = mine && tok < tpt && t * tpt + tok < x.n;
-      const int p = live ? x.p_lo + t * tpt + tok : -1;      // a row that is no token sees nothing
-      float m = -INFINITY, negm = 0.f, l = 0.f;              // negm = -m in base-2 units (0 while nothing is seen)
-      if (!mine) {
+      const int nt = x.n > tpt ? 2 : 1;
+      if (t >= nt) {
         it += n;
         ++seg;
         return true;
       }
+      const bool live = tok < tpt && t * tpt + tok < x.n;
+      const int p = live ? x.p_lo + t * tpt + tok : -1;      // a row that is no token sees nothing
+      float m = -INFINITY, negm = 0.f, l = 0.f;              // negm = -m in base-2 units (0 while nothing is seen)
       for (int i = 0; i < n; ++i, ++it) {
         const int j0 = x.r.tile(i0 + i) * kTN;
         const bool open = tile_open<kTN>(a, j0, x.p_lo, x.p_hi);
@@ -424,11 +600,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++done;
         tc_fence_after();
         if (!open && (t == 0 || C::kBoxes == 2)) {
-          // Take non-finite values out of this thread's position of the value tile: its 64-dim box t, or all
-          // of it where the other row tile's warps have no rows.
+          // Take non-finite values out of position r of the value tile: its 64-dim box t, or all of it where
+          // the other row tile has no rows.
           const int seq = 2 * it + 1, sl = seq % C::kSlots;
           if (!mbar_wait_warp(FULL(sl), (seq / C::kSlots) & 1, &abort_s, a.err)) return false;
-          const bool both = x.n > tpt && C::kBoxes == 2;
+          const bool both = nt == 2 && C::kBoxes == 2;
           bool found = false;
           for (int box = both ? t : 0; box < (both ? t + 1 : C::kBoxes); ++box) {
             const uint32_t rowaddr = sKV + sl * C::kTileBytes + box * C::kBoxBytes + r * 128;
@@ -461,70 +637,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sr[128];
         tmem_ld128(tS, sr);
         if (!open) {
-          const int c_hi = p - j0;
-          if (a.window == 0) {
+          // visible: j <= p, and j > p - window or j < sinks; 32 positions a word
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c > c_hi) sr[c] = 0xFF800000u;
-          } else {
-            const int c_lo = p - a.window - j0, c_s = a.sinks - j0;
+          for (int w = 0; w < 4; ++w) {
+            const int j = j0 + 32 * w;
+            uint32_t see = low_bits(p + 1 - j);
+            if (a.window > 0) see &= ~low_bits(p - a.window + 1 - j) | low_bits(a.sinks - j);
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c > c_hi || (c <= c_lo && c >= c_s)) sr[c] = 0xFF800000u;
+            for (int c = 0; c < 32; ++c) sr[32 * w + c] = (see >> c) & 1u ? sr[32 * w + c] : 0xFF800000u;
           }
         }
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          mx0 = fmaxf(mx0, __uint_as_float(sr[c]));
-          mx1 = fmaxf(mx1, __uint_as_float(sr[c + 1]));
-          mx2 = fmaxf(mx2, __uint_as_float(sr[c + 2]));
-          mx3 = fmaxf(mx3, __uint_as_float(sr[c + 3]));
+        for (int c = 0; c < 128; c += 8) {
+          mx0 = max3(mx0, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+          mx1 = max3(mx1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+          mx2 = max3(mx2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
+          mx3 = max3(mx3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
         }
         const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-        // Move the reference if the new maximum is well above it (or is the first).
+        // The reference moves if the new maximum is well above it (or is the first).
         const bool move = mx > m && (m == -INFINITY || (mx - m) * a.qk_scale > kLazy);
-        float alpha = 1.f;
-        if (move) {
-          const float nn = -(mx * a.qk_scale);
-          alpha = m == -INFINITY ? 0.f : ex2(nn - negm);
-          m = mx;
-          negm = nn;
-          l *= alpha;
-        }
-        if (i > 0 && __any_sync(0xFFFFFFFFu, move)) {
-          for (int c = 0; c < D; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(tO + c, v);
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          float alpha = 1.f;
+          if (move) {
+            const float nn = -(mx * a.qk_scale);
+            alpha = m == -INFINITY ? 0.f : ex2(nn - negm);
+            m = mx;
+            negm = nn;
+            l *= alpha;
+          }
+          if (i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t v[16];
+              tmem_ld16_wait(tO + c, v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-            tmem_st32(tO + c, v);
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+              tmem_st16(tO + c, v);
+            }
           }
         }
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+        const uint64_t scale2 = pair2(a.qk_scale, a.qk_scale), negm2 = pair2(negm, negm);
+        uint64_t sum0 = 0, sum1 = 0;   // two fp32 sums each
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float p0 = ex2(fmaf(__uint_as_float(sr[c + e]), a.qk_scale, negm));
-            const float p1 = ex2(fmaf(__uint_as_float(sr[c + e + 1]), a.qk_scale, negm));
-            const float p2 = ex2(fmaf(__uint_as_float(sr[c + e + 2]), a.qk_scale, negm));
-            const float p3 = ex2(fmaf(__uint_as_float(sr[c + e + 3]), a.qk_scale, negm));
-            l0 += p0;
-            l1 += p1;
-            l2 += p2;
-            l3 += p3;
+            const float2 x0 = unpair2(fma2(pair2(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])), scale2, negm2));
+            const float2 x1 = unpair2(fma2(pair2(__uint_as_float(sr[c + e + 2]), __uint_as_float(sr[c + e + 3])), scale2, negm2));
+            const float p0 = ex2(x0.x), p1 = ex2(x0.y), p2 = ex2(x1.x), p3 = ex2(x1.y);
+            sum0 = add2(sum0, pair2(p0, p1));
+            sum1 = add2(sum1, pair2(p2, p3));
             pk[e / 2] = pack16<FP16>(p0, p1);
             pk[e / 2 + 1] = pack16<FP16>(p2, p3);
           }
           tmem_st16(tS + c / 2, pk);
+          if (c == 32 || c == 96) {   // half of P is there: its part of the product can start
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(PFULL(t, c / 64));
+          }
         }
-        l += (l0 + l1) + (l2 + l3);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(PFULL(t));
+        const float2 s0 = unpair2(sum0), s1 = unpair2(sum1);
+        l += (s0.x + s0.y) + (s1.x + s1.y);
       }
       // ---- the item's result, or this share's part of it
       const int my_seg = seg++;
@@ -534,40 +712,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = i0 == 0 && n == x.r.count;
       const bool hurt = *(volatile int*)&bad_s[my_seg & 3] == my_seg + 1;
       const float inv = p < 0 ? 0.f : 1.f / l;
-      uint16_t* orow = a.o + (long long)(s.row0 + x.t0 + t * tpt + tok) * a.o_stride + (long long)(g * a.G + head) * D;
-      float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats;
+      uint16_t* orow = a.o + (long long)(s.row0 + x.t0 + t * tpt + tok) * a.o_stride + (long long)(g * a.G + r % a.G) * D;
+      float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats + t * 128 + r;
       bool nonfinite = false;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
         tmem_ld32(tO + c, v);
-        float f[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = p < 0 ? 0.f : __uint_as_float(v[e]);
+        for (int e = 0; e < 32; ++e) v[e] = p < 0 ? 0u : v[e];
         if (hurt && live) {
           float extra[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) extra[e] = 0.f;
           add_non_finite<FP16>(a, a.table + (size_t)b * a.max_pages, x.r, i0, n, x.p_lo, x.p_hi, p, g, c, extra);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] += extra[e];
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + extra[e]);
         }
         if (whole) {
-          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float f0 = f[e] * inv, f1 = f[e + 1] * inv;
-            nonfinite |= !isfinite(f0) || !isfinite(f1);
-            w[e / 2] = pack16<FP16>(f0, f1);
-          }
-          if (live) {
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(orow + c + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int k = 0; k < 4; ++k) {
+              const float f0 = __uint_as_float(v[e + 2 * k]) * inv, f1 = __uint_as_float(v[e + 2 * k + 1]) * inv;
+              nonfinite |= !isfinite(f0) || !isfinite(f1);
+              w[k] = pack16<FP16>(f0, f1);
+            }
+            if (live) *reinterpret_cast<uint4*>(orow + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) part[(c + e) * kItemRows + t * 128 + r] = f[e];
+          for (int e = 0; e < 32; ++e) part[(c + e) * kItemRows] = __uint_as_float(v[e]);
         }
       }
       tc_fence_before();
@@ -576,11 +752,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live && whole && nonfinite) raise_flag(a.err, kErrNonFinite);
       if (!whole) {
         if (live) {
-          part[D * kItemRows + t * 128 + r] = m == -INFINITY ? -1e30f : -negm;
-          part[(D + 1) * kItemRows + t * 128 + r] = l;
+          part[D * kItemRows] = m == -INFINITY ? -1e30f : -negm;
+          part[(D + 1) * kItemRows] = l;
         }
-        if (i0 == 0 && tid == 0)
-          split.rec[cta] = SplitRecord{s.row0 + x.t0, g, x.n, share_of(u + x.r.count - 1, total, ctas), x.p_lo};
+        if (i0 == 0 && tid == 0) {
+          // the last CTA with a part: the one whose share holds the item's last unit
+          const unsigned long long e = u + x.r.count, total = share_s.total;
+          int c = share_of(e - 1, total, share_s.ctas);
+          while (c > cta + 1 && snap(share_start(total, c, share_s.ctas), u, e, share_s.slack) >= e) --c;
+          split.rec[cta] = SplitRecord{s.row0 + x.t0, g, x.n, c, x.p_lo};
+        }
       }
       return true;
     });
@@ -593,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kSoftmaxWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
