@@ -29,8 +29,8 @@ namespace {
 constexpr int kTN = 128;                    // positions per cache tile
 constexpr int kThreads = 384;               // two softmax warpgroups, one for copies and products
 constexpr int kSoftmaxWarps = 8;
-// Registers a thread: 168 at launch; 2 * 208 + 88 = 3 * 168 after the split.
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+// Registers a thread: 168 at launch; 2 * 200 + 104 = 3 * 168 after the split.
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kItemRows = 256;              // two row tiles
 constexpr uint32_t kTmemO = 256;            // columns: S0 0, S1 128, O0 256, O1 384
 constexpr float kLazy = 8.f;                // base-2 units the running maximum may lag behind
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Chunk<D>;
   extern __shared__ uint8_t sm_raw[];
   // barriers: key/value slots (full, empty), q (full, empty), per row tile S full, P
-  // full (its first and its second half), O full, O empty; second half of the values clean
+  // full (its first and its second half), O full, O empty; values clean
   __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 2 + 8 + 3];
   __shared__ unsigned long long warp_s[kThreads / 32 * 2];
   __shared__ Share share_s;
@@ -524,54 +524,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t fmt = FP16 ? 0u : ((1u << 7) | (1u << 10));
       const uint32_t id_s = (1u << 4) | fmt | ((kTN >> 3) << 17) | ((128u >> 4) << 24);
       const uint32_t id_o = (1u << 4) | fmt | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
-      int it = 0, items = 0, cleans = 0, done[2] = {0, 0}, outs[2] = {0, 0};   // P tiles and items so far, per row tile
-      auto wait = [&](uint32_t bar, int phase) { return mbar_wait(bar, phase & 1, &abort_s, a.err); };
-      auto scores = [&](int t, int tile) {   // S_t = Q_t K^T
-        const int sl = (2 * tile) % C::kSlots;
+      constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
+      constexpr uint32_t kTurn = C::kSlots == 4 ? 2 : 3;                                   // log2 of the slots
+      const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV, C::kBoxBytes);
+      uint32_t q = 0;   // ring position of the tile's keys; its values follow
+      uint32_t items = 0, cleans = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
+      auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait(bar, phase & 1, &abort_s, a.err); };
+      auto landed = [&](uint32_t pos) { return wait(FULL(pos & (C::kSlots - 1)), pos >> kTurn); };
+      auto scores = [&](int t, uint32_t pos) {   // S_t = Q_t K^T
+        const uint64_t k = dk + (pos & (C::kSlots - 1)) * kTileUnits;
 #pragma unroll
         for (int box = 0; box < C::kBoxes; ++box)
-          tc_mma4_ss(tmem + t * 128, smem_desc_sw128(sQ + t * C::kTileBytes + box * C::kBoxBytes),
-                     smem_desc_sw128(sKV + sl * C::kTileBytes + box * C::kBoxBytes), id_s, box != 0);
+          tc_mma4_ss(tmem + t * 128, dq + t * kTileUnits + box * kBoxUnits, k + box * kBoxUnits, id_s, box != 0);
         tc_commit(SFULL(t));
       };
-      walk([&](int, const SeqRows&, int, const Item& x, int i0, int n, unsigned long long) {
-        const int nt = x.n > tpt ? 2 : 1;
-        if (!wait(QFULL, items) || !wait(FULL((2 * it) % C::kSlots), 2 * it / C::kSlots)) return false;
+      auto values = [&](int t, uint32_t pos, uint32_t done, bool first) {   // O_t (+)= P_t V, P in two halves
+        const uint64_t v = dv + (pos & (C::kSlots - 1)) * kTileUnits;
+        if (!wait(PFULL(t, 0), done)) return false;
         tc_fence_after();
-        for (int t = 0; t < nt; ++t) scores(t, it);
-        tc_commit(EMPTY((2 * it) % C::kSlots));
+        tc_mma4_ts(tmem + kTmemO + t * 128, tmem + t * 128, v, id_o, !first);
+        if (!wait(PFULL(t, 1), done)) return false;
+        tc_fence_after();
+        tc_mma4_ts(tmem + kTmemO + t * 128, tmem + t * 128 + 32, v + (8192u >> 4), id_o, 1u);
+        return true;
+      };
+      walk([&](int, const SeqRows&, int, const Item& x, int i0, int n, unsigned long long) {
+        const bool two = x.n > tpt;
+        if (!wait(QFULL, items++) || !landed(q)) return false;
+        tc_fence_after();
+        scores(0, q);
+        if (two) scores(1, q);
+        tc_commit(EMPTY(q & (C::kSlots - 1)));
         if (n == 1) tc_commit(QEMPTY);
-        for (int i = 0; i < n; ++i, ++it) {
+        for (int i = 0; i < n; ++i, q += 2) {
           const bool more = i + 1 < n;
-          const int sv = (2 * it + 1) % C::kSlots;
-          if (more && !wait(FULL((2 * it + 2) % C::kSlots), (2 * it + 2) / C::kSlots)) return false;
-          if (!wait(FULL(sv), (2 * it + 1) / C::kSlots)) return false;
-          if (nt == 2 && C::kBoxes == 2 && !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi) &&
-              !wait(CLEAN, cleans++))
+          if (!landed(q + 1)) return false;
+          if (two && C::kBoxes == 2 && !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi) && !wait(CLEAN, cleans++))
             return false;
-          for (int t = 0; t < nt; ++t) {
-            if (i == 0 && outs[t] > 0 && !wait(OEMPTY(t), outs[t] - 1)) return false;
-            for (int part = 0; part < 2; ++part) {
-              if (!wait(PFULL(t, part), done[t])) return false;
-              tc_fence_after();
-              tc_mma4_ts(tmem + kTmemO + t * 128, tmem + t * 128 + part * 32,
-                         desc_values(sKV + sv * C::kTileBytes + part * 8192, C::kBoxBytes), id_o, (i | part) != 0);
-            }
-            ++done[t];
-            if (t == nt - 1) tc_commit(EMPTY(sv));
-            if (more) {
-              scores(t, it + 1);
-              if (t == nt - 1) {
-                tc_commit(EMPTY((2 * it + 2) % C::kSlots));
-                if (i + 2 == n) tc_commit(QEMPTY);
-              }
-            } else {
-              tc_commit(OFULL(t));
-            }
+          if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
+          if (!values(0, q + 1, done0++, i == 0)) return false;
+          if (more) {
+            if (!landed(q + 2)) return false;
+            scores(0, q + 2);
+          } else {
+            tc_commit(OFULL(0));
           }
+          if (two) {
+            if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
+            if (!values(1, q + 1, done1++, i == 0)) return false;
+            if (more) scores(1, q + 2);
+            else tc_commit(OFULL(1));
+          }
+          tc_commit(EMPTY((q + 1) & (C::kSlots - 1)));
+          if (more) tc_commit(EMPTY((q + 2) & (C::kSlots - 1)));
+          if (i + 2 == n) tc_commit(QEMPTY);
         }
-        ++items;
-        for (int t = 0; t < nt; ++t) ++outs[t];
+        ++outs0;
+        outs1 += two;
         return true;
       });
     }
