@@ -40,9 +40,12 @@ struct Chunk {
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kTN * 128;                  // 128 rows of 64 dims
   static constexpr int kTileBytes = kBoxes * kBoxBytes;        // a row tile of q, a tile of keys or of values
-  static constexpr int kSlots = 4 * 32768 / kTileBytes;        // ring of key and value tiles
+  // Ring: stage s holds the values of the share's tile s - 1 and the keys of tile s, which are used one
+  // after the other, so that one wait and one release serve both.
+  static constexpr int kStages = 65536 / kTileBytes;
+  static constexpr int kStageBytes = 2 * kTileBytes;           // keys, then values
   static constexpr int kPartFloats = kItemRows * (D + 2);      // O by columns, then max, then sum
-  static size_t smem(int B) { return 1024 + (size_t)(2 + kSlots) * kTileBytes + ((size_t)B + 1) * 4; }
+  static size_t smem(int B) { return 1024 + (size_t)(2 + 2 * kStages) * kTileBytes + ((size_t)B + 1) * 4; }
 };
 
 struct ChunkSplit {
@@ -374,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a, const ChunkSplit split) {
   using C = Chunk<D>;
   extern __shared__ uint8_t sm_raw[];
-  // barriers: key/value slots (full, empty), q (full, empty), per row tile S full, P
+  // barriers: stages (full, empty), q (full, empty), per row tile S full, P
   // full (its first and its second half), O full, O empty; values clean
-  __shared__ __align__(8) uint64_t bars[2 * C::kSlots + 2 + 8 + 3];
+  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 + 8 + 3];
   __shared__ unsigned long long warp_s[kThreads / 32 * 2];
   __shared__ Share share_s;
   __shared__ uint32_t tmem_slot;
@@ -384,11 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int bad_s[4];   // segment + 1 whose values had non-finite ones that a row sees
   const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t sQ = base, sKV = base + 2 * C::kTileBytes;
-  uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (base - raw) + (2 + C::kSlots) * C::kTileBytes);
+  uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (base - raw) + (2 + 2 * C::kStages) * C::kTileBytes);
   const uint32_t bar0 = smem_u32(bars);
   auto FULL = [&](int s) { return bar0 + 8u * s; };
-  auto EMPTY = [&](int s) { return bar0 + 8u * (C::kSlots + s); };
-  constexpr int kB = 2 * C::kSlots;
+  auto EMPTY = [&](int s) { return bar0 + 8u * (C::kStages + s); };
+  constexpr int kB = 2 * C::kStages;
   const uint32_t QFULL = bar0 + 8u * kB, QEMPTY = QFULL + 8u, CLEAN = bar0 + 8u * (kB + 12);
   auto SFULL = [&](int t) { return bar0 + 8u * (kB + 2 + t); };
   auto PFULL = [&](int t, int part) { return bar0 + 8u * (kB + 4 + 2 * t + part); };
@@ -399,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tpt = 128 / a.G, tokens = 2 * tpt;
 
   if (tid == 0) {
-    for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(FULL(s), 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(FULL(s), 2);
       mbar_init(EMPTY(s), 1);
     }
     mbar_init(QFULL, 1);
@@ -466,14 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ppt = max(1, kTN >> a.page_shift), box_rows = min(kTN, 1 << a.page_shift);
     const int batch = 32 / ppt;                              // tiles whose page numbers the lanes hold
     int it = 0, items = 0;
-    bool stop = false;
     bad = false;
+    if (lane == 0) mbar_arrive(FULL(0));   // the first stage has no values
     walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, unsigned long long) {
       const bool two = x.n > tpt;
-      if (items > 0 && !mbar_wait_warp(QEMPTY, (items - 1) & 1, &abort_s, a.err)) {
-        stop = true;
-        return false;
-      }
+      if (items > 0 && !mbar_wait_warp(QEMPTY, (items - 1) & 1, &abort_s, a.err)) return false;
       if (lane == 0) {
         const uint32_t bytes = (uint32_t)(64 * 2 * a.G * tpt);
         mbar_arrive_expect_tx(QFULL, bytes * C::kBoxes * (two ? 2 : 1));
@@ -502,22 +502,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sub = lane / C::kBoxes, box = lane % C::kBoxes;   // one copy a lane: (page of the tile, 64-dim box)
         const int p = __shfl_sync(0xFFFFFFFFu, pg, (in * ppt + sub) & 31);
         for (int kv = 0; kv < 2; ++kv) {
-          const int seq = 2 * it + kv, sl = seq % C::kSlots;
-          if (seq >= C::kSlots && !mbar_wait_warp(EMPTY(sl), ((seq / C::kSlots) - 1) & 1, &abort_s, a.err)) {
-            stop = true;
+          const int seq = it + kv, st = seq % C::kStages;   // keys to stage it, values to stage it + 1
+          if (kv == 1 && seq >= C::kStages && !mbar_wait_warp(EMPTY(st), (seq / C::kStages - 1) & 1, &abort_s, a.err))
             return false;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(FULL(sl), C::kTileBytes);
+          if (lane == 0) mbar_arrive_expect_tx(FULL(st), C::kTileBytes);
           __syncwarp();
           if (lane < ppt * C::kBoxes)
-            tma_load_4d(sKV + sl * C::kTileBytes + box * C::kBoxBytes + sub * box_rows * 128, kv ? &maps.v : &maps.k,
-                        FULL(sl), box * 64, 0, g, p);
+            tma_load_4d(sKV + st * C::kStageBytes + kv * C::kTileBytes + box * C::kBoxBytes + sub * box_rows * 128,
+                        kv ? &maps.v : &maps.k, FULL(st), box * 64, 0, g, p);
         }
       }
       return true;
     });
+    if (lane == 0) mbar_arrive(FULL(it % C::kStages));   // the last stage has no keys
     if (bad) raise_flag(a.err, kErrBadPages);
-    (void)stop;
     } else if (warp == kSoftmaxWarps + 1) {
     // ---- tensor-core instructions
     if (lane == 0) {
@@ -525,21 +523,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_s = (1u << 4) | fmt | ((kTN >> 3) << 17) | ((128u >> 4) << 24);
       const uint32_t id_o = (1u << 4) | fmt | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
       constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
-      constexpr uint32_t kTurn = C::kSlots == 4 ? 2 : 3;                                   // log2 of the slots
-      const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV, C::kBoxBytes);
-      uint32_t q = 0;   // ring position of the tile's keys; its values follow
-      uint32_t items = 0, cleans = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
+      constexpr uint32_t kTurn = C::kStages == 2 ? 1 : 2;                                  // log2 of the stages
+      const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV + C::kTileBytes, C::kBoxBytes);
+      uint32_t it = 0, items = 0, cleans = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
       auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait(bar, phase & 1, &abort_s, a.err); };
-      auto landed = [&](uint32_t pos) { return wait(FULL(pos & (C::kSlots - 1)), pos >> kTurn); };
-      auto scores = [&](int t, uint32_t pos) {   // S_t = Q_t K^T
-        const uint64_t k = dk + (pos & (C::kSlots - 1)) * kTileUnits;
+      auto stage = [&](uint32_t tile) { return tile & (C::kStages - 1); };
+      auto landed = [&](uint32_t tile) { return wait(FULL(stage(tile)), tile >> kTurn); };
+      auto scores = [&](int t, uint32_t tile) {   // S_t = Q_t K^T
+        const uint64_t k = dk + stage(tile) * (2 * kTileUnits);
 #pragma unroll
         for (int box = 0; box < C::kBoxes; ++box)
           tc_mma4_ss(tmem + t * 128, dq + t * kTileUnits + box * kBoxUnits, k + box * kBoxUnits, id_s, box != 0);
         tc_commit(SFULL(t));
       };
-      auto values = [&](int t, uint32_t pos, uint32_t done, bool first) {   // O_t (+)= P_t V, P in two halves
-        const uint64_t v = dv + (pos & (C::kSlots - 1)) * kTileUnits;
+      auto values = [&](int t, uint32_t tile, uint32_t done, bool first) {   // O_t (+)= P_t V, P in two halves
+        const uint64_t v = dv + stage(tile + 1) * (2 * kTileUnits);
         if (!wait(PFULL(t, 0), done)) return false;
         tc_fence_after();
         tc_mma4_ts(tmem + kTmemO + t * 128, tmem + t * 128, v, id_o, !first);
@@ -550,33 +548,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       walk([&](int, const SeqRows&, int, const Item& x, int i0, int n, unsigned long long) {
         const bool two = x.n > tpt;
-        if (!wait(QFULL, items++) || !landed(q)) return false;
+        if (!wait(QFULL, items++) || (it == 0 && !landed(0))) return false;
         tc_fence_after();
-        scores(0, q);
-        if (two) scores(1, q);
-        tc_commit(EMPTY(q & (C::kSlots - 1)));
+        scores(0, it);
+        if (two) scores(1, it);
+        tc_commit(EMPTY(stage(it)));
         if (n == 1) tc_commit(QEMPTY);
-        for (int i = 0; i < n; ++i, q += 2) {
+        for (int i = 0; i < n; ++i, ++it) {
           const bool more = i + 1 < n;
-          if (!landed(q + 1)) return false;
+          if (!landed(it + 1)) return false;
           if (two && C::kBoxes == 2 && !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi) && !wait(CLEAN, cleans++))
             return false;
           if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
-          if (!values(0, q + 1, done0++, i == 0)) return false;
-          if (more) {
-            if (!landed(q + 2)) return false;
-            scores(0, q + 2);
-          } else {
-            tc_commit(OFULL(0));
-          }
+          if (!values(0, it, done0++, i == 0)) return false;
+          if (more) scores(0, it + 1);
+          else tc_commit(OFULL(0));
           if (two) {
             if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
-            if (!values(1, q + 1, done1++, i == 0)) return false;
-            if (more) scores(1, q + 2);
+            if (!values(1, it, done1++, i == 0)) return false;
+            if (more) scores(1, it + 1);
             else tc_commit(OFULL(1));
           }
-          tc_commit(EMPTY((q + 1) & (C::kSlots - 1)));
-          if (more) tc_commit(EMPTY((q + 2) & (C::kSlots - 1)));
+          if (more) tc_commit(EMPTY(stage(it + 1)));
           if (i + 2 == n) tc_commit(QEMPTY);
         }
         ++outs0;
@@ -611,12 +604,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!open && (t == 0 || C::kBoxes == 2)) {
           // Take non-finite values out of position r of the value tile: its 64-dim box t, or all of it where
           // the other row tile has no rows.
-          const int seq = 2 * it + 1, sl = seq % C::kSlots;
-          if (!mbar_wait_warp(FULL(sl), (seq / C::kSlots) & 1, &abort_s, a.err)) return false;
+          const int st = (it + 1) % C::kStages;
+          if (!mbar_wait_warp(FULL(st), ((it + 1) / C::kStages) & 1, &abort_s, a.err)) return false;
           const bool both = nt == 2 && C::kBoxes == 2;
           bool found = false;
           for (int box = both ? t : 0; box < (both ? t + 1 : C::kBoxes); ++box) {
-            const uint32_t rowaddr = sKV + sl * C::kTileBytes + box * C::kBoxBytes + r * 128;
+            const uint32_t rowaddr = sKV + st * C::kStageBytes + C::kTileBytes + box * C::kBoxBytes + r * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const uint32_t at = rowaddr + (((c + lane) & 7) << 4);
