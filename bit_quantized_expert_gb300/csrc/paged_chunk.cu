@@ -20,6 +20,7 @@
 //     searched for non-finite values, since 0 times one of them is not 0: they are taken out, and the rows that do
 //     see them get them back at the end.
 #include <cmath>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -32,7 +33,7 @@ constexpr int kSoftmaxWarps = 8;
 // Registers a thread: 168 at launch; 2 * 200 + 104 = 3 * 168 after the split.
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kItemRows = 256;              // two row tiles
-constexpr uint32_t kTmemO = 256;            // columns: S0 0, S1 128, O0 256, O1 384
+constexpr uint32_t kTmemO = 256;            // columns: S0 0, S1 128, O0 256, O1 384 (all 512 are allocated: base 0)
 constexpr float kLazy = 8.f;                // base-2 units the running maximum may lag behind
 
 template <int D>
@@ -42,7 +43,7 @@ struct Chunk {
   static constexpr int kTileBytes = kBoxes * kBoxBytes;        // a row tile of q, a tile of keys or of values
   // Ring: stage s holds the values of the share's tile s - 1 and the keys of tile s, which are used one
   // after the other, so that one wait and one release serve both.
-  static constexpr int kStages = 65536 / kTileBytes;
+  static constexpr int kStages = 2;
   static constexpr int kStageBytes = 2 * kTileBytes;           // keys, then values
   static constexpr int kPartFloats = kItemRows * (D + 2);      // O by columns, then max, then sum
   static size_t smem(int B) { return 1024 + (size_t)(2 + 2 * kStages) * kTileBytes + ((size_t)B + 1) * 4; }
@@ -312,6 +313,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -438,7 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
 
   // Walks the segments of the share: body(b, s, g, item, i0, n, u) for tiles i0 .. i0 + n - 1 of an item,
   // the first of them unit u; stops when the body returns false.
@@ -517,73 +523,99 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(FULL(it % C::kStages));   // the last stage has no keys
     if (bad) raise_flag(a.err, kErrBadPages);
     } else if (warp == kSoftmaxWarps + 1) {
-    // ---- tensor-core instructions
-    if (lane == 0) {
-      const uint32_t fmt = FP16 ? 0u : ((1u << 7) | (1u << 10));
-      const uint32_t id_s = (1u << 4) | fmt | ((kTN >> 3) << 17) | ((128u >> 4) << 24);
-      const uint32_t id_o = (1u << 4) | fmt | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
-      constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
-      constexpr uint32_t kTurn = C::kStages == 2 ? 1 : 2;                                  // log2 of the stages
-      const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV + C::kTileBytes, C::kBoxBytes);
-      uint32_t it = 0, items = 0, cleans = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
-      auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait(bar, phase & 1, &abort_s, a.err); };
-      auto stage = [&](uint32_t tile) { return tile & (C::kStages - 1); };
-      auto landed = [&](uint32_t tile) { return wait(FULL(stage(tile)), tile >> kTurn); };
-      auto scores = [&](int t, uint32_t tile) {   // S_t = Q_t K^T
-        const uint64_t k = dk + stage(tile) * (2 * kTileUnits);
+    // ---- tensor-core instructions.  The whole warp takes every step, one elected lane issues, and row tile
+    // and ring stage are constants of the unrolled code: descriptors and addresses then sit in uniform
+    // registers, and a product costs one issue slot beside the two softmax warps of this scheduler.  (A
+    // single lane's walk with computed descriptors took twice as long per product under that load.)
+    const bool go = elect_one();
+    constexpr uint32_t fmt = FP16 ? 0u : ((1u << 7) | (1u << 10));
+    constexpr uint32_t id_s = (1u << 4) | fmt | ((kTN >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
+    const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV + C::kTileBytes, C::kBoxBytes);
+    uint32_t it = 0, items = 0, cleans = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
+    auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait_warp(bar, phase & 1, &abort_s, a.err); };
+    // S_t = Q_t K^T with the keys of stage ST
+    auto scores = [&](auto t_c, auto st_c) {
+      constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
 #pragma unroll
-        for (int box = 0; box < C::kBoxes; ++box)
-          tc_mma4_ss(tmem + t * 128, dq + t * kTileUnits + box * kBoxUnits, k + box * kBoxUnits, id_s, box != 0);
-        tc_commit(SFULL(t));
-      };
-      auto values = [&](int t, uint32_t tile, uint32_t done, bool first) {   // O_t (+)= P_t V, P in two halves
-        const uint64_t v = dv + stage(tile + 1) * (2 * kTileUnits);
-        if (!wait(PFULL(t, 0), done)) return false;
-        tc_fence_after();
-        tc_mma4_ts(tmem + kTmemO + t * 128, tmem + t * 128, v, id_o, !first);
-        if (!wait(PFULL(t, 1), done)) return false;
-        tc_fence_after();
-        tc_mma4_ts(tmem + kTmemO + t * 128, tmem + t * 128 + 32, v + (8192u >> 4), id_o, 1u);
-        return true;
-      };
-      walk([&](int, const SeqRows&, int, const Item& x, int i0, int n, unsigned long long) {
-        const bool two = x.n > tpt;
-        if (!wait(QFULL, items++) || (it == 0 && !landed(0))) return false;
-        tc_fence_after();
-        scores(0, it);
-        if (two) scores(1, it);
-        tc_commit(EMPTY(stage(it)));
-        if (n == 1) tc_commit(QEMPTY);
-        for (int i = 0; i < n; ++i, ++it) {
-          const bool more = i + 1 < n;
-          if (!landed(it + 1)) return false;
-          if (two && C::kBoxes == 2 && !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi) && !wait(CLEAN, cleans++))
-            return false;
-          if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
-          if (!values(0, it, done0++, i == 0)) return false;
-          if (more) scores(0, it + 1);
-          else tc_commit(OFULL(0));
-          if (two) {
-            if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
-            if (!values(1, it, done1++, i == 0)) return false;
-            if (more) scores(1, it + 1);
-            else tc_commit(OFULL(1));
-          }
-          if (more) tc_commit(EMPTY(stage(it + 1)));
-          if (i + 2 == n) tc_commit(QEMPTY);
-        }
-        ++outs0;
-        outs1 += two;
-        return true;
-      });
-    }
+      for (int box = 0; box < C::kBoxes; ++box)
+        tc_mma4_ss(t * 128, dq + (t * kTileUnits + box * kBoxUnits), dk + (ST * 2 * kTileUnits + box * kBoxUnits), id_s,
+                   box != 0);
+      tc_commit(SFULL(t));
+    };
+    // O_t (+)= P_t V, P in two halves, with the values of stage ST; then the next tile's scores
+    auto turn = [&](auto t_c, auto st_c, uint32_t done, bool first, bool more) {
+      constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
+      const uint64_t v = dv + ST * 2 * kTileUnits;
+      if (!wait(PFULL(t, 0), done)) return false;
+      tc_fence_after();
+      if (go) tc_mma4_ts(kTmemO + t * 128, t * 128, v, id_o, !first);
+      __syncwarp();
+      if (!wait(PFULL(t, 1), done)) return false;
+      tc_fence_after();
+      if (go) {
+        tc_mma4_ts(kTmemO + t * 128, t * 128 + 32, v + (8192u >> 4), id_o, 1u);
+        if (more) scores(t_c, st_c);
+        else tc_commit(OFULL(t));
+      }
+      __syncwarp();
+      return true;
+    };
+    using Zero = std::integral_constant<int, 0>;
+    using One = std::integral_constant<int, 1>;
+    // body(stage as a constant) for the stage of a tile
+    static_assert(C::kStages == 2, "a tile's stage is its parity");
+    auto at_stage = [&](uint32_t tile, auto&& body) { return tile & 1 ? body(One{}) : body(Zero{}); };
+    walk([&](int, const SeqRows&, int, const Item& x, int i0, int n_any, unsigned long long) {
+      const int n = __shfl_sync(0xFFFFFFFFu, n_any, 0);
+      const bool two = __shfl_sync(0xFFFFFFFFu, (int)(x.n > tpt), 0) != 0;
+      if (!wait(QFULL, items++) || (it == 0 && !wait(FULL(0), 0))) return false;
+      tc_fence_after();
+      if (!at_stage(it, [&](auto st_c) {
+            if (go) {
+              scores(Zero{}, st_c);
+              if (two) scores(One{}, st_c);
+              tc_commit(EMPTY(decltype(st_c)::value));
+              if (n == 1) tc_commit(QEMPTY);
+            }
+            __syncwarp();
+            return true;
+          }))
+        return false;
+      for (int i = 0; i < n; ++i, ++it) {
+        const bool more = i + 1 < n;
+        const bool closed = two && C::kBoxes == 2 && !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi);
+        if (!at_stage(it + 1, [&](auto st_c) {   // the tile's values, the next one's keys
+              constexpr int ST = decltype(st_c)::value;
+              if (!wait(FULL(ST), (it + 1) >> 1)) return false;
+              if (closed && !wait(CLEAN, cleans++)) return false;
+              if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
+              if (!turn(Zero{}, st_c, done0++, i == 0, more)) return false;
+              if (two) {
+                if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
+                if (!turn(One{}, st_c, done1++, i == 0, more)) return false;
+              }
+              if (go) {
+                if (more) tc_commit(EMPTY(ST));
+                if (i + 2 == n) tc_commit(QEMPTY);
+              }
+              __syncwarp();
+              return true;
+            }))
+          return false;
+      }
+      ++outs0;
+      outs1 += two;
+      return true;
+    });
     }
   } else {
     // ---- softmax: row `r` of row tile `t`
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + t * 128 + lanes, tO = tmem + kTmemO + t * 128 + lanes;
+    const uint32_t tS = t * 128 + lanes, tO = kTmemO + t * 128 + lanes;
     int it = 0, seg = 0, done = 0, outs = 0;
     walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, unsigned long long u) {
       const int nt = x.n > tpt ? 2 : 1;
@@ -778,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kSoftmaxWarps + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem_slot, 512);
   }
 }
 
