@@ -34,6 +34,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kItemRows = 256;              // two row tiles
 constexpr uint32_t kTmemO = 256;            // columns: S0 0, S1 128, O0 256, O1 384 (all 512 are allocated: base 0)
+constexpr int kOutBytes = 32 * 64;          // a warp's staging of its 32 rows of o, 32 dims at a time
 constexpr float kLazy = 8.f;                // base-2 units the running maximum may lag behind
 
 template <int D>
@@ -41,12 +42,14 @@ struct Chunk {
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kTN * 128;                  // 128 rows of 64 dims
   static constexpr int kTileBytes = kBoxes * kBoxBytes;        // a row tile of q, a tile of keys or of values
-  // Ring: stage s holds the values of the share's tile s - 1 and the keys of tile s, which are used one
-  // after the other, so that one wait and one release serve both.
+  // Ring: a segment of n tiles takes n + 1 stages, the i-th with the values of its tile i - 1 and the keys
+  // of tile i, which are used one after the other, so that one wait and one release serve both.
   static constexpr int kStages = 2;
   static constexpr int kStageBytes = 2 * kTileBytes;           // keys, then values
   static constexpr int kPartFloats = kItemRows * (D + 2);      // O by columns, then max, then sum
-  static size_t smem(int B) { return 1024 + (size_t)(2 + 2 * kStages) * kTileBytes + ((size_t)B + 1) * 4; }
+  static size_t smem(int B) {
+    return 1024 + (size_t)(2 + 2 * kStages) * kTileBytes + kSoftmaxWarps * kOutBytes + ((size_t)B + 1) * 4;
+  }
 };
 
 struct ChunkSplit {
@@ -74,139 +77,136 @@ __device__ __forceinline__ Item item_of(const PagedArgs& a, const SeqRows& s, in
 // A CTA's share: units lo .. hi - 1 of (sequence, row block, head, cache tile), and the row block that holds
 // unit lo (or ends just before it), which begins at unit `at`.
 struct Share {
-  unsigned long long lo, hi, at, total;
+  uint32_t lo, hi, at, total, slack;
   int b, qt, ctas;
-  unsigned long long slack;
 };
 
 // A cut of the order within the item of units s .. e - 1, moved to the item's nearer end if that is within
 // `slack`: what a part costs (a partial result written, read and joined) is more than that many tiles of
 // imbalance.
-__device__ __forceinline__ unsigned long long snap(unsigned long long x, unsigned long long s, unsigned long long e,
-                                                   unsigned long long slack) {
-  const unsigned long long down = x - s, up = e - x;
+__device__ __forceinline__ uint32_t snap(uint32_t x, uint32_t s, uint32_t e, uint32_t slack) {
+  const uint32_t down = x - s, up = e - x;
   if (down <= slack && down <= up) return s;
   return up <= slack ? e : x;
 }
 
-// x / d, in 32 bits where x allows.
-__device__ __forceinline__ unsigned long long quotient(unsigned long long x, uint32_t d) {
-  return (x >> 32) == 0 ? (uint32_t)x / d : x / d;
-}
-
 // Where the c-th of n equal shares of `total` units begins.
-__device__ __forceinline__ unsigned long long share_start(unsigned long long total, int c, int n) {
-  const unsigned long long q = quotient(total, (uint32_t)n);
-  return q * c + (uint32_t)(total - q * n) * (uint32_t)c / (uint32_t)n;
+__device__ __forceinline__ uint32_t share_start(uint32_t total, int c, int n) {
+  const uint32_t q = total / n;
+  return q * c + (total - q * n) * c / n;
 }
 
-// Finds this CTA's share, the whole block together: row blocks per sequence are scanned into pre_s[0 .. B],
-// then their costs (tiles times heads), a run of consecutive row blocks a thread; the threads whose runs
-// hold the two cuts walk theirs once more.
-__device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint32_t* pre_s, unsigned long long* warp_s,
-                                           Share* share_s, bool& bad) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kWarps = kThreads / 32;
-  uint32_t* warp32_s = reinterpret_cast<uint32_t*>(warp_s + kWarps);
-  unsigned long long blocks = 0, total = 0;
-  {
-    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    uint32_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-      pre_s[b] = mine;
-      mine += (uint32_t)(load_seq(a, b, bad).n + tokens - 1) / (uint32_t)tokens;
-    }
-    uint32_t inc = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
-      if (lane >= off) inc += x;
-    }
-    if (lane == 31) warp32_s[warp] = inc;
-    __syncthreads();
-    uint32_t before = inc - mine, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t x = warp32_s[w];
-      before += w < warp ? x : 0u;
-      all += x;
-    }
-    for (int b = b0; b < b1; ++b) pre_s[b] += before;
-    if (tid == 0) pre_s[a.B] = all;
-    blocks = all;
-    __syncthreads();
-  }
-  const uint32_t per = (uint32_t)(blocks + kThreads - 1) / kThreads;
-  const uint32_t i0 = (uint32_t)min((unsigned long long)tid * per, blocks);
-  const uint32_t i1 = (uint32_t)min((unsigned long long)i0 + per, blocks);
-  int b_mine = 0;
-  if (i0 < i1) {
-    int lo = 0, hi = a.B - 1;   // the sequence that holds row block i0
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre_s[mid] <= i0) lo = mid;
-      else hi = mid - 1;
-    }
-    b_mine = lo;
-  }
-  // body(b, qt, tiles) for this thread's row blocks
-  auto each = [&](auto&& body) {
-    int b = b_mine;
-    for (uint32_t i = i0; i < i1; ++b) {
-      const SeqRows s = load_seq(a, b, bad);
-      for (; i < i1 && i < pre_s[b + 1]; ++i) {
-        const int qt = (int)(i - pre_s[b]);
-        body(b, qt, (uint32_t)item_of(a, s, qt, tokens).r.count);
-      }
-    }
-  };
-  unsigned long long mine = 0;
-  each([&](int, int, uint32_t c) { mine += c; });
+// Exclusive sums over the block; `sum` gets the total.  (Rolled up, like the rest of
+// the schedule: it runs once, and its time is that of fetching its instructions.)
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long mine, unsigned long long* warp_s,
+                                                      unsigned long long* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long inc = mine;
-#pragma unroll
+#pragma unroll 1
   for (int off = 1; off < 32; off <<= 1) {
     const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
     if (lane >= off) inc += x;
   }
+  __syncthreads();   // warp_s may still be read
   if (lane == 31) warp_s[warp] = inc;
   __syncthreads();
-  unsigned long long before = inc - mine;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  unsigned long long before = inc - mine, all = 0;
+#pragma unroll 1
+  for (int w = 0; w < kThreads / 32; ++w) {
     const unsigned long long x = warp_s[w];
-    before += w < warp ? x : 0ull;
-    total += x;
+    if (w < warp) before += x;
+    all += x;
   }
-  before *= a.Hkv;
-  mine *= a.Hkv;
-  total *= a.Hkv;
-  const int ctas = (int)min((unsigned long long)gridDim.x, total), cta = (int)blockIdx.x;   // no more shares than tiles
-  if (cta >= ctas) return;
-  const unsigned long long slack = max(2ull, quotient(total, (uint32_t)ctas) / 32);
-  const unsigned long long lo = share_start(total, cta, ctas), hi = share_start(total, cta + 1, ctas);
-  if ((lo >= before && lo < before + mine) || (hi >= before && hi < before + mine)) {
-    unsigned long long at = before;
-    each([&](int b, int qt, uint32_t c) {
-      const unsigned long long end = at + (unsigned long long)c * a.Hkv;
-      auto cut = [&](unsigned long long x) {
-        const unsigned long long s = at + quotient(x - at, c) * c;
-        return x == s ? x : snap(x, s, s + c, slack);
-      };
-      if (lo >= at && lo < end) {
-        share_s->lo = cut(lo);
-        share_s->at = at;
-        share_s->b = b;
-        share_s->qt = qt;
+  *sum = all;
+  return before;
+}
+
+// Finds this CTA's share, the whole block together: row blocks per sequence are scanned into pre_s[0 .. B],
+// then their costs (tiles times heads), a run of consecutive row blocks a thread; the threads whose runs
+// hold the two cuts walk theirs once more.  Leaves the share empty if there is nothing to do, or (bad) more
+// than 2^32 tiles.
+__device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint32_t* pre_s, unsigned long long* warp_s,
+                                           Share* share_s, bool& bad) {
+  const int tid = threadIdx.x;
+  unsigned long long sum;
+  {
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    uint32_t mine = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      pre_s[b] = mine;
+      mine += (uint32_t)(load_seq(a, b, bad).n + tokens - 1) / (uint32_t)tokens;
+    }
+    const uint32_t before = (uint32_t)block_scan(mine, warp_s, &sum);
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) pre_s[b] += before;
+    if (tid == 0) pre_s[a.B] = (uint32_t)sum;
+    __syncthreads();
+  }
+  const uint32_t blocks = (uint32_t)sum, per = (blocks + kThreads - 1) / kThreads;
+  const uint32_t i0 = min(tid * per, blocks), i1 = min(i0 + per, blocks);
+  int b_mine = 0;
+  if (i0 < i1) {
+    int hi = a.B - 1;   // the sequence that holds row block i0
+    while (b_mine < hi) {
+      const int mid = (b_mine + hi + 1) >> 1;
+      if (pre_s[mid] <= i0) b_mine = mid;
+      else hi = mid - 1;
+    }
+  }
+  const int cta = (int)blockIdx.x;
+  unsigned long long mine = 0;
+  uint32_t at = 0, lo = 0, hi = 0, slack = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {   // first the costs, then the cuts
+    int b = b_mine;
+#pragma unroll 1
+    for (uint32_t i = i0; i < i1; ++b) {
+      const SeqRows s = load_seq(a, b, bad);
+#pragma unroll 1
+      for (; i < i1 && i < pre_s[b + 1]; ++i) {
+        const int qt = (int)(i - pre_s[b]);
+        const uint32_t c = (uint32_t)item_of(a, s, qt, tokens).r.count;
+        if (pass == 0) {
+          mine += (unsigned long long)c * a.Hkv;
+          continue;
+        }
+        const uint32_t end = at + c * a.Hkv;
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+          const uint32_t x = side == 0 ? lo : hi;
+          if (x < at || x >= end) continue;
+          const uint32_t first = at + (x - at) / c * c, to = x == first ? x : snap(x, first, first + c, slack);
+          if (side == 0) {
+            share_s->lo = to;
+            share_s->at = at;
+            share_s->b = b;
+            share_s->qt = qt;
+          } else {
+            share_s->hi = to;
+          }
+        }
+        at = end;
       }
-      if (hi >= at && hi < end) share_s->hi = cut(hi);
-      at = end;
-    });
-  }
-  if (tid == 0) {
-    if (hi == total) share_s->hi = total;
-    share_s->total = total;
-    share_s->ctas = ctas;
-    share_s->slack = slack;
+    }
+    if (pass == 1) return;
+    at = (uint32_t)block_scan(mine, warp_s, &sum);
+    if (sum >> 32) bad = true;
+    if ((sum >> 32) || sum == 0) return;
+    const uint32_t total = (uint32_t)sum;
+    const int ctas = (int)min(gridDim.x, total);   // no more shares than tiles
+    if (cta >= ctas) return;
+    slack = max(2u, total / ctas / 32);
+    lo = share_start(total, cta, ctas);
+    hi = share_start(total, cta + 1, ctas);
+    if (tid == 0) {
+      share_s->total = total;
+      share_s->ctas = ctas;
+      share_s->slack = slack;
+      if (hi == total) share_s->hi = total;
+    }
+    const uint32_t end = at + (uint32_t)mine;
+    if ((lo < at || lo >= end) && (hi < at || hi >= end)) return;
   }
 }
 
@@ -313,6 +313,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ void ld_shared4(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(at) : "memory");
+}
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -348,6 +351,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // The lowest n bits (n any integer).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
+// Bit 15 of each half of w that holds a non-finite value (an exponent of ones, which one more carries into
+// the sign's place).
+template <bool FP16>
+__device__ __forceinline__ uint32_t non_finite_bits(uint32_t w) {
+  return FP16 ? (w & 0x7C007C00u) + 0x04000400u : (w & 0x7F807F80u) + 0x00800080u;
+}
+constexpr uint32_t kSigns = 0x80008000u;
 
 // 0xFFFF in each half of w that holds a non-finite value.
 template <bool FP16>
@@ -387,14 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // barriers: stages (full, empty), q (full, empty), per row tile S full, P
   // full (its first and its second half), O full, O empty; values clean
   __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 + 8 + 3];
-  __shared__ unsigned long long warp_s[kThreads / 32 * 2];
+  __shared__ unsigned long long warp_s[kThreads / 32];
   __shared__ Share share_s;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
   __shared__ int bad_s[4];   // segment + 1 whose values had non-finite ones that a row sees
   const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t sQ = base, sKV = base + 2 * C::kTileBytes;
-  uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (base - raw) + (2 + 2 * C::kStages) * C::kTileBytes);
+  const uint32_t sOut = sKV + C::kStages * C::kStageBytes;
+  uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (sOut - raw) + kSoftmaxWarps * kOutBytes);
   const uint32_t bar0 = smem_u32(bars);
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (C::kStages + s); };
@@ -410,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(FULL(s), 2);
+      mbar_init(FULL(s), 1);
       mbar_init(EMPTY(s), 1);
     }
     mbar_init(QFULL, 1);
@@ -449,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Walks the segments of the share: body(b, s, g, item, i0, n, u) for tiles i0 .. i0 + n - 1 of an item,
   // the first of them unit u; stops when the body returns false.
   auto walk = [&](auto&& body) {
-    unsigned long long u = share_s.lo, at = share_s.at;
-    const unsigned long long hi = share_s.hi;
+    uint32_t u = share_s.lo, at = share_s.at;
+    const uint32_t hi = share_s.hi;
     int b = share_s.b, qt = share_s.qt;
     while (u < hi) {
       const SeqRows s = load_seq(a, b, bad);
@@ -458,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item x = item_of(a, s, qt, tokens);
         for (int g = 0; g < a.Hkv && u < hi; ++g, at += x.r.count) {
           if (at + x.r.count <= u) continue;
-          const int i0 = (int)(u - at), n = (int)min((unsigned long long)(x.r.count - i0), hi - u);
+          const int i0 = (int)(u - at), n = (int)min((uint32_t)(x.r.count - i0), hi - u);
           if (!body(b, s, g, x, i0, n, u)) return;
           u += n;
         }
@@ -474,53 +486,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- copies
     const int ppt = max(1, kTN >> a.page_shift), box_rows = min(kTN, 1 << a.page_shift);
     const int batch = 32 / ppt;                              // tiles whose page numbers the lanes hold
-    int it = 0, items = 0;
+    int at = 0, items = 0;   // ring stages and segments so far
     bad = false;
-    if (lane == 0) mbar_arrive(FULL(0));   // the first stage has no values
-    walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, unsigned long long) {
+    walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
       const bool two = x.n > tpt;
-      if (items > 0 && !mbar_wait_warp(QEMPTY, (items - 1) & 1, &abort_s, a.err)) return false;
-      if (lane == 0) {
-        const uint32_t bytes = (uint32_t)(64 * 2 * a.G * tpt);
-        mbar_arrive_expect_tx(QFULL, bytes * C::kBoxes * (two ? 2 : 1));
-        for (int t = 0; t < (two ? 2 : 1); ++t)
-          for (int box = 0; box < C::kBoxes; ++box)
-            tma_load_3d(sQ + t * C::kTileBytes + box * C::kBoxBytes, &maps.q, QFULL, box * 64, g * a.G,
-                        s.row0 + x.t0 + t * tpt);
-      }
-      ++items;
       const int32_t* row = a.table + (size_t)b * a.max_pages;
-      int pg = 0;
-      for (int i = 0; i < n; ++i, ++it) {
-        const int in = i % batch;
-        if (in == 0) {
-          const int t = i0 + i + lane / ppt;
-          pg = a.num_pages;                                  // out of the map's range: zeros
-          if (t < x.r.count && lane / ppt < n - i) {
-            const int ip = ((x.r.tile(t) * kTN) >> a.page_shift) + lane % ppt;
-            if (ip < a.max_pages && page_needed(a, ip, x.p_lo, x.p_hi)) {
-              const int p = __ldg(row + ip);
-              if (p >= 0 && p < a.num_pages) pg = p;
-              else bad = true;
-            }
-          }
-        }
-        const int sub = lane / C::kBoxes, box = lane % C::kBoxes;   // one copy a lane: (page of the tile, 64-dim box)
-        const int p = __shfl_sync(0xFFFFFFFFu, pg, (in * ppt + sub) & 31);
-        for (int kv = 0; kv < 2; ++kv) {
-          const int seq = it + kv, st = seq % C::kStages;   // keys to stage it, values to stage it + 1
-          if (kv == 1 && seq >= C::kStages && !mbar_wait_warp(EMPTY(st), (seq / C::kStages - 1) & 1, &abort_s, a.err))
-            return false;
-          if (lane == 0) mbar_arrive_expect_tx(FULL(st), C::kTileBytes);
-          __syncwarp();
+      const int sub = lane / C::kBoxes, box = lane % C::kBoxes;   // one copy a lane: (page of the tile, 64-dim box)
+      // Page numbers of a batch of tiles, one a lane, read one batch ahead; a page that no row needs is not
+      // read, and takes, like a bad one, a number out of the map's range, which reads as zeros.
+      int pg = 0, ahead = 0;
+      bool need = false;
+      auto read_ahead = [&](int i) {
+        const int t = i0 + i + lane / ppt, ip = t < x.r.count ? ((x.r.tile(t) * kTN) >> a.page_shift) + lane % ppt : 0;
+        need = lane / ppt < n - i && t < x.r.count && ip < a.max_pages && page_needed(a, ip, x.p_lo, x.p_hi);
+        if (need) ahead = __ldg(row + ip);
+      };
+      read_ahead(0);
+      for (int i = 0; i <= n; ++i, ++at) {
+        // stage `at`: values of tile i - 1 (whose pages are at hand), then keys of tile i
+        const int st = at & 1;
+        if (at >= C::kStages && !mbar_wait_warp(EMPTY(st), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(FULL(st), i == 0 || i == n ? C::kTileBytes : 2 * C::kTileBytes);
+        __syncwarp();
+        auto copy = [&](const CUtensorMap* map, int half, int in) {
+          const int p = __shfl_sync(0xFFFFFFFFu, pg, (in * ppt + sub) & 31);
           if (lane < ppt * C::kBoxes)
-            tma_load_4d(sKV + st * C::kStageBytes + kv * C::kTileBytes + box * C::kBoxBytes + sub * box_rows * 128,
-                        kv ? &maps.v : &maps.k, FULL(st), box * 64, 0, g, p);
+            tma_load_4d(sKV + st * C::kStageBytes + half * C::kTileBytes + box * C::kBoxBytes + sub * box_rows * 128, map,
+                        FULL(st), box * 64, 0, g, p);
+        };
+        if (i > 0) copy(&maps.v, 1, (i - 1) % batch);
+        if (i < n) {
+          const int in = i % batch;
+          if (in == 0) {
+            const bool ok = ahead >= 0 && ahead < a.num_pages;
+            pg = need && ok ? ahead : a.num_pages;
+            bad |= need && !ok;
+            read_ahead(i + batch);
+          }
+          copy(&maps.k, 0, in);
+        }
+        if (i == 0) {   // the queries, once the segment before has done its last scores
+          if (items > 0 && !mbar_wait_warp(QEMPTY, (items - 1) & 1, &abort_s, a.err)) return false;
+          ++items;
+          if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(64 * 2 * a.G * tpt);
+            mbar_arrive_expect_tx(QFULL, bytes * C::kBoxes * (two ? 2 : 1));
+            for (int t = 0; t < (two ? 2 : 1); ++t)
+              for (int bx = 0; bx < C::kBoxes; ++bx)
+                tma_load_3d(sQ + t * C::kTileBytes + bx * C::kBoxBytes, &maps.q, QFULL, bx * 64, g * a.G,
+                            s.row0 + x.t0 + t * tpt);
+          }
         }
       }
       return true;
     });
-    if (lane == 0) mbar_arrive(FULL(it % C::kStages));   // the last stage has no keys
     if (bad) raise_flag(a.err, kErrBadPages);
     } else if (warp == kSoftmaxWarps + 1) {
     // ---- tensor-core instructions.  The whole warp takes every step, one elected lane issues, and row tile
@@ -533,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
     const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV + C::kTileBytes, C::kBoxBytes);
-    uint32_t it = 0, items = 0, cleans = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
+    uint32_t at = 0, items = 0, cleans = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
     auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait_warp(bar, phase & 1, &abort_s, a.err); };
     // S_t = Q_t K^T with the keys of stage ST
     auto scores = [&](auto t_c, auto st_c) {
@@ -567,28 +586,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     // body(stage as a constant) for the stage of a tile
     static_assert(C::kStages == 2, "a tile's stage is its parity");
     auto at_stage = [&](uint32_t tile, auto&& body) { return tile & 1 ? body(One{}) : body(Zero{}); };
-    walk([&](int, const SeqRows&, int, const Item& x, int i0, int n_any, unsigned long long) {
+    walk([&](int, const SeqRows&, int, const Item& x, int i0, int n_any, uint32_t) {
       const int n = __shfl_sync(0xFFFFFFFFu, n_any, 0);
       const bool two = __shfl_sync(0xFFFFFFFFu, (int)(x.n > tpt), 0) != 0;
-      if (!wait(QFULL, items++) || (it == 0 && !wait(FULL(0), 0))) return false;
-      tc_fence_after();
-      if (!at_stage(it, [&](auto st_c) {
+      if (!wait(QFULL, items++)) return false;
+      if (!at_stage(at, [&](auto st_c) {
+            constexpr int ST = decltype(st_c)::value;
+            if (!wait(FULL(ST), at >> 1)) return false;
+            tc_fence_after();
             if (go) {
               scores(Zero{}, st_c);
               if (two) scores(One{}, st_c);
-              tc_commit(EMPTY(decltype(st_c)::value));
+              tc_commit(EMPTY(ST));
               if (n == 1) tc_commit(QEMPTY);
             }
             __syncwarp();
             return true;
           }))
         return false;
-      for (int i = 0; i < n; ++i, ++it) {
+      ++at;
+      for (int i = 0; i < n; ++i, ++at) {
         const bool more = i + 1 < n;
         const bool closed = two && C::kBoxes == 2 && !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi);
-        if (!at_stage(it + 1, [&](auto st_c) {   // the tile's values, the next one's keys
+        if (!at_stage(at, [&](auto st_c) {   // the tile's values, the next one's keys
               constexpr int ST = decltype(st_c)::value;
-              if (!wait(FULL(ST), (it + 1) >> 1)) return false;
+              if (!wait(FULL(ST), at >> 1)) return false;
               if (closed && !wait(CLEAN, cleans++)) return false;
               if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
               if (!turn(Zero{}, st_c, done0++, i == 0, more)) return false;
@@ -597,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!turn(One{}, st_c, done1++, i == 0, more)) return false;
               }
               if (go) {
-                if (more) tc_commit(EMPTY(ST));
+                tc_commit(EMPTY(ST));
                 if (i + 2 == n) tc_commit(QEMPTY);
               }
               __syncwarp();
@@ -613,21 +635,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---- softmax: row `r` of row tile `t`
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G;
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G, head = r - tok * a.G;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = t * 128 + lanes, tO = kTmemO + t * 128 + lanes;
-    int it = 0, seg = 0, done = 0, outs = 0;
-    walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, unsigned long long u) {
+    int at = 0, seg = 0, done = 0, outs = 0;   // ring stages, segments, own tiles and items so far
+    walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t u) {
       const int nt = x.n > tpt ? 2 : 1;
       if (t >= nt) {
-        it += n;
+        at += n + 1;
         ++seg;
         return true;
       }
       const bool live = tok < tpt && t * tpt + tok < x.n;
       const int p = live ? x.p_lo + t * tpt + tok : -1;      // a row that is no token sees nothing
       float m = -INFINITY, negm = 0.f, l = 0.f;              // negm = -m in base-2 units (0 while nothing is seen)
-      for (int i = 0; i < n; ++i, ++it) {
+      ++at;   // the stage of the first tile's values
+      for (int i = 0; i < n; ++i, ++at) {
         const int j0 = x.r.tile(i0 + i) * kTN;
         const bool open = tile_open<kTN>(a, j0, x.p_lo, x.p_hi);
         if (!mbar_wait_warp(SFULL(t), done & 1, &abort_s, a.err)) return false;
@@ -636,31 +659,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!open && (t == 0 || C::kBoxes == 2)) {
           // Take non-finite values out of position r of the value tile: its 64-dim box t, or all of it where
           // the other row tile has no rows.
-          const int st = (it + 1) % C::kStages;
-          if (!mbar_wait_warp(FULL(st), ((it + 1) / C::kStages) & 1, &abort_s, a.err)) return false;
+          const int st = at & 1;
+          if (!mbar_wait_warp(FULL(st), (at >> 1) & 1, &abort_s, a.err)) return false;
           const bool both = nt == 2 && C::kBoxes == 2;
-          bool found = false;
-          for (int box = both ? t : 0; box < (both ? t + 1 : C::kBoxes); ++box) {
-            const uint32_t rowaddr = sKV + st * C::kStageBytes + C::kTileBytes + box * C::kBoxBytes + r * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint32_t at = rowaddr + (((c + lane) & 7) << 4);
-              uint32_t w0, w1, w2, w3;
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w0), "=r"(w1), "=r"(w2), "=r"(w3)
-                           : "r"(at)
-                           : "memory");
-              const uint32_t b0 = non_finite16<FP16>(w0), b1 = non_finite16<FP16>(w1), b2 = non_finite16<FP16>(w2),
-                             b3 = non_finite16<FP16>(w3);
-              if ((b0 | b1 | b2 | b3) != 0u) {
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w0 & ~b0), "r"(w1 & ~b1),
-                             "r"(w2 & ~b2), "r"(w3 & ~b3)
-                             : "memory");
-                found = true;
-              }
-            }
+          const uint32_t row = sKV + st * C::kStageBytes + C::kTileBytes + (both ? t * C::kBoxBytes : 0) + r * 128;
+          const int chunks = both ? 8 : 8 * C::kBoxes;   // of 16 bytes; lanes start at different ones
+          uint32_t any = 0;
+#pragma unroll 4
+          for (int c = 0; c < chunks; ++c) {
+            uint32_t w0, w1, w2, w3;
+            ld_shared4(row + (c >> 3) * C::kBoxBytes + (((c + lane) & 7) << 4), w0, w1, w2, w3);
+            any |= non_finite_bits<FP16>(w0) | non_finite_bits<FP16>(w1) | non_finite_bits<FP16>(w2) |
+                   non_finite_bits<FP16>(w3);
           }
-          if (found) {
+          if (any & kSigns) {
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+              const uint32_t at = row + (c >> 3) * C::kBoxBytes + ((c & 7) << 4);
+              uint32_t w0, w1, w2, w3;
+              ld_shared4(at, w0, w1, w2, w3);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w0 & ~non_finite16<FP16>(w0)),
+                           "r"(w1 & ~non_finite16<FP16>(w1)), "r"(w2 & ~non_finite16<FP16>(w2)),
+                           "r"(w3 & ~non_finite16<FP16>(w3))
+                           : "memory");
+            }
             const int j = j0 + r;
             if (j <= x.p_hi && (a.window == 0 || j > x.p_lo - a.window || j < a.sinks)) bad_s[seg & 3] = seg + 1;
             fence_proxy_async_smem();
@@ -677,8 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int j = j0 + 32 * w;
             uint32_t see = low_bits(p + 1 - j);
             if (a.window > 0) see &= ~low_bits(p - a.window + 1 - j) | low_bits(a.sinks - j);
+            if (__all_sync(0xFFFFFFFFu, see == 0xFFFFFFFFu)) continue;   // most words: the warp's rows are a few tokens
 #pragma unroll
-            for (int c = 0; c < 32; ++c) sr[32 * w + c] = (see >> c) & 1u ? sr[32 * w + c] : 0xFF800000u;
+            for (int c = 0; c < 32; ++c) sr[32 * w + c] = see & (1u << c) ? sr[32 * w + c] : 0xFF800000u;
           }
         }
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
@@ -746,15 +769,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = i0 == 0 && n == x.r.count;
       const bool hurt = *(volatile int*)&bad_s[my_seg & 3] == my_seg + 1;
       const float inv = p < 0 ? 0.f : 1.f / l;
-      uint16_t* orow = a.o + (long long)(s.row0 + x.t0 + t * tpt + tok) * a.o_stride + (long long)(g * a.G + r % a.G) * D;
+      const unsigned long long orow =
+          live ? reinterpret_cast<unsigned long long>(a.o + (long long)(s.row0 + x.t0 + t * tpt + tok) * a.o_stride +
+                                                      (long long)(g * a.G + head) * D)
+               : 0ull;
       float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats + t * 128 + r;
-      bool nonfinite = false;
+      const uint32_t out = sOut + warp * kOutBytes;
+      uint32_t nonfinite = 0;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
         tmem_ld32(tO + c, v);
+        if (p < 0) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = p < 0 ? 0u : v[e];
+          for (int e = 0; e < 32; ++e) v[e] = 0u;
+        }
         if (hurt && live) {
           float extra[32];
 #pragma unroll
@@ -764,17 +793,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + extra[e]);
         }
         if (whole) {
+          // 64 bytes a row through shared memory (16-byte pieces XOR-ed against bank conflicts), so that four
+          // lanes store one row's sectors and a store touches 8 rows, not 32.
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
+          for (int e = 0; e < 4; ++e) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float f0 = __uint_as_float(v[e + 2 * k]) * inv, f1 = __uint_as_float(v[e + 2 * k + 1]) * inv;
-              nonfinite |= !isfinite(f0) || !isfinite(f1);
-              w[k] = pack16<FP16>(f0, f1);
+              w[k] = pack16<FP16>(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
+              nonfinite |= non_finite_bits<FP16>(w[k]);
             }
-            if (live) *reinterpret_cast<uint4*>(orow + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
           }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = k * 8 + (lane >> 2);
+            const unsigned long long to = __shfl_sync(0xFFFFFFFFu, orow, rr);
+            uint4 w;
+            ld_shared4(out + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), w.x, w.y, w.z, w.w);
+            if (to != 0) *(reinterpret_cast<uint4*>(to + 2 * c) + (lane & 3)) = w;
+          }
+          __syncwarp();
         } else if (live) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) part[(c + e) * kItemRows] = __uint_as_float(v[e]);
@@ -783,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(OEMPTY(t));
-      if (live && whole && nonfinite) raise_flag(a.err, kErrNonFinite);
+      if (live && (nonfinite & kSigns)) raise_flag(a.err, kErrNonFinite);
       if (!whole) {
         if (live) {
           part[D * kItemRows] = m == -INFINITY ? -1e30f : -negm;
@@ -791,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (i0 == 0 && tid == 0) {
           // the last CTA with a part: the one whose share holds the item's last unit
-          const unsigned long long e = u + x.r.count, total = share_s.total;
+          const uint32_t e = u + x.r.count, total = share_s.total;
           int c = share_of(e - 1, total, share_s.ctas);
           while (c > cta + 1 && snap(share_start(total, c, share_s.ctas), u, e, share_s.slack) >= e) --c;
           split.rec[cta] = SplitRecord{s.row0 + x.t0, g, x.n, c, x.p_lo};
