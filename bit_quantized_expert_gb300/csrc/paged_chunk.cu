@@ -35,6 +35,7 @@ constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kItemRows = 256;              // two row tiles
 constexpr uint32_t kTmemO = 256;            // columns: S0 0, S1 128, O0 256, O1 384 (all 512 are allocated: base 0)
 constexpr int kOutBytes = 32 * 64;          // a warp's staging of its 32 rows of o, 32 dims at a time
+constexpr int kItemUnits = 2;               // what an item costs beside its tiles, in tiles
 constexpr float kLazy = 8.f;                // base-2 units the running maximum may lag behind
 
 template <int D>
@@ -74,19 +75,20 @@ __device__ __forceinline__ Item item_of(const PagedArgs& a, const SeqRows& s, in
   return x;
 }
 
-// A CTA's share: units lo .. hi - 1 of (sequence, row block, head, cache tile), and the row block that holds
+// A CTA's share: units lo .. hi - 1 of (sequence, row block, head, cache tile), an item's tiles standing behind
+// kItemUnits units for its start and end, and the row block that holds
 // unit lo (or ends just before it), which begins at unit `at`.
 struct Share {
   uint32_t lo, hi, at, total, slack;
   int b, qt, ctas;
 };
 
-// A cut of the order within the item of units s .. e - 1, moved to the item's nearer end if that is within
-// `slack`: what a part costs (a partial result written, read and joined) is more than that many tiles of
-// imbalance.
+// A cut of the order within the item of units s .. e - 1, moved to an end of the item that is within `slack`
+// tiles: what a part costs (a partial result written, read and joined) is more than that many tiles of
+// imbalance.  What remains between has tiles on both sides.
 __device__ __forceinline__ uint32_t snap(uint32_t x, uint32_t s, uint32_t e, uint32_t slack) {
   const uint32_t down = x - s, up = e - x;
-  if (down <= slack && down <= up) return s;
+  if (down <= kItemUnits + slack && down <= kItemUnits + up) return s;
   return up <= slack ? e : x;
 }
 
@@ -166,7 +168,7 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
 #pragma unroll 1
       for (; i < i1 && i < pre_s[b + 1]; ++i) {
         const int qt = (int)(i - pre_s[b]);
-        const uint32_t c = (uint32_t)item_of(a, s, qt, tokens).r.count;
+        const uint32_t c = (uint32_t)item_of(a, s, qt, tokens).r.count + kItemUnits;
         if (pass == 0) {
           mine += (unsigned long long)c * a.Hkv;
           continue;
@@ -343,6 +345,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -468,11 +475,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const SeqRows s = load_seq(a, b, bad);
       for (; u < hi && qt * tokens < s.n; ++qt) {
         const Item x = item_of(a, s, qt, tokens);
-        for (int g = 0; g < a.Hkv && u < hi; ++g, at += x.r.count) {
-          if (at + x.r.count <= u) continue;
-          const int i0 = (int)(u - at), n = (int)min((uint32_t)(x.r.count - i0), hi - u);
-          if (!body(b, s, g, x, i0, n, u)) return;
-          u += n;
+        const uint32_t units = (uint32_t)x.r.count + kItemUnits;
+        for (int g = 0; g < a.Hkv && u < hi; ++g, at += units) {
+          if (at + units <= u) continue;
+          const int i0 = max((int)(u - at) - kItemUnits, 0), i1 = (int)min(hi - at, units) - kItemUnits;
+          if (!body(b, s, g, x, i0, i1 - i0, u)) return;
+          u = min(hi, at + units);
         }
       }
       qt = 0;
@@ -769,13 +777,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = i0 == 0 && n == x.r.count;
       const bool hurt = *(volatile int*)&bad_s[my_seg & 3] == my_seg + 1;
       const float inv = p < 0 ? 0.f : 1.f / l;
-      const unsigned long long orow =
-          live ? reinterpret_cast<unsigned long long>(a.o + (long long)(s.row0 + x.t0 + t * tpt + tok) * a.o_stride +
-                                                      (long long)(g * a.G + head) * D)
-               : 0ull;
+      // Rows of the result are stored by four lanes each: lane 4 i + j stores bytes 16 j of rows i, i + 8, ...
+      unsigned long long to[4];
+      {
+        const unsigned long long orow =
+            live ? reinterpret_cast<unsigned long long>(a.o + (long long)(s.row0 + x.t0 + t * tpt + tok) * a.o_stride +
+                                                        (long long)(g * a.G + head) * D)
+                 : 0ull;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          to[k] = __shfl_sync(0xFFFFFFFFu, orow, k * 8 + (lane >> 2));
+          if (to[k] != 0) to[k] += (lane & 3) * 16;
+        }
+      }
       float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats + t * 128 + r;
       const uint32_t out = sOut + warp * kOutBytes;
-      uint32_t nonfinite = 0;
+      const uint64_t inv2 = pair2(inv, inv);
+      uint64_t check = 0;   // 0 unless a result is not finite: the sum of 0 times every one
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t v[32];
@@ -793,15 +811,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + extra[e]);
         }
         if (whole) {
-          // 64 bytes a row through shared memory (16-byte pieces XOR-ed against bank conflicts), so that four
-          // lanes store one row's sectors and a store touches 8 rows, not 32.
+          // 64 bytes a row through shared memory (16-byte pieces XOR-ed against bank conflicts), so that a store
+          // touches 8 rows, not 32.
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              w[k] = pack16<FP16>(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
-              nonfinite |= non_finite_bits<FP16>(w[k]);
+              const uint64_t f = mul2(pair2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1])), inv2);
+              check = fma2(f, 0ull, check);
+              const float2 y = unpair2(f);
+              w[k] = pack16<FP16>(y.x, y.y);
             }
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)),
                          "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
@@ -811,10 +831,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int rr = k * 8 + (lane >> 2);
-            const unsigned long long to = __shfl_sync(0xFFFFFFFFu, orow, rr);
             uint4 w;
             ld_shared4(out + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), w.x, w.y, w.z, w.w);
-            if (to != 0) *(reinterpret_cast<uint4*>(to + 2 * c) + (lane & 3)) = w;
+            if (to[k] != 0) *reinterpret_cast<uint4*>(to[k] + 2 * c) = w;
           }
           __syncwarp();
         } else if (live) {
@@ -825,7 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(OEMPTY(t));
-      if (live && (nonfinite & kSigns)) raise_flag(a.err, kErrNonFinite);
+      const float2 checks = unpair2(check);
+      if (live && !(checks.x + checks.y == 0.f)) raise_flag(a.err, kErrNonFinite);
       if (!whole) {
         if (live) {
           part[D * kItemRows] = m == -INFINITY ? -1e30f : -negm;
@@ -833,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (i0 == 0 && tid == 0) {
           // the last CTA with a part: the one whose share holds the item's last unit
-          const uint32_t e = u + x.r.count, total = share_s.total;
+          const uint32_t e = u + x.r.count + kItemUnits, total = share_s.total;
           int c = share_of(e - 1, total, share_s.ctas);
           while (c > cta + 1 && snap(share_start(total, c, share_s.ctas), u, e, share_s.slack) >= e) --c;
           split.rec[cta] = SplitRecord{s.row0 + x.t0, g, x.n, c, x.p_lo};
