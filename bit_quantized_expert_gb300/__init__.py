@@ -167,9 +167,13 @@ def _stream(stream) -> int:
     """A torch stream, a raw cudaStream_t handle (int), or None for torch's current stream."""
     if isinstance(stream, int):
         return stream
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    try:   # the handle alone: building a Stream object takes microseconds
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
 def dims(T, d, E, k, F, F_shared) -> Dims:
@@ -371,29 +375,31 @@ def alloc_gqa_paged_workspace(pd: GqaPagedDims, device="cuda"):
 
 def _paged_ints(t, n: int, name: str) -> int:
     """Pointer of a contiguous int32 tensor of at least n entries."""
-    if not t.is_cuda or t.element_size() != 4 or t.numel() < n or not t.is_contiguous():
+    if not t.is_cuda or t.itemsize != 4 or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of at least {n} entries")
     return t.data_ptr()
 
 
 def _paged_rows(t, rows: int, heads: int, D: int, stride: int, name: str) -> int:
     """Pointer of a 16-bit [rows, heads, D] tensor whose token stride is that of the dims (0: packed)."""
-    if (not t.is_cuda or t.element_size() != 2 or t.shape != (rows, heads, D) or t.stride(2) != 1
-            or (heads > 1 and t.stride(1) != D) or (rows > 1 and t.stride(0) != (stride or heads * D))):
+    st = t.stride()
+    if (not t.is_cuda or t.itemsize != 2 or t.shape != (rows, heads, D) or st[2] != 1 or (heads > 1 and st[1] != D)
+            or (rows > 1 and st[0] != (stride or heads * D))):
         raise ValueError(f"{name}: expected a 16-bit CUDA tensor [{rows}, {heads}, {D}] of token stride "
                          f"{stride or heads * D}")
     return t.data_ptr()
 
 
-def _paged_cache(t, pd: GqaPagedDims, name: str) -> int:
-    """Pointer of a 16-bit cache indexed [page, head, offset, D] whose strides are those of the dims."""
-    P, H, S, D = pd.num_pages, pd.n_kv_heads, pd.page_size, pd.head_dim
-    st = t.stride()
-    if (not t.is_cuda or t.element_size() != 2 or t.shape != (P, H, S, D) or st[3] != 1
-            or (P > 1 and st[0] != (pd.page_stride or H * S * D)) or (H > 1 and st[1] != (pd.head_stride or S * D))
-            or st[2] != (pd.row_stride or D)):
-        raise ValueError(f"{name}: expected a 16-bit CUDA tensor [{P}, {H}, {S}, {D}] with the strides of the dims")
-    return t.data_ptr()
+def _paged_caches(k, v, pd: GqaPagedDims):
+    """Pointers of two 16-bit caches indexed [page, head, offset, D] whose strides are those of the dims."""
+    P, H, S, D = shape = (pd.num_pages, pd.n_kv_heads, pd.page_size, pd.head_dim)
+    want = (pd.page_stride or H * S * D, pd.head_stride or S * D, pd.row_stride or D, 1)
+    for t in (k, v):
+        st = t.stride()
+        if (not t.is_cuda or t.itemsize != 2 or t.shape != shape
+                or (st != want and (st[2:] != want[2:] or (P > 1 and st[0] != want[0]) or (H > 1 and st[1] != want[1])))):
+            raise ValueError(f"caches: expected 16-bit CUDA tensors {list(shape)} with the strides of the dims")
+    return k.data_ptr(), v.data_ptr()
 
 
 def gqa_paged_plan(pd: GqaPagedDims, ctx_len, new_len, free_pages, n_free, block_table, q_start, kv_len, positions,
@@ -414,19 +420,20 @@ def gqa_paged_plan(pd: GqaPagedDims, ctx_len, new_len, free_pages, n_free, block
 def gqa_paged_append(pd: GqaPagedDims, k, v, slots, q_start, k_cache, v_cache, workspace, stream=None):
     """k, v [T, Hkv, D] into the slots of the caches (rows at or past q_start[B] are skipped)."""
     T, H, D = pd.n_tokens, pd.n_kv_heads, pd.head_dim
+    kc, vc = _paged_caches(k_cache, v_cache, pd)
     _check(load_library().gqa_paged_append(
         ctypes.byref(pd), _paged_rows(k, T, H, D, pd.k_stride, "k"), _paged_rows(v, T, H, D, pd.v_stride, "v"),
-        _paged_ints(slots, T, "slots"), _paged_ints(q_start, pd.n_seqs + 1, "q_start"), _paged_cache(k_cache, pd, "k_cache"),
-        _paged_cache(v_cache, pd, "v_cache"), _ptr(workspace), workspace.numel(), _stream(stream)), "gqa_paged_append")
+        _paged_ints(slots, T, "slots"), _paged_ints(q_start, pd.n_seqs + 1, "q_start"), kc, vc, _ptr(workspace),
+        workspace.numel(), _stream(stream)), "gqa_paged_append")
 
 
 def gqa_paged_attention(pd: GqaPagedDims, q, k_cache, v_cache, block_table, q_start, kv_len, o, workspace, stream=None):
     """Causal grouped-query attention of each sequence's new tokens (the last rows of its kv_len positions)
     over its pages, with pd's window and sinks.  q, o [T, Hq, D] of pd's type."""
     T, H, D, B = pd.n_tokens, pd.n_heads, pd.head_dim, pd.n_seqs
+    kc, vc = _paged_caches(k_cache, v_cache, pd)
     _check(load_library().gqa_paged_attention(
-        ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, "q"), _paged_cache(k_cache, pd, "k_cache"),
-        _paged_cache(v_cache, pd, "v_cache"), _paged_ints(block_table, B * pd.max_pages, "block_table"),
+        ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, "q"), kc, vc, _paged_ints(block_table, B * pd.max_pages, "block_table"),
         _paged_ints(q_start, B + 1, "q_start"), _paged_ints(kv_len, B, "kv_len"),
         _paged_rows(o, T, H, D, pd.o_stride, "o"), _ptr(workspace), workspace.numel(), _stream(stream)),
         "gqa_paged_attention")

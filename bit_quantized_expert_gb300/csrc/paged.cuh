@@ -97,10 +97,10 @@ __device__ __forceinline__ bool tile_open(const PagedArgs& a, int j0, int p_lo, 
 
 // ------------------------------------------------------------------------------------------
 // Split of the work over the CTAs.  The cache tiles of all items (an item is a block of query rows of
-// one key/value head), in order, are cut into equal consecutive shares, one a CTA.  An item that lies in
-// several shares leaves one partial result (unnormalised O, max and sum per row) in each, joined by a
-// second launch in order.  A CTA has at most two partials: slot 0 of an item that began before it, slot
-// 1 of one that goes on after it.
+// one key/value head), in order, each item's behind a few units that stand for its start and end, are cut
+// into equal consecutive shares, one a CTA.  An item that lies in several shares leaves one partial result
+// (unnormalised O, max and sum per row) in each, joined by a second launch in order.  A CTA has at most
+// two partials: slot 0 of an item that began before it, slot 1 of one that goes on after it.
 // ------------------------------------------------------------------------------------------
 constexpr int kPagedMaxCtas = 160;   // one CTA per SM, of 152
 
@@ -110,50 +110,51 @@ struct SplitRecord {
   int32_t p_lo;                  // position of the item's first token
 };
 
-// Exclusive sums of cost(b) over b = 0 .. B - 1 into pre_s[0 .. B], by a whole block of NT threads.
-template <int NT, class Cost>
-__device__ __forceinline__ void scan_sequences(int B, unsigned long long* pre_s, unsigned long long* warp_s, Cost cost) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (B + NT - 1) / NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  unsigned long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const unsigned long long c = cost(b);
-    pre_s[b] = mine;
-    mine += c;
-  }
+// Exclusive sums over a block of NT threads; `sum` gets the total.  (Rolled up, like the rest of the
+// schedule: it runs once, and its time is that of fetching its instructions.)
+template <int NT>
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long mine, unsigned long long* warp_s,
+                                                         unsigned long long* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long inc = mine;
-#pragma unroll
+#pragma unroll 1
   for (int off = 1; off < 32; off <<= 1) {
     const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
     if (lane >= off) inc += x;
   }
+  __syncthreads();   // warp_s may still be read
   if (lane == 31) warp_s[warp] = inc;
   __syncthreads();
-  unsigned long long before = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) before += w < warp ? warp_s[w] : 0;
-  before += inc - mine;
-  for (int b = b0; b < b1; ++b) pre_s[b] += before;
-  if (tid == NT - 1) pre_s[B] = before + mine;
-  __syncthreads();
-}
-
-// The sequence that holds unit `pos` of the order (pre_s[b] <= pos < pre_s[b + 1]), by binary search.
-__device__ __forceinline__ int find_sequence(const unsigned long long* pre_s, int B, unsigned long long pos) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre_s[mid] <= pos) lo = mid;
-    else hi = mid - 1;
+  unsigned long long before = inc - mine, all = 0;
+#pragma unroll 1
+  for (int w = 0; w < NT / 32; ++w) {
+    const unsigned long long x = warp_s[w];
+    if (w < warp) before += x;
+    all += x;
   }
-  return lo;
+  *sum = all;
+  return before;
 }
 
-// The CTA whose share [c * total / n, (c + 1) * total / n) holds unit `pos`.
-__device__ __forceinline__ int share_of(unsigned long long pos, unsigned long long total, int n) {
-  int c = (int)((pos * n) / total);
-  while ((unsigned long long)(c + 1) * total / n <= pos) ++c;
-  while (c > 0 && (unsigned long long)c * total / n > pos) --c;
+// A cut of the order within the item of units s .. e - 1 (`own` of them its start and end, then its tiles),
+// moved to an end of the item that is within `slack` tiles.  What remains between has tiles on both sides.
+__device__ __forceinline__ uint32_t snap(uint32_t x, uint32_t s, uint32_t e, uint32_t own, uint32_t slack) {
+  const uint32_t down = x - s, up = e - x;
+  if (down <= own + slack && down <= own + up) return s;
+  return up <= slack ? e : x;
+}
+
+// Where the c-th of n equal shares of `total` units begins.
+__device__ __forceinline__ uint32_t share_start(uint32_t total, int c, int n) {
+  const uint32_t q = total / n;
+  return q * c + (total - q * n) * c / n;
+}
+
+// The share that holds unit `pos`.
+__device__ __forceinline__ int share_of(uint32_t pos, uint32_t total, int n) {
+  int c = min((int)((float)pos / (float)total * (float)n), n - 1);   // within one of it
+  while (c + 1 < n && share_start(total, c + 1, n) <= pos) ++c;
+  while (c > 0 && share_start(total, c, n) > pos) --c;
   return c;
 }
 

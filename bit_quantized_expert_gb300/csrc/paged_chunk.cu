@@ -14,8 +14,8 @@
 //   * S and O stay in tensor memory (128 columns of fp32 a tile each).  P replaces S there, in 16 bits,
 //     as the A operand of the second product; V is read as it lies (positions by dims) through a
 //     descriptor whose major axis is the output's.
-//   * The running maximum that scales the numerators moves only when the new one is above it by 8 in
-//     base-2 units: p stays below 2^8, nothing overflows, and O is rescaled in a few tiles, not in all.
+//   * The running maximum that scales the numerators moves only when the new one is above it by 14 in
+//     base-2 units: p stays below 2^14, within fp16, and O is rescaled in a few tiles, not in all.
 //   * Only tiles that some row does not wholly see are masked.  In those, the value tile is also
 //     searched for non-finite values, since 0 times one of them is not 0: they are taken out, and the rows that do
 //     see them get them back at the end.
@@ -36,7 +36,7 @@ constexpr int kItemRows = 256;              // two row tiles
 constexpr uint32_t kTmemO = 256;            // columns: S0 0, S1 128, O0 256, O1 384 (all 512 are allocated: base 0)
 constexpr int kOutBytes = 32 * 64;          // a warp's staging of its 32 rows of o, 32 dims at a time
 constexpr int kItemUnits = 2;               // what an item costs beside its tiles, in tiles
-constexpr float kLazy = 8.f;                // base-2 units the running maximum may lag behind
+constexpr float kLazy = 14.f;               // base-2 units the running maximum may lag behind
 
 template <int D>
 struct Chunk {
@@ -83,46 +83,6 @@ struct Share {
   int b, qt, ctas;
 };
 
-// A cut of the order within the item of units s .. e - 1, moved to an end of the item that is within `slack`
-// tiles: what a part costs (a partial result written, read and joined) is more than that many tiles of
-// imbalance.  What remains between has tiles on both sides.
-__device__ __forceinline__ uint32_t snap(uint32_t x, uint32_t s, uint32_t e, uint32_t slack) {
-  const uint32_t down = x - s, up = e - x;
-  if (down <= kItemUnits + slack && down <= kItemUnits + up) return s;
-  return up <= slack ? e : x;
-}
-
-// Where the c-th of n equal shares of `total` units begins.
-__device__ __forceinline__ uint32_t share_start(uint32_t total, int c, int n) {
-  const uint32_t q = total / n;
-  return q * c + (total - q * n) * c / n;
-}
-
-// Exclusive sums over the block; `sum` gets the total.  (Rolled up, like the rest of
-// the schedule: it runs once, and its time is that of fetching its instructions.)
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long mine, unsigned long long* warp_s,
-                                                      unsigned long long* sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long inc = mine;
-#pragma unroll 1
-  for (int off = 1; off < 32; off <<= 1) {
-    const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
-    if (lane >= off) inc += x;
-  }
-  __syncthreads();   // warp_s may still be read
-  if (lane == 31) warp_s[warp] = inc;
-  __syncthreads();
-  unsigned long long before = inc - mine, all = 0;
-#pragma unroll 1
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const unsigned long long x = warp_s[w];
-    if (w < warp) before += x;
-    all += x;
-  }
-  *sum = all;
-  return before;
-}
-
 // Finds this CTA's share, the whole block together: row blocks per sequence are scanned into pre_s[0 .. B],
 // then their costs (tiles times heads), a run of consecutive row blocks a thread; the threads whose runs
 // hold the two cuts walk theirs once more.  Leaves the share empty if there is nothing to do, or (bad) more
@@ -139,7 +99,7 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
       pre_s[b] = mine;
       mine += (uint32_t)(load_seq(a, b, bad).n + tokens - 1) / (uint32_t)tokens;
     }
-    const uint32_t before = (uint32_t)block_scan(mine, warp_s, &sum);
+    const uint32_t before = (uint32_t)block_scan<kThreads>(mine, warp_s, &sum);
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) pre_s[b] += before;
     if (tid == 0) pre_s[a.B] = (uint32_t)sum;
@@ -178,7 +138,7 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
         for (int side = 0; side < 2; ++side) {
           const uint32_t x = side == 0 ? lo : hi;
           if (x < at || x >= end) continue;
-          const uint32_t first = at + (x - at) / c * c, to = x == first ? x : snap(x, first, first + c, slack);
+          const uint32_t first = at + (x - at) / c * c, to = x == first ? x : snap(x, first, first + c, kItemUnits, slack);
           if (side == 0) {
             share_s->lo = to;
             share_s->at = at;
@@ -192,12 +152,13 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
       }
     }
     if (pass == 1) return;
-    at = (uint32_t)block_scan(mine, warp_s, &sum);
+    at = (uint32_t)block_scan<kThreads>(mine, warp_s, &sum);
     if (sum >> 32) bad = true;
     if ((sum >> 32) || sum == 0) return;
     const uint32_t total = (uint32_t)sum;
     const int ctas = (int)min(gridDim.x, total);   // no more shares than tiles
     if (cta >= ctas) return;
+    // A part costs a result written, read and joined: more than two tiles of imbalance.
     slack = max(2u, total / ctas / 32);
     lo = share_start(total, cta, ctas);
     hi = share_start(total, cta + 1, ctas);
@@ -855,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the last CTA with a part: the one whose share holds the item's last unit
           const uint32_t e = u + x.r.count + kItemUnits, total = share_s.total;
           int c = share_of(e - 1, total, share_s.ctas);
-          while (c > cta + 1 && snap(share_start(total, c, share_s.ctas), u, e, share_s.slack) >= e) --c;
+          while (c > cta + 1 && snap(share_start(total, c, share_s.ctas), u, e, kItemUnits, share_s.slack) >= e) --c;
           split.rec[cta] = SplitRecord{s.row0 + x.t0, g, x.n, c, x.p_lo};
         }
       }

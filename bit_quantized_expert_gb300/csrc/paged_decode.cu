@@ -6,8 +6,8 @@
 //   * the tiles of all items, in order, are cut into equal shares, one per CTA and one CTA per SM: one long
 //     sequence is spread over every SM and a batch of very different lengths is balanced by construction
 //     (see paged.cuh); a share may hold the end of one item, several whole ones and the start of another;
-//   * one producer warp copies the tile's pages by tensor map into a ring (a page of the table is a box of
-//     16 to 64 rows), 32 page numbers at a time read ahead by its lanes; eight consumer warps take tiles
+//   * four warps copy the tile's pages by tensor map into a ring (a page of the table is a box of
+//     16 to 64 rows), 32 page numbers at a time read ahead by their lanes; eight consumer warps take tiles
 //     in turn (four warps a tile, 16 positions a warp) with m16n8k16 products: S = Q K^T with the heads as
 //     the 16-row operand (rows 8..15 zero), then O += P V with rows 0..7 the rounded numerators and rows
 //     8..15 their rounding remainders, so P keeps about twice the type's bits;
@@ -25,8 +25,11 @@ namespace {
 
 constexpr int kTN = 64;                        // positions per tile
 constexpr int kWarps = 8;                      // consumer warps: two groups of four, alternate tiles
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kCopyWarps = 4;
+constexpr int kThreads = (kWarps + kCopyWarps) * 32;
 constexpr int kRows = 8;                       // query heads per key/value head, at most
+constexpr int kItemUnits = 3;                  // what an item costs beside its tiles, in tiles (~3500 cycles)
+constexpr int kSlack = 1;                      // tiles that a cut moves to reach an item's end
 constexpr float kNegBig = -1e30f;              // running max before any position is seen
 
 template <int D>
@@ -38,7 +41,7 @@ struct Dec {
   static constexpr int kOStride = D + 8;                 // padded row of the joining buffer (floats)
   static constexpr int kJoinBytes = kWarps * kRows * kOStride * 4;
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
-  static size_t smem(int B) { return 1024 + (size_t)kStages * kStageBytes + kJoinBytes + ((size_t)B + 1) * 8; }
+  static size_t smem(int B) { return 1024 + (size_t)kStages * kStageBytes + kJoinBytes + ((size_t)B + 1) * 4; }
 };
 
 struct DecodeSplit {
@@ -96,14 +99,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_s;
   const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   float* join_s = reinterpret_cast<float*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes);
-  unsigned long long* pre_s =
-      reinterpret_cast<unsigned long long*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes + C::kJoinBytes);
+  uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes + C::kJoinBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = (int)blockIdx.x;
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&full[s]), kCopyWarps);
       mbar_init(smem_u32(&empty[s]), 4);
     }
     abort_s = 0;
@@ -114,51 +116,96 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- this CTA's share: units lo .. hi - 1 of (sequence, head, tile)
+  // ---- this CTA's share: units lo .. hi - 1 of (sequence, head, tile); pre_s: units before each sequence
   bool bad = false;
-  scan_sequences<kThreads>(a.B, pre_s, warp_s, [&](int b) {
-    const SeqRows s = load_seq(a, b, bad);
-    return s.n == 0 ? 0ull : (unsigned long long)visible_tiles<kTN>(a, s.p0, s.p0).count * a.Hkv;
-  });
+  uint32_t total;
+  {
+    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    unsigned long long mine = 0, sum;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const SeqRows s = load_seq(a, b, bad);
+      pre_s[b] = (uint32_t)mine;
+      if (s.n != 0) mine += (unsigned long long)(visible_tiles<kTN>(a, s.p0, s.p0).count + kItemUnits) * a.Hkv;
+    }
+    const uint32_t before = (uint32_t)block_scan<kThreads>(mine, warp_s, &sum);
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) pre_s[b] += before;
+    if (tid == 0) pre_s[a.B] = (uint32_t)sum;
+    if (sum >> 32) {   // refused: nothing is computed
+      bad = true;
+      sum = 0;
+    }
+    total = (uint32_t)sum;
+    __syncthreads();
+  }
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
-  const unsigned long long total = pre_s[a.B];
-  const int ctas = (int)min((unsigned long long)gridDim.x, total);   // every share holds a tile
+  const int ctas = (int)min(gridDim.x, total);   // every share holds a tile
   if (tid == 0) split.rec[cta].until = -1;
   if (cta >= ctas) return;
-  const unsigned long long lo = total * cta / ctas, hi = total * (cta + 1) / ctas;
-  const int b_first = find_sequence(pre_s, a.B, lo);
+  uint32_t lo = 0, hi = 0;
+  int b_first = 0;   // the sequence that holds unit lo
+#pragma unroll 1
+  for (int side = 1; side >= 0; --side) {
+    uint32_t x = share_start(total, cta + side, ctas);
+    int b = 0;
+    for (int top = a.B - 1; b < top;) {
+      const int mid = (b + top + 1) >> 1;
+      if (pre_s[mid] <= x) b = mid;
+      else top = mid - 1;
+    }
+    if (x < total) {
+      const uint32_t units = (pre_s[b + 1] - pre_s[b]) / a.Hkv, first = x - (x - pre_s[b]) % units;
+      x = snap(x, first, first + units, kItemUnits, kSlack);
+    }
+    if (side) {
+      hi = x;
+    } else {
+      lo = x;
+      b_first = b;
+    }
+  }
 
-  if (warp == kWarps) {
-    // ---- producer warp
+  if (warp >= kWarps) {
+    // ---- copies: every warp takes a quarter of a tile's boxes, since the copies of a warp's lanes are issued
+    // one by one (75 to 120 cycles each: 16 of them, the boxes of pages of 16, took as long as a tile's
+    // stream from memory).
+    const int pw = warp - kWarps;
     const int ppt = max(1, kTN >> a.page_shift);               // pages of a tile
     const int box_rows = min(kTN, 1 << a.page_shift);
+    const int copies = ppt * 2 * C::kBoxes;                    // (page, keys or values, 64-dim box)
+    const int c0 = copies * pw / kCopyWarps, mine = copies * (pw + 1) / kCopyWarps - c0;
+    const int sub = (c0 + lane) / (2 * C::kBoxes), kv = ((c0 + lane) / C::kBoxes) & 1, box = (c0 + lane) % C::kBoxes;
+    const int batch = 32 / ppt;                                // tiles whose page numbers the lanes hold
     int b = b_first, issued = 0;
     bool stop = false;
     bad = false;
-    for (unsigned long long u = lo; u < hi && !stop; ++b) {
+    for (uint32_t u = lo; u < hi && !stop; ++b) {
       if (pre_s[b + 1] <= u) continue;
       const SeqRows s = load_seq(a, b, bad);
       const TileRange r = visible_tiles<kTN>(a, s.p0, s.p0);
       const int32_t* row = a.table + (size_t)b * a.max_pages;
-      const unsigned long long end = min(pre_s[b + 1], hi);
+      const uint32_t end = min(pre_s[b + 1], hi);
       while (u < end && !stop) {
-        const int g = (int)((u - pre_s[b]) / r.count), i0 = (int)((u - pre_s[b]) % r.count);
-        const int n = (int)min((unsigned long long)(r.count - i0), end - u);
-        int pg = 0;                                            // this lane's page of the batch of tiles
-        const int batch = 32 / ppt;
-        for (int i = 0; i < n && !stop; ++i) {
+        const uint32_t units = r.count + kItemUnits, g = (u - pre_s[b]) / units, first = pre_s[b] + g * units;
+        const int i0 = max((int)(u - first) - kItemUnits, 0), n = (int)min(end - first, units) - kItemUnits - i0;
+        // Page numbers of a batch of tiles, one a lane, read one batch ahead; a page that the token does not need
+        // is not read, and takes, like a bad one, a number out of the map's range, which reads as zeros.
+        int pg = 0, ahead = 0;
+        bool need = false;
+        auto read_ahead = [&](int i) {
+          const int t = i0 + i + lane / ppt, ip = t < r.count ? ((r.tile(t) * kTN) >> a.page_shift) + lane % ppt : 0;
+          need = lane / ppt < n - i && t < r.count && ip < a.max_pages && page_needed(a, ip, s.p0, s.p0);
+          if (need) ahead = __ldg(row + ip);
+        };
+        read_ahead(0);
+        for (int i = 0; i < n; ++i) {
           const int in = i % batch;
           if (in == 0) {
-            const int t = i0 + i + lane / ppt;
-            pg = a.num_pages;                                  // out of the map's range: zeros
-            if (t < r.count && lane / ppt < n - i) {
-              const int ip = ((r.tile(t) * kTN) >> a.page_shift) + lane % ppt;
-              if (ip < a.max_pages && page_needed(a, ip, s.p0, s.p0)) {
-                const int p = __ldg(row + ip);
-                if (p >= 0 && p < a.num_pages) pg = p;
-                else bad = true;
-              }
-            }
+            const bool ok = ahead >= 0 && ahead < a.num_pages;
+            pg = need && ok ? ahead : a.num_pages;
+            bad |= need && !ok;
+            read_ahead(i + batch);
           }
           const int st = issued % C::kStages;
           if (issued >= C::kStages &&
@@ -166,30 +213,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             stop = true;
             break;
           }
-          const uint32_t dst = base + st * C::kStageBytes, bar = smem_u32(&full[st]);
+          const uint32_t bar = smem_u32(&full[st]);
           const int off = (r.tile(i0 + i) * kTN) & ((1 << a.page_shift) - 1);   // 64 in the second half of a page of 128
-          if (lane == 0) mbar_arrive_expect_tx(bar, C::kStageBytes);
+          if (lane == 0) mbar_arrive_expect_tx(bar, mine * box_rows * 128);
           __syncwarp();
-          // one copy a lane: (page of the tile, keys or values, 64-dim box)
-          const int copies = ppt * 2 * C::kBoxes, sub = lane / (2 * C::kBoxes), kv = (lane / C::kBoxes) & 1,
-                    box = lane % C::kBoxes;
           const int p = __shfl_sync(0xFFFFFFFFu, pg, (in * ppt + sub) & 31);
-          if (lane < copies)
-            tma_load_4d(dst + (kv * C::kBoxes + box) * C::kBoxBytes + sub * box_rows * 128, kv ? &maps.v : &maps.k, bar,
-                        box * 64, off, g, p);
+          if (lane < mine)
+            tma_load_4d(base + st * C::kStageBytes + (kv * C::kBoxes + box) * C::kBoxBytes + sub * box_rows * 128,
+                        kv ? &maps.v : &maps.k, bar, box * 64, off, (int)g, p);
           ++issued;
         }
-        u += n;
+        u = min(end, first + units);
       }
     }
     if (bad) raise_flag(a.err, kErrBadPages);
     // After a timeout, copies still in flight land before the CTA exits.
-    if (stop && lane == 0)
-      for (int i = max(0, issued - C::kStages); i < issued; ++i) {
-        const long long c0 = clock64();
-        while (!mbar_try_wait(smem_u32(&full[i % C::kStages]), (i / C::kStages) & 1) && clock64() - c0 < 4000000ll) {
-        }
+    if (stop && lane == 0) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < 4000000ll) {
       }
+    }
     return;
   }
 
@@ -202,14 +245,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int vpos = wq * 16 + 8 * (lmat & 1) + lrow;    // value row this lane addresses
   int it = 0;                                          // tiles of the share so far
   int b = b_first;
-  for (unsigned long long u = lo; u < hi; ++b) {
+  for (uint32_t u = lo; u < hi; ++b) {
     if (pre_s[b + 1] <= u) continue;
     const SeqRows s = load_seq(a, b, bad);
     const TileRange tr = visible_tiles<kTN>(a, s.p0, s.p0);
-    const unsigned long long end = min(pre_s[b + 1], hi);
+    const uint32_t end = min(pre_s[b + 1], hi);
     while (u < end) {
-      const int g = (int)((u - pre_s[b]) / tr.count), i0 = (int)((u - pre_s[b]) % tr.count);
-      const int n = (int)min((unsigned long long)(tr.count - i0), end - u);
+      const uint32_t units = tr.count + kItemUnits;
+      const int g = (int)((u - pre_s[b]) / units);
+      const uint32_t first = pre_s[b] + g * units;
+      const int i0 = max((int)(u - first) - kItemUnits, 0), n = (int)min(end - first, units) - kItemUnits - i0;
       uint32_t qa[D / 16][2];   // the heads as the 16-row operand: rows r < G
       {
         const bool live = r < a.G;
@@ -349,10 +394,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (i0 == 0 && !whole && tid == 0) {
-        const unsigned long long last = pre_s[b] + (unsigned long long)(g + 1) * tr.count - 1;
-        split.rec[cta] = SplitRecord{s.row0, g, 1, share_of(last, total, ctas), s.p0};
+        // the last CTA with a part: the one whose share holds the item's last unit
+        const uint32_t e = first + units;
+        int c = share_of(e - 1, total, ctas);
+        while (c > cta + 1 && snap(share_start(total, c, ctas), first, e, kItemUnits, kSlack) >= e) --c;
+        split.rec[cta] = SplitRecord{s.row0, g, 1, c, s.p0};
       }
-      u += n;
+      u = min(end, first + units);
       consumers_sync();   // the joining buffer is free again
     }
   }

@@ -139,8 +139,9 @@ moe_status gqa_paged_append(const gqa_paged_dims* dims, const uint16_t* k, const
  * Bit 16 is set for: rows of a sequence outside 0 .. T or falling (the sequence is skipped; sequences
  * that claim the same rows leave either's results there), kv_len outside 0 .. max_pages * page_size
  * (cut), more than max_new rows of a sequence (the first max_new are computed), a page number outside
- * 0 .. num_pages - 1 (its keys and values count as zeros), and, in the chunk form, work of 2^32 or more
- * (block of query rows, key/value head, 128 cached positions) triples (nothing is computed).
+ * 0 .. num_pages - 1 (its keys and values count as zeros), and work of 2^32 or more cache tiles over all
+ * sequences and heads (128 positions for a block of query rows, 64 in the single-token form: nothing is
+ * computed).
  * Returns MOE_ERR_INVALID_ARG for a null pointer or a value of dims outside its meaning;
  * MOE_ERR_UNSUPPORTED for values outside the limits of dims; MOE_ERR_MISALIGNED for a pointer off
  * its alignment or a stride that is not a multiple of 8; MOE_ERR_WORKSPACE; MOE_ERR_CUDA as in

@@ -133,4 +133,4 @@ def test_binding_refuses_tensors_that_do_not_fit():
     with pytest.raises(ValueError):
         moe._paged_rows(torch.zeros(37, 16, 128, dtype=torch.bfloat16), 37, 16, 128, 0, "q")
     with pytest.raises(ValueError):
-        moe._paged_cache(torch.zeros(100, 2, 64, 128, dtype=torch.bfloat16), d, "k_cache")
+        moe._paged_caches(*[torch.zeros(100, 2, 64, 128, dtype=torch.bfloat16)] * 2, d)
