@@ -14,7 +14,7 @@
 //   * all rows stand at one position and see the same set, so positions that they do not see are cut out
 //     of the value operand itself: whatever lies there, non-finite values included, has no effect;
 //   * running max, sum and O stay in registers; at an item's end the eight warps are joined in shared
-//     memory in a fixed order, and the result goes to o, or, for an item that other CTAs share, to a
+//     memory in a fixed order (one barrier an item: two joining buffers, every thread weighs for itself), and the result goes to o, or, for an item that other CTAs share, to a
 //     partial that a second launch joins in order.
 #include <cmath>
 
@@ -39,7 +39,8 @@ struct Dec {
   static constexpr int kStageBytes = 2 * kBoxes * kBoxBytes;
   static constexpr int kStages = 128 * 1024 / kStageBytes;
   static constexpr int kOStride = D + 8;                 // padded row of the joining buffer (floats)
-  static constexpr int kJoinBytes = kWarps * kRows * kOStride * 4;
+  static constexpr int kJoinFloats = kWarps * kRows * kOStride;
+  static constexpr int kJoinBytes = 2 * kJoinFloats * 4; // two buffers: an item's is read while the next one's is written
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
   static size_t smem(int B) { return 1024 + (size_t)kStages * kStageBytes + kJoinBytes + ((size_t)B + 1) * 4; }
 };
@@ -86,6 +87,12 @@ __device__ __forceinline__ uint32_t swz(int pos, int chunk) {
   return (uint32_t)((chunk >> 3) * (kTN * 128) + pos * 128 + (((chunk & 7) ^ (pos & 7)) << 4));
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
 template <int D, bool FP16>
@@ -94,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Dec<D>;
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages];
-  __shared__ float m_s[kWarps][kRows], l_s[kWarps][kRows], wt_s[kWarps][kRows];
+  __shared__ __align__(16) float ml_s[2][kRows][2][kWarps];   // per buffer and row: the warps' max, then sum
   __shared__ unsigned long long warp_s[kThreads / 32];
   __shared__ int abort_s;
   const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
@@ -243,166 +250,186 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lrow = lane & 7, lmat = lane >> 3;
   const int kpos = wq * 16 + 8 * (lmat >> 1) + lrow;   // key row this lane addresses
   const int vpos = wq * 16 + 8 * (lmat & 1) + lrow;    // value row this lane addresses
-  int it = 0;                                          // tiles of the share so far
+
+  // The segment at unit u: tiles i0 .. i0 + n - 1 of head g of sequence b (n = 0: the share is done).
+  struct Segment {
+    int g, i0, n, p0, row0;
+    uint32_t first, end;   // the item's first unit and the unit past its last
+    TileRange r;
+  };
+  uint32_t u = lo;
   int b = b_first;
-  for (uint32_t u = lo; u < hi; ++b) {
-    if (pre_s[b + 1] <= u) continue;
+  auto next_segment = [&]() {
+    Segment x;
+    x.n = 0;
+    if (u >= hi) return x;
+    while (pre_s[b + 1] <= u) ++b;
     const SeqRows s = load_seq(a, b, bad);
-    const TileRange tr = visible_tiles<kTN>(a, s.p0, s.p0);
-    const uint32_t end = min(pre_s[b + 1], hi);
-    while (u < end) {
-      const uint32_t units = tr.count + kItemUnits;
-      const int g = (int)((u - pre_s[b]) / units);
-      const uint32_t first = pre_s[b] + g * units;
-      const int i0 = max((int)(u - first) - kItemUnits, 0), n = (int)min(end - first, units) - kItemUnits - i0;
-      uint32_t qa[D / 16][2];   // the heads as the 16-row operand: rows r < G
-      {
-        const bool live = r < a.G;
-        const uint32_t* qh =
-            reinterpret_cast<const uint32_t*>(a.q + s.row0 * a.q_stride + (long long)(g * a.G + (live ? r : 0)) * D + c2);
+    x.r = visible_tiles<kTN>(a, s.p0, s.p0);
+    x.p0 = s.p0;
+    x.row0 = s.row0;
+    const uint32_t units = x.r.count + kItemUnits;
+    x.g = (int)((u - pre_s[b]) / units);
+    x.first = pre_s[b] + x.g * units;
+    x.end = x.first + units;
+    x.i0 = max((int)(u - x.first) - kItemUnits, 0);
+    x.n = (int)min(hi - x.first, units) - kItemUnits - x.i0;
+    u = min(hi, x.end);
+    return x;
+  };
+  uint32_t qa[D / 16][2];   // the heads as the 16-row operand: rows r < G
+  auto load_queries = [&](const Segment& x) {
+    const bool live = r < a.G && x.n > 0;
+    const uint32_t* qh = reinterpret_cast<const uint32_t*>(
+        a.q + (live ? x.row0 * a.q_stride + (long long)(x.g * a.G + r) * D : 0) + c2);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      qa[kk][0] = live ? __ldg(qh + 8 * kk) : 0u;
+      qa[kk][1] = live ? __ldg(qh + 8 * kk + 4) : 0u;
+    }
+  };
+
+  int it = 0, buf = 0;   // tiles of the share so far, joining buffer
+  Segment x = next_segment();
+  load_queries(x);
+  while (x.n > 0) {
+    float o[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float m_run = kNegBig, l_run = 0.f;
+    for (int i = (it ^ wg) & 1; i < x.n; i += 2) {   // tile it + i of the share goes to group (it + i) & 1
+      const int st = (it + i) % C::kStages;
+      if (mbar_wait_warp(smem_u32(&full[st]), ((it + i) / C::kStages) & 1, &abort_s, a.err)) {
+        const uint32_t sk = base + st * C::kStageBytes, sv = sk + C::kBoxes * C::kBoxBytes;
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          qa[kk][0] = live ? __ldg(qh + 8 * kk) : 0u;
-          qa[kk][1] = live ? __ldg(qh + 8 * kk + 4) : 0u;
+          uint32_t b0, b1, b2, b3;
+          ldsm4(sk + swz(kpos, 2 * kk + (lmat & 1)), b0, b1, b2, b3);
+          mma16<FP16>(sc[0], qa[kk][0], 0u, qa[kk][1], 0u, b0, b1);
+          mma16<FP16>(sc[1], qa[kk][0], 0u, qa[kk][1], 0u, b2, b3);
         }
-      }
-      float o[D / 8][4];
+        const int j0 = x.r.tile(x.i0 + i) * kTN;
+        uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;   // value pairs that the token sees
+        float s2[2][2] = {{sc[0][0] * a.qk_scale, sc[0][1] * a.qk_scale}, {sc[1][0] * a.qk_scale, sc[1][1] * a.qk_scale}};
+        const bool open = tile_open<kTN>(a, j0, x.p0, x.p0);
+        if (!open) {
+          const int j = j0 + wq * 16 + c2;
+          const bool v00 = paged_sees(a, x.p0, j), v01 = paged_sees(a, x.p0, j + 1);
+          const bool v10 = paged_sees(a, x.p0, j + 8), v11 = paged_sees(a, x.p0, j + 9);
+          s2[0][0] = v00 ? s2[0][0] : -INFINITY;
+          s2[0][1] = v01 ? s2[0][1] : -INFINITY;
+          s2[1][0] = v10 ? s2[1][0] : -INFINITY;
+          s2[1][1] = v11 ? s2[1][1] : -INFINITY;
+          keep0 = (v00 ? 0xFFFFu : 0u) | (v01 ? 0xFFFF0000u : 0u);
+          keep1 = (v10 ? 0xFFFFu : 0u) | (v11 ? 0xFFFF0000u : 0u);
+        }
+        float mx = fmaxf(fmaxf(s2[0][0], s2[0][1]), fmaxf(s2[1][0], s2[1][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        const float m_new = fmaxf(m_run, mx);
+        const float alpha = ex2(m_run - m_new);
+        m_run = m_new;
+        float p[2][2];
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-      float m_run = kNegBig, l_run = 0.f;
-      for (int i = (it ^ wg) & 1; i < n; i += 2) {   // tile it + i of the share goes to group (it + i) & 1
-        const int st = (it + i) % C::kStages;
-        const bool ok = mbar_wait_warp(smem_u32(&full[st]), ((it + i) / C::kStages) & 1, &abort_s, a.err);
-        if (ok) {
-          const uint32_t sk = base + st * C::kStageBytes, sv = sk + C::kBoxes * C::kBoxBytes;
-          float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t b0, b1, b2, b3;
-            ldsm4(sk + swz(kpos, 2 * kk + (lmat & 1)), b0, b1, b2, b3);
-            mma16<FP16>(sc[0], qa[kk][0], 0u, qa[kk][1], 0u, b0, b1);
-            mma16<FP16>(sc[1], qa[kk][0], 0u, qa[kk][1], 0u, b2, b3);
-          }
-          const int j0 = tr.tile(i0 + i) * kTN;
-          uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;   // value pairs that the token sees
-          float x[2][2] = {{sc[0][0] * a.qk_scale, sc[0][1] * a.qk_scale}, {sc[1][0] * a.qk_scale, sc[1][1] * a.qk_scale}};
-          const bool open = tile_open<kTN>(a, j0, s.p0, s.p0);
+          for (int e = 0; e < 2; ++e) p[j][e] = ex2(s2[j][e] - m_new);
+        l_run = l_run * alpha + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][0] *= alpha;
+          o[j][1] *= alpha;
+          o[j][2] *= alpha;
+          o[j][3] *= alpha;
+        }
+        const uint32_t a0 = pack16<FP16>(p[0][0], p[0][1]), a2 = pack16<FP16>(p[1][0], p[1][1]);
+        const float2 t0 = unpack16<FP16>(a0), t2 = unpack16<FP16>(a2);
+        const uint32_t a1 = pack16<FP16>(p[0][0] - t0.x, p[0][1] - t0.y);
+        const uint32_t a3 = pack16<FP16>(p[1][0] - t2.x, p[1][1] - t2.y);
+#pragma unroll
+        for (int jj = 0; jj < D / 16; ++jj) {
+          uint32_t b0, b1, b2, b3;
+          ldsm4_t(sv + swz(vpos, 2 * jj + (lmat >> 1)), b0, b1, b2, b3);
           if (!open) {
-            const int j = j0 + wq * 16 + c2;
-            const bool v00 = paged_sees(a, s.p0, j), v01 = paged_sees(a, s.p0, j + 1);
-            const bool v10 = paged_sees(a, s.p0, j + 8), v11 = paged_sees(a, s.p0, j + 9);
-            x[0][0] = v00 ? x[0][0] : -INFINITY;
-            x[0][1] = v01 ? x[0][1] : -INFINITY;
-            x[1][0] = v10 ? x[1][0] : -INFINITY;
-            x[1][1] = v11 ? x[1][1] : -INFINITY;
-            keep0 = (v00 ? 0xFFFFu : 0u) | (v01 ? 0xFFFF0000u : 0u);
-            keep1 = (v10 ? 0xFFFFu : 0u) | (v11 ? 0xFFFF0000u : 0u);
+            b0 &= keep0;
+            b1 &= keep1;
+            b2 &= keep0;
+            b3 &= keep1;
           }
-          float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-          const float m_new = fmaxf(m_run, mx);
-          const float alpha = exp2f(m_run - m_new);
-          m_run = m_new;
-          float p[2][2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) p[j][e] = exp2f(x[j][e] - m_new);
-          l_run = l_run * alpha + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            o[j][0] *= alpha;
-            o[j][1] *= alpha;
-            o[j][2] *= alpha;
-            o[j][3] *= alpha;
-          }
-          const uint32_t a0 = pack16<FP16>(p[0][0], p[0][1]), a2 = pack16<FP16>(p[1][0], p[1][1]);
-          const float2 t0 = unpack16<FP16>(a0), t2 = unpack16<FP16>(a2);
-          const uint32_t a1 = pack16<FP16>(p[0][0] - t0.x, p[0][1] - t0.y);
-          const uint32_t a3 = pack16<FP16>(p[1][0] - t2.x, p[1][1] - t2.y);
-#pragma unroll
-          for (int jj = 0; jj < D / 16; ++jj) {
-            uint32_t b0, b1, b2, b3;
-            ldsm4_t(sv + swz(vpos, 2 * jj + (lmat >> 1)), b0, b1, b2, b3);
-            if (!open) {
-              b0 &= keep0;
-              b1 &= keep1;
-              b2 &= keep0;
-              b3 &= keep1;
-            }
-            mma16<FP16>(o[2 * jj], a0, a1, a2, a3, b0, b1);
-            mma16<FP16>(o[2 * jj + 1], a0, a1, a2, a3, b2, b3);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
-      }
-      it += n;
-
-      // ---- join the eight warps in order
-      l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
-      l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 2);
-      if ((lane & 3) == 0) {
-        m_s[warp][r] = m_run;
-        l_s[warp][r] = l_run;
-      }
-      float* ow = join_s + (warp * kRows + r) * C::kOStride + c2;
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-        *reinterpret_cast<float2*>(ow + 8 * j) = make_float2(o[j][0] + o[j][2], o[j][1] + o[j][3]);
-      consumers_sync();
-      if (tid < kWarps * kRows) {
-        const int rr = tid & (kRows - 1), w = tid / kRows;
-        float M = m_s[0][rr];
-#pragma unroll
-        for (int v = 1; v < kWarps; ++v) M = fmaxf(M, m_s[v][rr]);
-        wt_s[w][rr] = exp2f(m_s[w][rr] - M);
-      }
-      consumers_sync();
-      const bool whole = i0 == 0 && n == tr.count;
-      float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats;
-      for (int e = tid; e < a.G * (D / 4); e += kWarps * 32) {
-        const int row = e / (D / 4), dim = (e % (D / 4)) * 4;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float L = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float4 v = *reinterpret_cast<const float4*>(join_s + (w * kRows + row) * C::kOStride + dim);
-          const float sw = wt_s[w][row];
-          acc.x += v.x * sw;
-          acc.y += v.y * sw;
-          acc.z += v.z * sw;
-          acc.w += v.w * sw;
-          L += l_s[w][row] * sw;
-        }
-        if (whole) {
-          const float inv = s.p0 < 0 ? 0.f : 1.f / L;
-          const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-          if (!isfinite(v.x) || !isfinite(v.y) || !isfinite(v.z) || !isfinite(v.w)) raise_flag(a.err, kErrNonFinite);
-          *reinterpret_cast<uint2*>(a.o + s.row0 * a.o_stride + (long long)(g * a.G + row) * D + dim) =
-              make_uint2(pack16<FP16>(v.x, v.y), pack16<FP16>(v.z, v.w));
-        } else {
-          *reinterpret_cast<float4*>(part + row * D + dim) = acc;
-          if (dim == 0) {
-            float M = m_s[0][row];
-#pragma unroll
-            for (int v = 1; v < kWarps; ++v) M = fmaxf(M, m_s[v][row]);
-            part[kRows * D + row] = M;
-            part[kRows * D + kRows + row] = L;
-          }
+          mma16<FP16>(o[2 * jj], a0, a1, a2, a3, b0, b1);
+          mma16<FP16>(o[2 * jj + 1], a0, a1, a2, a3, b2, b3);
         }
       }
-      if (i0 == 0 && !whole && tid == 0) {
-        // the last CTA with a part: the one whose share holds the item's last unit
-        const uint32_t e = first + units;
-        int c = share_of(e - 1, total, ctas);
-        while (c > cta + 1 && snap(share_start(total, c, ctas), first, e, kItemUnits, kSlack) >= e) --c;
-        split.rec[cta] = SplitRecord{s.row0, g, 1, c, s.p0};
-      }
-      u = min(end, first + units);
-      consumers_sync();   // the joining buffer is free again
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
     }
+    it += x.n;
+
+    // ---- join the eight warps in order; the next segment's queries are on their way meanwhile
+    l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
+    l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 2);
+    if ((lane & 3) == 0) {
+      ml_s[buf][r][0][warp] = m_run;
+      ml_s[buf][r][1][warp] = l_run;
+    }
+    float* ow = join_s + buf * C::kJoinFloats + (warp * kRows + r) * C::kOStride + c2;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+      *reinterpret_cast<float2*>(ow + 8 * j) = make_float2(o[j][0] + o[j][2], o[j][1] + o[j][3]);
+    const Segment now = x;
+    x = next_segment();
+    load_queries(x);
+    consumers_sync();
+    const bool whole = now.i0 == 0 && now.n == now.r.count;
+    float* part = split.part + ((size_t)cta * 2 + (now.i0 == 0 ? 1 : 0)) * C::kPartFloats;
+    for (int e = tid; e < a.G * (D / 4); e += kWarps * 32) {
+      const int row = e / (D / 4), dim = (e % (D / 4)) * 4;
+      float mw[kWarps], lw[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; w += 4) {
+        const float4 m4 = *reinterpret_cast<const float4*>(&ml_s[buf][row][0][w]);
+        const float4 l4 = *reinterpret_cast<const float4*>(&ml_s[buf][row][1][w]);
+        mw[w] = m4.x, mw[w + 1] = m4.y, mw[w + 2] = m4.z, mw[w + 3] = m4.w;
+        lw[w] = l4.x, lw[w + 1] = l4.y, lw[w + 2] = l4.z, lw[w + 3] = l4.w;
+      }
+      float M = mw[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, mw[w]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v =
+            *reinterpret_cast<const float4*>(join_s + buf * C::kJoinFloats + (w * kRows + row) * C::kOStride + dim);
+        const float sw = ex2(mw[w] - M);
+        acc.x += v.x * sw;
+        acc.y += v.y * sw;
+        acc.z += v.z * sw;
+        acc.w += v.w * sw;
+        L += lw[w] * sw;
+      }
+      if (whole) {
+        const float inv = now.p0 < 0 ? 0.f : 1.f / L;
+        const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (!isfinite(v.x) || !isfinite(v.y) || !isfinite(v.z) || !isfinite(v.w)) raise_flag(a.err, kErrNonFinite);
+        *reinterpret_cast<uint2*>(a.o + now.row0 * a.o_stride + (long long)(now.g * a.G + row) * D + dim) =
+            make_uint2(pack16<FP16>(v.x, v.y), pack16<FP16>(v.z, v.w));
+      } else {
+        *reinterpret_cast<float4*>(part + row * D + dim) = acc;
+        if (dim == 0) {
+          part[kRows * D + row] = M;
+          part[kRows * D + kRows + row] = L;
+        }
+      }
+    }
+    if (now.i0 == 0 && !whole && tid == 0) {
+      // the last CTA with a part: the one whose share holds the item's last unit
+      int c = share_of(now.end - 1, total, ctas);
+      while (c > cta + 1 && snap(share_start(total, c, ctas), now.first, now.end, kItemUnits, kSlack) >= now.end) --c;
+      split.rec[cta] = SplitRecord{now.row0, now.g, 1, c, now.p0};
+    }
+    buf ^= 1;
   }
 }
 
