@@ -26,6 +26,7 @@ struct PagedArgs {
   int B, T, max_new;
   int window, sinks;
   int fp16;
+  int small;                // few row blocks: one warp makes a CTA's schedule (kWarpSchedule)
   long long q_stride, o_stride, page_stride, head_stride, row_stride;
   float qk_scale;           // log2(e) / sqrt(D): scores in base-2 units
 };
@@ -110,17 +111,21 @@ struct SplitRecord {
   int32_t p_lo;                  // position of the item's first token
 };
 
-// Exclusive sums over a block of NT threads; `sum` gets the total.  (Rolled up, like the rest of the
-// schedule: it runs once, and its time is that of fetching its instructions.)
+// Exclusive sums over NT threads, a whole block, or (NT = 32) one warp; `sum` gets the total.  (Rolled up, like
+// the rest of the schedule: it runs once, and its time is that of fetching its instructions.)
 template <int NT>
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long mine, unsigned long long* warp_s,
-                                                         unsigned long long* sum) {
+__device__ __forceinline__ unsigned long long exclusive_scan(unsigned long long mine, unsigned long long* warp_s,
+                                                             unsigned long long* sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long inc = mine;
 #pragma unroll 1
   for (int off = 1; off < 32; off <<= 1) {
     const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
     if (lane >= off) inc += x;
+  }
+  if (NT == 32) {
+    *sum = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    return inc - mine;
   }
   __syncthreads();   // warp_s may still be read
   if (lane == 31) warp_s[warp] = inc;
@@ -135,6 +140,46 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long mine
   *sum = all;
   return before;
 }
+
+template <int NT>
+__device__ __forceinline__ void group_sync() {
+  if (NT == 32) __syncwarp();
+  else __syncthreads();
+}
+
+// Sums of cost(b) over the sequences before each, into pre_s[0 .. B], by NT threads together; returns the
+// total.
+template <int NT, class Cost>
+__device__ __forceinline__ unsigned long long scan_sequences(int B, uint32_t* pre_s, unsigned long long* warp_s, Cost cost) {
+  const int tid = threadIdx.x, per = (B + NT - 1) / NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  unsigned long long mine = 0, sum;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    pre_s[b] = (uint32_t)mine;
+    mine += cost(b);
+  }
+  const uint32_t before = (uint32_t)exclusive_scan<NT>(mine, warp_s, &sum);
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) pre_s[b] += before;
+  if (tid == 0) pre_s[B] = (uint32_t)sum;
+  group_sync<NT>();
+  return sum;
+}
+
+// The last sequence b with pre_s[b] <= x (x < pre_s[B]).
+__device__ __forceinline__ int find_sequence(const uint32_t* pre_s, int B, uint32_t x) {
+  int lo = 0, hi = B - 1;
+#pragma unroll 1
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre_s[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Row blocks (at most) up to which one warp makes the schedule, without the block's barriers.
+constexpr int kWarpSchedule = 128;
 
 // A cut of the order within the item of units s .. e - 1 (`own` of them its start and end, then its tiles),
 // moved to an end of the item that is within `slack` tiles.  What remains between has tiles on both sides.

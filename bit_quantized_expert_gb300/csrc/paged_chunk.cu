@@ -83,39 +83,19 @@ struct Share {
   int b, qt, ctas;
 };
 
-// Finds this CTA's share, the whole block together: row blocks per sequence are scanned into pre_s[0 .. B],
-// then their costs (tiles times heads), a run of consecutive row blocks a thread; the threads whose runs
-// hold the two cuts walk theirs once more.  Leaves the share empty if there is nothing to do, or (bad) more
-// than 2^32 tiles.
+// Finds this CTA's share, NT threads (the block or its first warp) together: row blocks per sequence are
+// scanned into pre_s[0 .. B], then their costs (units times heads), a run of consecutive row blocks a
+// thread; the threads whose runs hold the two cuts walk theirs once more.  Leaves the share empty if there
+// is nothing to do, or (bad) 2^32 units or more.
+template <int NT>
 __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint32_t* pre_s, unsigned long long* warp_s,
                                            Share* share_s, bool& bad) {
   const int tid = threadIdx.x;
-  unsigned long long sum;
-  {
-    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    uint32_t mine = 0;
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      pre_s[b] = mine;
-      mine += (uint32_t)(load_seq(a, b, bad).n + tokens - 1) / (uint32_t)tokens;
-    }
-    const uint32_t before = (uint32_t)block_scan<kThreads>(mine, warp_s, &sum);
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) pre_s[b] += before;
-    if (tid == 0) pre_s[a.B] = (uint32_t)sum;
-    __syncthreads();
-  }
-  const uint32_t blocks = (uint32_t)sum, per = (blocks + kThreads - 1) / kThreads;
+  unsigned long long sum = scan_sequences<NT>(
+      a.B, pre_s, warp_s, [&](int b) { return (uint32_t)(load_seq(a, b, bad).n + tokens - 1) / (uint32_t)tokens; });
+  const uint32_t blocks = (uint32_t)sum, per = (blocks + NT - 1) / NT;
   const uint32_t i0 = min(tid * per, blocks), i1 = min(i0 + per, blocks);
-  int b_mine = 0;
-  if (i0 < i1) {
-    int hi = a.B - 1;   // the sequence that holds row block i0
-    while (b_mine < hi) {
-      const int mid = (b_mine + hi + 1) >> 1;
-      if (pre_s[mid] <= i0) b_mine = mid;
-      else hi = mid - 1;
-    }
-  }
+  const int b_mine = i0 < i1 ? find_sequence(pre_s, a.B, i0) : 0;
   const int cta = (int)blockIdx.x;
   unsigned long long mine = 0;
   uint32_t at = 0, lo = 0, hi = 0, slack = 0;
@@ -138,7 +118,7 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
         for (int side = 0; side < 2; ++side) {
           const uint32_t x = side == 0 ? lo : hi;
           if (x < at || x >= end) continue;
-          const uint32_t first = at + (x - at) / c * c, to = x == first ? x : snap(x, first, first + c, kItemUnits, slack);
+          const uint32_t first = x - (x - at) % c, to = x == first ? x : snap(x, first, first + c, kItemUnits, slack);
           if (side == 0) {
             share_s->lo = to;
             share_s->at = at;
@@ -152,11 +132,11 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
       }
     }
     if (pass == 1) return;
-    at = (uint32_t)block_scan<kThreads>(mine, warp_s, &sum);
+    at = (uint32_t)exclusive_scan<NT>(mine, warp_s, &sum);
     if (sum >> 32) bad = true;
     if ((sum >> 32) || sum == 0) return;
     const uint32_t total = (uint32_t)sum;
-    const int ctas = (int)min(gridDim.x, total);   // no more shares than tiles
+    const int ctas = (int)min(gridDim.x, total);   // no more shares than units
     if (cta >= ctas) return;
     // A part costs a result written, read and joined: more than two tiles of imbalance.
     slack = max(2u, total / ctas / 32);
@@ -419,7 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   bool bad = false;
-  find_share(a, tokens, pre_s, warp_s, &share_s, bad);
+  if (a.small) {
+    if (warp == 0) find_share<32>(a, tokens, pre_s, warp_s, &share_s, bad);
+  } else {
+    find_share<kThreads>(a, tokens, pre_s, warp_s, &share_s, bad);
+  }
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
   if (tid == 0) split.rec[cta].until = -1;
   tc_fence_before();
@@ -453,8 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kSoftmaxWarps) {
     // ---- copies
-    const int ppt = max(1, kTN >> a.page_shift), box_rows = min(kTN, 1 << a.page_shift);
-    const int batch = 32 / ppt;                              // tiles whose page numbers the lanes hold
+    const int ppt_shift = 7 - a.page_shift, ppt = 1 << ppt_shift, box_rows = 1 << a.page_shift;   // pages of a tile
+    const int batch = 32 >> ppt_shift;                              // tiles whose page numbers the lanes hold
     int at = 0, items = 0;   // ring stages and segments so far
     bad = false;
     walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
@@ -466,8 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int pg = 0, ahead = 0;
       bool need = false;
       auto read_ahead = [&](int i) {
-        const int t = i0 + i + lane / ppt, ip = t < x.r.count ? ((x.r.tile(t) * kTN) >> a.page_shift) + lane % ppt : 0;
-        need = lane / ppt < n - i && t < x.r.count && ip < a.max_pages && page_needed(a, ip, x.p_lo, x.p_hi);
+        const int t = i0 + i + (lane >> ppt_shift);
+        const int ip = t < x.r.count ? (x.r.tile(t) << ppt_shift) + (lane & (ppt - 1)) : 0;
+        need = (lane >> ppt_shift) < n - i && t < x.r.count && ip < a.max_pages && page_needed(a, ip, x.p_lo, x.p_hi);
         if (need) ahead = __ldg(row + ip);
       };
       read_ahead(0);
@@ -483,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(sKV + st * C::kStageBytes + half * C::kTileBytes + box * C::kBoxBytes + sub * box_rows * 128, map,
                         FULL(st), box * 64, 0, g, p);
         };
-        if (i > 0) copy(&maps.v, 1, (i - 1) % batch);
+        if (i > 0) copy(&maps.v, 1, (i - 1) & (batch - 1));
         if (i < n) {
-          const int in = i % batch;
+          const int in = i & (batch - 1);
           if (in == 0) {
             const bool ok = ahead >= 0 && ahead < a.num_pages;
             pg = need && ok ? ahead : a.num_pages;

@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(16) float ml_s[2][kRows][2][kWarps];   // per buffer and row: the warps' max, then sum
   __shared__ unsigned long long warp_s[kThreads / 32];
   __shared__ int abort_s;
+  __shared__ uint32_t total_s;
   const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   float* join_s = reinterpret_cast<float*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes);
   uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes + C::kJoinBytes);
@@ -125,27 +126,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- this CTA's share: units lo .. hi - 1 of (sequence, head, tile); pre_s: units before each sequence
   bool bad = false;
-  uint32_t total;
-  {
-    const int per = (a.B + kThreads - 1) / kThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    unsigned long long mine = 0, sum;
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      const SeqRows s = load_seq(a, b, bad);
-      pre_s[b] = (uint32_t)mine;
-      if (s.n != 0) mine += (unsigned long long)(visible_tiles<kTN>(a, s.p0, s.p0).count + kItemUnits) * a.Hkv;
-    }
-    const uint32_t before = (uint32_t)block_scan<kThreads>(mine, warp_s, &sum);
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) pre_s[b] += before;
-    if (tid == 0) pre_s[a.B] = (uint32_t)sum;
-    if (sum >> 32) {   // refused: nothing is computed
-      bad = true;
-      sum = 0;
-    }
-    total = (uint32_t)sum;
-    __syncthreads();
+  auto cost = [&](int b) {
+    const SeqRows s = load_seq(a, b, bad);
+    return s.n == 0 ? 0ull : (unsigned long long)(visible_tiles<kTN>(a, s.p0, s.p0).count + kItemUnits) * a.Hkv;
+  };
+  auto note = [&](unsigned long long sum) {
+    if (sum >> 32) bad = true;                                          // refused: nothing is computed
+    if (tid == 0) total_s = (sum >> 32) ? 0u : (uint32_t)sum;
+  };
+  if (a.small) {
+    if (warp == 0) note(scan_sequences<32>(a.B, pre_s, warp_s, cost));
+  } else {
+    note(scan_sequences<kThreads>(a.B, pre_s, warp_s, cost));
   }
+  __syncthreads();
+  const uint32_t total = total_s;
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
   const int ctas = (int)min(gridDim.x, total);   // every share holds a tile
   if (tid == 0) split.rec[cta].until = -1;
@@ -155,12 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
   for (int side = 1; side >= 0; --side) {
     uint32_t x = share_start(total, cta + side, ctas);
-    int b = 0;
-    for (int top = a.B - 1; b < top;) {
-      const int mid = (b + top + 1) >> 1;
-      if (pre_s[mid] <= x) b = mid;
-      else top = mid - 1;
-    }
+    const int b = find_sequence(pre_s, a.B, x);
     if (x < total) {
       const uint32_t units = (pre_s[b + 1] - pre_s[b]) / a.Hkv, first = x - (x - pre_s[b]) % units;
       x = snap(x, first, first + units, kItemUnits, kSlack);
@@ -178,12 +168,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one by one (75 to 120 cycles each: 16 of them, the boxes of pages of 16, took as long as a tile's
     // stream from memory).
     const int pw = warp - kWarps;
-    const int ppt = max(1, kTN >> a.page_shift);               // pages of a tile
+    const int ppt_shift = max(0, 6 - a.page_shift), ppt = 1 << ppt_shift;   // pages of a tile
     const int box_rows = min(kTN, 1 << a.page_shift);
     const int copies = ppt * 2 * C::kBoxes;                    // (page, keys or values, 64-dim box)
     const int c0 = copies * pw / kCopyWarps, mine = copies * (pw + 1) / kCopyWarps - c0;
     const int sub = (c0 + lane) / (2 * C::kBoxes), kv = ((c0 + lane) / C::kBoxes) & 1, box = (c0 + lane) % C::kBoxes;
-    const int batch = 32 / ppt;                                // tiles whose page numbers the lanes hold
+    const int batch = 32 >> ppt_shift;                         // tiles whose page numbers the lanes hold
     int b = b_first, issued = 0;
     bool stop = false;
     bad = false;
@@ -201,13 +191,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pg = 0, ahead = 0;
         bool need = false;
         auto read_ahead = [&](int i) {
-          const int t = i0 + i + lane / ppt, ip = t < r.count ? ((r.tile(t) * kTN) >> a.page_shift) + lane % ppt : 0;
-          need = lane / ppt < n - i && t < r.count && ip < a.max_pages && page_needed(a, ip, s.p0, s.p0);
+          const int t = i0 + i + (lane >> ppt_shift);
+          const int ip = t < r.count ? ((r.tile(t) * kTN) >> a.page_shift) + (lane & (ppt - 1)) : 0;
+          need = (lane >> ppt_shift) < n - i && t < r.count && ip < a.max_pages && page_needed(a, ip, s.p0, s.p0);
           if (need) ahead = __ldg(row + ip);
         };
         read_ahead(0);
         for (int i = 0; i < n; ++i) {
-          const int in = i % batch;
+          const int in = i & (batch - 1);
           if (in == 0) {
             const bool ok = ahead >= 0 && ahead < a.num_pages;
             pg = need && ok ? ahead : a.num_pages;
