@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
   const int n_free = min(max(n_free_raw, 0), a.free_capacity);
   if (n_free != n_free_raw) bad = true;
   // Every CTA has read n_free (which n_free_out may be) before one of them writes n_free_out.
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
   __syncthreads();
 

@@ -118,6 +118,7 @@ __device__ __forceinline__ unsigned long long exclusive_scan(unsigned long long 
                                                              unsigned long long* sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long inc = mine;
+  __syncwarp();   // the lanes' runs differ in length
 #pragma unroll 1
   for (int off = 1; off < 32; off <<= 1) {
     const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
@@ -143,8 +144,8 @@ __device__ __forceinline__ unsigned long long exclusive_scan(unsigned long long 
 
 template <int NT>
 __device__ __forceinline__ void group_sync() {
-  if (NT == 32) __syncwarp();
-  else __syncthreads();
+  __syncwarp();
+  if (NT != 32) __syncthreads();
 }
 
 // Sums of cost(b) over the sequences before each, into pre_s[0 .. B], by NT threads together; returns the

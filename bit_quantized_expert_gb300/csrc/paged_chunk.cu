@@ -155,30 +155,39 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
 
 // Four products of one 64-wide piece of the inner axis, in one statement: every descriptor is in a register
 // before the first, so that the issuing warp, which shares its scheduler with softmax warps, waits for one
-// slot a product and not for its descriptor arithmetic.
+// slot a product and not for its descriptor arithmetic.  The whole warp comes here together; the lane with
+// `go` set issues, by predicate and not by branch, so that the warp never parts.
 // D[tmem] (+)= A[smem] B[smem]^T, both K-major in the 128-byte swizzle: 32 bytes a step.
-__device__ __forceinline__ void tc_mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void tc_mma4_ss(uint32_t go, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, t;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.ne.b32 t, %11, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, t;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, t;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, t;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, t, e;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.ne.b32 t, %11, 0;\n\tsetp.ne.b32 e, %12, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, t;\n\t}" ::"r"(d),
       "l"(a), "l"(a + 2u), "l"(a + 4u), "l"(a + 6u), "l"(b), "l"(b + 2u), "l"(b + 4u), "l"(b + 6u), "r"(idesc), "r"(acc),
-      "r"(1u)
+      "r"(1u), "r"(go)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]: A 16-bit pairs in tensor memory (8 columns a step), B as desc_values (2048
 // bytes a step).
-__device__ __forceinline__ void tc_mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void tc_mma4_ts(uint32_t go, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, t;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.ne.b32 t, %11, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, t;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, t;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, t;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, t, e;\n\tsetp.ne.b32 p, %10, 0;\n\tsetp.ne.b32 t, %11, 0;\n\tsetp.ne.b32 e, %12, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, t;\n\t}" ::"r"(d),
       "r"(a), "r"(a + 8u), "r"(a + 16u), "r"(a + 24u), "l"(b), "l"(b + 128u), "l"(b + 256u), "l"(b + 384u), "r"(idesc),
-      "r"(acc), "r"(1u)
+      "r"(acc), "r"(1u), "r"(go)
+      : "memory");
+}
+// tc_commit by the lane with `go` set.
+__device__ __forceinline__ void tc_commit_if(uint32_t go, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(go)
       : "memory");
 }
 
@@ -406,6 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
   if (tid == 0) split.rec[cta].until = -1;
+  // Lanes part ways in the schedule (and below, wherever a lane's own data decides).  Every such place ends in
+  // __syncwarp before the warp's next collective instruction (barriers, tensor-memory loads and stores): those
+  // assume a converged warp, which a join of branches alone does not promise.
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -467,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < ppt * C::kBoxes)
             tma_load_4d(sKV + st * C::kStageBytes + half * C::kTileBytes + box * C::kBoxBytes + sub * box_rows * 128, map,
                         FULL(st), box * 64, 0, g, p);
+          __syncwarp();
         };
         if (i > 0) copy(&maps.v, 1, (i - 1) & (batch - 1));
         if (i < n) {
@@ -490,17 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(sQ + t * C::kTileBytes + bx * C::kBoxBytes, &maps.q, QFULL, bx * 64, g * a.G,
                             s.row0 + x.t0 + t * tpt);
           }
+          __syncwarp();
         }
       }
       return true;
     });
     if (bad) raise_flag(a.err, kErrBadPages);
     } else if (warp == kSoftmaxWarps + 1) {
-    // ---- tensor-core instructions.  The whole warp takes every step, one elected lane issues, and row tile
-    // and ring stage are constants of the unrolled code: descriptors and addresses then sit in uniform
+    // ---- tensor-core instructions.  The whole warp takes every step, one elected lane issues (by predicate), and
+    // row tile and ring stage are constants of the unrolled code: descriptors and addresses then sit in uniform
     // registers, and a product costs one issue slot beside the two softmax warps of this scheduler.  (A
     // single lane's walk with computed descriptors took twice as long per product under that load.)
-    const bool go = elect_one();
+    const uint32_t go = elect_one() ? 1u : 0u;
     constexpr uint32_t fmt = FP16 ? 0u : ((1u << 7) | (1u << 10));
     constexpr uint32_t id_s = (1u << 4) | fmt | ((kTN >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
@@ -513,9 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
 #pragma unroll
       for (int box = 0; box < C::kBoxes; ++box)
-        tc_mma4_ss(t * 128, dq + (t * kTileUnits + box * kBoxUnits), dk + (ST * 2 * kTileUnits + box * kBoxUnits), id_s,
+        tc_mma4_ss(go, t * 128, dq + (t * kTileUnits + box * kBoxUnits), dk + (ST * 2 * kTileUnits + box * kBoxUnits), id_s,
                    box != 0);
-      tc_commit(SFULL(t));
+      tc_commit_if(go, SFULL(t));
     };
     // O_t (+)= P_t V, P in two halves, with the values of stage ST; then the next tile's scores
     auto turn = [&](auto t_c, auto st_c, uint32_t done, bool first, bool more) {
@@ -523,16 +538,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t v = dv + ST * 2 * kTileUnits;
       if (!wait(PFULL(t, 0), done)) return false;
       tc_fence_after();
-      if (go) tc_mma4_ts(kTmemO + t * 128, t * 128, v, id_o, !first);
-      __syncwarp();
+      tc_mma4_ts(go, kTmemO + t * 128, t * 128, v, id_o, !first);
       if (!wait(PFULL(t, 1), done)) return false;
       tc_fence_after();
-      if (go) {
-        tc_mma4_ts(kTmemO + t * 128, t * 128 + 32, v + (8192u >> 4), id_o, 1u);
-        if (more) scores(t_c, st_c);
-        else tc_commit(OFULL(t));
-      }
-      __syncwarp();
+      tc_mma4_ts(go, kTmemO + t * 128, t * 128 + 32, v + (8192u >> 4), id_o, 1u);
+      if (more) scores(t_c, st_c);
+      else tc_commit_if(go, OFULL(t));
       return true;
     };
     using Zero = std::integral_constant<int, 0>;
@@ -548,13 +559,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int ST = decltype(st_c)::value;
             if (!wait(FULL(ST), at >> 1)) return false;
             tc_fence_after();
-            if (go) {
-              scores(Zero{}, st_c);
-              if (two) scores(One{}, st_c);
-              tc_commit(EMPTY(ST));
-              if (n == 1) tc_commit(QEMPTY);
-            }
-            __syncwarp();
+            scores(Zero{}, st_c);
+            if (two) scores(One{}, st_c);
+            tc_commit_if(go, EMPTY(ST));
+            if (n == 1) tc_commit_if(go, QEMPTY);
             return true;
           }))
         return false;
@@ -572,11 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
                 if (!turn(One{}, st_c, done1++, i == 0, more)) return false;
               }
-              if (go) {
-                tc_commit(EMPTY(ST));
-                if (i + 2 == n) tc_commit(QEMPTY);
-              }
-              __syncwarp();
+              tc_commit_if(go, EMPTY(ST));
+              if (i + 2 == n) tc_commit_if(go, QEMPTY);
               return true;
             }))
           return false;
@@ -643,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (t == 1 && lane == 0) mbar_arrive(CLEAN);
+          __syncwarp();
         }
         uint32_t sr[128];
         tmem_ld128(tS, sr);
@@ -678,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             negm = nn;
             l *= alpha;
           }
+          __syncwarp();
           if (i > 0) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -710,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(PFULL(t, c / 64));
+            __syncwarp();
           }
         }
         const float2 s0 = unpair2(sum0), s1 = unpair2(sum1);
@@ -756,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + extra[e]);
         }
+        __syncwarp();
         if (whole) {
           // 64 bytes a row through shared memory (16-byte pieces XOR-ed against bank conflicts), so that a store
           // touches 8 rows, not 32.
@@ -786,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) part[(c + e) * kItemRows] = __uint_as_float(v[e]);
         }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -805,6 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           split.rec[cta] = SplitRecord{s.row0 + x.t0, g, x.n, c, x.p_lo};
         }
       }
+      __syncwarp();
       return true;
     });
   }
@@ -814,6 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (clock64() - c0 < 4000000ll) {
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == kSoftmaxWarps + 1) {

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     note(scan_sequences<kThreads>(a.B, pre_s, warp_s, cost));
   }
+  __syncwarp();
   __syncthreads();
   const uint32_t total = total_s;
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < mine)
             tma_load_4d(base + st * C::kStageBytes + (kv * C::kBoxes + box) * C::kBoxBytes + sub * box_rows * 128,
                         kv ? &maps.v : &maps.k, bar, box * 64, off, (int)g, p);
+          __syncwarp();
           ++issued;
         }
         u = min(end, first + units);
@@ -371,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Segment now = x;
     x = next_segment();
     load_queries(x);
+    __syncwarp();
     consumers_sync();
     const bool whole = now.i0 == 0 && now.n == now.r.count;
     float* part = split.part + ((size_t)cta * 2 + (now.i0 == 0 ? 1 : 0)) * C::kPartFloats;
@@ -420,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (c > cta + 1 && snap(share_start(total, c, ctas), now.first, now.end, kItemUnits, kSlack) >= now.end) --c;
       split.rec[cta] = SplitRecord{now.row0, now.g, 1, c, now.p0};
     }
+    __syncwarp();   // lanes part above; the next tiles' products are collective
     buf ^= 1;
   }
 }
