@@ -209,13 +209,17 @@ __device__ __forceinline__ uint64_t desc_values(uint32_t saddr, uint32_t box_byt
       "=r"(v[o + 7]), "=r"(v[o + 8]), "=r"(v[o + 9]), "=r"(v[o + 10]), "=r"(v[o + 11]), "=r"(v[o + 12]),           \
       "=r"(v[o + 13]), "=r"(v[o + 14]), "=r"(v[o + 15])
 
-// 32 consecutive columns of this thread's row, load and wait in one statement.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// 64 consecutive columns of this thread's row: two loads and one wait in one statement.
+__device__ __forceinline__ void tmem_ld64(uint32_t t, uint32_t (&r)[64]) {
   asm volatile(
-      "{\n\ttcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;\n\t}"
-      : R16(r, 0), R16(r, 16)
-      : "r"(taddr)
+      "{\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : R16(r, 0), R16(r, 16), R16(r, 32), R16(r, 48)
+      : "r"(t), "r"(t + 32u)
       : "memory");
 }
 
@@ -247,13 +251,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
           taddr),
       I16(v, 0)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      I16(v, 0), I16(v, 16)
       : "memory");
 }
 #undef I16
@@ -324,7 +321,7 @@ __device__ __forceinline__ uint32_t non_finite16(uint32_t w) {
   return __vcmpeq2(w & mask, mask);
 }
 
-// What the rows that see non-finite values add to dims d0 .. d0 + 31 of their result: the sum of those
+// What the rows that see non-finite values add to dims d0 .. d0 + 63 of their result: the sum of those
 // values over the positions that the row sees in this segment's masked tiles.
 template <bool FP16>
 __device__ __noinline__ void add_non_finite(const PagedArgs& a, const int32_t* table, TileRange r, int i0, int n, int p_lo,
@@ -337,7 +334,7 @@ __device__ __noinline__ void add_non_finite(const PagedArgs& a, const int32_t* t
       const int page = table[j >> a.page_shift];
       if (page < 0 || page >= a.num_pages) continue;
       const uint16_t* v = a.vc + page * a.page_stride + g * a.head_stride + (j & ((1 << a.page_shift) - 1)) * a.row_stride + d0;
-      for (int e = 0; e < 32; e += 2) {
+      for (int e = 0; e < 64; e += 2) {
         const uint32_t w = *reinterpret_cast<const uint32_t*>(v + e), bad = non_finite16<FP16>(w);
         const float2 x = unpack16<FP16>(w);
         if (bad & 0xFFFFu) acc[e] += x.x;
@@ -747,60 +744,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats + t * 128 + r;
       const uint32_t out = sOut + warp * kOutBytes;
       const uint64_t inv2 = pair2(inv, inv);
-      uint64_t check = 0;   // 0 unless a result is not finite: the sum of 0 times every one
+      uint64_t check0 = 0, check1 = 0;   // 0 unless a result is not finite: the sums of 0 times every one
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(tO + c, v);
+      for (int c = 0; c < D; c += 64) {
+        uint32_t v[64];
+        tmem_ld64(tO + c, v);
         if (p < 0) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0u;
+          for (int e = 0; e < 64; ++e) v[e] = 0u;
         }
         if (hurt && live) {
-          float extra[32];
+          float extra[64];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) extra[e] = 0.f;
+          for (int e = 0; e < 64; ++e) extra[e] = 0.f;
           add_non_finite<FP16>(a, a.table + (size_t)b * a.max_pages, x.r, i0, n, x.p_lo, x.p_hi, p, g, c, extra);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + extra[e]);
+          for (int e = 0; e < 64; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + extra[e]);
         }
         __syncwarp();
         if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {   // pairs 2 e, 2 e + 2 become words e, e + 1
+            const uint64_t f0 = mul2(pair2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), inv2);
+            const uint64_t f1 = mul2(pair2(__uint_as_float(v[2 * e + 2]), __uint_as_float(v[2 * e + 3])), inv2);
+            check0 = fma2(f0, 0ull, check0);
+            check1 = fma2(f1, 0ull, check1);
+            const float2 y0 = unpair2(f0), y1 = unpair2(f1);
+            v[e] = pack16<FP16>(y0.x, y0.y);
+            v[e + 1] = pack16<FP16>(y1.x, y1.y);
+          }
           // 64 bytes a row through shared memory (16-byte pieces XOR-ed against bank conflicts), so that a store
           // touches 8 rows, not 32.
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)),
+                           "r"(v[16 * half + 4 * e]), "r"(v[16 * half + 4 * e + 1]), "r"(v[16 * half + 4 * e + 2]),
+                           "r"(v[16 * half + 4 * e + 3])
+                           : "memory");
+            __syncwarp();
+            uint4 w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint64_t f = mul2(pair2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1])), inv2);
-              check = fma2(f, 0ull, check);
-              const float2 y = unpair2(f);
-              w[k] = pack16<FP16>(y.x, y.y);
+              const int rr = k * 8 + (lane >> 2);
+              ld_shared4(out + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), w[k].x, w[k].y, w[k].z, w[k].w);
             }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
-          }
-          __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = k * 8 + (lane >> 2);
-            uint4 w;
-            ld_shared4(out + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), w.x, w.y, w.z, w.w);
-            if (to[k] != 0) *reinterpret_cast<uint4*>(to[k] + 2 * c) = w;
+            for (int k = 0; k < 4; ++k)
+              if (to[k] != 0) *reinterpret_cast<uint4*>(to[k] + 2 * c + 64 * half) = w[k];
+            __syncwarp();
           }
-          __syncwarp();
         } else if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) part[(c + e) * kItemRows] = __uint_as_float(v[e]);
+          for (int e = 0; e < 64; ++e) part[(c + e) * kItemRows] = __uint_as_float(v[e]);
         }
         __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(OEMPTY(t));
-      const float2 checks = unpair2(check);
+      const float2 checks = unpair2(add2(check0, check1));
       if (live && !(checks.x + checks.y == 0.f)) raise_flag(a.err, kErrNonFinite);
       if (!whole) {
         if (live) {
