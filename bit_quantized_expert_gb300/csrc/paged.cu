@@ -55,6 +55,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = (int)blockIdx.x, ctas = (int)gridDim.x;
   bool bad = false;
+  pdl_wait();
+  pdl_launch_dependents();
 
   // Exclusive sums over the sequences, four consecutive ones a thread, in 64 bits: the lengths are
   // unchecked, so their sum may pass 32.
@@ -191,31 +193,52 @@ struct AppendArgs {
   uint16_t *kc, *vc;
   uint32_t* err;
   int Hkv, B, T, page_shift, num_pages;
-  int units;   // 16-byte units of a head row (8 or 16)
+  int unit_shift;   // log2 of the 16-byte units of a head row (8 or 16)
   long long k_stride, v_stride, page_stride, head_stride, row_stride;
 };
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendBatch = 4;
 
-// Grid-stride over (token, head, 16-byte unit) of the keys and of the values (blockIdx.y).
+// The keys or the values (blockIdx.y), units of 16 bytes numbered by (token, head, unit of the row) in Index;
+// four units a thread and turn, their slots and their data loaded together, so that one round trip to
+// memory lies between the start and the stores.  Bound by memory: 8192 tokens of two heads of 128 are
+// 33.6 MB with both ways.
+template <class Index>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const bool values = blockIdx.y != 0;
+  const uint16_t* src = values ? a.v : a.k;
+  uint16_t* dst = values ? a.vc : a.kc;
+  const long long stride = values ? a.v_stride : a.k_stride;
+  const Index per = (Index)a.Hkv << a.unit_shift, n = (Index)a.T * per;
   const int rows = min(max(__ldg(a.q_start + a.B), 0), a.T);
-  const uint16_t* src = blockIdx.y == 0 ? a.k : a.v;
-  uint16_t* dst = blockIdx.y == 0 ? a.kc : a.vc;
-  const long long stride = blockIdx.y == 0 ? a.k_stride : a.v_stride;
-  const int per = a.Hkv * a.units;
-  const long long n = (long long)rows * per;
-  for (long long i = (long long)blockIdx.x * kAppendThreads + threadIdx.x; i < n;
-       i += (long long)gridDim.x * kAppendThreads) {
-    const int t = (int)(i / per), r = (int)(i % per), h = r / a.units, u = r % a.units;
-    const int slot = __ldg(a.slots + t), page = slot >> a.page_shift;
-    if (slot < 0 || page >= a.num_pages) {
-      if (slot != -1) raise_flag(a.err, kErrBadPages);
-      continue;
+  const Index step = (Index)gridDim.x * kAppendThreads;
+  for (Index i0 = (Index)blockIdx.x * kAppendThreads + threadIdx.x; i0 < n; i0 += step * kAppendBatch) {
+    int t[kAppendBatch], r[kAppendBatch], slot[kAppendBatch];
+    uint4 x[kAppendBatch];
+#pragma unroll
+    for (int j = 0; j < kAppendBatch; ++j) {
+      const Index i = i0 + j * step;
+      t[j] = i < n ? (int)(i / per) : a.T;
+      r[j] = i < n ? (int)(i - (Index)t[j] * per) : 0;
+      if (t[j] < rows) {
+        slot[j] = __ldg(a.slots + t[j]);
+        x[j] = __ldg(reinterpret_cast<const uint4*>(src + t[j] * stride) + r[j]);
+      }
     }
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + t * stride) + r);
-    const int off = slot & ((1 << a.page_shift) - 1);
-    *(reinterpret_cast<uint4*>(dst + page * a.page_stride + h * a.head_stride + off * a.row_stride) + u) = x;
+#pragma unroll
+    for (int j = 0; j < kAppendBatch; ++j) {
+      if (t[j] >= rows) continue;
+      const int page = slot[j] >> a.page_shift, off = slot[j] & ((1 << a.page_shift) - 1);
+      if (slot[j] < 0 || page >= a.num_pages) {
+        if (slot[j] != -1) raise_flag(a.err, kErrBadPages);
+        continue;
+      }
+      const int h = r[j] >> a.unit_shift, u = r[j] & ((1 << a.unit_shift) - 1);
+      *(reinterpret_cast<uint4*>(dst + page * a.page_stride + h * a.head_stride + off * a.row_stride) + u) = x[j];
+    }
   }
 }
 
@@ -393,17 +416,19 @@ extern "C" moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* 
   if (smem > 48 * 1024 && cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                2 * (kPagedMaxSeqs + 1) * (int)sizeof(long long)) != cudaSuccess)
     return MOE_ERR_CUDA;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = ctas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, plan_kernel, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -419,12 +444,23 @@ extern "C" moe_status gqa_paged_append(const gqa_paged_dims* dims, const uint16_
   int sms = 0;
   if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
   AppendArgs a = {k, v, slots, q_start, k_cache, v_cache, static_cast<uint32_t*>(workspace), d.n_kv_heads, d.n_seqs,
-                  d.n_tokens, log2_of(d.page_size), d.num_pages, d.head_dim / 8, d.k_stride, d.v_stride, d.page_stride,
+                  d.n_tokens, log2_of(d.page_size), d.num_pages, log2_of(d.head_dim / 8), d.k_stride, d.v_stride, d.page_stride,
                   d.head_stride, d.row_stride};
-  const long long units = (long long)d.n_tokens * d.n_kv_heads * a.units;
-  const int grid = (int)std::min((units + kAppendThreads - 1) / kAppendThreads, (long long)sms * 8);
-  append_kernel<<<dim3(grid, 2), kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const long long units = ((long long)d.n_tokens * d.n_kv_heads) << a.unit_shift;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min((units + kAppendThreads - 1) / kAppendThreads, (long long)sms * 4), 2);
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  // 32-bit unit numbers unless the last turn's could pass them.
+  const bool wide = units + (long long)cfg.gridDim.x * kAppendThreads * kAppendBatch >= (1ll << 32);
+  const cudaError_t e = wide ? cudaLaunchKernelEx(&cfg, append_kernel<unsigned long long>, a)
+                             : cudaLaunchKernelEx(&cfg, append_kernel<uint32_t>, a);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 extern "C" moe_status gqa_paged_attention(const gqa_paged_dims* dims, const uint16_t* q, const uint16_t* k_cache,

@@ -853,16 +853,27 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const PagedArgs a, cons
   const int tpt = 128 / a.G, t = slot >> 7, r = slot & 127, tok = r / a.G;
   if (tok >= tpt || t * tpt + tok >= rec.rows) return;
   auto part = [&](int c) { return split.part + ((size_t)c * 2 + (c == first ? 1 : 0)) * C::kPartFloats; };
+  // Two parts at a time, everything of both in flight at once (most items have two or three).
   float M = -1e30f, L = 0.f, acc[E];
-  for (int c = first; c <= rec.until; ++c) M = fmaxf(M, __ldcg(part(c) + D * kItemRows + slot));
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int c = first; c <= rec.until; ++c) {
-    const float* pc = part(c);
-    const float w = exp2f(__ldcg(pc + D * kItemRows + slot) - M);
-    L += __ldcg(pc + (D + 1) * kItemRows + slot) * w;
+  for (int c = first; c <= rec.until; c += 2) {
+    const bool second = c < rec.until;
+    const float *p0 = part(c), *p1 = second ? part(c + 1) : p0;
+    const float m0 = __ldcg(p0 + D * kItemRows + slot), l0 = __ldcg(p0 + (D + 1) * kItemRows + slot);
+    const float m1 = second ? __ldcg(p1 + D * kItemRows + slot) : -1e30f;
+    const float l1 = second ? __ldcg(p1 + (D + 1) * kItemRows + slot) : 0.f;
+    float o0[E], o1[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += __ldcg(pc + (warp * E + e) * kItemRows + slot) * w;
+    for (int e = 0; e < E; ++e) {
+      o0[e] = __ldcg(p0 + (warp * E + e) * kItemRows + slot);
+      o1[e] = second ? __ldcg(p1 + (warp * E + e) * kItemRows + slot) : 0.f;
+    }
+    const float top = fmaxf(M, fmaxf(m0, m1)), w = exp2f(M - top), w0 = exp2f(m0 - top), w1 = exp2f(m1 - top);
+    M = top;
+    L = L * w + l0 * w0 + l1 * w1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * w + o0[e] * w0 + o1[e] * w1;
   }
   bool nonfinite = false;
   uint32_t w[E / 2];
