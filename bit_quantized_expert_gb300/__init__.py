@@ -353,9 +353,9 @@ def gqa_paged_dims(n_heads, n_kv_heads, head_dim, page_size, num_pages, max_page
     (0: n_tokens; 1: the single-token form of the attention).  dtype: "bf16" or "fp16".  Strides in
     elements, 0 for packed; cache_strides: (page, head, row) of both caches, as .stride()[:3] of a cache
     indexed [page, head, offset, D]."""
-    pg, hd, row = cache_strides
-    return GqaPagedDims(n_heads, n_kv_heads, head_dim, page_size, num_pages, max_pages, n_seqs, n_tokens, max_new, window,
-                        sinks, _PAGED_DTYPES[dtype], q_stride, o_stride, k_stride, v_stride, pg, hd, row)
+    return GqaPagedDims(*(int(x) for x in (
+        n_heads, n_kv_heads, head_dim, page_size, num_pages, max_pages, n_seqs, n_tokens, max_new, window, sinks,
+        _PAGED_DTYPES[dtype], q_stride, o_stride, k_stride, v_stride, *cache_strides)))
 
 
 def gqa_paged_workspace_bytes(pd: GqaPagedDims) -> int:
@@ -373,33 +373,57 @@ def alloc_gqa_paged_workspace(pd: GqaPagedDims, device="cuda"):
     return ws
 
 
-def _paged_ints(t, n: int, name: str) -> int:
+_paged_types = None   # 16-bit types that stand for each dtype of the dims (bit patterns included)
+
+
+def _load_paged_types():
+    global _paged_types
+    import torch
+    bits = (torch.int16, torch.uint16)
+    _paged_types = ((torch.bfloat16, *bits), (torch.float16, *bits), (torch.int32,))
+
+
+def _paged_device() -> int:
+    """The current device, on which every tensor of a paged call must be."""
+    import torch
+    if _paged_types is None:
+        _load_paged_types()
+    return torch.cuda.current_device()
+
+
+def _paged_ints(t, n: int, dev: int, name: str) -> int:
     """Pointer of a contiguous int32 tensor of at least n entries."""
-    if not t.is_cuda or t.itemsize != 4 or t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of at least {n} entries")
+    if t.get_device() != dev or t.dtype not in _paged_types[2] or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 tensor of at least {n} entries on device {dev}")
     return t.data_ptr()
 
 
-def _paged_rows(t, rows: int, heads: int, D: int, stride: int, name: str) -> int:
-    """Pointer of a 16-bit [rows, heads, D] tensor whose token stride is that of the dims (0: packed)."""
+def _paged_rows(t, rows: int, heads: int, D: int, stride: int, dtype: int, dev: int, name: str) -> int:
+    """Pointer of a [rows, heads, D] tensor whose token stride is that of the dims (0: packed)."""
     st = t.stride()
-    if (not t.is_cuda or t.itemsize != 2 or t.shape != (rows, heads, D) or st[2] != 1 or (heads > 1 and st[1] != D)
-            or (rows > 1 and st[0] != (stride or heads * D))):
-        raise ValueError(f"{name}: expected a 16-bit CUDA tensor [{rows}, {heads}, {D}] of token stride "
-                         f"{stride or heads * D}")
+    if (t.get_device() != dev or t.dtype not in _paged_types[dtype] or t.shape != (rows, heads, D) or st[2] != 1
+            or (heads > 1 and st[1] != D) or (rows > 1 and st[0] != (stride or heads * D))):
+        raise ValueError(f"{name}: expected a tensor [{rows}, {heads}, {D}] of token stride {stride or heads * D} and the "
+                         f"dims' type on device {dev}")
     return t.data_ptr()
 
 
-def _paged_caches(k, v, pd: GqaPagedDims):
-    """Pointers of two 16-bit caches indexed [page, head, offset, D] whose strides are those of the dims."""
+def _paged_caches(k, v, pd: GqaPagedDims, dev: int):
+    """Pointers of two caches indexed [page, head, offset, D] whose strides are those of the dims."""
     P, H, S, D = shape = (pd.num_pages, pd.n_kv_heads, pd.page_size, pd.head_dim)
-    want = (pd.page_stride or H * S * D, pd.head_stride or S * D, pd.row_stride or D, 1)
+    want, types = (pd.page_stride or H * S * D, pd.head_stride or S * D, pd.row_stride or D, 1), _paged_types[pd.dtype]
     for t in (k, v):
         st = t.stride()
-        if (not t.is_cuda or t.itemsize != 2 or t.shape != shape
+        if (t.get_device() != dev or t.dtype not in types or t.shape != shape
                 or (st != want and (st[2:] != want[2:] or (P > 1 and st[0] != want[0]) or (H > 1 and st[1] != want[1])))):
-            raise ValueError(f"caches: expected 16-bit CUDA tensors {list(shape)} with the strides of the dims")
+            raise ValueError(f"caches: expected tensors {list(shape)} with the strides and the type of the dims on device {dev}")
     return k.data_ptr(), v.data_ptr()
+
+
+def _paged_workspace(ws, dev: int) -> int:
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on device {dev}")
+    return ws.data_ptr()
 
 
 def gqa_paged_plan(pd: GqaPagedDims, ctx_len, new_len, free_pages, n_free, block_table, q_start, kv_len, positions,
@@ -407,36 +431,36 @@ def gqa_paged_plan(pd: GqaPagedDims, ctx_len, new_len, free_pages, n_free, block
     """Tables of one step from the sequences' lengths, on the GPU: q_start [B + 1], kv_len [B], positions
     [T] (or None) and slots [T] are written, block_table [B, max_pages] gets fresh pages from the end of
     free_pages[:n_free], n_free_out (may be n_free) what is left.  All int32."""
-    B, T = pd.n_seqs, pd.n_tokens
+    dev, B, T = _paged_device(), pd.n_seqs, pd.n_tokens
     _check(load_library().gqa_paged_plan(
-        ctypes.byref(pd), _paged_ints(ctx_len, B, "ctx_len"), _paged_ints(new_len, B, "new_len"),
-        _paged_ints(free_pages, 0, "free_pages"), free_pages.numel(), _paged_ints(n_free, 1, "n_free"),
-        _paged_ints(block_table, B * pd.max_pages, "block_table"), _paged_ints(q_start, B + 1, "q_start"),
-        _paged_ints(kv_len, B, "kv_len"), None if positions is None else _paged_ints(positions, T, "positions"),
-        _paged_ints(slots, T, "slots"), _paged_ints(n_free_out, 1, "n_free_out"), _ptr(workspace), workspace.numel(),
-        _stream(stream)), "gqa_paged_plan")
+        ctypes.byref(pd), _paged_ints(ctx_len, B, dev, "ctx_len"), _paged_ints(new_len, B, dev, "new_len"),
+        _paged_ints(free_pages, 0, dev, "free_pages"), free_pages.numel(), _paged_ints(n_free, 1, dev, "n_free"),
+        _paged_ints(block_table, B * pd.max_pages, dev, "block_table"), _paged_ints(q_start, B + 1, dev, "q_start"),
+        _paged_ints(kv_len, B, dev, "kv_len"), None if positions is None else _paged_ints(positions, T, dev, "positions"),
+        _paged_ints(slots, T, dev, "slots"), _paged_ints(n_free_out, 1, dev, "n_free_out"), _paged_workspace(workspace, dev),
+        workspace.nbytes, _stream(stream)), "gqa_paged_plan")
 
 
 def gqa_paged_append(pd: GqaPagedDims, k, v, slots, q_start, k_cache, v_cache, workspace, stream=None):
     """k, v [T, Hkv, D] into the slots of the caches (rows at or past q_start[B] are skipped)."""
-    T, H, D = pd.n_tokens, pd.n_kv_heads, pd.head_dim
-    kc, vc = _paged_caches(k_cache, v_cache, pd)
+    dev, T, H, D, dt = _paged_device(), pd.n_tokens, pd.n_kv_heads, pd.head_dim, pd.dtype
+    kc, vc = _paged_caches(k_cache, v_cache, pd, dev)
     _check(load_library().gqa_paged_append(
-        ctypes.byref(pd), _paged_rows(k, T, H, D, pd.k_stride, "k"), _paged_rows(v, T, H, D, pd.v_stride, "v"),
-        _paged_ints(slots, T, "slots"), _paged_ints(q_start, pd.n_seqs + 1, "q_start"), kc, vc, _ptr(workspace),
-        workspace.numel(), _stream(stream)), "gqa_paged_append")
+        ctypes.byref(pd), _paged_rows(k, T, H, D, pd.k_stride, dt, dev, "k"), _paged_rows(v, T, H, D, pd.v_stride, dt, dev, "v"),
+        _paged_ints(slots, T, dev, "slots"), _paged_ints(q_start, pd.n_seqs + 1, dev, "q_start"), kc, vc,
+        _paged_workspace(workspace, dev), workspace.nbytes, _stream(stream)), "gqa_paged_append")
 
 
 def gqa_paged_attention(pd: GqaPagedDims, q, k_cache, v_cache, block_table, q_start, kv_len, o, workspace, stream=None):
     """Causal grouped-query attention of each sequence's new tokens (the last rows of its kv_len positions)
     over its pages, with pd's window and sinks.  q, o [T, Hq, D] of pd's type."""
-    T, H, D, B = pd.n_tokens, pd.n_heads, pd.head_dim, pd.n_seqs
-    kc, vc = _paged_caches(k_cache, v_cache, pd)
+    dev, T, H, D, B, dt = _paged_device(), pd.n_tokens, pd.n_heads, pd.head_dim, pd.n_seqs, pd.dtype
+    kc, vc = _paged_caches(k_cache, v_cache, pd, dev)
     _check(load_library().gqa_paged_attention(
-        ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, "q"), kc, vc, _paged_ints(block_table, B * pd.max_pages, "block_table"),
-        _paged_ints(q_start, B + 1, "q_start"), _paged_ints(kv_len, B, "kv_len"),
-        _paged_rows(o, T, H, D, pd.o_stride, "o"), _ptr(workspace), workspace.numel(), _stream(stream)),
-        "gqa_paged_attention")
+        ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, dt, dev, "q"), kc, vc,
+        _paged_ints(block_table, B * pd.max_pages, dev, "block_table"), _paged_ints(q_start, B + 1, dev, "q_start"),
+        _paged_ints(kv_len, B, dev, "kv_len"), _paged_rows(o, T, H, D, pd.o_stride, dt, dev, "o"),
+        _paged_workspace(workspace, dev), workspace.nbytes, _stream(stream)), "gqa_paged_attention")
 
 
 def gdn_dims(T, H, d_k=128, d_v=128) -> GdnDims:

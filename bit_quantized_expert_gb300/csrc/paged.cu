@@ -277,7 +277,7 @@ int check_paged_dims(const gqa_paged_dims* in, gqa_paged_dims* out) {
   if (d.page_size != 16 && d.page_size != 32 && d.page_size != 64 && d.page_size != 128) return MOE_ERR_UNSUPPORTED;
   const long long lim = 1ll << 31;
   if ((long long)d.num_pages * d.page_size >= lim || (long long)d.num_pages * d.page_size * d.n_kv_heads >= lim ||
-      (long long)d.max_pages * d.page_size >= lim || (long long)d.n_tokens * d.n_heads >= lim ||
+      (long long)d.max_pages * d.page_size > lim / 2 || (long long)d.n_tokens * d.n_heads >= lim ||
       (long long)d.n_seqs * d.n_kv_heads >= lim)
     return MOE_ERR_UNSUPPORTED;
   const long long D = d.head_dim;

@@ -52,6 +52,8 @@ __device__ __forceinline__ SeqRows load_seq(const PagedArgs& a, int b, bool& bad
   return s;
 }
 
+// Positions, windows and their differences stay within 32 bits: a row of the block table spans at most 2^30
+// positions, and a window that no position can pass is taken as none.
 // Whether the token at position p sees position j.
 __device__ __forceinline__ bool paged_sees(const PagedArgs& a, int p, int j) {
   return j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);

@@ -62,7 +62,7 @@ extern "C" {
  *   n_heads, n_kv_heads, head_dim   Hq, Hkv, D: Hq % Hkv == 0, Hq / Hkv <= 8, D = 64 or 128
  *   page_size    positions per page: 16, 32, 64 or 128
  *   num_pages    pages of the pool, num_pages * page_size * Hkv < 2^31
- *   max_pages    entries of a block-table row, max_pages * page_size < 2^31
+ *   max_pages    entries of a block-table row, max_pages * page_size <= 2^30
  *   n_seqs       B, sequences, 0 .. 4096
  *   n_tokens     T, rows of q, k, v, o, positions and slots, T * Hq < 2^31.  May exceed the sum of the
  *                new tokens: the rows behind the last sequence are neither used nor written

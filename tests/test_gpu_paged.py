@@ -407,6 +407,74 @@ def test_two_calls_at_once_on_two_streams():
     assert np.array_equal(P.to_f64(host(a.dev["o"]), "bf16"), ra) and np.array_equal(P.to_f64(host(b.dev["o"]), "bf16"), rb)
 
 
+def test_binding_refuses_what_does_not_fit():
+    """Wrong types, shapes, strides, contiguity and host tensors raise before anything is launched."""
+    b = Batch([(20, 3), (5, 1)], seed=21)
+    x = b.upload()
+    good = dict(q=x["q"], k_cache=x["kc"], v_cache=x["vc"], block_table=x["table"], q_start=x["q_start"], kv_len=x["kv_len"],
+                o=x["o"], workspace=x["ws"])
+    wide = torch.zeros((4, 16, 256), dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(q=x["q"].to(torch.float16)), dict(q=x["q"].float()), dict(q=x["q"][:3]), dict(q=x["q"].cpu()),
+                dict(q=wide[:, :, :128]), dict(o=x["o"].view(4, 2048)), dict(k_cache=x["kc"].transpose(1, 2)),
+                dict(v_cache=x["vc"][1:]), dict(k_cache=x["kc"].half(), v_cache=x["vc"].half()),
+                dict(block_table=x["table"].long()), dict(block_table=x["table"][:1]), dict(q_start=x["q_start"][1:]),
+                dict(kv_len=x["kv_len"].float()), dict(kv_len=x["kv_len"].cpu()), dict(workspace=x["ws"].cpu())):
+        with pytest.raises(ValueError):
+            moe.gqa_paged_attention(b.dims, **{**good, **bad})
+    with pytest.raises(moe.MoeError):
+        moe.gqa_paged_attention(b.dims, **{**good, "workspace": x["ws"][:-256]})
+    # bit patterns are as good as the type
+    moe.gqa_paged_attention(b.dims, **{**good, "q": x["q"].view(torch.int16), "o": x["o"].view(torch.int16)})
+    b.check(P.to_f64(host(x["o"]), "bf16"))
+
+
+def test_nothing_to_do_on_the_gpu():
+    """No tokens: nothing is launched or written; no sequence with rows: nothing is written."""
+    b = Batch([(20, 0), (5, 0)], pad=4, seed=22)
+    o, flags = b.run()
+    assert flags == 0 and (o == 7.0).all()
+    b.max_new = 1
+    o, flags = b.run()
+    assert flags == 0 and (o == 7.0).all()
+    d = moe.gqa_paged_dims(16, 2, 128, 64, b.P, b.M, 2, 0)
+    z = torch.zeros((0, 16, 128), dtype=torch.bfloat16, device="cuda")
+    x = b.dev
+    moe.gqa_paged_attention(d, z, x["kc"], x["vc"], x["table"], x["q_start"], x["kv_len"], z, moe.alloc_gqa_paged_workspace(d))
+
+
+def test_many_short_chunks():
+    """More row blocks than one warp schedules: the block makes the schedule (300 and 4096 sequences)."""
+    r = np.random.default_rng(23)
+    _ok(Batch([(int(c), int(n)) for c, n in zip(r.integers(0, 200, 300), r.integers(0, 12, 300))], Hq=4, Hkv=1, D=64, page=16,
+              seed=23), "300 sequences")
+    _ok(Batch([(int(c), int(n)) for c, n in zip(r.integers(0, 20, 4096), r.integers(0, 3, 4096))], Hq=2, Hkv=1, D=64, page=16,
+              seed=24, max_new=2), "4096 sequences")
+    _ok(Batch([(int(c), 1) for c in r.integers(0, 40, 4096)], Hq=2, Hkv=2, D=64, page=16, seed=25), "4096 single tokens")
+
+
+def test_one_long_prompt():
+    """Thousands of new tokens of one sequence with nothing cached: row blocks of 1 to 9 tiles, many of them
+    whole in a share, checked on every 13th row."""
+    b = Batch([(0, 1200)], Hq=4, Hkv=1, seed=26)
+    o, flags = b.run()
+    assert flags == 0
+    rows = np.arange(0, 1200, 13)
+    sub = Batch([(0, 1200)], Hq=4, Hkv=1, seed=26)
+    ref, mag, smax = (np.zeros((1200, 4, 128)), np.zeros((1200, 4, 128)), np.zeros((1200, 4)))
+    for t in rows:
+        one = P.attention(sub.q[t:t + 1], sub.kc, sub.vc, sub.table, [0, 1], [t + 1])
+        ref[t], mag[t], smax[t] = one[0][0], one[1][0], one[2][0]
+    b.check(o, (ref, mag, smax), rows)
+
+
+def test_sequences_that_share_pages():
+    """Two sequences whose tables name the same pages (a common prompt)."""
+    for new in (1, 12):
+        b = Batch([(100, new), (96, new)], Hq=8, page=32, seed=27)
+        b.table[1, :3] = b.table[0, :3]
+        _ok(b, f"new {new}")
+
+
 # ---------------------------------------------------------------- plan
 def _plan_case(ctx, new, page, num_pages, M, pad, seed, n_free=None, table=None):
     r = np.random.default_rng(seed)

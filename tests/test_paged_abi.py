@@ -70,7 +70,7 @@ INVALID, UNSUPPORTED, MISALIGNED = 1, 2, 3
     (dict(head_dim=96), UNSUPPORTED), (dict(head_dim=256), UNSUPPORTED), (dict(n_heads=18), UNSUPPORTED),
     (dict(page_size=48), UNSUPPORTED), (dict(page_size=256), UNSUPPORTED), (dict(n_seqs=4097), UNSUPPORTED),
     (dict(num_pages=1 << 24, page_size=128), UNSUPPORTED), (dict(num_pages=1 << 24), UNSUPPORTED),
-    (dict(max_pages=1 << 25), UNSUPPORTED), (dict(n_tokens=1 << 27), UNSUPPORTED),
+    (dict(max_pages=1 << 25), UNSUPPORTED), (dict(max_pages=(1 << 24) + 1), UNSUPPORTED), (dict(n_tokens=1 << 27), UNSUPPORTED),
     (dict(q_stride=2047), INVALID), (dict(q_stride=2052), MISALIGNED), (dict(k_stride=248), INVALID),
     (dict(v_stride=260), MISALIGNED), (dict(o_stride=1 << 39), UNSUPPORTED), (dict(q_stride=-2048), INVALID),
     (dict(cache_strides=(16384, 8192, 132)), MISALIGNED), (dict(cache_strides=(16384, 8192, 64)), INVALID),
@@ -104,7 +104,7 @@ def test_null_dims(lib):
 
 
 @pytest.mark.parametrize("extra", [
-    {}, dict(page_size=16), dict(page_size=128), dict(head_dim=64), dict(n_heads=2), dict(dtype="fp16"), dict(max_new=1),
+    {}, dict(max_pages=1 << 24), dict(page_size=16), dict(page_size=128), dict(head_dim=64), dict(n_heads=2), dict(dtype="fp16"), dict(max_new=1),
     dict(window=100, sinks=4), dict(window=2**31 - 1, sinks=2**31 - 1), dict(q_stride=2560, k_stride=2560, v_stride=2560),
     dict(cache_strides=(16384, 128, 256)),              # position-major pages
     dict(cache_strides=(32768, 8192, 128)),             # keys and values interleaved page by page
@@ -123,14 +123,16 @@ def test_nothing_to_do(lib, name):
     assert call(moe.gqa_paged_dims(**{**GOOD, "n_tokens": 0}), **none) == (1 if name == "plan" else 0)
 
 
-def test_binding_refuses_tensors_that_do_not_fit():
-    """The binding raises before it calls the library: host tensors, and shapes that are not the dims'."""
+def test_binding_refuses_host_tensors():
+    """The binding raises before it calls the library (tensors that are not on the device of the call)."""
     import torch
-    d = moe.gqa_paged_dims(**GOOD)
-    x = torch.zeros(8, dtype=torch.int32)
+    moe._load_paged_types()
+    d, x = moe.gqa_paged_dims(**GOOD), torch.zeros(37, 16, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
-        moe._paged_ints(x, 4, "x")
+        moe._paged_ints(torch.zeros(8, dtype=torch.int32), 4, 0, "x")
     with pytest.raises(ValueError):
-        moe._paged_rows(torch.zeros(37, 16, 128, dtype=torch.bfloat16), 37, 16, 128, 0, "q")
+        moe._paged_rows(x, 37, 16, 128, 0, 0, 0, "q")
     with pytest.raises(ValueError):
-        moe._paged_caches(*[torch.zeros(100, 2, 64, 128, dtype=torch.bfloat16)] * 2, d)
+        moe._paged_caches(*[torch.zeros(100, 2, 64, 128, dtype=torch.bfloat16)] * 2, d, 0)
+    with pytest.raises(ValueError):
+        moe._paged_workspace(torch.zeros(1024, dtype=torch.uint8), 0)
