@@ -14,8 +14,8 @@
 //   * S and O stay in tensor memory (128 columns of fp32 a tile each).  P replaces S there, in 16 bits,
 //     as the A operand of the second product; V is read as it lies (positions by dims) through a
 //     descriptor whose major axis is the output's.
-//   * The running maximum that scales the numerators moves only when the new one is above it by 14 in
-//     base-2 units: p stays below 2^14, within fp16, and O is rescaled in a few tiles, not in all.
+//   * The running maximum that scales the numerators moves only when the new one is above it by kLazy
+//     base-2 units: O is rescaled in a few tiles, not in all.
 //   * Only tiles that some row does not wholly see are masked.  In those, the value tile is also
 //     searched for non-finite values, since 0 times one of them is not 0: they are taken out, and the rows that do
 //     see them get them back at the end.
@@ -36,7 +36,14 @@ constexpr int kItemRows = 256;              // two row tiles
 constexpr uint32_t kTmemO = 256;            // columns: S0 0, S1 128, O0 256, O1 384 (all 512 are allocated: base 0)
 constexpr int kOutBytes = 32 * 64;          // a warp's staging of its 32 rows of o, 32 dims at a time
 constexpr int kItemUnits = 2;               // what an item costs beside its tiles, in tiles
-constexpr float kLazy = 14.f;               // base-2 units the running maximum may lag behind
+// Base-2 units by which the numerators' reference may lag behind the row's maximum, and by which it stands
+// below the maximum that sets it: fp16 numerators use its range from 2^15 down, since it keeps 2^-25 at best and a
+// long cache of small ones would be summed as nothing.  bf16 has fp32's range, and lags more: of 14 units and 6,
+// 2048 tokens at 32768 take 364 and 374 us.
+template <bool FP16>
+constexpr float kLazy = FP16 ? 6.f : 14.f;
+template <bool FP16>
+constexpr float kLift = FP16 ? 9.f : 0.f;
 
 template <int D>
 struct Chunk {
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool live = tok < tpt && t * tpt + tok < x.n;
       const int p = live ? x.p_lo + t * tpt + tok : -1;      // a row that is no token sees nothing
-      float m = -INFINITY, negm = 0.f, l = 0.f;              // negm = -m in base-2 units (0 while nothing is seen)
+      float m = -INFINITY, negm = 0.f, l = 0.f;              // negm = kLift - m in base-2 units (0 while nothing is seen)
       ++at;   // the stage of the first tile's values
       for (int i = 0; i < n; ++i, ++at) {
         const int j0 = x.r.tile(i0 + i) * kTN;
@@ -671,11 +678,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
         // The reference moves if the new maximum is well above it (or is the first).
-        const bool move = mx > m && (m == -INFINITY || (mx - m) * a.qk_scale > kLazy);
+        const bool move = mx > m && (m == -INFINITY || (mx - m) * a.qk_scale > kLazy<FP16>);
         if (__any_sync(0xFFFFFFFFu, move)) {
           float alpha = 1.f;
           if (move) {
-            const float nn = -(mx * a.qk_scale);
+            const float nn = kLift<FP16> - mx * a.qk_scale;
             alpha = m == -INFINITY ? 0.f : ex2(nn - negm);
             m = mx;
             negm = nn;

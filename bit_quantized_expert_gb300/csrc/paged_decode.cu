@@ -31,6 +31,11 @@ constexpr int kRows = 8;                       // query heads per key/value head
 constexpr int kItemUnits = 3;                  // what an item costs beside its tiles, in tiles (~3500 cycles)
 constexpr int kSlack = 1;                      // tiles that a cut moves to reach an item's end
 constexpr float kNegBig = -1e30f;              // running max before any position is seen
+// Base-2 units by which numerators stand above e^(s - max): fp16 keeps 2^-25 at best, so they use its range
+// from 2^15 down, or a long cache of small ones would be summed as nothing.  (All parts of an item are
+// scaled alike, so the joins do not see it.)  bf16 has fp32's range.
+template <bool FP16>
+constexpr float kLift = FP16 ? 15.f : 0.f;
 
 template <int D>
 struct Dec {
@@ -323,11 +328,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_new = fmaxf(m_run, mx);
         const float alpha = ex2(m_run - m_new);
         m_run = m_new;
+        const float m_ref = m_new - kLift<FP16>;
         float p[2][2];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) p[j][e] = ex2(s2[j][e] - m_new);
+          for (int e = 0; e < 2; ++e) p[j][e] = ex2(s2[j][e] - m_ref);
         l_run = l_run * alpha + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {

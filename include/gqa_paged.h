@@ -29,8 +29,9 @@
  * table entries of pages that no row sees are not read, so a window's passed pages may be freed.
  * Sums and softmax statistics are fp32; o is rounded once to the 16-bit type.  In the chunk form the
  * softmax's numerators are rounded to the 16-bit type before the product with V (the tensor cores'
- * operand type: at most half a step each, relative to the numerator); the single-token form keeps their
- * rounding remainders.  Results are identical from run to run.
+ * operand type: at most half a step each, relative to the numerator, or in fp16 2^-34 relative to the row's
+ * largest one); the single-token form keeps their rounding remainders (fp16: 2^-40).  Results are
+ * identical from run to run.
  *
  * Conventions are those of moe.h: device pointers owned by the caller, 16-byte aligned (the int32 arrays
  * 4-byte aligned, so they may be slices); work is

@@ -244,6 +244,35 @@ def test_scores_that_grow_along_the_cache():
         _ok(b, f"new {new}")
 
 
+@pytest.mark.parametrize("new", [1, 20])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_weight_spread_over_tiny_numerators(new, dtype):
+    """One position e^18 above all others, which alone have values: fp16 holds no number as small as e^-18, so
+    the numerators have to use its range from 2^15 down.  160 sequences over the same pages, so that a share
+    is about one of them.  Bar as above, but with numerators held to 2^-25 of 2^-9 (chunks) or of 2^-15
+    (single tokens) of the row's largest."""
+    b = Batch([(16384 - new, new)], Hq=1, Hkv=1, D=64, page=128, dtype=dtype, seed=28)
+    one = bits(np.ones(1), dtype)[0]
+    b.q[:], b.kc[b.table[0, :128]], b.vc[b.table[0, :128]] = 0, 0, one
+    b.q[:, 0, 0], b.kc[b.table[0, 0], 0, 0, 0] = bits(np.array([8.0, 18.0]), dtype)
+    b.vc[b.table[0, 0], 0, 0] = 0
+    ref, mag, smax = b.oracle()
+    n = 160
+    b.table, b.q, b.kv_len = np.repeat(b.table, n, 0), np.tile(b.q, (n, 1, 1)), np.repeat(b.kv_len, n)
+    b.k, b.v = (np.tile(x, (n, 1, 1)) for x in (b.k, b.v))
+    b.q_start, b.seqs = (np.arange(n + 1) * new).astype(np.int32), b.seqs * n
+    b.T = b.rows = n * new
+    o, flags = b.run()
+    assert flags == 0
+    u = U[dtype]
+    tol = u * np.abs(ref) + mag * ((2.0 ** -17 if new == 1 else u) + 2.0 ** -19 + 2 * smax[..., None] * 6 * 2.0 ** -23)
+    if dtype == "fp16":
+        tol = tol + 2.0 ** -25 * (1 + 16384 * 2.0 ** (-15 if new == 1 else -9))
+    ratio = (np.abs(o.reshape(n, new, 1, 64) - ref) / tol).max()
+    print(f"{dtype}, {new} new: max |o - ref| / bar = {ratio:.3f}")
+    assert ratio <= 1.0
+
+
 # ---------------------------------------------------------------- what a row does not see
 def _slot(b, s, p):
     return b.table[s, p // b.page], p % b.page
