@@ -258,6 +258,16 @@ int check_pointers(const void* const (&tables)[N], const void* const (&wide)[M])
   return MOE_OK;
 }
 
+// int32 arrays of one call, by address and entries.
+struct Ints {
+  const int32_t* p;
+  long long n;
+};
+bool overlap(const Ints& x, const Ints& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return x.n > 0 && y.n > 0 && a < b + (uintptr_t)y.n * 4 && b < a + (uintptr_t)x.n * 4;
+}
+
 int log2_of(int v) {
   int s = 0;
   while ((1 << s) < v) ++s;
@@ -401,10 +411,22 @@ extern "C" moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* 
   if (st != MOE_OK) return (moe_status)st;
   if (d.n_seqs == 0) return MOE_OK;
   if (free_capacity < 0 || (free_capacity > 0 && free_pages == nullptr)) return MOE_ERR_INVALID_ARG;
-  if ((st = check_pointers({ctx_len, new_len, n_free, block_table, q_start, kv_len, slots, n_free_out}, {workspace})) != MOE_OK)
+  if (d.n_tokens > 0 && slots == nullptr) return MOE_ERR_INVALID_ARG;
+  if ((st = check_pointers({ctx_len, new_len, n_free, block_table, q_start, kv_len, n_free_out}, {workspace})) != MOE_OK)
     return (moe_status)st;
-  if (misaligned(positions, 4) || misaligned(free_pages, 4)) return MOE_ERR_MISALIGNED;
+  if (misaligned(slots, 4) || misaligned(positions, 4) || misaligned(free_pages, 4)) return MOE_ERR_MISALIGNED;
   if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
+  // The CTAs read the inputs, the table's held entries too, while others write the outputs.
+  const Ints in[4] = {{n_free, 1}, {ctx_len, d.n_seqs}, {new_len, d.n_seqs}, {free_pages, free_capacity}};
+  const Ints out[6] = {{n_free_out, 1},         {block_table, (long long)d.n_seqs * d.max_pages},
+                       {q_start, d.n_seqs + 1}, {kv_len, d.n_seqs},
+                       {slots, d.n_tokens},     {positions, positions == nullptr ? 0 : d.n_tokens}};
+  for (int i = 0; i < 6; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (overlap(out[i], in[j]) && !(i == 0 && j == 0 && n_free_out == n_free)) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return MOE_ERR_INVALID_ARG;
+  }
   PlanArgs a = {ctx_len,    new_len, free_pages, n_free,     block_table,
                 q_start,    kv_len,  positions,  slots,      n_free_out,
                 static_cast<uint32_t*>(workspace), d.n_seqs, d.n_tokens, log2_of(d.page_size), d.num_pages, d.max_pages,

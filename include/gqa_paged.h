@@ -102,7 +102,7 @@ size_t gqa_paged_workspace_bytes(const gqa_paged_dims* dims);
  *   q_start      [B + 1]         out: first row of each sequence; q_start[B] rows are in use
  *   kv_len       [B]             out: ctx_len + new_len
  *   positions    [T] or NULL     out: position of each new token in its sequence
- *   slots        [T]             out: cache slot of each new token
+ *   slots        [T]             out: cache slot of each new token (may be NULL if T is 0)
  *   n_free_out   [1]             out: *n_free less the pages taken; may be n_free itself
  * Sequence b holds ceil(ctx_len / page_size) pages and needs ceil(kv_len / page_size).  The fresh ones
  * are taken from the end of the free list: in order of (sequence, page), the m-th is
@@ -112,7 +112,8 @@ size_t gqa_paged_workspace_bytes(const gqa_paged_dims* dims);
  * no entries, q_start is cut at T) or a row of the block table (kv_len is cut at max_pages * page_size,
  * the slots past it are -1); *n_free outside its range (cut); a free list that runs out (the entries and slots become -1), or that holds
  * or a held page that is, a number outside 0 .. num_pages - 1 (likewise).
- * Returns as gqa_paged_attention; n_seqs == 0 is a no-op.  One launch. */
+ * Returns as gqa_paged_attention, and MOE_ERR_INVALID_ARG if an output overlaps an input or another output
+ * (but n_free_out == n_free); n_seqs == 0 is a no-op.  One launch. */
 moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* ctx_len, const int32_t* new_len,
                           const int32_t* free_pages, int32_t free_capacity, const int32_t* n_free,
                           int32_t* block_table, int32_t* q_start, int32_t* kv_len, int32_t* positions, int32_t* slots,

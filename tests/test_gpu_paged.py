@@ -567,6 +567,20 @@ def test_plan_sizes_at_the_ends():
     _plan_run(_plan_case([48] * 4, [0] * 4, 16, 12, 3, 0, 1))                    # full rows, no free page
 
 
+def test_plan_without_rows():
+    """T = 0 with empty tensors for the tokens and the free list (whose pointers are null)."""
+    d = moe.gqa_paged_dims(4, 2, 64, 16, 8, 3, 2, 0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ws, none = moe.alloc_gqa_paged_workspace(d), torch.zeros(0, **i32)
+    ctx, table, free = torch.tensor([5, 0], **i32), torch.full((2, 3), 4, **i32), torch.zeros(1, **i32)
+    starts, kv = torch.full((3,), 9, **i32), torch.full((2,), 9, **i32)
+    moe.gqa_paged_plan(d, ctx, torch.zeros(2, **i32), none, free, table, starts, kv, none, none, free, ws)
+    assert starts.tolist() == [0, 0, 0] and kv.tolist() == [5, 0] and free.item() == 0 and (table == 4).all()
+    assert moe.read_error_flags(ws) == 0
+    with pytest.raises(moe.MoeError):   # lengths updated in place: refused
+        moe.gqa_paged_plan(d, ctx, torch.zeros(2, **i32), none, free, table, starts, ctx, none, none, free, ws)
+
+
 @pytest.mark.parametrize("what", ["exhausted", "empty", "over_row", "over_T", "negative", "bad_free", "bad_held", "n_free_high",
                                   "n_free_negative", "huge"])
 def test_plan_out_of_range(what):

@@ -60,6 +60,24 @@ def test_pointers_and_workspace(lib, name):
         assert call(d, free=None, cap=0, ws=None) == 1 and call(d, free=None, cap=0, nb=0) == 4
 
 
+def test_plan_refuses_outputs_that_overlap(lib):
+    """Every output against every input and every other output, by its last or first 4 bytes."""
+    d = moe.gqa_paged_dims(**GOOD)
+    B, T, M, cap = d.n_seqs, d.n_tokens, d.max_pages, 100
+    size = dict(ctx=B, new=B, free=cap, n_free=1, table=B * M, q_start=B + 1, kv_len=B, positions=T, slots=T, n_out=1)
+    apart = {n: 4096 * (i + 1) for i, n in enumerate(size)}
+    plan = _calls(lib)["plan"][0]
+    for out in ("table", "q_start", "kv_len", "positions", "slots", "n_out"):
+        for other in size:
+            if other == out:
+                continue
+            ends = [apart[other] + 4 * (size[other] - 1), apart[other] - 4 * (size[out] - 1)]
+            for at in ends:
+                if (out, other) == ("n_out", "n_free"):
+                    continue   # the same counter is allowed
+                assert plan(d, **{**apart, out: at, "ws": 1 << 20}) == 1, (out, other)
+
+
 INVALID, UNSUPPORTED, MISALIGNED = 1, 2, 3
 
 
