@@ -7,8 +7,8 @@
 //     positions) that its rows see.
 //   * Work split.  Shares of the cache tiles of all items, one per SM (paged.cuh).
 //   * Roles.  Warps 0..3 and 4..7: softmax of the first and second row tile, one row a thread; warp 8:
-//     copies; warp 9: tensor-core instructions; warps 10 and 11 fill the warpgroup (registers are moved to
-//     the softmax by warpgroups).  While one row tile's softmax runs, the other's
+//     copies; warp 9: tensor-core instructions; warps 10 and 11: the values of masked tiles.  (Registers are
+//     moved to the softmax by warpgroups.)  While one row tile's softmax runs, the other's
 //     products do:  S0 = Q0 K^T | S1 = Q1 K^T, then per cache tile  O0 += P0 V, S0 = Q0 K'^T,
 //     O1 += P1 V, S1 = Q1 K'^T.
 //   * S and O stay in tensor memory (128 columns of fp32 a tile each).  P replaces S there, in 16 bits,
@@ -30,6 +30,7 @@ namespace {
 constexpr int kTN = 128;                    // positions per cache tile
 constexpr int kThreads = 384;               // two softmax warpgroups, one for copies and products
 constexpr int kSoftmaxWarps = 8;
+constexpr int kScanWarps = 2;
 // Registers a thread: 168 at launch; 2 * 200 + 104 = 3 * 168 after the split.
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kItemRows = 256;              // two row tiles
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(FULL(s), 1);
-      mbar_init(EMPTY(s), 1);
+      mbar_init(EMPTY(s), 1 + kScanWarps);
     }
     mbar_init(QFULL, 1);
     mbar_init(QEMPTY, 1);
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(OFULL(t), 1);
       mbar_init(OEMPTY(t), 4);
     }
-    mbar_init(CLEAN, 4);
+    mbar_init(CLEAN, kScanWarps);
     abort_s = 0;
     for (int i = 0; i < 4; ++i) bad_s[i] = 0;
     share_s.lo = share_s.hi = 0;
@@ -573,15 +574,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++at;
       for (int i = 0; i < n; ++i, ++at) {
         const bool more = i + 1 < n;
-        const bool closed = two && C::kBoxes == 2 && !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi);
+        const bool closed = !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi);
         if (!at_stage(at, [&](auto st_c) {   // the tile's values, the next one's keys
               constexpr int ST = decltype(st_c)::value;
               if (!wait(FULL(ST), at >> 1)) return false;
               if (closed && !wait(CLEAN, cleans++)) return false;
+              // (the second row tile's result too, where this item has none: bad_s is a short ring)
               if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
+              if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
               if (!turn(Zero{}, st_c, done0++, i == 0, more)) return false;
               if (two) {
-                if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
                 if (!turn(One{}, st_c, done1++, i == 0, more)) return false;
               }
               tc_commit_if(go, EMPTY(ST));
@@ -594,6 +596,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       outs1 += two;
       return true;
     });
+    } else {
+    // ---- values of masked tiles: non-finite ones are taken out, two positions a thread.  (Beside the softmax,
+    // which would spend 700 cycles of its chain on it, twice: one row tile's product would also wait for the other's.)
+    // These warps see every stage, and a stage is free only with their word, so that they keep step with the ring.
+    uint32_t at = 0;
+    int seg = 0;
+    walk([&](int, const SeqRows&, int, const Item& x, int i0, int n, uint32_t) {
+      for (int i = 0; i <= n; ++i, ++at) {
+        const uint32_t st = at & 1;
+        if (!mbar_wait_warp(FULL(st), (at >> 1) & 1, &abort_s, a.err)) return false;
+        const int j0 = i > 0 ? x.r.tile(i0 + i - 1) * kTN : 0;
+        if (i > 0 && !tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) {
+#pragma unroll 1
+          for (int r = (warp - kSoftmaxWarps - 2) * 32 + lane; r < kTN; r += kScanWarps * 32) {
+            const uint32_t row = sKV + st * C::kStageBytes + C::kTileBytes + r * 128;
+            uint32_t any = 0;
+#pragma unroll 8
+            for (int c = 0; c < 8 * C::kBoxes; ++c) {   // of 16 bytes; lanes start at different ones
+              uint32_t w0, w1, w2, w3;
+              ld_shared4(row + (c >> 3) * C::kBoxBytes + (((c + lane) & 7) << 4), w0, w1, w2, w3);
+              any |= non_finite_bits<FP16>(w0) | non_finite_bits<FP16>(w1) | non_finite_bits<FP16>(w2) |
+                     non_finite_bits<FP16>(w3);
+            }
+            if (any & kSigns) {
+#pragma unroll 1
+              for (int c = 0; c < 8 * C::kBoxes; ++c) {
+                const uint32_t to = row + (c >> 3) * C::kBoxBytes + ((c & 7) << 4);
+                uint32_t w0, w1, w2, w3;
+                ld_shared4(to, w0, w1, w2, w3);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w0 & ~non_finite16<FP16>(w0)),
+                             "r"(w1 & ~non_finite16<FP16>(w1)), "r"(w2 & ~non_finite16<FP16>(w2)),
+                             "r"(w3 & ~non_finite16<FP16>(w3))
+                             : "memory");
+              }
+              const int j = j0 + r;
+              if (j <= x.p_hi && (a.window == 0 || j > x.p_lo - a.window || j < a.sinks)) bad_s[seg & 3] = seg + 1;
+              fence_proxy_async_smem();
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(CLEAN);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(EMPTY(st));
+        __syncwarp();
+      }
+      ++seg;
+      return true;
+    });
     }
   } else {
     // ---- softmax: row `r` of row tile `t`
@@ -601,59 +652,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G, head = r - tok * a.G;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = t * 128 + lanes, tO = kTmemO + t * 128 + lanes;
-    int at = 0, seg = 0, done = 0, outs = 0;   // ring stages, segments, own tiles and items so far
+    int seg = 0, done = 0, outs = 0;   // segments, own tiles and items so far
     walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t u) {
       const int nt = x.n > tpt ? 2 : 1;
       if (t >= nt) {
-        at += n + 1;
         ++seg;
         return true;
       }
       const bool live = tok < tpt && t * tpt + tok < x.n;
       const int p = live ? x.p_lo + t * tpt + tok : -1;      // a row that is no token sees nothing
       float m = -INFINITY, negm = 0.f, l = 0.f;              // negm = kLift - m in base-2 units (0 while nothing is seen)
-      ++at;   // the stage of the first tile's values
-      for (int i = 0; i < n; ++i, ++at) {
+      for (int i = 0; i < n; ++i) {
         const int j0 = x.r.tile(i0 + i) * kTN;
         const bool open = tile_open<kTN>(a, j0, x.p_lo, x.p_hi);
         if (!mbar_wait_warp(SFULL(t), done & 1, &abort_s, a.err)) return false;
         ++done;
         tc_fence_after();
-        if (!open && (t == 0 || C::kBoxes == 2)) {
-          // Take non-finite values out of position r of the value tile: its 64-dim box t, or all of it where
-          // the other row tile has no rows.
-          const int st = at & 1;
-          if (!mbar_wait_warp(FULL(st), (at >> 1) & 1, &abort_s, a.err)) return false;
-          const bool both = nt == 2 && C::kBoxes == 2;
-          const uint32_t row = sKV + st * C::kStageBytes + C::kTileBytes + (both ? t * C::kBoxBytes : 0) + r * 128;
-          const int chunks = both ? 8 : 8 * C::kBoxes;   // of 16 bytes; lanes start at different ones
-          uint32_t any = 0;
-#pragma unroll 4
-          for (int c = 0; c < chunks; ++c) {
-            uint32_t w0, w1, w2, w3;
-            ld_shared4(row + (c >> 3) * C::kBoxBytes + (((c + lane) & 7) << 4), w0, w1, w2, w3);
-            any |= non_finite_bits<FP16>(w0) | non_finite_bits<FP16>(w1) | non_finite_bits<FP16>(w2) |
-                   non_finite_bits<FP16>(w3);
-          }
-          if (any & kSigns) {
-#pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-              const uint32_t at = row + (c >> 3) * C::kBoxBytes + ((c & 7) << 4);
-              uint32_t w0, w1, w2, w3;
-              ld_shared4(at, w0, w1, w2, w3);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w0 & ~non_finite16<FP16>(w0)),
-                           "r"(w1 & ~non_finite16<FP16>(w1)), "r"(w2 & ~non_finite16<FP16>(w2)),
-                           "r"(w3 & ~non_finite16<FP16>(w3))
-                           : "memory");
-            }
-            const int j = j0 + r;
-            if (j <= x.p_hi && (a.window == 0 || j > x.p_lo - a.window || j < a.sinks)) bad_s[seg & 3] = seg + 1;
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (t == 1 && lane == 0) mbar_arrive(CLEAN);
-          __syncwarp();
-        }
         uint32_t sr[128];
         tmem_ld128(tS, sr);
         if (!open) {
