@@ -513,9 +513,6 @@ extern "C" moe_status gqa_paged_attention(const gqa_paged_dims* dims, const uint
   if (device_sms(&sms) != MOE_OK || !encode_pages(&maps.k, k_cache, d, tile) || !encode_pages(&maps.v, v_cache, d, tile) ||
       (!single && !encode_queries(&maps.q, q, d)))
     return MOE_ERR_CUDA;
-  // Row blocks that the sequences can have at most: one each, and one more for every full block of rows.
-  const long long blocks = d.n_seqs + (single ? 0 : (long long)d.n_tokens / (2 * (128 / a.G)));
-  a.small = blocks <= kWarpSchedule;
   void* scratch = static_cast<uint8_t*>(workspace) + kWsHeadBytes;
   const int ctas = std::min(sms, kPagedMaxCtas);
   const auto launch = single ? launch_paged_decode : launch_paged_chunk;

@@ -26,7 +26,6 @@ struct PagedArgs {
   int B, T, max_new;
   int window, sinks;
   int fp16;
-  int small;                // few row blocks: one warp makes a CTA's schedule (kWarpSchedule)
   long long q_stride, o_stride, page_stride, head_stride, row_stride;
   float qk_scale;           // log2(e) / sqrt(D): scores in base-2 units
 };
@@ -113,59 +112,59 @@ struct SplitRecord {
   int32_t p_lo;                  // position of the item's first token
 };
 
-// Exclusive sums over NT threads, a whole block, or (NT = 32) one warp; `sum` gets the total.  (Rolled up, like
-// the rest of the schedule: it runs once, and its time is that of fetching its instructions.)
+// The schedule is made by every CTA for itself, by a block of NT threads together: it stands before all work, and
+// its time is a chain of latencies (5 row blocks a lane of one warp took twice as long as one a thread).
+
+// Exclusive sums over the block; `over`: the total passes 32 bits (and the sums mean nothing).
 template <int NT>
-__device__ __forceinline__ unsigned long long exclusive_scan(unsigned long long mine, unsigned long long* warp_s,
-                                                             unsigned long long* sum) {
+__device__ __forceinline__ uint32_t exclusive_scan(unsigned long long mine, uint32_t* warp_s, uint32_t* sum, bool* over) {
+  static_assert(NT % 32 == 0 && NT <= 512, "one warp scans the warps' sums, 16 lanes wide");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long inc = mine;
-  __syncwarp();   // the lanes' runs differ in length
-#pragma unroll 1
+  uint32_t inc = (uint32_t)mine;
+  bool carry = (mine >> 32) != 0;   // sums only grow, so none is wrong unless some addition carries
+  __syncwarp();                     // the lanes' runs differ in length
+#pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const unsigned long long x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
-    if (lane >= off) inc += x;
+    const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, off);
+    if (lane >= off) {
+      inc += x;
+      carry |= inc < x;
+    }
   }
-  if (NT == 32) {
-    *sum = __shfl_sync(0xFFFFFFFFu, inc, 31);
-    return inc - mine;
-  }
-  __syncthreads();   // warp_s may still be read
   if (lane == 31) warp_s[warp] = inc;
   __syncthreads();
-  unsigned long long before = inc - mine, all = 0;
-#pragma unroll 1
-  for (int w = 0; w < NT / 32; ++w) {
-    const unsigned long long x = warp_s[w];
-    if (w < warp) before += x;
-    all += x;
+  uint32_t w = lane < NT / 32 ? warp_s[lane] : 0u;
+#pragma unroll
+  for (int off = 1; off < 16; off <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, w, off);
+    if (lane >= off) {
+      w += x;
+      carry |= lane < 16 && w < x;
+    }
   }
-  *sum = all;
-  return before;
+  *sum = __shfl_sync(0xFFFFFFFFu, w, 15);
+  const uint32_t before = __shfl_sync(0xFFFFFFFFu, w, (warp + 15) & 15);
+  *over = __syncthreads_or(carry) != 0;   // (warp_s may be written again after it)
+  return (warp == 0 ? 0u : before) + inc - (uint32_t)mine;
 }
 
-template <int NT>
-__device__ __forceinline__ void group_sync() {
-  __syncwarp();
-  if (NT != 32) __syncthreads();
-}
-
-// Sums of cost(b) over the sequences before each, into pre_s[0 .. B], by NT threads together; returns the
-// total.
+// Sums of cost(b) over the sequences before each, into pre_s[0 .. B], by the block; returns the total.
 template <int NT, class Cost>
-__device__ __forceinline__ unsigned long long scan_sequences(int B, uint32_t* pre_s, unsigned long long* warp_s, Cost cost) {
+__device__ __forceinline__ uint32_t scan_sequences(int B, uint32_t* pre_s, uint32_t* warp_s, bool* over, Cost cost) {
   const int tid = threadIdx.x, per = (B + NT - 1) / NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  unsigned long long mine = 0, sum;
+  unsigned long long mine = 0;
+  uint32_t sum;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     pre_s[b] = (uint32_t)mine;
     mine += cost(b);
   }
-  const uint32_t before = (uint32_t)exclusive_scan<NT>(mine, warp_s, &sum);
+  const uint32_t before = exclusive_scan<NT>(mine, warp_s, &sum, over);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) pre_s[b] += before;
-  if (tid == 0) pre_s[B] = (uint32_t)sum;
-  group_sync<NT>();
+  if (tid == 0) pre_s[B] = sum;
+  __syncwarp();
+  __syncthreads();
   return sum;
 }
 
@@ -181,9 +180,6 @@ __device__ __forceinline__ int find_sequence(const uint32_t* pre_s, int B, uint3
   return lo;
 }
 
-// Row blocks (at most) up to which one warp makes the schedule, without the block's barriers.
-constexpr int kWarpSchedule = 128;
-
 // A cut of the order within the item of units s .. e - 1 (`own` of them its start and end, then its tiles),
 // moved to an end of the item that is within `slack` tiles.  What remains between has tiles on both sides.
 __device__ __forceinline__ uint32_t snap(uint32_t x, uint32_t s, uint32_t e, uint32_t own, uint32_t slack) {
@@ -192,18 +188,16 @@ __device__ __forceinline__ uint32_t snap(uint32_t x, uint32_t s, uint32_t e, uin
   return up <= slack ? e : x;
 }
 
-// Where the c-th of n equal shares of `total` units begins.
+// Where the c-th of n equal shares of `total` units begins: the first shares take one of those left over.
 __device__ __forceinline__ uint32_t share_start(uint32_t total, int c, int n) {
   const uint32_t q = total / n;
-  return q * c + (total - q * n) * c / n;
+  return q * c + min((uint32_t)c, total - q * n);
 }
 
 // The share that holds unit `pos`.
 __device__ __forceinline__ int share_of(uint32_t pos, uint32_t total, int n) {
-  int c = min((int)((float)pos / (float)total * (float)n), n - 1);   // within one of it
-  while (c + 1 < n && share_start(total, c + 1, n) <= pos) ++c;
-  while (c > 0 && share_start(total, c, n) > pos) --c;
-  return c;
+  const uint32_t q = total / n, more = total - q * n, wide = (q + 1) * more;   // `more` shares of q + 1, then of q
+  return (int)(pos < wide ? pos / (q + 1) : more + (pos - wide) / q);
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,

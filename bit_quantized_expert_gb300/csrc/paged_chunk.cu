@@ -55,7 +55,7 @@ struct Chunk {
   // of tile i, which are used one after the other, so that one wait and one release serve both.
   static constexpr int kStages = 2;
   static constexpr int kStageBytes = 2 * kTileBytes;           // keys, then values
-  static constexpr int kPartFloats = kItemRows * (D + 2);      // O by columns, then max, then sum
+  static constexpr int kPartFloats = kItemRows * (D + 2);      // O by four columns of all rows, then max, then sum
   static size_t smem(int B) {
     return 1024 + (size_t)(2 + 2 * kStages) * kTileBytes + kSoftmaxWarps * kOutBytes + ((size_t)B + 1) * 4;
   }
@@ -91,74 +91,73 @@ struct Share {
   int b, qt, ctas;
 };
 
-// Finds this CTA's share, NT threads (the block or its first warp) together: row blocks per sequence are
-// scanned into pre_s[0 .. B], then their costs (units times heads), a run of consecutive row blocks a
-// thread; the threads whose runs hold the two cuts walk theirs once more.  Leaves the share empty if there
-// is nothing to do, or (bad) 2^32 units or more.
-template <int NT>
-__device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint32_t* pre_s, unsigned long long* warp_s,
+// Finds this CTA's share, by the block together: row blocks per sequence are scanned into pre_s[0 .. B], then
+// their costs (units times heads), a run of consecutive row blocks a thread; the threads whose runs hold the
+// two cuts walk theirs once more.  Leaves the share empty if there is nothing to do, or (bad) 2^32 units or more.
+__device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint32_t* pre_s, uint32_t* warp_s,
                                            Share* share_s, bool& bad) {
-  const int tid = threadIdx.x;
-  unsigned long long sum = scan_sequences<NT>(
-      a.B, pre_s, warp_s, [&](int b) { return (uint32_t)(load_seq(a, b, bad).n + tokens - 1) / (uint32_t)tokens; });
-  const uint32_t blocks = (uint32_t)sum, per = (blocks + NT - 1) / NT;
+  const int tid = threadIdx.x, cta = (int)blockIdx.x;
+  bool over;
+  const uint32_t blocks = scan_sequences<kThreads>(a.B, pre_s, warp_s, &over, [&](int b) {
+    return (uint32_t)(load_seq(a, b, bad).n + tokens - 1) / (uint32_t)tokens;
+  });
+  if (over) {
+    bad = true;
+    return;
+  }
+  const uint32_t per = (blocks + kThreads - 1) / kThreads;
   const uint32_t i0 = min(tid * per, blocks), i1 = min(i0 + per, blocks);
-  const int b_mine = i0 < i1 ? find_sequence(pre_s, a.B, i0) : 0;
-  const int cta = (int)blockIdx.x;
-  unsigned long long mine = 0;
-  uint32_t at = 0, lo = 0, hi = 0, slack = 0;
+  // body(b, qt, units of an item) for the row blocks i0 .. i1 - 1
+  auto run = [&](auto&& body) {
+    if (i0 >= i1) return;
+    uint32_t i = i0;
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {   // first the costs, then the cuts
-    int b = b_mine;
-#pragma unroll 1
-    for (uint32_t i = i0; i < i1; ++b) {
+    for (int b = find_sequence(pre_s, a.B, i0); i < i1; ++b) {
       const SeqRows s = load_seq(a, b, bad);
 #pragma unroll 1
       for (; i < i1 && i < pre_s[b + 1]; ++i) {
         const int qt = (int)(i - pre_s[b]);
-        const uint32_t c = (uint32_t)item_of(a, s, qt, tokens).r.count + kItemUnits;
-        if (pass == 0) {
-          mine += (unsigned long long)c * a.Hkv;
-          continue;
-        }
-        const uint32_t end = at + c * a.Hkv;
-#pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
-          const uint32_t x = side == 0 ? lo : hi;
-          if (x < at || x >= end) continue;
-          const uint32_t first = x - (x - at) % c, to = x == first ? x : snap(x, first, first + c, kItemUnits, slack);
-          if (side == 0) {
-            share_s->lo = to;
-            share_s->at = at;
-            share_s->b = b;
-            share_s->qt = qt;
-          } else {
-            share_s->hi = to;
-          }
-        }
-        at = end;
+        body(b, qt, (uint32_t)item_of(a, s, qt, tokens).r.count + kItemUnits);
       }
     }
-    if (pass == 1) return;
-    at = (uint32_t)exclusive_scan<NT>(mine, warp_s, &sum);
-    if (sum >> 32) bad = true;
-    if ((sum >> 32) || sum == 0) return;
-    const uint32_t total = (uint32_t)sum;
-    const int ctas = (int)min(gridDim.x, total);   // no more shares than units
-    if (cta >= ctas) return;
-    // A part costs a result written, read and joined: more than two tiles of imbalance.
-    slack = max(2u, total / ctas / 32);
-    lo = share_start(total, cta, ctas);
-    hi = share_start(total, cta + 1, ctas);
-    if (tid == 0) {
-      share_s->total = total;
-      share_s->ctas = ctas;
-      share_s->slack = slack;
-      if (hi == total) share_s->hi = total;
-    }
-    const uint32_t end = at + (uint32_t)mine;
-    if ((lo < at || lo >= end) && (hi < at || hi >= end)) return;
+  };
+  unsigned long long mine = 0;
+  run([&](int, int, uint32_t units) { mine += (unsigned long long)units * a.Hkv; });
+  uint32_t total;
+  uint32_t at = exclusive_scan<kThreads>(mine, warp_s, &total, &over);
+  if (over) bad = true;
+  if (over || total == 0) return;
+  const int ctas = (int)min(gridDim.x, total);   // no more shares than units
+  if (cta >= ctas) return;
+  const uint32_t lo = share_start(total, cta, ctas), hi = share_start(total, cta + 1, ctas);
+  // A part costs a result written, read and joined: more than two tiles of imbalance.
+  const uint32_t slack = max(2u, (total / ctas) >> 5);
+  if (tid == 0) {
+    share_s->total = total;
+    share_s->ctas = ctas;
+    share_s->slack = slack;
+    if (hi == total) share_s->hi = total;
   }
+  const uint32_t end = at + (uint32_t)mine;
+  if ((lo < at || lo >= end) && (hi < at || hi >= end)) return;
+  run([&](int b, int qt, uint32_t units) {
+    const uint32_t past = at + units * a.Hkv;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const uint32_t x = side == 0 ? lo : hi;
+      if (x < at || x >= past) continue;
+      const uint32_t first = x - (x - at) % units, to = x == first ? x : snap(x, first, first + units, kItemUnits, slack);
+      if (side == 0) {
+        share_s->lo = to;
+        share_s->at = at;
+        share_s->b = b;
+        share_s->qt = qt;
+      } else {
+        share_s->hi = to;
+      }
+    }
+    at = past;
+  });
 }
 
 // Four products of one 64-wide piece of the inner axis, in one statement: every descriptor is in a register
@@ -329,7 +328,7 @@ __device__ __forceinline__ uint32_t non_finite16(uint32_t w) {
   return __vcmpeq2(w & mask, mask);
 }
 
-// What the rows that see non-finite values add to dims d0 .. d0 + 63 of their result: the sum of those
+// What the rows that see non-finite values add to dims d0 .. d0 + 15 of their result: the sum of those
 // values over the positions that the row sees in this segment's masked tiles.
 template <bool FP16>
 __device__ __noinline__ void add_non_finite(const PagedArgs& a, const int32_t* table, TileRange r, int i0, int n, int p_lo,
@@ -342,7 +341,7 @@ __device__ __noinline__ void add_non_finite(const PagedArgs& a, const int32_t* t
       const int page = table[j >> a.page_shift];
       if (page < 0 || page >= a.num_pages) continue;
       const uint16_t* v = a.vc + page * a.page_stride + g * a.head_stride + (j & ((1 << a.page_shift) - 1)) * a.row_stride + d0;
-      for (int e = 0; e < 64; e += 2) {
+      for (int e = 0; e < 16; e += 2) {
         const uint32_t w = *reinterpret_cast<const uint32_t*>(v + e), bad = non_finite16<FP16>(w);
         const float2 x = unpack16<FP16>(w);
         if (bad & 0xFFFFu) acc[e] += x.x;
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // barriers: stages (full, empty), q (full, empty), per row tile S full, P
   // full (its first and its second half), O full, O empty; values clean
   __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 + 8 + 3];
-  __shared__ unsigned long long warp_s[kThreads / 32];
+  __shared__ uint32_t warp_s[kThreads / 32];
   __shared__ Share share_s;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_s;
@@ -413,11 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   bool bad = false;
-  if (a.small) {
-    if (warp == 0) find_share<32>(a, tokens, pre_s, warp_s, &share_s, bad);
-  } else {
-    find_share<kThreads>(a, tokens, pre_s, warp_s, &share_s, bad);
-  }
+  find_share(a, tokens, pre_s, warp_s, &share_s, bad);
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
   if (tid == 0) split.rec[cta].until = -1;
   // Lanes part ways in the schedule (and below, wherever a lane's own data decides).  Every such place ends in
@@ -747,7 +742,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++outs;
       tc_fence_after();
       const bool whole = i0 == 0 && n == x.r.count;
-      const bool hurt = *(volatile int*)&bad_s[my_seg & 3] == my_seg + 1;
+      if (*(volatile int*)&bad_s[my_seg & 3] == my_seg + 1) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t v[16];
+          float extra[16];
+          tmem_ld16_wait(tO + c, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) extra[e] = 0.f;
+          if (live) add_non_finite<FP16>(a, a.table + (size_t)b * a.max_pages, x.r, i0, n, x.p_lo, x.p_hi, p, g, c, extra);
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + extra[e]);
+          tmem_st16(tO + c, v);
+          tmem_wait_st();
+        }
+      }
+      __syncwarp();
+      // (O of a row that sees nothing is 0: its tiles are masked.)
       const float inv = p < 0 ? 0.f : 1.f / l;
       // Rows of the result are stored by four lanes each: lane 4 i + j stores bytes 16 j of rows i, i + 8, ...
       unsigned long long to[4];
@@ -762,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (to[k] != 0) to[k] += (lane & 3) * 16;
         }
       }
-      float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats + t * 128 + r;
+      float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats + 4 * (t * 128 + r);
       const uint32_t out = sOut + warp * kOutBytes;
       const uint64_t inv2 = pair2(inv, inv);
       uint64_t check0 = 0, check1 = 0;   // 0 unless a result is not finite: the sums of 0 times every one
@@ -770,19 +782,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < D; c += 64) {
         uint32_t v[64];
         tmem_ld64(tO + c, v);
-        if (p < 0) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e) v[e] = 0u;
-        }
-        if (hurt && live) {
-          float extra[64];
-#pragma unroll
-          for (int e = 0; e < 64; ++e) extra[e] = 0.f;
-          add_non_finite<FP16>(a, a.table + (size_t)b * a.max_pages, x.r, i0, n, x.p_lo, x.p_hi, p, g, c, extra);
-#pragma unroll
-          for (int e = 0; e < 64; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + extra[e]);
-        }
-        __syncwarp();
         if (whole) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {   // pairs 2 e, 2 e + 2 become words e, e + 1
@@ -818,7 +817,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else if (live) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) part[(c + e) * kItemRows] = __uint_as_float(v[e]);
+          for (int e = 0; e < 64; e += 4)
+            *reinterpret_cast<uint4*>(part + (c + e) * kItemRows) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
         __syncwarp();
       }
@@ -829,8 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live && !(checks.x + checks.y == 0.f)) raise_flag(a.err, kErrNonFinite);
       if (!whole) {
         if (live) {
-          part[D * kItemRows] = m == -INFINITY ? -1e30f : -negm;
-          part[(D + 1) * kItemRows] = l;
+          float* stats = part + D * kItemRows - 3 * (t * 128 + r);
+          stats[0] = m == -INFINITY ? -1e30f : -negm;
+          stats[kItemRows] = l;
         }
         if (i0 == 0 && tid == 0) {
           // the last CTA with a part: the one whose share holds the item's last unit
@@ -884,17 +885,23 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const PagedArgs a, cons
     const float m0 = __ldcg(p0 + D * kItemRows + slot), l0 = __ldcg(p0 + (D + 1) * kItemRows + slot);
     const float m1 = second ? __ldcg(p1 + D * kItemRows + slot) : -1e30f;
     const float l1 = second ? __ldcg(p1 + (D + 1) * kItemRows + slot) : 0.f;
-    float o0[E], o1[E];
+    float4 o0[E / 4], o1[E / 4];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      o0[e] = __ldcg(p0 + (warp * E + e) * kItemRows + slot);
-      o1[e] = second ? __ldcg(p1 + (warp * E + e) * kItemRows + slot) : 0.f;
+    for (int e = 0; e < E / 4; ++e) {
+      o0[e] = __ldcg(reinterpret_cast<const float4*>(p0 + (warp * E + 4 * e) * kItemRows) + slot);
+      o1[e] = second ? __ldcg(reinterpret_cast<const float4*>(p1 + (warp * E + 4 * e) * kItemRows) + slot)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const float top = fmaxf(M, fmaxf(m0, m1)), w = exp2f(M - top), w0 = exp2f(m0 - top), w1 = exp2f(m1 - top);
     M = top;
     L = L * w + l0 * w0 + l1 * w1;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * w + o0[e] * w0 + o1[e] * w1;
+    for (int e = 0; e < E / 4; ++e) {
+      acc[4 * e] = acc[4 * e] * w + o0[e].x * w0 + o1[e].x * w1;
+      acc[4 * e + 1] = acc[4 * e + 1] * w + o0[e].y * w0 + o1[e].y * w1;
+      acc[4 * e + 2] = acc[4 * e + 2] * w + o0[e].z * w0 + o1[e].z * w1;
+      acc[4 * e + 3] = acc[4 * e + 3] * w + o0[e].w * w0 + o1[e].w * w1;
+    }
   }
   bool nonfinite = false;
   uint32_t w[E / 2];

@@ -107,9 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages];
   __shared__ __align__(16) float ml_s[2][kRows][2][kWarps];   // per buffer and row: the warps' max, then sum
-  __shared__ unsigned long long warp_s[kThreads / 32];
+  __shared__ uint32_t warp_s[kThreads / 32];
   __shared__ int abort_s;
-  __shared__ uint32_t total_s;
   const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   float* join_s = reinterpret_cast<float*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes);
   uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes + C::kJoinBytes);
@@ -135,18 +134,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const SeqRows s = load_seq(a, b, bad);
     return s.n == 0 ? 0ull : (unsigned long long)(visible_tiles<kTN>(a, s.p0, s.p0).count + kItemUnits) * a.Hkv;
   };
-  auto note = [&](unsigned long long sum) {
-    if (sum >> 32) bad = true;                                          // refused: nothing is computed
-    if (tid == 0) total_s = (sum >> 32) ? 0u : (uint32_t)sum;
-  };
-  if (a.small) {
-    if (warp == 0) note(scan_sequences<32>(a.B, pre_s, warp_s, cost));
-  } else {
-    note(scan_sequences<kThreads>(a.B, pre_s, warp_s, cost));
+  bool over;
+  uint32_t total = scan_sequences<kThreads>(a.B, pre_s, warp_s, &over, cost);
+  if (over) {   // refused: nothing is computed
+    bad = true;
+    total = 0;
   }
-  __syncwarp();
-  __syncthreads();
-  const uint32_t total = total_s;
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
   const int ctas = (int)min(gridDim.x, total);   // every share holds a tile
   if (tid == 0) split.rec[cta].until = -1;
