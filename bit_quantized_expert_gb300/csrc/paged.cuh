@@ -113,7 +113,7 @@ struct SplitRecord {
 };
 
 // The schedule is made by every CTA for itself, by a block of NT threads together: it stands before all work, and
-// its time is a chain of latencies (5 row blocks a lane of one warp took twice as long as one a thread).
+// its time is a chain of latencies (34 sequences mixed: 4,300 cycles; by one warp without barriers, 6,700).
 
 // Exclusive sums over the block; `over`: the total passes 32 bits (and the sums mean nothing).
 template <int NT>
