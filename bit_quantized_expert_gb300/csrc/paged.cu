@@ -1,10 +1,11 @@
 // Paged key/value cache: the plan (block tables and slot maps), the append, and the C ABI of the three
 // calls (contracts in include/gqa_paged.h).
 //
-//   plan_kernel    one cluster of one to eight CTAs.  Every CTA scans the sequences' new and fresh-page
-//                  counts into shared memory (at most 4096 of each), then the cluster writes the table
-//                  entries (one warp a sequence) and the token rows (one thread a row, its sequence by
-//                  binary search) together.
+//   plan_kernel    one cluster of eight CTAs.  Every CTA scans the sequences' new and fresh-page counts
+//                  into shared memory (at most 4096 of each), then the cluster writes the table entries
+//                  (one warp a sequence) and the token rows (one thread a row, its sequence by binary
+//                  search) together.  Bound by latency: in a graph 3.8 us for 64 single tokens, 7.6 for
+//                  4096, 4.2 for 8 prompts of 1024; by one CTA 3.8, 19.3 and 9.9, by four 3.8, 8.6 and 4.9.
 //   append_kernel  16 bytes a thread, head rows contiguous on both sides.
 #include <algorithm>
 #include <climits>
@@ -18,6 +19,7 @@ namespace moe {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCtas = 8;   // the portable cluster size
 constexpr int kPlanSeqsPerThread = kPagedMaxSeqs / kPlanThreads;
 
 struct PlanArgs {
@@ -202,8 +204,8 @@ constexpr int kAppendBatch = 4;
 
 // The keys or the values (blockIdx.y), units of 16 bytes numbered by (token, head, unit of the row) in Index;
 // four units a thread and turn, their slots and their data loaded together, so that one round trip to
-// memory lies between the start and the stores.  Bound by memory: 8192 tokens of two heads of 128 are
-// 33.6 MB with both ways.
+// memory lies between the start and the stores.  Bound by memory: 8 prompts of up to 4096 tokens, 23.5 MB both
+// ways, take 4.2 us in a graph (with 2, 8 or 16 CTAs an SM in place of 4: 5.3, 5.8, 6.4).
 template <class Index>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
   pdl_wait();
@@ -431,21 +433,18 @@ extern "C" moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* 
                 q_start,    kv_len,  positions,  slots,      n_free_out,
                 static_cast<uint32_t*>(workspace), d.n_seqs, d.n_tokens, log2_of(d.page_size), d.num_pages, d.max_pages,
                 free_capacity};
-  // One CTA per 2048 rows or 256 sequences, up to the portable cluster size.
-  const long long want = std::max(((long long)d.n_tokens + 2047) / 2048, ((long long)d.n_seqs + 255) / 256);
-  const int ctas = want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
   const size_t smem = 2 * ((size_t)d.n_seqs + 1) * sizeof(long long);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                2 * (kPagedMaxSeqs + 1) * (int)sizeof(long long)) != cudaSuccess)
     return MOE_ERR_CUDA;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.x = kPlanCtas;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(kPlanCtas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
