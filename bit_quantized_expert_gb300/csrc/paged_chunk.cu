@@ -19,6 +19,12 @@
 //   * Only tiles that some row does not wholly see are masked.  In those, the value tile is also
 //     searched for non-finite values, since 0 times one of them is not 0: they are taken out, and the rows that do
 //     see them get them back at the end.
+//
+// Bound by the softmax's chain: a cache tile of a row tile takes ~1,400 cycles of softmax (512 of them exponentials, at
+// 32 a cycle and SM), then P V and the next scores, ~2,800 in all where both row tiles' products are 2,048.
+// Tensor memory is full, so the next scores cannot start before P is consumed.  Measured (16 query and 2
+// key/value heads of 128): 2048 tokens behind 32768 positions 338 us (1.65 PFLOP/s) in a graph, tensor pipe 75 %
+// active; a prompt of 512 15.6 us; 4096 tokens with a window of 1024 57 us.
 #include <cmath>
 #include <type_traits>
 
@@ -36,7 +42,7 @@ constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 constexpr int kItemRows = 256;              // two row tiles
 constexpr uint32_t kTmemO = 256;            // columns: S0 0, S1 128, O0 256, O1 384 (all 512 are allocated: base 0)
 constexpr int kOutBytes = 32 * 64;          // a warp's staging of its 32 rows of o, 32 dims at a time
-constexpr int kItemUnits = 2;               // what an item costs beside its tiles, in tiles
+constexpr int kItemUnits = 2;               // what an item costs beside its tiles, in tiles (~5,000 cycles)
 // Base-2 units by which the numerators' reference may lag behind the row's maximum, and by which it stands
 // below the maximum that sets it: fp16 numerators use its range from 2^15 down, since it keeps 2^-25 at best and a
 // long cache of small ones would be summed as nothing.  bf16 has fp32's range, and lags more: of 14 units and 6,
@@ -861,7 +867,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of one split item (blockIdx.x: the CTA that began it) for 32 of its rows (blockIdx.y), in
-// order; a warp takes a quarter of the dims, a lane a row.
+// order; a warp takes a quarter of the dims, a lane a row.  Bound by latency (a launch, the record, the parts from L2):
+// 2 us of a graph where nothing is split, 3 where a window chunk's 64 cuts are.
 template <int D, bool FP16>
 __global__ void __launch_bounds__(128) chunk_join_kernel(const PagedArgs a, const ChunkSplit split) {
   using C = Chunk<D>;

@@ -16,6 +16,10 @@
 //   * running max, sum and O stay in registers; at an item's end the eight warps are joined in shared
 //     memory in a fixed order (one barrier an item: two joining buffers, every thread weighs for itself), and the result goes to o, or, for an item that other CTAs share, to a
 //     partial that a second launch joins in order.
+//
+// Measured (16 query and 2 key/value heads of 128, in a graph): 64 sequences of 1 to 32768 positions, 139 MB, 28.5 us
+// (4.9 TB/s), of which ~5 us are fixed steps: launch, schedule, first copies, joins; one sequence of 32768, 33.6
+// MB, 10.6 us.  tcgen05 would not help: eight heads fill an eighth of its 64-row tiles, and bytes bound the rest.
 #include <cmath>
 
 #include "paged.cuh"
