@@ -23,7 +23,7 @@
 // Bound by the softmax's chain: a cache tile of a row tile takes ~1,400 cycles of softmax (512 of them exponentials, at
 // 32 a cycle and SM), then P V and the next scores, ~2,800 in all where both row tiles' products are 2,048.
 // Tensor memory is full, so the next scores cannot start before P is consumed.  Measured (16 query and 2
-// key/value heads of 128): 2048 tokens behind 32768 positions 338 us (1.65 PFLOP/s) in a graph, tensor pipe 75 %
+// key/value heads of 128): 2048 tokens behind 32768 positions 338 us (1.68 PFLOP/s) in a graph, tensor pipe 75 %
 // active; a prompt of 512 15.6 us; 4096 tokens with a window of 1024 57 us.
 #include <cmath>
 #include <type_traits>
