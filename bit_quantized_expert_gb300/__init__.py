@@ -373,29 +373,35 @@ def alloc_gqa_paged_workspace(pd: GqaPagedDims, device="cuda"):
     return ws
 
 
-_paged_types = None   # 16-bit types that stand for each dtype of the dims (bit patterns included)
+# A paged call's checks cost more host time than its launch, so they read each property once and look nothing up
+# that stays: the types that stand for each dtype of the dims (bit patterns included), and torch's functions for the current
+# device and its current stream's handle.
+_paged_types = _int32 = _device = _raw_stream = None
 
 
 def _load_paged_types():
-    global _paged_types
+    global _paged_types, _int32, _device, _raw_stream
     import torch
     bits = (torch.int16, torch.uint16)
-    _paged_types = ((torch.bfloat16, *bits), (torch.float16, *bits), (torch.int32,))
+    _paged_types, _int32 = ((torch.bfloat16, *bits), (torch.float16, *bits)), torch.int32
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
 def _paged_device() -> int:
     """The current device, on which every tensor of a paged call must be."""
-    import torch
-    if _paged_types is None:
+    if _device is None:
+        import torch
+        torch.cuda.init()
         _load_paged_types()
-    return torch.cuda.current_device()
+    return _device()
 
 
 def _paged_ints(t, n: int, dev: int, name: str) -> int:
     """Pointer of a contiguous int32 tensor of at least n entries."""
-    if t.get_device() != dev or t.dtype not in _paged_types[2] or t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous int32 tensor of at least {n} entries on device {dev}")
-    return t.data_ptr()
+    if t.get_device() == dev and t.dtype is _int32 and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous int32 tensor of at least {n} entries on device {dev}")
 
 
 def _paged_rows(t, rows: int, heads: int, D: int, stride: int, dtype: int, dev: int, name: str) -> int:
@@ -438,7 +444,7 @@ def gqa_paged_plan(pd: GqaPagedDims, ctx_len, new_len, free_pages, n_free, block
         _paged_ints(block_table, B * pd.max_pages, dev, "block_table"), _paged_ints(q_start, B + 1, dev, "q_start"),
         _paged_ints(kv_len, B, dev, "kv_len"), None if positions is None else _paged_ints(positions, T, dev, "positions"),
         _paged_ints(slots, T, dev, "slots"), _paged_ints(n_free_out, 1, dev, "n_free_out"), _paged_workspace(workspace, dev),
-        workspace.nbytes, _stream(stream)), "gqa_paged_plan")
+        workspace.nbytes, _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_plan")
 
 
 def gqa_paged_append(pd: GqaPagedDims, k, v, slots, q_start, k_cache, v_cache, workspace, stream=None):
@@ -448,7 +454,7 @@ def gqa_paged_append(pd: GqaPagedDims, k, v, slots, q_start, k_cache, v_cache, w
     _check(load_library().gqa_paged_append(
         ctypes.byref(pd), _paged_rows(k, T, H, D, pd.k_stride, dt, dev, "k"), _paged_rows(v, T, H, D, pd.v_stride, dt, dev, "v"),
         _paged_ints(slots, T, dev, "slots"), _paged_ints(q_start, pd.n_seqs + 1, dev, "q_start"), kc, vc,
-        _paged_workspace(workspace, dev), workspace.nbytes, _stream(stream)), "gqa_paged_append")
+        _paged_workspace(workspace, dev), workspace.nbytes, _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_append")
 
 
 def gqa_paged_attention(pd: GqaPagedDims, q, k_cache, v_cache, block_table, q_start, kv_len, o, workspace, stream=None):
@@ -460,7 +466,7 @@ def gqa_paged_attention(pd: GqaPagedDims, q, k_cache, v_cache, block_table, q_st
         ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, dt, dev, "q"), kc, vc,
         _paged_ints(block_table, B * pd.max_pages, dev, "block_table"), _paged_ints(q_start, B + 1, dev, "q_start"),
         _paged_ints(kv_len, B, dev, "kv_len"), _paged_rows(o, T, H, D, pd.o_stride, dt, dev, "o"),
-        _paged_workspace(workspace, dev), workspace.nbytes, _stream(stream)), "gqa_paged_attention")
+        _paged_workspace(workspace, dev), workspace.nbytes, _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_attention")
 
 
 def gdn_dims(T, H, d_k=128, d_v=128) -> GdnDims:

@@ -434,8 +434,9 @@ extern "C" moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* 
                 static_cast<uint32_t*>(workspace), d.n_seqs, d.n_tokens, log2_of(d.page_size), d.num_pages, d.max_pages,
                 free_capacity};
   const size_t smem = 2 * ((size_t)d.n_seqs + 1) * sizeof(long long);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               2 * (kPagedMaxSeqs + 1) * (int)sizeof(long long)) != cudaSuccess)
+  static std::atomic<uint64_t> ready{0};
+  if (allow_smem(reinterpret_cast<const void*>(plan_kernel), 2 * (kPagedMaxSeqs + 1) * (int)sizeof(long long), &ready) !=
+      cudaSuccess)
     return MOE_ERR_CUDA;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -2,6 +2,8 @@
 // of the tables that live on the GPU (contracts in include/gqa_paged.h).
 #pragma once
 
+#include <atomic>
+
 #include "../../include/gqa_paged.h"
 #include "common.cuh"
 #include "kernels.h"
@@ -229,6 +231,19 @@ template <bool FP16>
 __device__ __forceinline__ float2 unpack16(uint32_t x) {
   if (FP16) return __half22float2(*reinterpret_cast<const __half2*>(&x));
   return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+}
+
+// Lets `kernel` use `bytes` of shared memory on the current device, once for each of the first 64 (bits of `ready`;
+// racing first calls set the same value).
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (ready->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready->fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // ------------------------------------------------------------------------------------------

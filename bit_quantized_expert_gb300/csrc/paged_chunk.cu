@@ -928,8 +928,8 @@ __global__ void __launch_bounds__(128) chunk_join_kernel(const PagedArgs a, cons
 
 template <int D, bool FP16>
 cudaError_t launch(const PagedMaps& maps, const PagedArgs& a, const ChunkSplit& split, int ctas, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Chunk<D>::smem(kPagedMaxSeqs));
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(chunk_kernel<D, FP16>), (int)Chunk<D>::smem(kPagedMaxSeqs), &ready);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

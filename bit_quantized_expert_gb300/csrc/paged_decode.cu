@@ -512,8 +512,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Page
 
 template <int D, bool FP16>
 cudaError_t launch(const PagedMaps& maps, const PagedArgs& a, const DecodeSplit& split, int ctas, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Dec<D>::smem(kPagedMaxSeqs));
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(decode_kernel<D, FP16>), (int)Dec<D>::smem(kPagedMaxSeqs), &ready);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
