@@ -108,10 +108,12 @@ __device__ __forceinline__ bool tile_open(const PagedArgs& a, int j0, int p_lo, 
 // ------------------------------------------------------------------------------------------
 constexpr int kPagedMaxCtas = 160;   // one CTA per SM, of 152
 
-// What the joining launch needs of a CTA whose last item goes on in later CTAs (until < 0: none).
+// What the joining launch needs of a CTA whose last item goes on in later CTAs.
 struct SplitRecord {
-  int32_t row, g, rows, until;   // first row of o, head group, tokens of the item, last CTA with a part
-  int32_t p_lo;                  // position of the item's first token
+  int32_t row, g, rows;   // first row of o, head group, tokens of the item
+  int32_t p_lo;           // position of the item's first token
+  int32_t until;          // the last CTA with a part of the item that begins here (< 0: none goes on)
+  int32_t first;          // the CTA where the item that goes on begins: this one, or (chunk form) an earlier one
 };
 
 // The schedule is made by every CTA for itself, by a block of NT threads together: it stands before all work, and

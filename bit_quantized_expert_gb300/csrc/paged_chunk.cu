@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool bad = false;
   find_share(a, tokens, pre_s, warp_s, &share_s, bad);
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
-  if (tid == 0) split.rec[cta].until = -1;
+  if (tid == 0) split.rec[cta].until = split.rec[cta].first = -1;
   // Lanes part ways in the schedule (and below, wherever a lane's own data decides).  Every such place ends in
   // __syncwarp before the warp's next collective instruction (barriers, tensor-memory loads and stores): those
   // assume a converged warp, which a join of branches alone does not promise.
@@ -839,12 +839,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           stats[0] = m == -INFINITY ? -1e30f : -negm;
           stats[kItemRows] = l;
         }
-        if (i0 == 0 && tid == 0) {
-          // the last CTA with a part: the one whose share holds the item's last unit
-          const uint32_t e = u + x.r.count + kItemUnits, total = share_s.total;
-          int c = share_of(e - 1, total, share_s.ctas);
-          while (c > cta + 1 && snap(share_start(total, c, share_s.ctas), u, e, kItemUnits, share_s.slack) >= e) --c;
-          split.rec[cta] = SplitRecord{s.row0 + x.t0, g, x.n, c, x.p_lo};
+        if (i0 + n < x.r.count && tid == 0) {   // the item goes on: who begins it, and who ends it
+          const uint32_t first = i0 == 0 ? u : u - kItemUnits - i0, end = first + x.r.count + kItemUnits;
+          const uint32_t total = share_s.total;
+          const int ctas = share_s.ctas;
+          auto cut_at = [&](int c) { return snap(share_start(total, c, ctas), first, end, kItemUnits, share_s.slack); };
+          int c = share_of(i0 == 0 ? end - 1 : first, total, ctas);
+          if (i0 == 0) {
+            while (c > cta + 1 && cut_at(c) >= end) --c;
+            split.rec[cta] = SplitRecord{s.row0 + x.t0, g, x.n, x.p_lo, c, cta};
+          } else {
+            while (c + 1 < cta && cut_at(c + 1) <= first) ++c;
+            split.rec[cta].first = c;
+          }
         }
       }
       __syncwarp();
@@ -866,64 +873,159 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of one split item (blockIdx.x: the CTA that began it) for 32 of its rows (blockIdx.y), in
-// order; a warp takes a quarter of the dims, a lane a row.  Bound by latency (a launch, the record, the parts from L2):
-// 2 us of a graph where nothing is split, 3 where a window chunk's 64 cuts are.
+// Joins the parts of the split items, a row a lane.  Few parts, which is most items: block y of the CTA that began the
+// item takes rows 32 y .. 32 y + 31, a warp a quarter of the dims, all parts in order.  Many (one sequence's few
+// rows are cut into as many parts as there are SMs for its heads): the blocks of all its CTAs but the last share
+// the pairs of 32 rows and an eighth of the dims, a warp takes every fourth part, and the warps' results are
+// joined in order through shared memory.  Bound by latency (a launch, the record, the parts from L2), so what
+// counts is loads in flight (119 registers: with at most 64, a prompt of 2048 took 40 us, not 31): 2 us of a graph where
+// nothing is split, 3 where a window chunk's 64 cuts are.  8 tokens behind 32768 positions, 76 parts a head: 22 us in
+// all; joined as few 73.  `Many` begins at 6: at 4, 512 tokens behind 8192 take 45 us, not 40; at 10, 256 take
+// 30, not 29.
+constexpr int kJoinWarps = 4;
+constexpr int kJoinMany = 6;   // parts
+
 template <int D, bool FP16>
-__global__ void __launch_bounds__(128) chunk_join_kernel(const PagedArgs a, const ChunkSplit split) {
+__global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const PagedArgs a, const ChunkSplit split) {
   using C = Chunk<D>;
-  constexpr int E = D / 4;
+  constexpr int kFewDims = D / 4, kManyDims = D / 8;
+  __shared__ float acc_s[kJoinWarps][kManyDims][32], m_s[kJoinWarps][32], l_s[kJoinWarps][32];
   pdl_wait();
   pdl_launch_dependents();
-  const int first = (int)blockIdx.x;
-  const SplitRecord rec = split.rec[first];
-  if (rec.until < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = (int)blockIdx.y * 32 + lane;
-  const int tpt = 128 / a.G, t = slot >> 7, r = slot & 127, tok = r / a.G;
-  if (tok >= tpt || t * tpt + tok >= rec.rows) return;
+  SplitRecord rec = split.rec[blockIdx.x];
+  const int first = rec.first;
+  if (first < 0) return;
+  if (first != (int)blockIdx.x) rec = split.rec[first];
+  const int n = rec.until - first + 1;
+  if (first != (int)blockIdx.x && n < kJoinMany) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tpt = 128 / a.G;
   auto part = [&](int c) { return split.part + ((size_t)c * 2 + (c == first ? 1 : 0)) * C::kPartFloats; };
-  // Two parts at a time, everything of both in flight at once (most items have two or three).
-  float M = -1e30f, L = 0.f, acc[E];
+
+  // Parts c0, c0 + S, ... of a row's N dims from d on: K at a time, everything of them in flight at once.
+  float M, L;
+  auto sum_parts = [&](auto n_c, auto k_c, float* acc, int c0, int S, int d, int slot) {
+    constexpr int N = decltype(n_c)::value, K = decltype(k_c)::value;
+    M = -1e30f;
+    L = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int c = first; c <= rec.until; c += 2) {
-    const bool second = c < rec.until;
-    const float *p0 = part(c), *p1 = second ? part(c + 1) : p0;
-    const float m0 = __ldcg(p0 + D * kItemRows + slot), l0 = __ldcg(p0 + (D + 1) * kItemRows + slot);
-    const float m1 = second ? __ldcg(p1 + D * kItemRows + slot) : -1e30f;
-    const float l1 = second ? __ldcg(p1 + (D + 1) * kItemRows + slot) : 0.f;
-    float4 o0[E / 4], o1[E / 4];
+    for (int e = 0; e < N; ++e) acc[e] = 0.f;
+    for (int c = c0; c <= rec.until; c += K * S) {
+      // (a part past the last is read as the first and weighs nothing: loads without branches)
+      float m[K], l[K];
+      float4 o[K][N / 4];
 #pragma unroll
-    for (int e = 0; e < E / 4; ++e) {
-      o0[e] = __ldcg(reinterpret_cast<const float4*>(p0 + (warp * E + 4 * e) * kItemRows) + slot);
-      o1[e] = second ? __ldcg(reinterpret_cast<const float4*>(p1 + (warp * E + 4 * e) * kItemRows) + slot)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < K; ++k) {
+        const float* p = part(c + k * S <= rec.until ? c + k * S : c);
+        m[k] = __ldcg(p + D * kItemRows + slot);
+        l[k] = __ldcg(p + (D + 1) * kItemRows + slot);
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) o[k][e] = __ldcg(reinterpret_cast<const float4*>(p + (d + 4 * e) * kItemRows) + slot);
+      }
+#pragma unroll
+      for (int k = 1; k < K; ++k)
+        if (c + k * S > rec.until) {
+          m[k] = -1e30f;
+          l[k] = 0.f;
+#pragma unroll
+          for (int e = 0; e < N / 4; ++e) o[k][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < K; ++k) top = fmaxf(top, m[k]);
+      const float w = exp2f(M - top);
+      M = top;
+      L *= w;
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[e] *= w;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float x = exp2f(m[k] - top);
+        L += l[k] * x;
+#pragma unroll
+        for (int e = 0; e < N / 4; ++e) {
+          acc[4 * e] += o[k][e].x * x;
+          acc[4 * e + 1] += o[k][e].y * x;
+          acc[4 * e + 2] += o[k][e].z * x;
+          acc[4 * e + 3] += o[k][e].w * x;
+        }
+      }
     }
-    const float top = fmaxf(M, fmaxf(m0, m1)), w = exp2f(M - top), w0 = exp2f(m0 - top), w1 = exp2f(m1 - top);
-    M = top;
-    L = L * w + l0 * w0 + l1 * w1;
+  };
+  // The row's result for N dims from d on, of unnormalised values `v` and their sum.
+  auto store = [&](auto n_c, const float* v, float sum, int d, int slot) {
+    constexpr int N = decltype(n_c)::value;
+    const int t = slot >> 7, r = slot & 127, tok = r / a.G;
+    const float inv = rec.p_lo + t * tpt + tok < 0 ? 0.f : 1.f / sum;   // a row before position 0 sees nothing
+    bool nonfinite = false;
+    uint32_t w[N / 2];
 #pragma unroll
-    for (int e = 0; e < E / 4; ++e) {
-      acc[4 * e] = acc[4 * e] * w + o0[e].x * w0 + o1[e].x * w1;
-      acc[4 * e + 1] = acc[4 * e + 1] * w + o0[e].y * w0 + o1[e].y * w1;
-      acc[4 * e + 2] = acc[4 * e + 2] * w + o0[e].z * w0 + o1[e].z * w1;
-      acc[4 * e + 3] = acc[4 * e + 3] * w + o0[e].w * w0 + o1[e].w * w1;
+    for (int e = 0; e < N; e += 2) {
+      const float x = v[e] * inv, y = v[e + 1] * inv;
+      nonfinite |= !isfinite(x) || !isfinite(y);
+      w[e / 2] = pack16<FP16>(x, y);
     }
-  }
-  bool nonfinite = false;
-  uint32_t w[E / 2];
-  const float inv = rec.p_lo + t * tpt + tok < 0 ? 0.f : 1.f / L;   // a row before position 0 sees nothing
+    if (nonfinite) raise_flag(a.err, kErrNonFinite);
+    uint16_t* o = a.o + (long long)(rec.row + t * tpt + tok) * a.o_stride + (long long)(rec.g * a.G + r % a.G) * D + d;
+    if constexpr (N >= 8) {
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const float x = acc[e] * inv, y = acc[e + 1] * inv;
-    nonfinite |= !isfinite(x) || !isfinite(y);
-    w[e / 2] = pack16<FP16>(x, y);
-  }
-  if (nonfinite) raise_flag(a.err, kErrNonFinite);
-  uint16_t* orow = a.o + (long long)(rec.row + t * tpt + tok) * a.o_stride + (long long)(rec.g * a.G + r % a.G) * D + warp * E;
+      for (int e = 0; e < N / 8; ++e)
+        *reinterpret_cast<uint4*>(o + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+    } else {
 #pragma unroll
-  for (int e = 0; e < E / 8; ++e)
-    *reinterpret_cast<uint4*>(orow + 8 * e) = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+      for (int e = 0; e < N / 2; ++e) *reinterpret_cast<uint32_t*>(o + 2 * e) = w[e];
+    }
+  };
+  auto is_live = [&](int slot) {
+    const int t = slot >> 7, tok = (slot & 127) / a.G;
+    return tok < tpt && t * tpt + tok < rec.rows;
+  };
+
+  using Two = std::integral_constant<int, 2>;
+  using Four = std::integral_constant<int, 4>;
+  if (n < kJoinMany) {
+    using Dims = std::integral_constant<int, kFewDims>;
+    const int slot = (int)blockIdx.y * 32 + lane;
+    if (!is_live(slot)) return;
+    float acc[kFewDims];
+    sum_parts(Dims{}, Two{}, acc, first, 1, warp * kFewDims, slot);
+    store(Dims{}, acc, L, warp * kFewDims, slot);
+    return;
+  }
+  using Dims = std::integral_constant<int, kManyDims>;
+  const int slots = rec.rows <= tpt ? rec.rows * a.G : 128 + (rec.rows - tpt) * a.G;   // up to the last token's
+  const int blocks = (n - 1) * (int)gridDim.y;
+  for (int x = ((int)blockIdx.x - first) * (int)gridDim.y + (int)blockIdx.y; x < (slots + 31) / 32 * 8; x += blocks) {
+    const int slot = (x >> 3) * 32 + lane, d = (x & 7) * kManyDims;
+    const bool live = is_live(slot);
+    if (live) {
+      float acc[kManyDims];
+      sum_parts(Dims{}, Four{}, acc, first + warp, kJoinWarps, d, slot);
+#pragma unroll
+      for (int e = 0; e < kManyDims; ++e) acc_s[warp][e][lane] = acc[e];
+      m_s[warp][lane] = M;
+      l_s[warp][lane] = L;
+    }
+    __syncwarp();
+    __syncthreads();
+    if (live) {
+      constexpr int N = kManyDims / kJoinWarps;   // this warp's dims
+      float top = m_s[0][lane], sum = 0.f, y[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) y[e] = 0.f;
+#pragma unroll
+      for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, m_s[k][lane]);
+#pragma unroll
+      for (int k = 0; k < kJoinWarps; ++k) {
+        const float w = exp2f(m_s[k][lane] - top);
+        sum += l_s[k][lane] * w;
+#pragma unroll
+        for (int e = 0; e < N; ++e) y[e] += acc_s[k][warp * N + e][lane] * w;
+      }
+      store(std::integral_constant<int, N>{}, y, sum, d + warp * N, slot);
+    }
+    __syncwarp();
+    __syncthreads();   // before acc_s is written again
+  }
 }
 
 template <int D, bool FP16>
@@ -944,7 +1046,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedArgs& a, const ChunkSplit& 
   e = cudaLaunchKernelEx(&cfg, chunk_kernel<D, FP16>, maps, a, split);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(ctas, kItemRows / 32);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D, FP16>, a, split);
 }

@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the last CTA with a part: the one whose share holds the item's last unit
       int c = share_of(now.end - 1, total, ctas);
       while (c > cta + 1 && snap(share_start(total, c, ctas), now.first, now.end, kItemUnits, kSlack) >= now.end) --c;
-      split.rec[cta] = SplitRecord{now.row0, now.g, 1, c, now.p0};
+      split.rec[cta] = SplitRecord{now.row0, now.g, 1, now.p0, c, cta};
     }
     __syncwarp();   // lanes part above; the next tiles' products are collective
     buf ^= 1;

@@ -225,6 +225,13 @@ def test_chunk_over_a_long_cache():
     _ok(Batch([(6000, 9), (0, 3), (3000, 20)], Hq=4, Hkv=2, seed=5))
 
 
+@pytest.mark.parametrize("seqs,Hq,Hkv,D", [([(20000, 3)], 8, 1, 128), ([(9000, 40)], 4, 2, 64), ([(6000, 33)], 16, 2, 128),
+                                           ([(30000, 2), (50, 4), (7000, 17)], 6, 1, 64)])
+def test_few_rows_over_long_caches(seqs, Hq, Hkv, D):
+    """Items cut into many parts (up to one a SM), of one row tile and of two."""
+    _ok(Batch(seqs, Hq=Hq, Hkv=Hkv, D=D, seed=29))
+
+
 @pytest.mark.parametrize("q_scale", [8.0, 0.01])
 def test_chunks_peaked_and_flat(q_scale):
     _ok(Batch([(1000, 40), (100, 30)], Hq=8, q_scale=q_scale, seed=7))
