@@ -22,9 +22,10 @@
 //
 // Bound by the softmax's chain: a cache tile of a row tile takes ~1,400 cycles of softmax (512 of them exponentials, at
 // 32 a cycle and SM), then P V and the next scores, ~2,800 in all where both row tiles' products are 2,048.
-// Tensor memory is full, so the next scores cannot start before P is consumed.  Measured (16 query and 2
-// key/value heads of 128): 2048 tokens behind 32768 positions 338 us (1.68 PFLOP/s) in a graph, tensor pipe 75 %
-// active; a prompt of 512 15.6 us; 4096 tokens with a window of 1024 57 us.
+// At 128 dims tensor memory is full, so the next scores cannot start before P is consumed; at 64 there is room, but an
+// order that used it (two barriers more a tile) was slower (297 against 276 us behind 32768 positions).  Measured (16 query and 2
+// key/value heads of 128): 2048 tokens behind 32768 positions 340 us (1.67 PFLOP/s) in a graph, tensor pipe 75 %
+// active; a prompt of 512 15.4 us; 4096 tokens with a window of 1024 54 us.
 #include <cmath>
 #include <type_traits>
 
@@ -222,17 +223,15 @@ __device__ __forceinline__ uint64_t desc_values(uint32_t saddr, uint32_t box_byt
       "=r"(v[o + 7]), "=r"(v[o + 8]), "=r"(v[o + 9]), "=r"(v[o + 10]), "=r"(v[o + 11]), "=r"(v[o + 12]),           \
       "=r"(v[o + 13]), "=r"(v[o + 14]), "=r"(v[o + 15])
 
-// 64 consecutive columns of this thread's row: two loads and one wait in one statement.
-__device__ __forceinline__ void tmem_ld64(uint32_t t, uint32_t (&r)[64]) {
+// 32 consecutive columns of this thread's row.
+__device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t (&r)[32]) {
   asm volatile(
       "{\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
-      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;\n\t}"
-      : R16(r, 0), R16(r, 16), R16(r, 32), R16(r, 48)
-      : "r"(t), "r"(t + 32u)
+      : R16(r, 0), R16(r, 16)
+      : "r"(t)
       : "memory");
 }
 
@@ -785,12 +784,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t inv2 = pair2(inv, inv);
       uint64_t check0 = 0, check1 = 0;   // 0 unless a result is not finite: the sums of 0 times every one
 #pragma unroll 1
-      for (int c = 0; c < D; c += 64) {
-        uint32_t v[64];
-        tmem_ld64(tO + c, v);
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tO + c, v);
         if (whole) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {   // pairs 2 e, 2 e + 2 become words e, e + 1
+          for (int e = 0; e < 16; e += 2) {   // pairs 2 e, 2 e + 2 become words e, e + 1
             const uint64_t f0 = mul2(pair2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), inv2);
             const uint64_t f1 = mul2(pair2(__uint_as_float(v[2 * e + 2]), __uint_as_float(v[2 * e + 3])), inv2);
             check0 = fma2(f0, 0ull, check0);
@@ -802,28 +801,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 64 bytes a row through shared memory (16-byte pieces XOR-ed against bank conflicts), so that a store
           // touches 8 rows, not 32.
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int e = 0; e < 4; ++e)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)),
+                         "r"(v[4 * e]), "r"(v[4 * e + 1]), "r"(v[4 * e + 2]), "r"(v[4 * e + 3])
+                         : "memory");
+          __syncwarp();
+          uint4 w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)),
-                           "r"(v[16 * half + 4 * e]), "r"(v[16 * half + 4 * e + 1]), "r"(v[16 * half + 4 * e + 2]),
-                           "r"(v[16 * half + 4 * e + 3])
-                           : "memory");
-            __syncwarp();
-            uint4 w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int rr = k * 8 + (lane >> 2);
-              ld_shared4(out + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), w[k].x, w[k].y, w[k].z, w[k].w);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (to[k] != 0) *reinterpret_cast<uint4*>(to[k] + 2 * c + 64 * half) = w[k];
-            __syncwarp();
+          for (int k = 0; k < 4; ++k) {
+            const int rr = k * 8 + (lane >> 2);
+            ld_shared4(out + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), w[k].x, w[k].y, w[k].z, w[k].w);
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (to[k] != 0) *reinterpret_cast<uint4*>(to[k] + 2 * c) = w[k];
         } else if (live) {
 #pragma unroll
-          for (int e = 0; e < 64; e += 4)
+          for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<uint4*>(part + (c + e) * kItemRows) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
         __syncwarp();
