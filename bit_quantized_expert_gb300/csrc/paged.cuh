@@ -116,6 +116,11 @@ struct SplitRecord {
   int32_t first;          // the CTA where the item that goes on begins: this one, or (chunk form) an earlier one
 };
 
+// (From L2: the launch that wrote it may have ended just now.)
+__device__ __forceinline__ SplitRecord load_record(const SplitRecord* r) {
+  return SplitRecord{__ldcg(&r->row), __ldcg(&r->g), __ldcg(&r->rows), __ldcg(&r->p_lo), __ldcg(&r->until), __ldcg(&r->first)};
+}
+
 // The schedule is made by every CTA for itself, by a block of NT threads together: it stands before all work, and
 // its time is a chain of latencies (34 sequences mixed: 4,300 cycles; by one warp without barriers, 6,700).
 

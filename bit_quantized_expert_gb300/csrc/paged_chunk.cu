@@ -886,10 +886,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const Paged
   __shared__ float acc_s[kJoinWarps][kManyDims][32], m_s[kJoinWarps][32], l_s[kJoinWarps][32];
   pdl_wait();
   pdl_launch_dependents();
-  SplitRecord rec = split.rec[blockIdx.x];
+  SplitRecord rec = load_record(split.rec + blockIdx.x);
   const int first = rec.first;
   if (first < 0) return;
-  if (first != (int)blockIdx.x) rec = split.rec[first];
+  if (first != (int)blockIdx.x) rec = load_record(split.rec + first);
   const int n = rec.until - first + 1;
   if (first != (int)blockIdx.x && n < kJoinMany) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tpt = 128 / a.G;

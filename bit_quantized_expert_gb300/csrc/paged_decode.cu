@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Page
   pdl_wait();
   pdl_launch_dependents();
   const int first = (int)blockIdx.x, row = (int)blockIdx.y;
-  const SplitRecord rec = split.rec[first];
+  const SplitRecord rec = load_record(split.rec + first);
   if (rec.until < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int parts = rec.until - first + 1;

@@ -379,6 +379,22 @@ def test_lengths_out_of_range(new):
         b.check(o, clean, rows, change)
 
 
+@pytest.mark.parametrize("new", [1, 2])
+def test_more_work_than_can_be_numbered(new):
+    """Lengths whose cache tiles pass 2^32 over all sequences and heads (every other sequence claims the same
+    rows, each over 2^30 positions): flagged, and nothing is computed."""
+    B, H, page, M = 132, 8, 128, 1 << 23
+    d = moe.gqa_paged_dims(H, H, 64, page, 4, M, B, new, max_new=new)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kc, vc = (torch.zeros(4, H, page, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, o = torch.ones(new, H, 64, dtype=torch.bfloat16, device="cuda"), torch.full((new, H, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    table, kv = torch.zeros(B, M, **i32), torch.full((B,), M * page, **i32)
+    starts, ws = torch.arange(B + 1, **i32) % 2 * new, moe.alloc_gqa_paged_workspace(d)
+    assert B // 2 * H * (M * page // (64 if new == 1 else 128)) >= 2 ** 32
+    moe.gqa_paged_attention(d, q, kc, vc, table, starts.int(), kv, o, ws)
+    assert moe.read_error_flags(ws) == moe.ERR_BAD_PAGES and (o == 7.0).all()
+
+
 def test_more_rows_than_max_new():
     """The first max_new rows of the sequence are computed, the rest left as they were."""
     for limit in (1, 5):
