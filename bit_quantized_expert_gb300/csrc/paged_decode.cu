@@ -148,22 +148,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ctas = (int)min(gridDim.x, total);   // every share holds a tile
   if (tid == 0) split.rec[cta].until = -1;
   if (cta >= ctas) return;
-  uint32_t lo = 0, hi = 0;
-  int b_first = 0;   // the sequence that holds unit lo
-#pragma unroll 1
-  for (int side = 1; side >= 0; --side) {
-    uint32_t x = share_start(total, cta + side, ctas);
+  // Its two cuts, by the even lanes and the odd ones of every warp.
+  uint32_t lo, hi;
+  int b_first;   // the sequence that holds unit lo
+  {
+    uint32_t x = share_start(total, cta + (lane & 1), ctas);
     const int b = find_sequence(pre_s, a.B, x);
     if (x < total) {
       const uint32_t units = (pre_s[b + 1] - pre_s[b]) / a.Hkv, first = x - (x - pre_s[b]) % units;
       x = snap(x, first, first + units, kItemUnits, kSlack);
     }
-    if (side) {
-      hi = x;
-    } else {
-      lo = x;
-      b_first = b;
-    }
+    __syncwarp();
+    lo = __shfl_sync(0xFFFFFFFFu, x, 0);
+    hi = __shfl_sync(0xFFFFFFFFu, x, 1);
+    b_first = __shfl_sync(0xFFFFFFFFu, b, 0);
   }
 
   if (warp >= kWarps) {
