@@ -129,7 +129,14 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
     }
   };
   unsigned long long mine = 0;
-  run([&](int, int, uint32_t units) { mine += (unsigned long long)units * a.Hkv; });
+  int b_last = 0, qt_last = 0;
+  uint32_t units_last = 0;
+  run([&](int b, int qt, uint32_t units) {
+    mine += (unsigned long long)units * a.Hkv;
+    b_last = b;
+    qt_last = qt;
+    units_last = units;
+  });
   uint32_t total;
   uint32_t at = exclusive_scan<kThreads>(mine, warp_s, &total, &over);
   if (over) bad = true;
@@ -147,7 +154,7 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
   }
   const uint32_t end = at + (uint32_t)mine;
   if ((lo < at || lo >= end) && (hi < at || hi >= end)) return;
-  run([&](int b, int qt, uint32_t units) {
+  auto cut = [&](int b, int qt, uint32_t units) {
     const uint32_t past = at + units * a.Hkv;
 #pragma unroll 1
     for (int side = 0; side < 2; ++side) {
@@ -164,7 +171,9 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
       }
     }
     at = past;
-  });
+  };
+  if (i1 - i0 == 1) cut(b_last, qt_last, units_last);   // most schedules: nothing to walk again
+  else run(cut);
 }
 
 // Four products of one 64-wide piece of the inner axis, in one statement: every descriptor is in a register
