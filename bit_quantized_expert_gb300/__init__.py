@@ -373,9 +373,9 @@ def alloc_gqa_paged_workspace(pd: GqaPagedDims, device="cuda"):
     return ws
 
 
-# A paged call's checks cost more host time than its launch, so they read each property once and look nothing up
-# that stays: the types that stand for each dtype of the dims (bit patterns included), and torch's functions for the current
-# device and its current stream's handle.
+# A paged call's checks cost more host time than its launch, so they read each property once and look nothing
+# up that stays: the types that stand for each dtype of the dims (bit patterns included), and torch's
+# functions for the current device and its current stream's handle.
 _paged_types = _int32 = _device = _raw_stream = None
 
 
@@ -384,8 +384,8 @@ def _load_paged_types():
     import torch
     bits = (torch.int16, torch.uint16)
     _paged_types, _int32 = ((torch.bfloat16, *bits), (torch.float16, *bits)), torch.int32
-    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # last: _paged_device looks at it
 
 
 def _paged_device() -> int:
@@ -454,7 +454,8 @@ def gqa_paged_append(pd: GqaPagedDims, k, v, slots, q_start, k_cache, v_cache, w
     _check(load_library().gqa_paged_append(
         ctypes.byref(pd), _paged_rows(k, T, H, D, pd.k_stride, dt, dev, "k"), _paged_rows(v, T, H, D, pd.v_stride, dt, dev, "v"),
         _paged_ints(slots, T, dev, "slots"), _paged_ints(q_start, pd.n_seqs + 1, dev, "q_start"), kc, vc,
-        _paged_workspace(workspace, dev), workspace.nbytes, _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_append")
+        _paged_workspace(workspace, dev), workspace.nbytes,
+        _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_append")
 
 
 def gqa_paged_attention(pd: GqaPagedDims, q, k_cache, v_cache, block_table, q_start, kv_len, o, workspace, stream=None):
@@ -466,7 +467,8 @@ def gqa_paged_attention(pd: GqaPagedDims, q, k_cache, v_cache, block_table, q_st
         ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, dt, dev, "q"), kc, vc,
         _paged_ints(block_table, B * pd.max_pages, dev, "block_table"), _paged_ints(q_start, B + 1, dev, "q_start"),
         _paged_ints(kv_len, B, dev, "kv_len"), _paged_rows(o, T, H, D, pd.o_stride, dt, dev, "o"),
-        _paged_workspace(workspace, dev), workspace.nbytes, _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_attention")
+        _paged_workspace(workspace, dev), workspace.nbytes,
+        _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_attention")
 
 
 def gdn_dims(T, H, d_k=128, d_v=128) -> GdnDims:
