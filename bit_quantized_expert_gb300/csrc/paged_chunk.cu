@@ -274,6 +274,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       I16(v, 0)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      I16(v, 0), I16(v, 16)
+      : "memory");
+}
 #undef I16
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -677,20 +684,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_warp(SFULL(t), done & 1, &abort_s, a.err)) return false;
         ++done;
         tc_fence_after();
+        if (!open) {
+          // Masked where it lies, 32 positions at a time, before it is loaded: visible is j <= p, and j > p - window or
+          // j < sinks.  (A short loop: unrolled over the loaded scores the masks were ~6 KB of instructions that
+          // every masked tile fetched anew, 1,000 to 2,600 cycles.)
+          auto seen = [&](int j) {
+            const uint32_t see = low_bits(p + 1 - j);
+            return a.window > 0 ? see & (~low_bits(p - a.window + 1 - j) | low_bits(a.sinks - j)) : see;
+          };
+          uint32_t words = 0;   // those that some row of the warp does not wholly see: few, as its rows are few tokens
+#pragma unroll
+          for (int w = 0; w < 4; ++w) words |= __all_sync(0xFFFFFFFFu, seen(j0 + 32 * w) == 0xFFFFFFFFu) ? 0u : 1u << w;
+#pragma unroll 1
+          while (words != 0) {
+            const int c = 32 * (__ffs(words) - 1);
+            words &= words - 1;
+            const uint32_t see = seen(j0 + c);
+            uint32_t v[32] = {};
+            if (__any_sync(0xFFFFFFFFu, see != 0u)) tmem_ld32(tS + c, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = see & (1u << e) ? v[e] : 0xFF800000u;
+            tmem_st32(tS + c, v);
+          }
+          tmem_wait_st();
+        }
         uint32_t sr[128];
         tmem_ld128(tS, sr);
-        if (!open) {
-          // visible: j <= p, and j > p - window or j < sinks; 32 positions a word
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int j = j0 + 32 * w;
-            uint32_t see = low_bits(p + 1 - j);
-            if (a.window > 0) see &= ~low_bits(p - a.window + 1 - j) | low_bits(a.sinks - j);
-            if (__all_sync(0xFFFFFFFFu, see == 0xFFFFFFFFu)) continue;   // most words: the warp's rows are a few tokens
-#pragma unroll
-            for (int c = 0; c < 32; ++c) sr[32 * w + c] = see & (1u << c) ? sr[32 * w + c] : 0xFF800000u;
-          }
-        }
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 128; c += 8) {
