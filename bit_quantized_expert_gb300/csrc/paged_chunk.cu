@@ -24,8 +24,8 @@
 // 32 a cycle and SM), then P V and the next scores, ~2,800 in all where both row tiles' products are 2,048.
 // At 128 dims tensor memory is full, so the next scores cannot start before P is consumed; at 64 there is room, but an
 // order that used it (two barriers more a tile) was slower (297 against 276 us behind 32768 positions).  Measured (16 query and 2
-// key/value heads of 128): 2048 tokens behind 32768 positions 340 us (1.67 PFLOP/s) in a graph, tensor pipe 75 %
-// active; a prompt of 512 15.4 us; 4096 tokens with a window of 1024 54 us.
+// key/value heads of 128): 2048 tokens behind 32768 positions 341 us (1.66 PFLOP/s) in a graph, tensor pipe 74 %
+// active; a prompt of 512 15.3 us; 4096 tokens with a window of 1024 54 us.
 #include <cmath>
 #include <type_traits>
 

@@ -19,7 +19,7 @@
 //
 // Measured (16 query and 2 key/value heads of 128, in a graph): 64 sequences of 1 to 32768 positions, 139 MB, 28.5 us
 // (4.9 TB/s), of which ~5 us are fixed steps: launch, schedule, first copies, joins; one sequence of 32768, 33.6
-// MB, 10.6 us.  tcgen05 would not help: eight heads fill an eighth of its 64-row tiles, and bytes bound the rest.
+// MB, 10.5 us.  tcgen05 would not help: eight heads fill an eighth of its 64-row tiles, and bytes bound the rest.
 #include <cmath>
 
 #include "paged.cuh"
