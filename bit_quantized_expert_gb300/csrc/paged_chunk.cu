@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Chunk<D>;
   extern __shared__ uint8_t sm_raw[];
   // barriers: stages (full, empty), q (full, empty), per row tile S full, P
-  // full (its first and its second half), O full, O empty; values clean
-  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 2 + 8 + 3];
+  // full (its first and its second half), O full, O empty; values clean (a stage each)
+  __shared__ __align__(8) uint64_t bars[3 * C::kStages + 2 + 8 + 2];
   __shared__ uint32_t warp_s[kThreads / 32];
   __shared__ Share share_s;
   __shared__ uint32_t tmem_slot;
@@ -393,11 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (C::kStages + s); };
   constexpr int kB = 2 * C::kStages;
-  const uint32_t QFULL = bar0 + 8u * kB, QEMPTY = QFULL + 8u, CLEAN = bar0 + 8u * (kB + 12);
+  const uint32_t QFULL = bar0 + 8u * kB, QEMPTY = QFULL + 8u;
   auto SFULL = [&](int t) { return bar0 + 8u * (kB + 2 + t); };
   auto PFULL = [&](int t, int part) { return bar0 + 8u * (kB + 4 + 2 * t + part); };
   auto OFULL = [&](int t) { return bar0 + 8u * (kB + 8 + t); };
   auto OEMPTY = [&](int t) { return bar0 + 8u * (kB + 10 + t); };
+  auto CLEAN = [&](int s) { return bar0 + 8u * (kB + 12 + s); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = (int)blockIdx.x;
   const int tpt = 128 / a.G, tokens = 2 * tpt;
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(FULL(s), 1);
       mbar_init(EMPTY(s), 1 + kScanWarps);
+      mbar_init(CLEAN(s), kScanWarps);
     }
     mbar_init(QFULL, 1);
     mbar_init(QEMPTY, 1);
@@ -416,7 +418,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(OFULL(t), 1);
       mbar_init(OEMPTY(t), 4);
     }
-    mbar_init(CLEAN, kScanWarps);
     abort_s = 0;
     for (int i = 0; i < 4; ++i) bad_s[i] = 0;
     share_s.lo = share_s.hi = 0;
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
     const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV + C::kTileBytes, C::kBoxBytes);
-    uint32_t at = 0, items = 0, cleans = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
+    uint32_t at = 0, items = 0, cleans[2] = {0, 0}, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
     auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait_warp(bar, phase & 1, &abort_s, a.err); };
     // S_t = Q_t K^T with the keys of stage ST
     auto scores = [&](auto t_c, auto st_c) {
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!at_stage(at, [&](auto st_c) {   // the tile's values, the next one's keys
               constexpr int ST = decltype(st_c)::value;
               if (!wait(FULL(ST), at >> 1)) return false;
-              if (closed && !wait(CLEAN, cleans++)) return false;
+              if (closed && !wait(CLEAN(ST), cleans[ST]++)) return false;
               // (the second row tile's result too, where this item has none: bad_s is a short ring)
               if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
               if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
@@ -616,6 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- values of masked tiles: non-finite ones are taken out, two positions a thread.  (Beside the softmax,
     // which would spend 700 cycles of its chain on it, twice: one row tile's product would also wait for the other's.)
     // These warps see every stage, and a stage is free only with their word, so that they keep step with the ring.
+    // Their word that a tile is done goes to its stage's own barrier: a stage is filled again only after both of them and the
+    // product have left it, so neither can speak twice there before the other has spoken, nor twice before the product's
+    // warp has looked.  (One barrier for all tiles would count a quick warp's two tiles as both warps' first.)
     uint32_t at = 0;
     int seg = 0;
     walk([&](int, const SeqRows&, int, const Item& x, int i0, int n, uint32_t) {
@@ -652,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(CLEAN);
+          if (lane == 0) mbar_arrive(CLEAN(st));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(EMPTY(st));

@@ -740,3 +740,32 @@ def test_serving_steps(page, window, sinks, dtype):
     replayed = _serve(page, window, sinks, dtype, graph=True)      # the same step captured once and replayed
     for a, b in zip(eager, replayed):
         assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64)])
+@pytest.mark.parametrize("rows", [(64, 96), (96, 128), (64, 128)], ids=["first", "second", "both"])
+def test_unseen_values_of_one_tile_beside_a_clean_one(rows, dtype, D):
+    """Non-finite values that no row sees, in the leading tile only and there in one of the halves that the chunk form
+    searches side by side, before a masked window tile without any: one half takes much longer than the other, tile after
+    tile.  The results are those over a finite cache, bit by bit, in every one of many repeats."""
+    b = Batch([(c, 40) for c in (700, 1000, 1357, 2000, 431, 900, 1100, 1600)], Hq=16, Hkv=4, D=D, page=128, window=300, sinks=64,
+              dtype=dtype, seed=30)
+    live = np.zeros((b.P, 1, b.page, 1), bool)
+    for s, L in enumerate(b.kv_len):
+        for p in range(L):
+            page, at = _slot(b, s, p)
+            live[page, 0, at] = True
+    b.kc, b.vc = np.where(live, b.kc, 0).astype(np.uint16), np.where(live, b.vc, 0).astype(np.uint16)
+    clean, flags = b.run()
+    assert flags == 0
+    b.check(clean)
+    for s, (c, _) in enumerate(b.seqs):
+        assert 64 <= rows[0] < rows[1] <= c + 1 - 300   # behind the leading positions, before every row's window
+        b.kc[b.table[s, 0], :, rows[0]:rows[1]] = b.vc[b.table[s, 0], :, rows[0]:rows[1]] = NAN[dtype]
+    o, flags = b.run()
+    assert flags == 0 and np.array_equal(o, clean)
+    for i in range(100):
+        b.dev["o"].fill_(7.0)
+        b.attend()
+        assert np.array_equal(P.to_f64(host(b.dev["o"]), dtype), clean), i
+    assert moe.read_error_flags(b.dev["ws"]) == 0
