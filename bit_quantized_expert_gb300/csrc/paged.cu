@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
     const int b = tid * kPlanSeqsPerThread + i;
     nr[i] = fr[i] = 0;
     if (b < a.B) {
-      const PlanSeq s = plan_seq(a, __ldg(a.ctx_len + b), __ldg(a.new_len + b), bad);
+      const PlanSeq s = plan_seq(a, a.ctx_len[b], a.new_len[b], bad);
       nr[i] = s.n;
       fr[i] = s.held - s.old;
     }
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
   // The m-th fresh page, or -1.
   auto fresh_page = [&](long long m) {
     if (m >= n_free) return -1;
-    const int p = __ldg(a.free_pages + (n_free - 1 - m));
+    const int p = a.free_pages[n_free - 1 - m];
     if (p >= 0 && p < a.num_pages) return p;
     bad = true;
     return -1;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
   for (int b = tid + cta * kPlanThreads; b <= a.B; b += ctas * kPlanThreads) {
     a.q_start[b] = (int)min(start_s[b], (long long)a.T);
     if (b < a.B) {
-      const PlanSeq s = plan_seq(a, __ldg(a.ctx_len + b), __ldg(a.new_len + b), bad);
+      const PlanSeq s = plan_seq(a, a.ctx_len[b], a.new_len[b], bad);
       a.kv_len[b] = s.kv;
     }
   }
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
     const long long m0 = base_s[b];
     const int cnt = (int)(base_s[b + 1] - m0);
     if (cnt == 0) continue;
-    const PlanSeq s = plan_seq(a, __ldg(a.ctx_len + b), __ldg(a.new_len + b), bad);
+    const PlanSeq s = plan_seq(a, a.ctx_len[b], a.new_len[b], bad);
     int32_t* row = a.table + (size_t)b * a.max_pages + s.old;
     for (int i = lane; i < cnt; i += 32) row[i] = fresh_page(m0 + i);
   }
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanArgs a)
       else hi = mid - 1;
     }
     const int b = lo;
-    const PlanSeq s = plan_seq(a, __ldg(a.ctx_len + b), __ldg(a.new_len + b), bad);
+    const PlanSeq s = plan_seq(a, a.ctx_len[b], a.new_len[b], bad);
     const long long pos = (long long)s.ctx + (t - start_s[b]);
     if (a.positions != nullptr) a.positions[t] = (int)min(pos, (long long)INT_MAX);
     int page = -1;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   uint16_t* dst = values ? a.vc : a.kc;
   const long long stride = values ? a.v_stride : a.k_stride;
   const Index per = (Index)a.Hkv << a.unit_shift, n = (Index)a.T * per;
-  const int rows = min(max(__ldg(a.q_start + a.B), 0), a.T);
+  const int rows = min(max(a.q_start[a.B], 0), a.T);
   const Index step = (Index)gridDim.x * kAppendThreads;
   for (Index i0 = (Index)blockIdx.x * kAppendThreads + threadIdx.x; i0 < n; i0 += step * kAppendBatch) {
     int t[kAppendBatch], r[kAppendBatch], slot[kAppendBatch];
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
       t[j] = i < n ? (int)(i / per) : a.T;
       r[j] = i < n ? (int)(i - (Index)t[j] * per) : 0;
       if (t[j] < rows) {
-        slot[j] = __ldg(a.slots + t[j]);
-        x[j] = __ldg(reinterpret_cast<const uint4*>(src + t[j] * stride) + r[j]);
+        slot[j] = a.slots[t[j]];
+        x[j] = __ldcg(reinterpret_cast<const uint4*>(src + t[j] * stride) + r[j]);
       }
     }
 #pragma unroll

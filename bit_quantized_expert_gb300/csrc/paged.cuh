@@ -32,6 +32,10 @@ struct PagedArgs {
   float qk_scale;           // log2(e) / sqrt(D): scores in base-2 units
 };
 
+// Everything that an earlier call may have written (tables, lengths, slots, queries, keys and values) is read by ordinary
+// loads, after pdl_wait: a launch waits there for the calls before it, but its CTAs may be resident while those still
+// write, and the read-only path (__ldg) is for data that no one changes while the kernel runs.
+
 // One sequence's rows and length, cut to what the buffers hold.  A sequence whose rows do not lie in
 // the buffers has none.
 struct SeqRows {
@@ -41,7 +45,7 @@ struct SeqRows {
 };
 
 __device__ __forceinline__ SeqRows load_seq(const PagedArgs& a, int b, bool& bad) {
-  const int r0 = __ldg(a.q_start + b), r1 = __ldg(a.q_start + b + 1), len = __ldg(a.kv_len + b);
+  const int r0 = a.q_start[b], r1 = a.q_start[b + 1], len = a.kv_len[b];
   const bool rows_ok = r0 >= 0 && r1 >= r0 && r1 <= a.T;
   SeqRows s;
   s.row0 = rows_ok ? r0 : 0;

@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = i0 + i + (lane >> ppt_shift);
         const int ip = t < x.r.count ? (x.r.tile(t) << ppt_shift) + (lane & (ppt - 1)) : 0;
         need = (lane >> ppt_shift) < n - i && t < x.r.count && ip < a.max_pages && page_needed(a, ip, x.p_lo, x.p_hi);
-        if (need) ahead = __ldg(row + ip);
+        if (need) ahead = row[ip];
       };
       read_ahead(0);
       for (int i = 0; i <= n; ++i, ++at) {

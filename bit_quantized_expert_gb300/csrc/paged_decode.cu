@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = i0 + i + (lane >> ppt_shift);
           const int ip = t < r.count ? ((r.tile(t) * kTN) >> a.page_shift) + (lane & (ppt - 1)) : 0;
           need = (lane >> ppt_shift) < n - i && t < r.count && ip < a.max_pages && page_needed(a, ip, s.p0, s.p0);
-          if (need) ahead = __ldg(row + ip);
+          if (need) ahead = row[ip];
         };
         read_ahead(0);
         for (int i = 0; i < n; ++i) {
@@ -270,15 +270,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     u = min(hi, x.end);
     return x;
   };
-  uint32_t qa[D / 16][2];   // the heads as the 16-row operand: rows r < G
+  // The heads as the 16-row operand.  Rows past the group's heads repeat its first one: every row has sums of its own,
+  // and theirs are not stored, so no value needs a look before the products do.
+  uint32_t qa[D / 16][2];
   auto load_queries = [&](const Segment& x) {
-    const bool live = r < a.G && x.n > 0;
     const uint32_t* qh = reinterpret_cast<const uint32_t*>(
-        a.q + (live ? x.row0 * a.q_stride + (long long)(x.g * a.G + r) * D : 0) + c2);
+        a.q + (x.n > 0 ? x.row0 * a.q_stride + (long long)(x.g * a.G + (r < a.G ? r : 0)) * D : 0) + c2);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      qa[kk][0] = live ? __ldg(qh + 8 * kk) : 0u;
-      qa[kk][1] = live ? __ldg(qh + 8 * kk + 4) : 0u;
+      qa[kk][0] = qh[8 * kk];
+      qa[kk][1] = qh[8 * kk + 4];
     }
   };
 

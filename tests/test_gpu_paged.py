@@ -769,3 +769,67 @@ def test_unseen_values_of_one_tile_beside_a_clean_one(rows, dtype, D):
         b.attend()
         assert np.array_equal(P.to_f64(host(b.dev["o"]), dtype), clean), i
     assert moe.read_error_flags(b.dev["ws"]) == 0
+
+
+def _serve_packed(packed, graph):
+    """Four steps of three sequences, three layers; the int32 arrays one after the other in one buffer (packed), each 4-byte
+    aligned only, or each in its own.  Returns every step's tables and outputs."""
+    B, Hq, H, D, page, T, num, M = 3, 8, 2, 64, 16, 90, 40, 9
+    steps = [[40, 1, 33], [1, 17, 1], [1, 1, 1], [0, 66, 1]]
+    r = np.random.default_rng(31)
+    sizes = dict(ctx=B, q_start=B + 1, new=B, kv_len=B, n_free=1, free=num, slots=T, table=B * M, positions=T)
+    pool = torch.zeros(1 + sum(sizes.values()), dtype=torch.int32, device="cuda")
+    at, x = 1, {}
+    for name, n in sizes.items():
+        x[name] = pool[at:at + n] if packed else torch.zeros(n, dtype=torch.int32, device="cuda")
+        at += n
+    x["table"].fill_(-1)
+    x["free"].copy_(dev(r.permutation(num)))
+    x["n_free"].fill_(num)
+    d = moe.gqa_paged_dims(Hq, H, D, page, num, M, B, T)
+    ws = moe.alloc_gqa_paged_workspace(d)
+    q, k, v = (torch.zeros((3, T, h, D), dtype=torch.bfloat16, device="cuda") for h in (Hq, H, H))
+    o = torch.full_like(q, 7.0)
+    kc, vc = (torch.full((3, num, H, page, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step():
+        moe.gqa_paged_plan(d, x["ctx"], x["new"], x["free"], x["n_free"], x["table"], x["q_start"], x["kv_len"], x["positions"],
+                           x["slots"], x["n_free"], ws)
+        for l in range(3):
+            moe.gqa_paged_append(d, k[l], v[l], x["slots"], x["q_start"], kc[l], vc[l], ws)
+            moe.gqa_paged_attention(d, q[l], kc[l], vc[l], x["table"], x["q_start"], x["kv_len"], o[l], ws)
+
+    if graph:
+        step()                       # nothing new: no page taken, no row written
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+    seen = []
+    for lens in steps:
+        x["new"].copy_(dev(np.array(lens)))
+        for t in (q, k, v):
+            t.copy_(torch.stack([dev(bits(r.standard_normal(t.shape[1:]), "bf16"), "bf16") for _ in range(3)]))
+        o.fill_(7.0)
+        g.replay() if graph else step()
+        assert moe.read_error_flags(ws) == 0
+        seen.append([t.cpu().numpy().copy() for t in x.values()] + [host(o[l]) for l in range(3)])
+        for l in range(3):
+            ref, mag, smax = P.attention(host(q[l]), host(kc[l]), host(vc[l]), x["table"].view(B, M).cpu().numpy(),
+                                         x["q_start"].cpu().numpy(), x["kv_len"].cpu().numpy())
+            tol = 2.0 ** -8 * np.abs(ref) + mag * (2.0 ** -8 + 2.0 ** -19 + 2 * smax[..., None] * (D // 16 + 2) * 2.0 ** -23)
+            rows = sum(lens)
+            got = P.to_f64(host(o[l]), "bf16")
+            assert (np.abs(got - ref)[:rows] <= tol[:rows]).all() and (got[rows:] == 7.0).all()
+        x["ctx"].copy_(x["kv_len"])
+    return seen
+
+
+def test_serving_steps_with_every_table_in_one_buffer():
+    """A table that one call writes shares its memory sectors with those that calls before it have read: the same tables and
+    outputs as with buffers of their own, eager and captured."""
+    want = _serve_packed(False, False)
+    for graph in (False, True):
+        for a, b in zip(_serve_packed(True, graph), want):
+            for x, y in zip(a, b):
+                assert np.array_equal(x, y)

@@ -154,3 +154,13 @@ def test_binding_refuses_host_tensors():
         moe._paged_caches(*[torch.zeros(100, 2, 64, 128, dtype=torch.bfloat16)] * 2, d, 0)
     with pytest.raises(ValueError):
         moe._paged_workspace(torch.zeros(1024, dtype=torch.uint8), 0)
+
+
+def test_kernels_read_tables_coherently():
+    """The paged kernels start while the call before them still runs, and the tables and rows that it writes must not come
+    from the read-only data path, which promises nothing about data that changes while the kernel runs."""
+    for name in ("paged.cuh", "paged.cu", "paged_decode.cu", "paged_chunk.cu"):
+        with open(os.path.join(moe.PKG_DIR, "csrc", name)) as f:
+            text = f.read()
+        for form in ("__ldg(", ".nc.", "__restrict__"):
+            assert form not in text, (name, form)
