@@ -52,6 +52,10 @@ template <bool FP16>
 constexpr float kLazy = FP16 ? 6.f : 14.f;
 template <bool FP16>
 constexpr float kLift = FP16 ? 9.f : 0.f;
+// Base-2 units from which on a row's reference is taken off its scores before they are scaled (far_tiles).  Nearer ones
+// are scaled and shifted in one fma, by a shift that is the scaled reference rounded: off by at most 2^-8 units here, but
+// from 2^24 units on by as much as fp16 numerators have room for (2^16 at the top), from 2^31 on by all of bf16's range.
+constexpr float kFar = 65536.f;
 
 template <int D>
 struct Chunk {
@@ -372,6 +376,106 @@ __device__ __noinline__ void add_non_finite(const PagedArgs& a, const int32_t* t
   }
 }
 
+// A row's scores of the tile at position j0 that the token at position p does not see become -infinity.  Masked where
+// they lie, 32 positions at a time, before they are loaded: visible is j <= p, and j > p - window or j < sinks.  (A short
+// loop: unrolled over the loaded scores the masks were ~6 KB of instructions that every masked tile fetched anew, 1,000
+// to 2,600 cycles.)
+__device__ __forceinline__ void mask_scores(const PagedArgs& a, uint32_t tS, int p, int j0) {
+  auto seen = [&](int j) {
+    const uint32_t see = low_bits(p + 1 - j);
+    return a.window > 0 ? see & (~low_bits(p - a.window + 1 - j) | low_bits(a.sinks - j)) : see;
+  };
+  uint32_t words = 0;   // those that some row of the warp does not wholly see: few, as its rows are few tokens
+#pragma unroll
+  for (int w = 0; w < 4; ++w) words |= __all_sync(0xFFFFFFFFu, seen(j0 + 32 * w) == 0xFFFFFFFFu) ? 0u : 1u << w;
+#pragma unroll 1
+  while (words != 0) {
+    const int c = 32 * (__ffs(words) - 1);
+    words &= words - 1;
+    const uint32_t see = seen(j0 + c);
+    uint32_t v[32] = {};
+    if (__any_sync(0xFFFFFFFFu, see != 0u)) tmem_ld32(tS + c, v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = see & (1u << e) ? v[e] : 0xFF800000u;
+    tmem_st32(tS + c, v);
+  }
+  tmem_wait_st();
+}
+
+// O of this thread's row times `by`.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t tO, float by) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t v[16];
+    tmem_ld16_wait(tO + c, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * by);
+    tmem_st16(tO + c, v);
+  }
+}
+
+// Softmax of tiles i .. n - 1 of a segment (the first one's scores are there, masked) for a warp with a row beyond kFar:
+// numerators 2^((s - m) scale + kLift), 32 scores at a time.  Apart from the other tiles' loop: with the subtraction on a
+// path of its own in there, 2048 tokens at 32768 took 348 us and at 64 dims 277, so 339 and 270.  done < 0: a wait timed out.
+struct FarRow {
+  float m, l;
+  int done;
+};
+template <int D, bool FP16>
+__device__ __noinline__ FarRow far_tiles(const PagedArgs& a, Item x, int i0, int i, int n, int p, uint32_t tS, uint32_t tO,
+                                         uint32_t sfull, int done, uint32_t pfull, volatile int* abort_s, float m, float l) {
+  for (bool waited = true; i < n; ++i, waited = false) {
+    if (!waited) {
+      const int j0 = x.r.tile(i0 + i) * kTN;
+      if (!mbar_wait_warp(sfull, done & 1, abort_s, a.err)) return FarRow{m, l, -1};
+      ++done;
+      tc_fence_after();
+      if (!tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) mask_scores(a, tS, p, j0);
+    }
+    float mx = -INFINITY, alpha = 1.f, sum = 0.f;
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(tS + c, v);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
+    }
+    if (mx > m && (m == -INFINITY || (mx - m) * a.qk_scale > kLazy<FP16>)) {
+      alpha = ex2((m - mx) * a.qk_scale);   // 0 if nothing was seen before
+      m = mx;
+      l *= alpha;
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    __syncwarp();
+    if (i > 0) rescale<D>(tO, alpha);
+    // (numerators of 32 scores take the place of the 16 before them, which have been read)
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      uint32_t v[32], pk[16];
+      tmem_ld32(tS + c, v);
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const float p0 = ex2(fmaf(__uint_as_float(v[e]) - ref, a.qk_scale, kLift<FP16>));
+        const float p1 = ex2(fmaf(__uint_as_float(v[e + 1]) - ref, a.qk_scale, kLift<FP16>));
+        sum += p0 + p1;
+        pk[e / 2] = pack16<FP16>(p0, p1);
+      }
+      tmem_st16(tS + c / 2, pk);
+      if (c == 32 || c == 96) {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(pfull + 8u * (c / 64));
+        __syncwarp();
+      }
+    }
+    l += sum;
+  }
+  return FarRow{m, l, done};
+}
+
 template <int D, bool FP16>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ PagedMaps maps, const PagedArgs a, const ChunkSplit split) {
@@ -688,30 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_warp(SFULL(t), done & 1, &abort_s, a.err)) return false;
         ++done;
         tc_fence_after();
-        if (!open) {
-          // Masked where it lies, 32 positions at a time, before it is loaded: visible is j <= p, and j > p - window or
-          // j < sinks.  (A short loop: unrolled over the loaded scores the masks were ~6 KB of instructions that
-          // every masked tile fetched anew, 1,000 to 2,600 cycles.)
-          auto seen = [&](int j) {
-            const uint32_t see = low_bits(p + 1 - j);
-            return a.window > 0 ? see & (~low_bits(p - a.window + 1 - j) | low_bits(a.sinks - j)) : see;
-          };
-          uint32_t words = 0;   // those that some row of the warp does not wholly see: few, as its rows are few tokens
-#pragma unroll
-          for (int w = 0; w < 4; ++w) words |= __all_sync(0xFFFFFFFFu, seen(j0 + 32 * w) == 0xFFFFFFFFu) ? 0u : 1u << w;
-#pragma unroll 1
-          while (words != 0) {
-            const int c = 32 * (__ffs(words) - 1);
-            words &= words - 1;
-            const uint32_t see = seen(j0 + c);
-            uint32_t v[32] = {};
-            if (__any_sync(0xFFFFFFFFu, see != 0u)) tmem_ld32(tS + c, v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = see & (1u << e) ? v[e] : 0xFF800000u;
-            tmem_st32(tS + c, v);
-          }
-          tmem_wait_st();
-        }
+        if (!open) mask_scores(a, tS, p, j0);
         uint32_t sr[128];
         tmem_ld128(tS, sr);
         float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
@@ -726,6 +807,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The reference moves if the new maximum is well above it (or is the first).
         const bool move = mx > m && (m == -INFINITY || (mx - m) * a.qk_scale > kLazy<FP16>);
         if (__any_sync(0xFFFFFFFFu, move)) {
+          if (__any_sync(0xFFFFFFFFu, move && p >= 0 && fabsf(mx) * a.qk_scale > kFar)) {   // the tiles from here on in another way
+            const FarRow row = far_tiles<D, FP16>(a, x, i0, i, n, p, tS, tO, SFULL(t), done, PFULL(t, 0), &abort_s, m, l);
+            if (row.done < 0) return false;
+            m = row.m;
+            l = row.l;
+            done = row.done;
+            negm = kLift<FP16> - m * a.qk_scale;
+            break;
+          }
           float alpha = 1.f;
           if (move) {
             const float nn = kLift<FP16> - mx * a.qk_scale;
@@ -735,16 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l *= alpha;
           }
           __syncwarp();
-          if (i > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t v[16];
-              tmem_ld16_wait(tO + c, v);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tmem_st16(tO + c, v);
-            }
-          }
+          if (i > 0) rescale<D>(tO, alpha);
         }
         const uint64_t scale2 = pair2(a.qk_scale, a.qk_scale), negm2 = pair2(negm, negm);
         uint64_t sum0 = 0, sum1 = 0;   // two fp32 sums each

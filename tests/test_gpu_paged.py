@@ -833,3 +833,69 @@ def test_serving_steps_with_every_table_in_one_buffer():
         for a, b in zip(_serve_packed(True, graph), want):
             for x, y in zip(a, b):
                 assert np.array_equal(x, y)
+
+
+# ---------------------------------------------------------------- scores of any size
+def _far_scores(dtype, scale, seqs, D=128, Hq=4, Hkv=2, window=0):
+    """Every score is one exact product of two 16-bit values, scale^2 times 1, 0.5, -0.5 or -1 (its sign and size by
+    position), so that the softmax is over equal scores and no rounding of a score can move it."""
+    b = Batch(seqs, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, seed=32, window=window)
+    size = bits(np.array([scale]), dtype)[0]
+    b.q[:] = 0
+    b.q[:, :, 3] = size
+    levels = bits(scale * np.array(LEVELS[window % 3]), dtype)
+    for s, L in enumerate(b.kv_len):
+        for i in range(-(-int(L) // b.page)):
+            p = i * b.page + np.arange(b.page)
+            b.kc[b.table[s, i]] = 0
+            b.kc[b.table[s, i], :, :, 3] = levels[p * 7 // 3 % len(levels)]
+    return b
+
+
+LEVELS = [(-1.0,), (-0.5, -1.0), (1.0, 0.5, -1.0)]
+
+
+def _check_far(b, label):
+    """No error of a score (they are exact, and equal where they count): the rounding of the output, of the numerators, and a
+    few dozen steps of 2^-24."""
+    o, flags = b.run()
+    assert flags == 0, flags
+    ref, mag, _ = b.oracle()
+    u, single = U[b.dtype], b.max_new == 1
+    tol = u * np.abs(ref) + mag * ((2.0 ** -17 if single else u) + 2.0 ** -19)
+    if b.dtype == "fp16":
+        tol = tol + 2.0 ** -25 + int(b.kv_len.max()) * 6.0 * (2.0 ** -40 if single else 2.0 ** -34)
+    ratio = (np.abs(o - ref) / tol).max()
+    print(f"{label}: max |o - ref| / bar = {ratio:.3f}")
+    assert ratio <= 1.0
+
+
+# q . k / sqrt(D) from 2^20 to the type's end, where the rounding of a score in units of its own size is more than the
+# range of the softmax's numerators
+FAR = [("bf16", 2.0 ** 12), ("bf16", 2.0 ** 17), ("bf16", 3e4), ("bf16", 1e9), ("bf16", 1.3e16), ("bf16", 7e18),
+       ("fp16", 2.0 ** 12), ("fp16", 2.0 ** 13), ("fp16", 2.0 ** 14), ("fp16", 5e4), ("fp16", 65504.0)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype,scale", FAR)
+def test_chunks_of_far_scores(dtype, scale, D):
+    for window in (300, 301, 302):
+        _check_far(_far_scores(dtype, scale, [(0, 1), (0, 5), (300, 30), (700, 3)], D=D, window=window), f"{dtype} {scale} {window}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("new,ctx", [(1, 300), (1, 20000), (20, 300), (3, 20000)])
+def test_far_scores_close_together(new, ctx, dtype):
+    """Scores of 2^20 less a whole number that falls along the cache: the maximum moves again and again, and the weights
+    reach over many positions.  (The bar is the usual one: an ulp of a score is what limits it.)"""
+    b = Batch([(ctx, new), (40, new), (0, new)], Hq=4, Hkv=2, dtype=dtype, seed=36)
+    b.q[:] = 0
+    b.q[:, :, 0], b.q[:, :, 70] = bits(np.array([1024.0]), dtype)[0], bits(np.array([1.0]), dtype)[0]
+    for s, L in enumerate(b.kv_len):
+        for i in range(-(-int(L) // b.page)):
+            page = b.table[s, i]
+            p = i * b.page + np.arange(b.page)
+            b.kc[page] = 0
+            b.kc[page, :, :, 0] = bits(np.array([1024.0]), dtype)[0]
+            b.kc[page, :, :, 70] = bits(np.maximum(p * 256.0 // int(L) - 256.0, -256.0), dtype)
+    _ok(b, f"{dtype} {new} new behind {ctx}")
