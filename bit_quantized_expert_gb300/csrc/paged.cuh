@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <cfloat>
 
 #include "../../include/gqa_paged.h"
 #include "common.cuh"
@@ -96,6 +97,10 @@ __device__ __forceinline__ bool page_needed(const PagedArgs& a, int ip, int p_lo
   const int j0 = ip << a.page_shift, j1 = j0 + (1 << a.page_shift) - 1;
   return j0 <= p_hi && (a.window == 0 || j1 > p_lo - a.window || j0 < a.sinks);
 }
+
+// The maximum of no scores: the lowest finite value, since a visible score may be any finite one, and since two of it
+// differ by 0 (of infinities the difference, a weight's exponent, is none).  The sum beside it is 0.
+constexpr float kUnseen = -FLT_MAX;
 
 // Whether every row at positions p_lo .. p_hi sees every position j0 .. j0 + TN - 1.
 template <int TN>

@@ -943,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole) {
         if (live) {
           float* stats = part + D * kItemRows - 3 * (t * 128 + r);
-          stats[0] = m == -INFINITY ? -1e30f : -negm;
+          stats[0] = m == -INFINITY ? kUnseen : -negm;
           stats[kItemRows] = l;
         }
         if (i0 + n < x.r.count && tid == 0) {   // the item goes on: who begins it, and who ends it
@@ -1012,7 +1012,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const Paged
   float M, L;
   auto sum_parts = [&](auto n_c, auto k_c, float* acc, int c0, int S, int d, int slot) {
     constexpr int N = decltype(n_c)::value, K = decltype(k_c)::value;
-    M = -1e30f;
+    M = kUnseen;
     L = 0.f;
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = 0.f;
@@ -1031,7 +1031,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const Paged
 #pragma unroll
       for (int k = 1; k < K; ++k)
         if (c + k * S > rec.until) {
-          m[k] = -1e30f;
+          m[k] = kUnseen;
           l[k] = 0.f;
 #pragma unroll
           for (int e = 0; e < N / 4; ++e) o[k][e] = make_float4(0.f, 0.f, 0.f, 0.f);

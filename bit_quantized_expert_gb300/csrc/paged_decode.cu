@@ -34,7 +34,6 @@ constexpr int kThreads = (kWarps + kCopyWarps) * 32;
 constexpr int kRows = 8;                       // query heads per key/value head, at most
 constexpr int kItemUnits = 3;                  // what an item costs beside its tiles, in tiles (~3500 cycles)
 constexpr int kSlack = 1;                      // tiles that a cut moves to reach an item's end
-constexpr float kNegBig = -1e30f;              // running max before any position is seen
 // Base-2 units by which numerators stand above e^(s - max): fp16 keeps 2^-25 at best, so they use its range
 // from 2^15 down, or a long cache of small ones would be summed as nothing.  (All parts of an item are
 // scaled alike, so the joins do not see it.)  bf16 has fp32's range.
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float o[D / 8][4];
 #pragma unroll
     for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m_run = kNegBig, l_run = 0.f;
+    float m_run = kUnseen, l_run = 0.f;
     for (int i = (it ^ wg) & 1; i < x.n; i += 2) {   // tile it + i of the share goes to group (it + i) & 1
       const int st = (it + i) % C::kStages;
       if (mbar_wait_warp(smem_u32(&full[st]), ((it + i) / C::kStages) & 1, &abort_s, a.err)) {
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Page
   if (rec.until < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int parts = rec.until - first + 1;
-  float m = kNegBig, l = 0.f, acc[E];
+  float m = kUnseen, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int i0 = warp; i0 < parts; i0 += kJoinWarps * kJoinBatch) {
@@ -456,7 +455,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Page
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i) {
       const int c = i0 + i * kJoinWarps;
-      mb[i] = kNegBig;
+      mb[i] = kUnseen;
       lb[i] = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) ob[i][e] = 0.f;

@@ -899,3 +899,13 @@ def test_far_scores_close_together(new, ctx, dtype):
             b.kc[page, :, :, 0] = bits(np.array([1024.0]), dtype)[0]
             b.kc[page, :, :, 70] = bits(np.maximum(p * 256.0 // int(L) - 256.0, -256.0), dtype)
     _ok(b, f"{dtype} {new} new behind {ctx}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [1, 3])
+@pytest.mark.parametrize("scale", [1e9, 1.3e16, 7e18])
+def test_far_scores_of_split_rows(scale, new, D):
+    """A long sequence cut over many SMs, and short ones; all scores far below zero, and mixed ones."""
+    for window in (0, 30001, 30002):
+        b = _far_scores("bf16", scale, [(20000, new), (0, new), (60, new)], D=D, Hq=2, Hkv=1, window=window)
+        _check_far(b, f"{scale} {new} {window}")
