@@ -323,12 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_new = fmaxf(m_run, mx);
         const float alpha = ex2(m_run - m_new);
         m_run = m_new;
-        const float m_ref = m_new - kLift<FP16>;
-        float p[2][2];
+        float p[2][2];   // (lifted after the difference: a maximum of 2^24 or more less the lift would be rounded by up to 16)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) p[j][e] = ex2(s2[j][e] - m_ref);
+          for (int e = 0; e < 2; ++e) p[j][e] = ex2((s2[j][e] - m_new) + kLift<FP16>);
         l_run = l_run * alpha + ((p[0][0] + p[0][1]) + (p[1][0] + p[1][1]));
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) {

@@ -909,3 +909,10 @@ def test_far_scores_of_split_rows(scale, new, D):
     for window in (0, 30001, 30002):
         b = _far_scores("bf16", scale, [(20000, new), (0, new), (60, new)], D=D, Hq=2, Hkv=1, window=window)
         _check_far(b, f"{scale} {new} {window}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype,scale", FAR)
+def test_single_tokens_of_far_scores(dtype, scale, D):
+    for window in (300, 301, 302):
+        _check_far(_far_scores(dtype, scale, [(0, 1), (5, 1), (300, 1), (7000, 1)], D=D, window=window), f"{dtype} {scale} {window}")
