@@ -352,10 +352,14 @@ def gqa_paged_dims(n_heads, n_kv_heads, head_dim, page_size, num_pages, max_page
     """Shapes of the paged calls (include/gqa_paged.h).  max_new: bound on the new tokens of one sequence
     (0: n_tokens; 1: the single-token form of the attention).  dtype: "bf16" or "fp16".  Strides in
     elements, 0 for packed; cache_strides: (page, head, row) of both caches, as .stride()[:3] of a cache
-    indexed [page, head, offset, D]."""
-    return GqaPagedDims(*(int(x) for x in (
-        n_heads, n_kv_heads, head_dim, page_size, num_pages, max_pages, n_seqs, n_tokens, max_new, window, sinks,
-        _PAGED_DTYPES[dtype], q_stride, o_stride, k_stride, v_stride, *cache_strides)))
+    indexed [page, head, offset, D].  ValueError for a number that its field does not hold (a field of the
+    structure would keep its low bits: a window of 2^32 + 64 would be one of 64)."""
+    sizes = [int(x) for x in (n_heads, n_kv_heads, head_dim, page_size, num_pages, max_pages, n_seqs, n_tokens, max_new,
+                              window, sinks, _PAGED_DTYPES[dtype])]
+    strides = [int(x) for x in (q_stride, o_stride, k_stride, v_stride, *cache_strides)]
+    if min(sizes) < -2**31 or max(sizes) >= 2**31 or min(strides) < -2**63 or max(strides) >= 2**63:
+        raise ValueError("gqa_paged_dims: sizes are 32-bit, strides 64-bit integers")
+    return GqaPagedDims(*sizes, *strides)
 
 
 def gqa_paged_workspace_bytes(pd: GqaPagedDims) -> int:

@@ -164,3 +164,12 @@ def test_kernels_read_tables_coherently():
             text = f.read()
         for form in ("__ldg(", ".nc.", "__restrict__"):
             assert form not in text, (name, form)
+
+
+@pytest.mark.parametrize("bad", [dict(window=2**32 + 64), dict(window=2**31), dict(sinks=2**32), dict(n_tokens=2**32 + 37),
+                                 dict(max_new=2**32 + 1), dict(page_size=-2**31 - 1), dict(q_stride=2**64 + 2048),
+                                 dict(cache_strides=(2**64 + 16384, 8192, 128))])
+def test_dims_that_do_not_fit_their_fields(bad):
+    """A number past its field's range is refused, not taken modulo 2^32 or 2^64."""
+    with pytest.raises(ValueError):
+        moe.gqa_paged_dims(**{**GOOD, **bad})
