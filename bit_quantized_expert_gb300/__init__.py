@@ -408,6 +408,14 @@ def _paged_ints(t, n: int, dev: int, name: str) -> int:
     raise ValueError(f"{name}: expected a contiguous int32 tensor of at least {n} entries on device {dev}")
 
 
+def _paged_table(t, rows: int, width: int, dev: int) -> int:
+    """Pointer of a block table: a tensor of at least `rows` rows of exactly `width` entries, or its entries in one
+    dimension (a wider row would be read as if the next one began inside it)."""
+    if t.dim() > 1 and t.shape[1:] != (width,):
+        raise ValueError(f"block_table: expected rows of {width} entries, the dims' max_pages, not {tuple(t.shape)}")
+    return _paged_ints(t, rows * width, dev, "block_table")
+
+
 def _paged_rows(t, rows: int, heads: int, D: int, stride: int, dtype: int, dev: int, name: str) -> int:
     """Pointer of a [rows, heads, D] tensor whose token stride is that of the dims (0: packed)."""
     st = t.stride()
@@ -445,7 +453,7 @@ def gqa_paged_plan(pd: GqaPagedDims, ctx_len, new_len, free_pages, n_free, block
     _check(load_library().gqa_paged_plan(
         ctypes.byref(pd), _paged_ints(ctx_len, B, dev, "ctx_len"), _paged_ints(new_len, B, dev, "new_len"),
         _paged_ints(free_pages, 0, dev, "free_pages"), free_pages.numel(), _paged_ints(n_free, 1, dev, "n_free"),
-        _paged_ints(block_table, B * pd.max_pages, dev, "block_table"), _paged_ints(q_start, B + 1, dev, "q_start"),
+        _paged_table(block_table, B, pd.max_pages, dev), _paged_ints(q_start, B + 1, dev, "q_start"),
         _paged_ints(kv_len, B, dev, "kv_len"), None if positions is None else _paged_ints(positions, T, dev, "positions"),
         _paged_ints(slots, T, dev, "slots"), _paged_ints(n_free_out, 1, dev, "n_free_out"), _paged_workspace(workspace, dev),
         workspace.nbytes, _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_plan")
@@ -469,7 +477,7 @@ def gqa_paged_attention(pd: GqaPagedDims, q, k_cache, v_cache, block_table, q_st
     kc, vc = _paged_caches(k_cache, v_cache, pd, dev)
     _check(load_library().gqa_paged_attention(
         ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, dt, dev, "q"), kc, vc,
-        _paged_ints(block_table, B * pd.max_pages, dev, "block_table"), _paged_ints(q_start, B + 1, dev, "q_start"),
+        _paged_table(block_table, B, pd.max_pages, dev), _paged_ints(q_start, B + 1, dev, "q_start"),
         _paged_ints(kv_len, B, dev, "kv_len"), _paged_rows(o, T, H, D, pd.o_stride, dt, dev, "o"),
         _paged_workspace(workspace, dev), workspace.nbytes,
         _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_attention")

@@ -173,3 +173,18 @@ def test_dims_that_do_not_fit_their_fields(bad):
     """A number past its field's range is refused, not taken modulo 2^32 or 2^64."""
     with pytest.raises(ValueError):
         moe.gqa_paged_dims(**{**GOOD, **bad})
+
+
+def test_binding_refuses_tables_of_other_widths():
+    """A block table whose rows are not max_pages wide would be read across its rows."""
+    import torch
+    moe._load_paged_types()
+    host = -1   # what a host tensor gives as its device
+    table = torch.zeros(4, 20, dtype=torch.int32)
+    assert moe._paged_table(table, 4, 20, host) == table.data_ptr()
+    assert moe._paged_table(table, 3, 20, host) == table.data_ptr()
+    assert moe._paged_table(table.view(-1), 4, 20, host) == table.data_ptr()
+    for bad in (torch.zeros(4, 32, dtype=torch.int32), torch.zeros(8, 10, dtype=torch.int32), table[:3], table.t(),
+                torch.zeros(2, 2, 20, dtype=torch.int32), table.long(), torch.zeros(79, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            moe._paged_table(bad, 4, 20, host)
