@@ -916,3 +916,70 @@ def test_far_scores_of_split_rows(scale, new, D):
 def test_single_tokens_of_far_scores(dtype, scale, D):
     for window in (300, 301, 302):
         _check_far(_far_scores(dtype, scale, [(0, 1), (5, 1), (300, 1), (7000, 1)], D=D, window=window), f"{dtype} {scale} {window}")
+
+
+# ---------------------------------------------------------------- windows whose items are cut
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("seqs,window,sinks,Hq,Hkv,D,page", [
+    ([(20000, 9)], 6000, 0, 6, 2, 128, 64), ([(20000, 9)], 6000, 4, 6, 2, 64, 16), ([(23000, 3)], 6000, 300, 5, 1, 128, 128),
+    ([(9000, 40), (30, 2), (15000, 60)], 3000, 130, 3, 1, 64, 32), ([(3000, 1000)], 1024, 4, 12, 4, 128, 64),
+    ([(1500, 700), (2100, 300)], 1024, 300, 12, 4, 64, 16), ([(20000, 8)], 17000, 5, 8, 1, 128, 64)])
+def test_window_chunks_cut_over_many_sms(seqs, window, sinks, Hq, Hkv, D, page, dtype):
+    """Items with a gap between the leading positions and the window, cut into two or three parts (the chunks of hundreds) and
+    into 23 to 131: the gap inside a part and between two.  Pages in the gap are gone from the table.  At most some 80 rows
+    are checked, spread over the sequences."""
+    b = Batch(seqs, Hq=Hq, Hkv=Hkv, D=D, page=page, dtype=dtype, window=window, sinks=sinks, seed=33)
+    for s, (c, _) in enumerate(seqs):
+        b.table[s, -(-sinks // page):max(c - window + 1, 0) // page] = 1 << 29
+    o, flags = b.run()
+    assert flags == 0
+    table, rows = np.where(b.table >= b.P, 0, b.table), np.arange(0, b.rows, max(1, b.rows // 80))
+    ref = [np.zeros(b.q.shape), np.zeros(b.q.shape), np.zeros(b.q.shape[:2])]
+    for t in rows:
+        s = int(np.searchsorted(b.q_start, t, "right")) - 1
+        p = int(b.kv_len[s] - (b.q_start[s + 1] - t))
+        one = P.attention(b.q[t:t + 1], b.kc, b.vc, table[s:s + 1], [0, 1], [p + 1], window, sinks, dtype)
+        for x, y in zip(ref, one):
+            x[t] = y[0]
+    b.check(o, ref, rows, label=f"{dtype} window {window} sinks {sinks}")
+
+
+@pytest.mark.parametrize("value", [0x7F80, 0x7FC0], ids=["inf", "nan"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_non_finite_values_in_the_last_part_of_a_cut_item(D, value):
+    """A value of one of the chunk's own positions, in the masked tiles that end an item cut over many SMs, and one at the
+    window's edge that only the first rows see."""
+    n, window = 30, 6000
+    b = Batch([(20000, n)], Hq=6, Hkv=2, D=D, page=64, window=window, sinks=4, seed=34)
+    clean = b.oracle()
+    own, edge = _slot(b, 0, 20000 + 12), _slot(b, 0, 20000 - window + 1 + 7)
+    b.vc[own[0], 1, own[1], 9] = value
+    b.vc[edge[0], 0, edge[1], 40] = value
+    o, flags = b.run()
+    assert flags == moe.ERR_NON_FINITE
+    hit = np.zeros(o.shape, bool)
+    hit[12:, 3:, 9] = True        # rows from the position on
+    hit[:8, :3, 40] = True        # rows whose window still holds it
+    assert not np.isfinite(o[hit]).any()
+    b.check(np.where(hit, 0.0, o), tuple(np.where(hit, 0.0, x) if x.ndim == 3 else x for x in clean))
+
+
+# ---------------------------------------------------------------- fp16, to what the contract states
+@pytest.mark.parametrize("new", [1, 30])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sinks,q_scale", [(0, 0, 1.0), (0, 0, 0.01), (500, 4, 1.0), (0, 0, 6.0)])
+def test_fp16_numerators_as_stated(new, D, window, sinks, q_scale):
+    """The bar above with what fp16 numerators are stated to lose: 2^-40 of the row's largest where single tokens keep the
+    rounding's remainder, 2^-34 in chunks (and 2^-25 where the output itself is subnormal)."""
+    b = Batch([(0, new), (3, new), (700, new), (2050, new), (5000, new)], Hq=8, D=D, dtype="fp16", window=window, sinks=sinks,
+              q_scale=q_scale, page=32, seed=35)
+    o, flags = b.run()
+    assert flags == 0
+    ref, mag, smax = b.oracle()
+    vmax = np.abs(np.nan_to_num(P.to_f64(b.vc, "fp16"), nan=0.0)).max()
+    tol = U["fp16"] * np.abs(ref) + mag * ((2.0 ** -22 if new == 1 else 2.0 ** -11) + 2.0 ** -19 +
+                                          2 * smax[..., None] * (D // 16 + 2) * 2.0 ** -23)
+    tol = tol + 2.0 ** -25 + int(b.kv_len.max()) * vmax * (2.0 ** -40 if new == 1 else 2.0 ** -34)
+    ratio = (np.abs(o - ref) / tol).max()
+    print(f"fp16, {new} new, D {D}: max |o - ref| / bar = {ratio:.3f}")
+    assert ratio <= 1.0
