@@ -232,6 +232,13 @@ struct PagedMaps {
   CUtensorMap q;      // chunk form: {D, Hq, T}, box {64, G, tokens of a tile}
 };
 
+// 2^x.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Two fp32 values rounded to a pair of the 16-bit type (lo in the low half), and back.
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {

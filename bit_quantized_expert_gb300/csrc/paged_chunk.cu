@@ -288,12 +288,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 #undef I16
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void ld_shared4(uint32_t at, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(at) : "memory");
 }
@@ -575,200 +569,200 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == kSoftmaxWarps) {
-    // ---- copies
-    const int ppt_shift = 7 - a.page_shift, ppt = 1 << ppt_shift, box_rows = 1 << a.page_shift;   // pages of a tile
-    const int batch = 32 >> ppt_shift;                              // tiles whose page numbers the lanes hold
-    int at = 0, items = 0;   // ring stages and segments so far
-    bad = false;
-    walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
-      const bool two = x.n > tpt;
-      const int32_t* row = a.table + (size_t)b * a.max_pages;
-      const int sub = lane / C::kBoxes, box = lane % C::kBoxes;   // one copy a lane: (page of the tile, 64-dim box)
-      // Page numbers of a batch of tiles, one a lane, read one batch ahead; a page that no row needs is not
-      // read, and takes, like a bad one, a number out of the map's range, which reads as zeros.
-      int pg = 0, ahead = 0;
-      bool need = false;
-      auto read_ahead = [&](int i) {
-        const int t = i0 + i + (lane >> ppt_shift);
-        const int ip = t < x.r.count ? (x.r.tile(t) << ppt_shift) + (lane & (ppt - 1)) : 0;
-        need = (lane >> ppt_shift) < n - i && t < x.r.count && ip < a.max_pages && page_needed(a, ip, x.p_lo, x.p_hi);
-        if (need) ahead = row[ip];
-      };
-      read_ahead(0);
-      for (int i = 0; i <= n; ++i, ++at) {
-        // stage `at`: values of tile i - 1 (whose pages are at hand), then keys of tile i
-        const int st = at & 1;
-        if (at >= C::kStages && !mbar_wait_warp(EMPTY(st), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(FULL(st), i == 0 || i == n ? C::kTileBytes : 2 * C::kTileBytes);
-        __syncwarp();
-        auto copy = [&](const CUtensorMap* map, int half, int in) {
-          const int p = __shfl_sync(0xFFFFFFFFu, pg, (in * ppt + sub) & 31);
-          if (lane < ppt * C::kBoxes)
-            tma_load_4d(sKV + st * C::kStageBytes + half * C::kTileBytes + box * C::kBoxBytes + sub * box_rows * 128, map,
-                        FULL(st), box * 64, 0, g, p);
-          __syncwarp();
+      // ---- copies
+      const int ppt_shift = 7 - a.page_shift, ppt = 1 << ppt_shift, box_rows = 1 << a.page_shift;   // pages of a tile
+      const int batch = 32 >> ppt_shift;                              // tiles whose page numbers the lanes hold
+      int at = 0, items = 0;   // ring stages and segments so far
+      bad = false;
+      walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
+        const bool two = x.n > tpt;
+        const int32_t* row = a.table + (size_t)b * a.max_pages;
+        const int sub = lane / C::kBoxes, box = lane % C::kBoxes;   // one copy a lane: (page of the tile, 64-dim box)
+        // Page numbers of a batch of tiles, one a lane, read one batch ahead; a page that no row needs is not
+        // read, and takes, like a bad one, a number out of the map's range, which reads as zeros.
+        int pg = 0, ahead = 0;
+        bool need = false;
+        auto read_ahead = [&](int i) {
+          const int t = i0 + i + (lane >> ppt_shift);
+          const int ip = t < x.r.count ? (x.r.tile(t) << ppt_shift) + (lane & (ppt - 1)) : 0;
+          need = (lane >> ppt_shift) < n - i && t < x.r.count && ip < a.max_pages && page_needed(a, ip, x.p_lo, x.p_hi);
+          if (need) ahead = row[ip];
         };
-        if (i > 0) copy(&maps.v, 1, (i - 1) & (batch - 1));
-        if (i < n) {
-          const int in = i & (batch - 1);
-          if (in == 0) {
-            const bool ok = ahead >= 0 && ahead < a.num_pages;
-            pg = need && ok ? ahead : a.num_pages;
-            bad |= need && !ok;
-            read_ahead(i + batch);
-          }
-          copy(&maps.k, 0, in);
-        }
-        if (i == 0) {   // the queries, once the segment before has done its last scores
-          if (items > 0 && !mbar_wait_warp(QEMPTY, (items - 1) & 1, &abort_s, a.err)) return false;
-          ++items;
-          if (lane == 0) {
-            const uint32_t bytes = (uint32_t)(64 * 2 * a.G * tpt);
-            mbar_arrive_expect_tx(QFULL, bytes * C::kBoxes * (two ? 2 : 1));
-            for (int t = 0; t < (two ? 2 : 1); ++t)
-              for (int bx = 0; bx < C::kBoxes; ++bx)
-                tma_load_3d(sQ + t * C::kTileBytes + bx * C::kBoxBytes, &maps.q, QFULL, bx * 64, g * a.G,
-                            s.row0 + x.t0 + t * tpt);
-          }
+        read_ahead(0);
+        for (int i = 0; i <= n; ++i, ++at) {
+          // stage `at`: values of tile i - 1 (whose pages are at hand), then keys of tile i
+          const int st = at & 1;
+          if (at >= C::kStages && !mbar_wait_warp(EMPTY(st), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(FULL(st), i == 0 || i == n ? C::kTileBytes : 2 * C::kTileBytes);
           __syncwarp();
+          auto copy = [&](const CUtensorMap* map, int half, int in) {
+            const int p = __shfl_sync(0xFFFFFFFFu, pg, (in * ppt + sub) & 31);
+            if (lane < ppt * C::kBoxes)
+              tma_load_4d(sKV + st * C::kStageBytes + half * C::kTileBytes + box * C::kBoxBytes + sub * box_rows * 128, map,
+                          FULL(st), box * 64, 0, g, p);
+            __syncwarp();
+          };
+          if (i > 0) copy(&maps.v, 1, (i - 1) & (batch - 1));
+          if (i < n) {
+            const int in = i & (batch - 1);
+            if (in == 0) {
+              const bool ok = ahead >= 0 && ahead < a.num_pages;
+              pg = need && ok ? ahead : a.num_pages;
+              bad |= need && !ok;
+              read_ahead(i + batch);
+            }
+            copy(&maps.k, 0, in);
+          }
+          if (i == 0) {   // the queries, once the segment before has done its last scores
+            if (items > 0 && !mbar_wait_warp(QEMPTY, (items - 1) & 1, &abort_s, a.err)) return false;
+            ++items;
+            if (lane == 0) {
+              const uint32_t bytes = (uint32_t)(64 * 2 * a.G * tpt);
+              mbar_arrive_expect_tx(QFULL, bytes * C::kBoxes * (two ? 2 : 1));
+              for (int t = 0; t < (two ? 2 : 1); ++t)
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                  tma_load_3d(sQ + t * C::kTileBytes + bx * C::kBoxBytes, &maps.q, QFULL, bx * 64, g * a.G,
+                              s.row0 + x.t0 + t * tpt);
+            }
+            __syncwarp();
+          }
         }
-      }
-      return true;
-    });
-    if (bad) raise_flag(a.err, kErrBadPages);
+        return true;
+      });
+      if (bad) raise_flag(a.err, kErrBadPages);
     } else if (warp == kSoftmaxWarps + 1) {
-    // ---- tensor-core instructions.  The whole warp takes every step, one elected lane issues (by predicate), and
-    // row tile and ring stage are constants of the unrolled code: descriptors and addresses then sit in uniform
-    // registers, and a product costs one issue slot beside the two softmax warps of this scheduler.  (A
-    // single lane's walk with computed descriptors took twice as long per product under that load.)
-    const uint32_t go = elect_one() ? 1u : 0u;
-    constexpr uint32_t fmt = FP16 ? 0u : ((1u << 7) | (1u << 10));
-    constexpr uint32_t id_s = (1u << 4) | fmt | ((kTN >> 3) << 17) | ((128u >> 4) << 24);
-    constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
-    constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
-    const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV + C::kTileBytes, C::kBoxBytes);
-    uint32_t at = 0, items = 0, cleans[2] = {0, 0}, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
-    auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait_warp(bar, phase & 1, &abort_s, a.err); };
-    // S_t = Q_t K^T with the keys of stage ST
-    auto scores = [&](auto t_c, auto st_c) {
-      constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
-#pragma unroll
-      for (int box = 0; box < C::kBoxes; ++box)
-        tc_mma4_ss(go, t * 128, dq + (t * kTileUnits + box * kBoxUnits), dk + (ST * 2 * kTileUnits + box * kBoxUnits), id_s,
-                   box != 0);
-      tc_commit_if(go, SFULL(t));
-    };
-    // O_t (+)= P_t V, P in two halves, with the values of stage ST; then the next tile's scores
-    auto turn = [&](auto t_c, auto st_c, uint32_t done, bool first, bool more) {
-      constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
-      const uint64_t v = dv + ST * 2 * kTileUnits;
-      if (!wait(PFULL(t, 0), done)) return false;
-      tc_fence_after();
-      tc_mma4_ts(go, kTmemO + t * 128, t * 128, v, id_o, !first);
-      if (!wait(PFULL(t, 1), done)) return false;
-      tc_fence_after();
-      tc_mma4_ts(go, kTmemO + t * 128, t * 128 + 32, v + (8192u >> 4), id_o, 1u);
-      if (more) scores(t_c, st_c);
-      else tc_commit_if(go, OFULL(t));
-      return true;
-    };
-    using Zero = std::integral_constant<int, 0>;
-    using One = std::integral_constant<int, 1>;
-    // body(stage as a constant) for the stage of a tile
-    static_assert(C::kStages == 2, "a tile's stage is its parity");
-    auto at_stage = [&](uint32_t tile, auto&& body) { return tile & 1 ? body(One{}) : body(Zero{}); };
-    walk([&](int, const SeqRows&, int, const Item& x, int i0, int n_any, uint32_t) {
-      const int n = __shfl_sync(0xFFFFFFFFu, n_any, 0);
-      const bool two = __shfl_sync(0xFFFFFFFFu, (int)(x.n > tpt), 0) != 0;
-      if (!wait(QFULL, items++)) return false;
-      if (!at_stage(at, [&](auto st_c) {
-            constexpr int ST = decltype(st_c)::value;
-            if (!wait(FULL(ST), at >> 1)) return false;
-            tc_fence_after();
-            scores(Zero{}, st_c);
-            if (two) scores(One{}, st_c);
-            tc_commit_if(go, EMPTY(ST));
-            if (n == 1) tc_commit_if(go, QEMPTY);
-            return true;
-          }))
-        return false;
-      ++at;
-      for (int i = 0; i < n; ++i, ++at) {
-        const bool more = i + 1 < n;
-        const bool closed = !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi);
-        if (!at_stage(at, [&](auto st_c) {   // the tile's values, the next one's keys
+      // ---- tensor-core instructions.  The whole warp takes every step, one elected lane issues (by predicate), and
+      // row tile and ring stage are constants of the unrolled code: descriptors and addresses then sit in uniform
+      // registers, and a product costs one issue slot beside the two softmax warps of this scheduler.  (A
+      // single lane's walk with computed descriptors took twice as long per product under that load.)
+      const uint32_t go = elect_one() ? 1u : 0u;
+      constexpr uint32_t fmt = FP16 ? 0u : ((1u << 7) | (1u << 10));
+      constexpr uint32_t id_s = (1u << 4) | fmt | ((kTN >> 3) << 17) | ((128u >> 4) << 24);
+      constexpr uint32_t id_o = (1u << 4) | fmt | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
+      constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
+      const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV + C::kTileBytes, C::kBoxBytes);
+      uint32_t at = 0, items = 0, cleans[2] = {0, 0}, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
+      auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait_warp(bar, phase & 1, &abort_s, a.err); };
+      // S_t = Q_t K^T with the keys of stage ST
+      auto scores = [&](auto t_c, auto st_c) {
+        constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
+  #pragma unroll
+        for (int box = 0; box < C::kBoxes; ++box)
+          tc_mma4_ss(go, t * 128, dq + (t * kTileUnits + box * kBoxUnits), dk + (ST * 2 * kTileUnits + box * kBoxUnits), id_s,
+                     box != 0);
+        tc_commit_if(go, SFULL(t));
+      };
+      // O_t (+)= P_t V, P in two halves, with the values of stage ST; then the next tile's scores
+      auto turn = [&](auto t_c, auto st_c, uint32_t done, bool first, bool more) {
+        constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
+        const uint64_t v = dv + ST * 2 * kTileUnits;
+        if (!wait(PFULL(t, 0), done)) return false;
+        tc_fence_after();
+        tc_mma4_ts(go, kTmemO + t * 128, t * 128, v, id_o, !first);
+        if (!wait(PFULL(t, 1), done)) return false;
+        tc_fence_after();
+        tc_mma4_ts(go, kTmemO + t * 128, t * 128 + 32, v + (8192u >> 4), id_o, 1u);
+        if (more) scores(t_c, st_c);
+        else tc_commit_if(go, OFULL(t));
+        return true;
+      };
+      using Zero = std::integral_constant<int, 0>;
+      using One = std::integral_constant<int, 1>;
+      // body(stage as a constant) for the stage of a tile
+      static_assert(C::kStages == 2, "a tile's stage is its parity");
+      auto at_stage = [&](uint32_t tile, auto&& body) { return tile & 1 ? body(One{}) : body(Zero{}); };
+      walk([&](int, const SeqRows&, int, const Item& x, int i0, int n_any, uint32_t) {
+        const int n = __shfl_sync(0xFFFFFFFFu, n_any, 0);
+        const bool two = __shfl_sync(0xFFFFFFFFu, (int)(x.n > tpt), 0) != 0;
+        if (!wait(QFULL, items++)) return false;
+        if (!at_stage(at, [&](auto st_c) {
               constexpr int ST = decltype(st_c)::value;
               if (!wait(FULL(ST), at >> 1)) return false;
-              if (closed && !wait(CLEAN(ST), cleans[ST]++)) return false;
-              // (the second row tile's result too, where this item has none: bad_s is a short ring)
-              if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
-              if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
-              if (!turn(Zero{}, st_c, done0++, i == 0, more)) return false;
-              if (two) {
-                if (!turn(One{}, st_c, done1++, i == 0, more)) return false;
-              }
+              tc_fence_after();
+              scores(Zero{}, st_c);
+              if (two) scores(One{}, st_c);
               tc_commit_if(go, EMPTY(ST));
-              if (i + 2 == n) tc_commit_if(go, QEMPTY);
+              if (n == 1) tc_commit_if(go, QEMPTY);
               return true;
             }))
           return false;
-      }
-      ++outs0;
-      outs1 += two;
-      return true;
-    });
+        ++at;
+        for (int i = 0; i < n; ++i, ++at) {
+          const bool more = i + 1 < n;
+          const bool closed = !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi);
+          if (!at_stage(at, [&](auto st_c) {   // the tile's values, the next one's keys
+                constexpr int ST = decltype(st_c)::value;
+                if (!wait(FULL(ST), at >> 1)) return false;
+                if (closed && !wait(CLEAN(ST), cleans[ST]++)) return false;
+                // (the second row tile's result too, where this item has none: bad_s is a short ring)
+                if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
+                if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
+                if (!turn(Zero{}, st_c, done0++, i == 0, more)) return false;
+                if (two) {
+                  if (!turn(One{}, st_c, done1++, i == 0, more)) return false;
+                }
+                tc_commit_if(go, EMPTY(ST));
+                if (i + 2 == n) tc_commit_if(go, QEMPTY);
+                return true;
+              }))
+            return false;
+        }
+        ++outs0;
+        outs1 += two;
+        return true;
+      });
     } else {
-    // ---- values of masked tiles: non-finite ones are taken out, two positions a thread.  (Beside the softmax,
-    // which would spend 700 cycles of its chain on it, twice: one row tile's product would also wait for the other's.)
-    // These warps see every stage, and a stage is free only with their word, so that they keep step with the ring.
-    // Their word that a tile is done goes to its stage's own barrier: a stage is filled again only after both of them and the
-    // product have left it, so neither can speak twice there before the other has spoken, nor twice before the product's
-    // warp has looked.  (One barrier for all tiles would count a quick warp's two tiles as both warps' first.)
-    uint32_t at = 0;
-    int seg = 0;
-    walk([&](int, const SeqRows&, int, const Item& x, int i0, int n, uint32_t) {
-      for (int i = 0; i <= n; ++i, ++at) {
-        const uint32_t st = at & 1;
-        if (!mbar_wait_warp(FULL(st), (at >> 1) & 1, &abort_s, a.err)) return false;
-        const int j0 = i > 0 ? x.r.tile(i0 + i - 1) * kTN : 0;
-        if (i > 0 && !tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) {
-#pragma unroll 1
-          for (int r = (warp - kSoftmaxWarps - 2) * 32 + lane; r < kTN; r += kScanWarps * 32) {
-            const uint32_t row = sKV + st * C::kStageBytes + C::kTileBytes + r * 128;
-            uint32_t any = 0;
-#pragma unroll 8
-            for (int c = 0; c < 8 * C::kBoxes; ++c) {   // of 16 bytes; lanes start at different ones
-              uint32_t w0, w1, w2, w3;
-              ld_shared4(row + (c >> 3) * C::kBoxBytes + (((c + lane) & 7) << 4), w0, w1, w2, w3);
-              any |= non_finite_bits<FP16>(w0) | non_finite_bits<FP16>(w1) | non_finite_bits<FP16>(w2) |
-                     non_finite_bits<FP16>(w3);
-            }
-            if (any & kSigns) {
-#pragma unroll 1
-              for (int c = 0; c < 8 * C::kBoxes; ++c) {
-                const uint32_t to = row + (c >> 3) * C::kBoxBytes + ((c & 7) << 4);
+      // ---- values of masked tiles: non-finite ones are taken out, two positions a thread.  (Beside the softmax,
+      // which would spend 700 cycles of its chain on it, twice: one row tile's product would also wait for the other's.)
+      // These warps see every stage, and a stage is free only with their word, so that they keep step with the ring.
+      // Their word that a tile is done goes to its stage's own barrier: a stage is filled again only after both of them and the
+      // product have left it, so neither can speak twice there before the other has spoken, nor twice before the product's
+      // warp has looked.  (One barrier for all tiles would count a quick warp's two tiles as both warps' first.)
+      uint32_t at = 0;
+      int seg = 0;
+      walk([&](int, const SeqRows&, int, const Item& x, int i0, int n, uint32_t) {
+        for (int i = 0; i <= n; ++i, ++at) {
+          const uint32_t st = at & 1;
+          if (!mbar_wait_warp(FULL(st), (at >> 1) & 1, &abort_s, a.err)) return false;
+          const int j0 = i > 0 ? x.r.tile(i0 + i - 1) * kTN : 0;
+          if (i > 0 && !tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) {
+  #pragma unroll 1
+            for (int r = (warp - kSoftmaxWarps - 2) * 32 + lane; r < kTN; r += kScanWarps * 32) {
+              const uint32_t row = sKV + st * C::kStageBytes + C::kTileBytes + r * 128;
+              uint32_t any = 0;
+  #pragma unroll 8
+              for (int c = 0; c < 8 * C::kBoxes; ++c) {   // of 16 bytes; lanes start at different ones
                 uint32_t w0, w1, w2, w3;
-                ld_shared4(to, w0, w1, w2, w3);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w0 & ~non_finite16<FP16>(w0)),
-                             "r"(w1 & ~non_finite16<FP16>(w1)), "r"(w2 & ~non_finite16<FP16>(w2)),
-                             "r"(w3 & ~non_finite16<FP16>(w3))
-                             : "memory");
+                ld_shared4(row + (c >> 3) * C::kBoxBytes + (((c + lane) & 7) << 4), w0, w1, w2, w3);
+                any |= non_finite_bits<FP16>(w0) | non_finite_bits<FP16>(w1) | non_finite_bits<FP16>(w2) |
+                       non_finite_bits<FP16>(w3);
               }
-              const int j = j0 + r;
-              if (j <= x.p_hi && (a.window == 0 || j > x.p_lo - a.window || j < a.sinks)) bad_s[seg & 3] = seg + 1;
-              fence_proxy_async_smem();
+              if (any & kSigns) {
+  #pragma unroll 1
+                for (int c = 0; c < 8 * C::kBoxes; ++c) {
+                  const uint32_t to = row + (c >> 3) * C::kBoxBytes + ((c & 7) << 4);
+                  uint32_t w0, w1, w2, w3;
+                  ld_shared4(to, w0, w1, w2, w3);
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(w0 & ~non_finite16<FP16>(w0)),
+                               "r"(w1 & ~non_finite16<FP16>(w1)), "r"(w2 & ~non_finite16<FP16>(w2)),
+                               "r"(w3 & ~non_finite16<FP16>(w3))
+                               : "memory");
+                }
+                const int j = j0 + r;
+                if (j <= x.p_hi && (a.window == 0 || j > x.p_lo - a.window || j < a.sinks)) bad_s[seg & 3] = seg + 1;
+                fence_proxy_async_smem();
+              }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(CLEAN(st));
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(CLEAN(st));
+          if (lane == 0) mbar_arrive(EMPTY(st));
+          __syncwarp();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(EMPTY(st));
-        __syncwarp();
-      }
-      ++seg;
-      return true;
-    });
+        ++seg;
+        return true;
+      });
     }
   } else {
     // ---- softmax: row `r` of row tile `t`

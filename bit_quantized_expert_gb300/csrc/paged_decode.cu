@@ -14,8 +14,9 @@
 //   * all rows stand at one position and see the same set, so positions that they do not see are cut out
 //     of the value operand itself: whatever lies there, non-finite values included, has no effect;
 //   * running max, sum and O stay in registers; at an item's end the eight warps are joined in shared
-//     memory in a fixed order (one barrier an item: two joining buffers, every thread weighs for itself), and the result goes to o, or, for an item that other CTAs share, to a
-//     partial that a second launch joins in order.
+//     memory in a fixed order (one barrier an item: two joining buffers, every thread weighs for
+//     itself), and the result goes to o, or, for an item that other CTAs share, to a partial that a
+//     second launch joins in order.
 //
 // Measured (16 query and 2 key/value heads of 128, in a graph): 64 sequences of 1 to 32768 positions, 139 MB, 28.5 us
 // (4.9 TB/s), of which ~5 us are fixed steps: launch, schedule, first copies, joins; one sequence of 32768, 33.6
@@ -93,12 +94,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& r0, uint32_t& r
 // tensor map's 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz(int pos, int chunk) {
   return (uint32_t)((chunk >> 3) * (kTN * 128) + pos * 128 + (((chunk & 7) ^ (pos & 7)) << 4));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
