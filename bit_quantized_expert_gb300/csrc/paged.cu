@@ -4,8 +4,10 @@
 //   plan_kernel    one cluster of eight CTAs.  Every CTA scans the sequences' new and fresh-page counts
 //                  into shared memory (at most 4096 of each), then the cluster writes the table entries
 //                  (one warp a sequence) and the token rows (one thread a row, its sequence by binary
-//                  search) together.  Bound by latency: in a graph 3.8 us for 64 single tokens, 7.6 for
-//                  4096, 4.2 for 8 prompts of 1024; by one CTA 3.8, 19.3 and 9.9, by four 3.8, 8.6 and 4.9.
+//                  search) together.  Bound by latency: in a graph 4.3 us for 64 single tokens, 7.7 for
+//                  1024 sequences with 96 chunks, 8.3 for 4096 single tokens.  (64 and 4096 single tokens and 8
+//                  prompts of 1024 when the cluster's size was chosen: by one CTA 3.8, 19.3 and 9.9 us, by four
+//                  3.8, 8.6 and 4.9, by eight 3.8, 7.6 and 4.2.)
 //   append_kernel  16 bytes a thread, head rows contiguous on both sides.
 #include <algorithm>
 #include <climits>
@@ -204,8 +206,9 @@ constexpr int kAppendBatch = 4;
 
 // The keys or the values (blockIdx.y), units of 16 bytes numbered by (token, head, unit of the row) in Index;
 // four units a thread and turn, their slots and their data loaded together, so that one round trip to
-// memory lies between the start and the stores.  Bound by memory: 8 prompts of up to 4096 tokens, 23.5 MB both
-// ways, take 4.2 us in a graph (with 2, 8 or 16 CTAs an SM in place of 4: 5.3, 5.8, 6.4).
+// memory lies between the start and the stores.  8 prompts of up to 4096 tokens, 23.5 MB both ways, take 6.2 us in a
+// graph where keys and values come from memory (3.8 TB/s, the launch and that round trip among them), 4.2 where they lie
+// in L2, as behind a projection (with 2, 8 or 16 CTAs an SM in place of 4: 5.3, 5.8, 6.4).
 template <class Index>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
   pdl_wait();

@@ -24,8 +24,9 @@
 // 32 a cycle and SM), then P V and the next scores, ~2,800 in all where both row tiles' products are 2,048.
 // At 128 dims tensor memory is full, so the next scores cannot start before P is consumed; at 64 there is room, but an
 // order that used it (two barriers more a tile) was slower (297 against 276 us behind 32768 positions).  Measured (16 query and 2
-// key/value heads of 128): 2048 tokens behind 32768 positions 341 us (1.66 PFLOP/s) in a graph, tensor pipe 74 %
-// active; a prompt of 512 15.3 us; 4096 tokens with a window of 1024 54 us.
+// key/value heads of 128, in a graph, no inputs in L2): 2048 tokens behind 32768 positions 341 us at best (1.66 PFLOP/s),
+// 357 in the middle, with the clock that the power limit leaves; tensor pipe 74.6 % active; a prompt of 512 16.4 us; 4096
+// tokens with a window of 1024 57.9 us; 2048 tokens behind 32768 positions with heads of 64 271 us.
 #include <cmath>
 #include <type_traits>
 
@@ -980,9 +981,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the pairs of 32 rows and an eighth of the dims, a warp takes every fourth part, and the warps' results are
 // joined in order through shared memory.  Bound by latency (a launch, the record, the parts from L2), so what
 // counts is loads in flight (119 registers: with at most 64, a prompt of 2048 took 40 us, not 31): 2 us of a graph where
-// nothing is split, 3 where a window chunk's 64 cuts are.  8 tokens behind 32768 positions, 76 parts a head: 22 us in
-// all; joined as few 73.  `Many` begins at 6: at 4, 512 tokens behind 8192 take 45 us, not 40; at 10, 256 take
-// 30, not 29.
+// nothing is split, 3 where a window chunk's 64 cuts are.  8 tokens behind 32768 positions, 76 parts a head: 25 us in
+// all (22 with the cache in L2, and joined as few 73).  `Many` begins at 6: at 4, 512 tokens behind 8192 take 45 us, not
+// 40; at 10, 256 take 30, not 29.
 constexpr int kJoinWarps = 4;
 constexpr int kJoinMany = 6;   // parts
 

@@ -18,9 +18,10 @@
 //     itself), and the result goes to o, or, for an item that other CTAs share, to a partial that a
 //     second launch joins in order.
 //
-// Measured (16 query and 2 key/value heads of 128, in a graph): 64 sequences of 1 to 32768 positions, 139 MB, 28.5 us
-// (4.9 TB/s), of which ~5 us are fixed steps: launch, schedule, first copies, joins; one sequence of 32768, 33.6
-// MB, 10.5 us.  tcgen05 would not help: eight heads fill an eighth of its 64-row tiles, and bytes bound the rest.
+// Measured (16 query and 2 key/value heads of 128, in a graph, no cache in L2): 64 sequences of 1 to 32768 positions, 139
+// MB, 28.7 us (4.8 TB/s), of which ~5 us are fixed steps: launch, schedule, first copies, joins; one sequence of 32768,
+// 33.6 MB, 14.0 us (10.5 with its cache in L2); 64 sequences with heads of 64, 69.5 MB, 18.2 us.  tcgen05
+// would not help: eight heads fill an eighth of its 64-row tiles, and bytes bound the rest.
 #include <cmath>
 
 #include "paged.cuh"

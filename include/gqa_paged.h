@@ -30,8 +30,10 @@
  * Sums and softmax statistics are fp32; o is rounded once to the 16-bit type.  In the chunk form the
  * softmax's numerators are rounded to the 16-bit type before the product with V (the tensor cores'
  * operand type: at most half a step each, relative to the numerator, or in fp16 2^-34 relative to the row's
- * largest one); the single-token form keeps their rounding remainders (fp16: 2^-40).  Results are
- * identical from run to run.
+ * largest one); the single-token form keeps their rounding remainders (fp16: 2^-40).  The form follows
+ * max_new, so a sequence with one new token in a call that has room for more is rounded as a chunk.
+ * Identical calls give identical results; the work of a whole call is cut and joined by one rule, so the
+ * last bits of a sequence's outputs may differ with what else is in the call.
  *
  * Conventions are those of moe.h: device pointers owned by the caller, 16-byte aligned (the int32 arrays
  * 4-byte aligned, so they may be slices); work is
@@ -41,8 +43,9 @@
  * caller's workspace (clear its first 4 bytes once with moe_clear_error_flags; read them with
  * moe_read_error_flags); calls that may run at the same time need workspaces of their own.  Bits these
  * calls may set: 1 (a bounded wait timed out; o invalid), 8 (an output is not finite, which only
- * non-finite visible inputs or overflowing scores cause) and 16 (a length, page or slot out of range;
- * what each call does then stands with it: no call reads or writes out of bounds).
+ * non-finite visible inputs, scores past fp32's range or bf16 values of 2^84 and more cause) and 16 (a
+ * length, page or slot out of range; what each call does then stands with it: no call reads or writes
+ * out of bounds).
  */
 #ifndef GQA_PAGED_GB300_H_
 #define GQA_PAGED_GB300_H_
@@ -110,8 +113,8 @@ size_t gqa_paged_workspace_bytes(const gqa_paged_dims* dims);
  * q_start[B]) is left as it was.
  * Bit 16 is set for: a negative length (taken as 0); lengths whose sum passes T (the rows past T have
  * no entries, q_start is cut at T) or a row of the block table (kv_len is cut at max_pages * page_size,
- * the slots past it are -1); *n_free outside its range (cut); a free list that runs out (the entries and slots become -1), or that holds
- * or a held page that is, a number outside 0 .. num_pages - 1 (likewise).
+ * the slots past it are -1); *n_free outside its range (cut); a free list that runs out (the entries and
+ * slots become -1), or that holds, or a held page that is, a number outside 0 .. num_pages - 1 (likewise).
  * Returns as gqa_paged_attention, and MOE_ERR_INVALID_ARG if an output overlaps an input or another output
  * (but n_free_out == n_free); n_seqs == 0 is a no-op.  One launch. */
 moe_status gqa_paged_plan(const gqa_paged_dims* dims, const int32_t* ctx_len, const int32_t* new_len,
