@@ -15,8 +15,8 @@ import os
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libmoe_gb300.so")
 
-# Symbols declared in include/moe.h, include/gqa_attention.h, include/gqa_paged.h,
-# include/deltanet_scan.h and include/moe_probe.h.
+# Symbols declared in include/moe.h, include/gqa_attention.h, include/gqa_paged.h, include/gqa_paged8.h,
+# include/gqa_rotary.h, include/deltanet_scan.h and include/moe_probe.h.
 EXPORTED = ("moe_status_string", "moe_max_tiles", "moe_workspace_bytes", "moe_route",
             "moe_expert_forward", "moe_layer_forward", "moe_layer_forward_opts", "moe_rmsnorm_router",
             "moe_clear_error_flags",
@@ -24,7 +24,8 @@ EXPORTED = ("moe_status_string", "moe_max_tiles", "moe_workspace_bytes", "moe_ro
             "moe_layer_forward_host", "moe_decode_stream_probe", "gqa_decode_workspace_bytes",
             "gqa_decode_attention", "gdn_scan_workspace_bytes", "gdn_scan", "gdn_scan_opts",
             "moe_wait_timeout_probe", "moe_layer_forward_host_opts", "gqa_paged_workspace_bytes",
-            "gqa_paged_plan", "gqa_paged_append", "gqa_paged_attention")
+            "gqa_paged_plan", "gqa_paged_append", "gqa_paged_attention", "gqa_paged8_workspace_bytes",
+            "gqa_paged8_append", "gqa_paged8_read", "gqa_paged8_attention", "gqa_rotary_table", "gqa_rotary")
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_MISALIGNED",
           4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_CUDA"}
@@ -64,6 +65,18 @@ class GqaPagedDims(ctypes.Structure):
         "n_heads", "n_kv_heads", "head_dim", "page_size", "num_pages", "max_pages", "n_seqs", "n_tokens", "max_new",
         "window", "sinks", "dtype")] + [(n, ctypes.c_int64) for n in (
             "q_stride", "o_stride", "k_stride", "v_stride", "page_stride", "head_stride", "row_stride")]
+
+
+class GqaRotaryDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_heads", "n_kv_heads", "head_dim", "rot_dim", "n_tokens", "pairs", "dtype")] + [
+            ("amplitude", ctypes.c_float)] + [(n, ctypes.c_int64) for n in (
+                "q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+
+
+class GqaRotaryScaling(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("kind", ctypes.c_int32)] + [(n, ctypes.c_double) for n in (
+        "base", "factor", "original", "low", "high")]
 
 
 class GdnDims(ctypes.Structure):
@@ -134,6 +147,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gqa_paged_append.argtypes = [P(GqaPagedDims)] + [VP] * 7 + [S, VP]
     lib.gqa_paged_attention.restype = ctypes.c_int
     lib.gqa_paged_attention.argtypes = [P(GqaPagedDims)] + [VP] * 8 + [S, VP]
+    lib.gqa_paged8_workspace_bytes.restype = S
+    lib.gqa_paged8_workspace_bytes.argtypes = [P(GqaPagedDims)]
+    for name, pointers in (("gqa_paged8_append", 10), ("gqa_paged8_read", 10), ("gqa_paged8_attention", 10)):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = [P(GqaPagedDims)] + [VP] * pointers + [S, VP]
+    lib.gqa_rotary_table.restype = ctypes.c_int
+    lib.gqa_rotary_table.argtypes = [P(GqaRotaryScaling), VP]
+    lib.gqa_rotary.restype = ctypes.c_int
+    lib.gqa_rotary.argtypes = [P(GqaRotaryDims)] + [VP] * 8
     lib.gdn_scan_workspace_bytes.restype = S
     lib.gdn_scan_workspace_bytes.argtypes = [P(GdnDims)]
     lib.gdn_scan.restype = ctypes.c_int
@@ -380,14 +402,15 @@ def alloc_gqa_paged_workspace(pd: GqaPagedDims, device="cuda"):
 # A paged call's checks cost more host time than its launch, so they read each property once and look nothing
 # up that stays: the types that stand for each dtype of the dims (bit patterns included), and torch's
 # functions for the current device and its current stream's handle.
-_paged_types = _int32 = _device = _raw_stream = None
+_paged_types = _int32 = _int64 = _float32 = _byte_types = _device = _raw_stream = None
 
 
 def _load_paged_types():
-    global _paged_types, _int32, _device, _raw_stream
+    global _paged_types, _int32, _int64, _float32, _byte_types, _device, _raw_stream
     import torch
     bits = (torch.int16, torch.uint16)
     _paged_types, _int32 = ((torch.bfloat16, *bits), (torch.float16, *bits)), torch.int32
+    _int64, _float32, _byte_types = torch.int64, torch.float32, (torch.uint8, torch.int8, torch.float8_e4m3fn)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
     _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # last: _paged_device looks at it
 
@@ -481,6 +504,125 @@ def gqa_paged_attention(pd: GqaPagedDims, q, k_cache, v_cache, block_table, q_st
         _paged_ints(kv_len, B, dev, "kv_len"), _paged_rows(o, T, H, D, pd.o_stride, dt, dev, "o"),
         _paged_workspace(workspace, dev), workspace.nbytes,
         _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged_attention")
+
+
+def gqa_paged8_workspace_bytes(pd: GqaPagedDims) -> int:
+    n = load_library().gqa_paged8_workspace_bytes(ctypes.byref(pd))
+    if n == 0:
+        raise MoeError(1, "gqa_paged8_workspace_bytes")
+    return n
+
+
+def alloc_gqa_paged8_workspace(pd: GqaPagedDims, device="cuda"):
+    """Workspace of the calls on an 8-bit cache (and of gqa_paged_plan) for these dims, its error word cleared."""
+    import torch
+    ws = torch.empty(gqa_paged8_workspace_bytes(pd), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _paged8_caches(k, v, ks, vs, pd: GqaPagedDims, dev: int):
+    """Pointers of two caches of bytes (or torch.float8_e4m3fn) indexed [page, head, offset, D] whose strides are those of
+    the dims, and of their scales, contiguous fp32 [num_pages, Hkv, page_size / 16]."""
+    P, H, S, D = shape = (pd.num_pages, pd.n_kv_heads, pd.page_size, pd.head_dim)
+    want = (pd.page_stride or H * S * D, pd.head_stride or S * D, pd.row_stride or D, 1)
+    for t in (k, v):
+        st = t.stride()
+        if (t.get_device() != dev or t.dtype not in _byte_types or t.shape != shape
+                or (st != want and (st[2:] != want[2:] or (P > 1 and st[0] != want[0]) or (H > 1 and st[1] != want[1])))):
+            raise ValueError(f"caches: expected 8-bit tensors {list(shape)} with the strides of the dims on device {dev}")
+    for t in (ks, vs):
+        if t.get_device() != dev or t.dtype is not _float32 or t.shape != (P, H, S // 16) or not t.is_contiguous():
+            raise ValueError(f"scales: expected contiguous fp32 tensors {[P, H, S // 16]} on device {dev}")
+    return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr()
+
+
+def gqa_paged8_append(pd: GqaPagedDims, k, v, block_table, q_start, kv_len, k_cache, v_cache, k_scale, v_scale, workspace,
+                      stream=None):
+    """k, v [T, Hkv, D] of pd's type, quantised (e4m3 codes, one scale for 16 positions of a head) into the positions
+    that q_start and kv_len give their rows, the last ones of each sequence.  The caches are 8-bit
+    [num_pages, Hkv, page_size, D], the scales fp32 [num_pages, Hkv, page_size / 16] (include/gqa_paged8.h)."""
+    dev, T, H, D, B, dt = _paged_device(), pd.n_tokens, pd.n_kv_heads, pd.head_dim, pd.n_seqs, pd.dtype
+    kc, vc, ks, vs = _paged8_caches(k_cache, v_cache, k_scale, v_scale, pd, dev)
+    _check(load_library().gqa_paged8_append(
+        ctypes.byref(pd), _paged_rows(k, T, H, D, pd.k_stride, dt, dev, "k"), _paged_rows(v, T, H, D, pd.v_stride, dt, dev, "v"),
+        _paged_table(block_table, B, pd.max_pages, dev), _paged_ints(q_start, B + 1, dev, "q_start"),
+        _paged_ints(kv_len, B, dev, "kv_len"), kc, vc, ks, vs, _paged_workspace(workspace, dev), workspace.nbytes,
+        _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged8_append")
+
+
+def gqa_paged8_read(pd: GqaPagedDims, k_cache, v_cache, k_scale, v_scale, block_table, q_start, kv_len, k, v, workspace,
+                    stream=None):
+    """The cached keys and values of each sequence's last rows, in pd's type, into k and v [T, Hkv, D]."""
+    dev, T, H, D, B, dt = _paged_device(), pd.n_tokens, pd.n_kv_heads, pd.head_dim, pd.n_seqs, pd.dtype
+    kc, vc, ks, vs = _paged8_caches(k_cache, v_cache, k_scale, v_scale, pd, dev)
+    _check(load_library().gqa_paged8_read(
+        ctypes.byref(pd), kc, vc, ks, vs, _paged_table(block_table, B, pd.max_pages, dev),
+        _paged_ints(q_start, B + 1, dev, "q_start"), _paged_ints(kv_len, B, dev, "kv_len"),
+        _paged_rows(k, T, H, D, pd.k_stride, dt, dev, "k"), _paged_rows(v, T, H, D, pd.v_stride, dt, dev, "v"),
+        _paged_workspace(workspace, dev), workspace.nbytes,
+        _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged8_read")
+
+
+def gqa_paged8_attention(pd: GqaPagedDims, q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, kv_len, o, workspace,
+                         stream=None):
+    """gqa_paged_attention over an 8-bit cache.  q, o [T, Hq, D] of pd's type."""
+    dev, T, H, D, B, dt = _paged_device(), pd.n_tokens, pd.n_heads, pd.head_dim, pd.n_seqs, pd.dtype
+    kc, vc, ks, vs = _paged8_caches(k_cache, v_cache, k_scale, v_scale, pd, dev)
+    _check(load_library().gqa_paged8_attention(
+        ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, dt, dev, "q"), kc, vc, ks, vs,
+        _paged_table(block_table, B, pd.max_pages, dev), _paged_ints(q_start, B + 1, dev, "q_start"),
+        _paged_ints(kv_len, B, dev, "kv_len"), _paged_rows(o, T, H, D, pd.o_stride, dt, dev, "o"),
+        _paged_workspace(workspace, dev), workspace.nbytes,
+        _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged8_attention")
+
+
+_ROTARY_PAIRS = {"half": 0, "interleaved": 1}
+_ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
+
+
+def gqa_rotary_dims(n_heads, n_kv_heads, head_dim, rot_dim, n_tokens, layout="half", dtype="bf16", amplitude=1.0, q_stride=0,
+                    k_stride=0, q_out_stride=0, k_out_stride=0) -> GqaRotaryDims:
+    """Shapes of gqa_rotary (include/gqa_rotary.h).  layout: "half" (dims i and i + rot_dim / 2) or "interleaved" (2 i and
+    2 i + 1); token strides in elements, 0 for packed.  ValueError for a number that its field does not hold."""
+    sizes = [int(x) for x in (n_heads, n_kv_heads, head_dim, rot_dim, n_tokens, _ROTARY_PAIRS[layout], _PAGED_DTYPES[dtype])]
+    strides = [int(x) for x in (q_stride, k_stride, q_out_stride, k_out_stride)]
+    if min(sizes) < -2**31 or max(sizes) >= 2**31 or min(strides) < -2**63 or max(strides) >= 2**63:
+        raise ValueError("gqa_rotary_dims: sizes are 32-bit, strides 64-bit integers")
+    return GqaRotaryDims(*sizes, float(amplitude), *strides)
+
+
+def gqa_rotary_table(rot_dim, base=10000.0, scaling="none", factor=1.0, original=0.0, low=1.0, high=32.0, device="cuda"):
+    """Frequencies of the rot_dim / 2 pairs, made once per model: int64 [rot_dim / 2] on `device`, whose bits are turns a
+    position in units of 2^-64.  scaling for contexts past the length of the training, by `factor`: "none", "linear",
+    "base" or "by_parts" (with the `original` length, and the turns over it from which on (`high`) a pair stays or up
+    to which (`low`) it is stretched)."""
+    import torch
+    if not 0 <= int(rot_dim) < 2**31:
+        raise ValueError("gqa_rotary_table: rot_dim is a 32-bit integer")
+    sc = GqaRotaryScaling(int(rot_dim), _ROTARY_SCALINGS[scaling], float(base), float(factor), float(original), float(low),
+                          float(high))
+    turns = (ctypes.c_uint64 * max(1, sc.rot_dim // 2))()
+    _check(load_library().gqa_rotary_table(ctypes.byref(sc), turns), "gqa_rotary_table")
+    return torch.tensor([x - 2**64 if x >= 2**63 else x for x in turns], dtype=torch.int64).to(device)
+
+
+def gqa_rotary(rd: GqaRotaryDims, q, k, positions, table, q_out, k_out, n_rows=None, stream=None):
+    """The pairs of q [T, Hq, D] and k [T, Hkv, D] turned by their rows' positions (int32 [T]) into q_out and k_out, which
+    may be q and k.  table: gqa_rotary_table's.  n_rows: an int32 tensor whose first entry is the number of rows in use
+    (q_start[B:] of a plan), or None.  A tensor without heads is None."""
+    dev, T, D, dt = _paged_device(), rd.n_tokens, rd.head_dim, rd.dtype
+
+    def rows(x, heads, stride, name):
+        return None if heads == 0 else _paged_rows(x, T, heads, D, stride, dt, dev, name)
+    if table.get_device() != dev or table.dtype is not _int64 or table.numel() != rd.rot_dim // 2 or not table.is_contiguous():
+        raise ValueError(f"table: expected a contiguous int64 tensor of {rd.rot_dim // 2} entries on device {dev}")
+    _check(load_library().gqa_rotary(
+        ctypes.byref(rd), rows(q, rd.n_heads, rd.q_stride, "q"), rows(k, rd.n_kv_heads, rd.k_stride, "k"),
+        _paged_ints(positions, T, dev, "positions"), table.data_ptr(),
+        None if n_rows is None else _paged_ints(n_rows, 1, dev, "n_rows"), rows(q_out, rd.n_heads, rd.q_out_stride, "q_out"),
+        rows(k_out, rd.n_kv_heads, rd.k_out_stride, "k_out"), _raw_stream(dev) if stream is None else _stream(stream)),
+        "gqa_rotary")
 
 
 def gdn_dims(T, H, d_k=128, d_v=128) -> GdnDims:

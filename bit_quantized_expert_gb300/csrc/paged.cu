@@ -247,22 +247,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   }
 }
 
-bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
-
-// 1 for a null pointer, then 3 for one off its grid: 4 bytes for the int32 tables, 16 for all else.
-template <size_t N, size_t M>
-int check_pointers(const void* const (&tables)[N], const void* const (&wide)[M]) {
-  for (const void* p : tables)
-    if (p == nullptr) return MOE_ERR_INVALID_ARG;
-  for (const void* p : wide)
-    if (p == nullptr) return MOE_ERR_INVALID_ARG;
-  for (const void* p : tables)
-    if (misaligned(p, 4)) return MOE_ERR_MISALIGNED;
-  for (const void* p : wide)
-    if (misaligned(p, 16)) return MOE_ERR_MISALIGNED;
-  return MOE_OK;
-}
-
 // int32 arrays of one call, by address and entries.
 struct Ints {
   const int32_t* p;
@@ -273,11 +257,7 @@ bool overlap(const Ints& x, const Ints& y) {
   return x.n > 0 && y.n > 0 && a < b + (uintptr_t)y.n * 4 && b < a + (uintptr_t)x.n * 4;
 }
 
-int log2_of(int v) {
-  int s = 0;
-  while ((1 << s) < v) ++s;
-  return s;
-}
+}  // namespace
 
 // The dims rules, and the dims with every default filled in.
 int check_paged_dims(const gqa_paged_dims* in, gqa_paged_dims* out) {
@@ -363,6 +343,8 @@ int device_sms(int* sms) {
   return MOE_OK;
 }
 
+namespace {
+
 // One cache as the tensor maps see it; boxes of `rows` positions of one page and head.
 bool encode_pages(CUtensorMap* m, const uint16_t* cache, const gqa_paged_dims& d, int rows) {
   EncodeTiledFn f = encode_fn();
@@ -379,6 +361,8 @@ bool encode_pages(CUtensorMap* m, const uint16_t* cache, const gqa_paged_dims& d
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
 // The queries in boxes of one row tile: the G heads of a group for floor(128 / G) tokens.
 bool encode_queries(CUtensorMap* m, const uint16_t* q, const gqa_paged_dims& d) {
   EncodeTiledFn f = encode_fn();
@@ -394,7 +378,6 @@ bool encode_queries(CUtensorMap* m, const uint16_t* q, const gqa_paged_dims& d) 
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
 }  // namespace moe
 
 using namespace moe;

@@ -270,6 +270,38 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
 }
 
 // ------------------------------------------------------------------------------------------
+// Host side of the calls
+// ------------------------------------------------------------------------------------------
+inline bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+// 1 for a null pointer, then 3 for one off its grid: 4 bytes for the int32 tables, 16 for all else.
+template <size_t N, size_t M>
+int check_pointers(const void* const (&tables)[N], const void* const (&wide)[M]) {
+  for (const void* p : tables)
+    if (p == nullptr) return MOE_ERR_INVALID_ARG;
+  for (const void* p : wide)
+    if (p == nullptr) return MOE_ERR_INVALID_ARG;
+  for (const void* p : tables)
+    if (misaligned(p, 4)) return MOE_ERR_MISALIGNED;
+  for (const void* p : wide)
+    if (misaligned(p, 16)) return MOE_ERR_MISALIGNED;
+  return MOE_OK;
+}
+
+inline int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+// The dims rules, and the dims with every default filled in.
+int check_paged_dims(const gqa_paged_dims* in, gqa_paged_dims* out);
+PagedArgs paged_args(const gqa_paged_dims& d);
+int device_sms(int* sms);
+// The queries in boxes of one row tile: the G heads of a group for floor(128 / G) tokens.
+bool encode_queries(CUtensorMap* m, const uint16_t* q, const gqa_paged_dims& d);
+
+// ------------------------------------------------------------------------------------------
 // The two forms and their joining launch
 // ------------------------------------------------------------------------------------------
 size_t paged_decode_scratch(int D, int ctas);      // bytes of partials and records

@@ -1,0 +1,413 @@
+// Paged key/value cache in 8 bits: the append, the read, and the C ABI of its calls (contracts in
+// include/gqa_paged8.h).
+//
+//   append8_kernel  a warp takes the 16 positions of one block of one head, keys or values: the largest new value
+//                   gives the scale (a power of two, found from the bits of that value, so that quantising is
+//                   exact but for the codes' own rounding), then all rows of the block are written.  No two warps
+//                   have a block in common, so a scale and the codes under it change together.
+//   read8_kernel    the same walk, codes times scale into 16-bit rows.
+// Every CTA scans the sequences' block counts for itself, so that a warp finds its block by a search in shared memory.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "paged8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWalkThreads = 256;
+constexpr int kWalkCtasPerSm = 4;
+
+// Arguments of the append and of the read: `k`, `v` are rows of 16-bit values.
+struct WalkArgs : PagedArgs {
+  uint16_t *k, *v;
+  uint8_t *kc8, *vc8;
+  float *ks, *vs;
+  long long k_stride, v_stride;
+};
+
+// The blocks of 16 positions that hold a sequence's rows: first .. first + n - 1 (block -1 and below: before position 0).
+struct Blocks {
+  int first, n;
+};
+__device__ __forceinline__ Blocks blocks_of(const SeqRows& s, bool from_zero) {
+  if (s.n == 0 || (from_zero && s.p0 + s.n <= 0)) return Blocks{0, 0};
+  const int first = (from_zero ? max(s.p0, 0) : s.p0) >> kBlock8Shift;
+  return Blocks{first, ((s.p0 + s.n - 1) >> kBlock8Shift) - first + 1};
+}
+
+// One block of one head: sequence, page (-1: none) and offsets o0 .. o1 - 1 that rows row0 .. have.
+struct Unit {
+  int g, page, off, row0, o0, o1;
+};
+
+// body(unit) for every block, a warp each; blockIdx.y: keys or values.
+template <bool FROM_ZERO, class Body>
+__device__ __forceinline__ void walk_blocks(const WalkArgs& a, uint32_t* pre_s, uint32_t* warp_s, Body&& body) {
+  bool bad = false, over;
+  const uint32_t total = scan_sequences<kWalkThreads>(a.B, pre_s, warp_s, &over, [&](int b) {
+    return (unsigned long long)blocks_of(load_seq(a, b, bad), FROM_ZERO).n * a.Hkv;
+  });
+  if (over) bad = true;   // (cannot be: T * Hq and B * Hkv are below 2^31)
+  const uint32_t warps = gridDim.x * (kWalkThreads / 32);
+  for (uint32_t u = blockIdx.x * (kWalkThreads / 32) + (threadIdx.x >> 5); !over && u < total; u += warps) {
+    const int b = find_sequence(pre_s, a.B, u);
+    const SeqRows s = load_seq(a, b, bad);
+    const uint32_t at = u - pre_s[b], block = at / a.Hkv;
+    const int j0 = (blocks_of(s, FROM_ZERO).first + (int)block) << kBlock8Shift;   // its first position
+    Unit x;
+    x.g = (int)(at - block * a.Hkv);
+    x.o0 = max((FROM_ZERO ? max(s.p0, 0) : s.p0) - j0, 0);
+    x.o1 = min(s.p0 + s.n - j0, 1 << kBlock8Shift);
+    x.row0 = s.row0 + (j0 - s.p0);   // the row that offset 0 would have
+    x.page = -1;
+    if (j0 >= 0) {
+      x.page = a.table[(size_t)b * a.max_pages + (j0 >> a.page_shift)];
+      if (x.page < 0 || x.page >= a.num_pages) {
+        bad = true;
+        x.page = -1;
+      }
+    }
+    x.off = j0 & ((1 << a.page_shift) - 1);
+    body(x);
+    __syncwarp();
+  }
+  if (bad) raise_flag(a.err, kErrBadPages);
+}
+
+// A lane has 8 dims (16 bytes of a row, 8 codes) of every (256 / D)-th row.
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kWalkThreads) append8_kernel(const WalkArgs a) {
+  constexpr int kLanes = D / 8, kStep = 32 / kLanes, kTurns = 16 / kStep;
+  extern __shared__ uint32_t pre_s[];
+  __shared__ uint32_t warp_s[kWalkThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const bool values = blockIdx.y != 0;
+  const uint16_t* src = values ? a.v : a.k;
+  uint8_t* dst = values ? a.vc8 : a.kc8;
+  float* scales = values ? a.vs : a.ks;
+  const long long stride = values ? a.v_stride : a.k_stride;
+  const int lane = threadIdx.x & 31, r0 = lane / kLanes, dim = (lane % kLanes) * 8;
+  walk_blocks<true>(a, pre_s, warp_s, [&](const Unit& u) {
+    if (u.page < 0) return;
+    uint8_t* to = dst + u.page * a.page_stride + u.g * a.head_stride + (u.off + r0) * a.row_stride + dim;
+    float* scale = scales + scale_index(u.page, a.Hkv, u.g, a.page_shift, u.off);
+    // Everything that is needed, in flight together: new rows, and what the block holds before them.
+    uint4 x[kTurns];
+    uint2 old[kTurns];
+    float was = u.o0 > 0 ? *scale : kLeastScale;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int o = r0 + i * kStep;
+      x[i] = make_uint4(0, 0, 0, 0);
+      old[i] = make_uint2(0, 0);
+      if (o >= u.o0 && o < u.o1)
+        x[i] = __ldcg(reinterpret_cast<const uint4*>(src + (long long)(u.row0 + o) * stride + u.g * D + dim));
+      else if (o < u.o0)
+        old[i] = __ldcg(reinterpret_cast<const uint2*>(to + (long long)i * kStep * a.row_stride));
+    }
+    if (!scale_ok(was)) {
+      raise_flag(a.err, kErrBadPages);
+      was = kLeastScale;
+    }
+    uint32_t top = 0;   // bits of the largest magnitude (as fp32, whose order is that of its bits)
+    bool lost = false;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack16<FP16>(w[e]);
+        const uint32_t m0 = __float_as_uint(fabsf(f.x)), m1 = __float_as_uint(fabsf(f.y));
+        constexpr uint32_t kMost = (127u + 60u + 8u) << 23 | 0x600000u;   // 448 * 2^60
+        lost |= m0 > kMost || m1 > kMost;
+        top = max(top, max(m0 > kMost ? 0u : m0, m1 > kMost ? 0u : m1));
+      }
+    }
+    __syncwarp();
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    // top = 1.m * 2^(E - 127) <= 448 * 2^e = 1.75 * 2^(8 + e) from e = E - 135 on, or one more where 1.m > 1.75
+    const int e = min(max((int)(top >> 23) - 135 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0), -60), 60);
+    const float s = fmaxf(__uint_as_float((uint32_t)(e + 127) << 23), was);
+    const bool power = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+    const float inv = 1.f / s, ratio = was / s;
+    auto code = [&](float v) {
+      const float y = power ? v * inv : v / s;
+      return fabsf(v) <= 448.f * kMostScale ? y : __uint_as_float(0x7FC00000u);
+    };
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int o = r0 + i * kStep;
+      if (o >= u.o1 || (o < u.o0 && ratio == 1.f)) continue;
+      uint2 c;
+      if (o >= u.o0) {
+        const float2 f0 = unpack16<FP16>(x[i].x), f1 = unpack16<FP16>(x[i].y), f2 = unpack16<FP16>(x[i].z),
+                     f3 = unpack16<FP16>(x[i].w);
+        c.x = to_codes4(code(f0.x), code(f0.y), code(f1.x), code(f1.y));
+        c.y = to_codes4(code(f2.x), code(f2.y), code(f3.x), code(f3.y));
+      } else {
+        uint32_t h[4];
+        codes_to_half4(old[i].x, h[0], h[1]);
+        codes_to_half4(old[i].y, h[2], h[3]);
+        const float2 f0 = unpack16<true>(h[0]), f1 = unpack16<true>(h[1]), f2 = unpack16<true>(h[2]), f3 = unpack16<true>(h[3]);
+        c.x = to_codes4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
+        c.y = to_codes4(f2.x * ratio, f2.y * ratio, f3.x * ratio, f3.y * ratio);
+      }
+      *reinterpret_cast<uint2*>(to + (long long)i * kStep * a.row_stride) = c;
+    }
+    if (lane == 0) *scale = s;
+    if (lost) raise_flag(a.err, kErrNonFinite);
+  });
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kWalkThreads) read8_kernel(const WalkArgs a) {
+  constexpr int kLanes = D / 8, kStep = 32 / kLanes, kTurns = 16 / kStep;
+  extern __shared__ uint32_t pre_s[];
+  __shared__ uint32_t warp_s[kWalkThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  const bool values = blockIdx.y != 0;
+  const uint8_t* src = values ? a.vc8 : a.kc8;
+  uint16_t* dst = values ? a.v : a.k;
+  const float* scales = values ? a.vs : a.ks;
+  const long long stride = values ? a.v_stride : a.k_stride;
+  const int lane = threadIdx.x & 31, r0 = lane / kLanes, dim = (lane % kLanes) * 8;
+  walk_blocks<false>(a, pre_s, warp_s, [&](const Unit& u) {
+    uint2 x[kTurns];
+    float s = 0.f;
+    if (u.page >= 0) s = scales[scale_index(u.page, a.Hkv, u.g, a.page_shift, u.off)];
+    const uint8_t* from = src + u.page * a.page_stride + u.g * a.head_stride + (u.off + r0) * a.row_stride + dim;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int o = r0 + i * kStep;
+      x[i] = make_uint2(0, 0);
+      if (u.page >= 0 && o >= u.o0 && o < u.o1)
+        x[i] = __ldcg(reinterpret_cast<const uint2*>(from + (long long)i * kStep * a.row_stride));
+    }
+    if (u.page >= 0 && !scale_ok(s)) {
+      raise_flag(a.err, kErrBadPages);
+      s = kLeastScale;
+    }
+    auto pair = [&](uint32_t h) {
+      const float2 f = unpack16<true>(h);
+      float y0 = f.x * s, y1 = f.y * s;
+      if (FP16) {   // (comparisons, so that NaN stays)
+        y0 = y0 > 65504.f ? 65504.f : y0 < -65504.f ? -65504.f : y0;
+        y1 = y1 > 65504.f ? 65504.f : y1 < -65504.f ? -65504.f : y1;
+      }
+      return pack16<FP16>(y0, y1);
+    };
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int o = r0 + i * kStep;
+      if (o < u.o0 || o >= u.o1) continue;
+      uint32_t h[4];
+      codes_to_half4(x[i].x, h[0], h[1]);
+      codes_to_half4(x[i].y, h[2], h[3]);
+      *reinterpret_cast<uint4*>(dst + (long long)(u.row0 + o) * stride + u.g * D + dim) =
+          make_uint4(pair(h[0]), pair(h[1]), pair(h[2]), pair(h[3]));
+    }
+  });
+}
+
+// A warp a row and head, position by position.
+constexpr int kPlainWarps = 8;
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kPlainWarps * 32) attention8_kernel(const Paged8Args a) {
+  constexpr int E = D / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int b = (int)blockIdx.x, h = (int)blockIdx.y, g = h / a.G, lane = threadIdx.x & 31;
+  bool bad = false, nonfinite = false;
+  const SeqRows s = load_seq(a, b, bad);
+  for (int i = (int)blockIdx.z * kPlainWarps + (threadIdx.x >> 5); i < s.n; i += (int)gridDim.z * kPlainWarps) {
+    const int p = s.p0 + i;
+    float q[E], o[E], m = kUnseen, l = 0.f;
+    for (int e = 0; e < E; ++e) {
+      const uint32_t w = a.q[(s.row0 + i) * a.q_stride + h * D + lane * E + e];
+      q[e] = unpack16<FP16>(w).x * a.qk_scale;
+      o[e] = 0.f;
+    }
+    for (int j = 0; j <= p; ++j) {
+      if (!paged_sees(a, p, j)) {
+        j = max(j, p - a.window);
+        continue;
+      }
+      const int page = a.table[(size_t)b * a.max_pages + (j >> a.page_shift)], off = j & ((1 << a.page_shift) - 1);
+      float k[E], v[E], x = 0.f;
+      for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
+      if (page >= 0 && page < a.num_pages) {
+        const long long at = page * a.page_stride + g * a.head_stride + off * a.row_stride + lane * E;
+        const int si = scale_index(page, a.Hkv, g, a.page_shift, off);
+        float ks = a.ks[si], vs = a.vs[si];
+        if (!scale_ok(ks)) bad = true, ks = kLeastScale;
+        if (!scale_ok(vs)) bad = true, vs = kLeastScale;
+        for (int e = 0; e < E; ++e) {
+          k[e] = unpack16<true>(codes_to_half2(a.kc8[at + e])).x * ks;
+          v[e] = unpack16<true>(codes_to_half2(a.vc8[at + e])).x * vs;
+        }
+      } else {
+        bad = true;
+      }
+      for (int e = 0; e < E; ++e) x += q[e] * k[e];
+      for (int off2 = 16; off2 > 0; off2 >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off2);
+      const float top = fmaxf(m, x), old = ex2(m - top), w = ex2(x - top);
+      m = top;
+      l = l * old + w;
+      for (int e = 0; e < E; ++e) o[e] = o[e] * old + w * v[e];
+    }
+    for (int e = 0; e < E; ++e) {
+      const float y = p < 0 ? 0.f : o[e] / l;
+      nonfinite |= !isfinite(y);
+      a.o[(s.row0 + i) * a.o_stride + h * D + lane * E + e] = (uint16_t)pack16<FP16>(y, 0.f);
+    }
+  }
+  if (bad) raise_flag(a.err, kErrBadPages);
+  if (nonfinite) raise_flag(a.err, kErrNonFinite);
+}
+
+// The dims rules of gqa_paged.h, and the caches' strides in bytes on 16-byte boundaries.
+int check_paged8_dims(const gqa_paged_dims* in, gqa_paged_dims* d) {
+  const int st = check_paged_dims(in, d);
+  if (st != MOE_OK) return st;
+  return d->page_stride % 16 != 0 || d->head_stride % 16 != 0 || d->row_stride % 16 != 0 ? MOE_ERR_MISALIGNED : MOE_OK;
+}
+
+template <class Args>
+void fill(Args* a, const gqa_paged_dims& d, const int32_t* block_table, const int32_t* q_start, const int32_t* kv_len,
+          void* workspace) {
+  std::memset(a, 0, sizeof(*a));
+  static_cast<PagedArgs&>(*a) = paged_args(d);
+  a->table = block_table;
+  a->q_start = q_start;
+  a->kv_len = kv_len;
+  a->err = static_cast<uint32_t*>(workspace);
+}
+
+template <template <int, bool> class K>
+cudaError_t launch_walk(const WalkArgs& a, int D, int sms, cudaStream_t st) {
+  // At most this many blocks: a sequence's rows touch two more than a sixteenth of them, and one each.
+  const long long blocks = std::min((long long)a.T, (long long)a.T / 16 + 2ll * std::min(a.B, a.T)) * a.Hkv;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min((blocks + kWalkThreads / 32 - 1) / (kWalkThreads / 32), (long long)sms * kWalkCtasPerSm), 2);
+  cfg.blockDim = dim3(kWalkThreads);
+  cfg.dynamicSmemBytes = ((size_t)a.B + 1) * 4;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (D == 128)
+    return a.fp16 ? cudaLaunchKernelEx(&cfg, K<128, true>::fn, a) : cudaLaunchKernelEx(&cfg, K<128, false>::fn, a);
+  return a.fp16 ? cudaLaunchKernelEx(&cfg, K<64, true>::fn, a) : cudaLaunchKernelEx(&cfg, K<64, false>::fn, a);
+}
+template <int D, bool FP16>
+struct Append8 {
+  static constexpr auto fn = append8_kernel<D, FP16>;
+};
+template <int D, bool FP16>
+struct Read8 {
+  static constexpr auto fn = read8_kernel<D, FP16>;
+};
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t gqa_paged8_workspace_bytes(const gqa_paged_dims* dims) {
+  gqa_paged_dims d;
+  return check_paged8_dims(dims, &d) == MOE_OK ? gqa_paged_workspace_bytes(dims) : 0;
+}
+
+extern "C" moe_status gqa_paged8_append(const gqa_paged_dims* dims, const uint16_t* k, const uint16_t* v,
+                                        const int32_t* block_table, const int32_t* q_start, const int32_t* kv_len,
+                                        uint8_t* k_cache, uint8_t* v_cache, float* k_scale, float* v_scale, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  gqa_paged_dims d;
+  int st = check_paged8_dims(dims, &d);
+  if (st != MOE_OK) return (moe_status)st;
+  if (d.n_seqs == 0 || d.n_tokens == 0) return MOE_OK;
+  if ((st = check_pointers({block_table, q_start, kv_len}, {k, v, k_cache, v_cache, k_scale, v_scale, workspace})) != MOE_OK)
+    return (moe_status)st;
+  if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
+  int sms = 0;
+  if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
+  WalkArgs a;
+  fill(&a, d, block_table, q_start, kv_len, workspace);
+  a.k = const_cast<uint16_t*>(k);
+  a.v = const_cast<uint16_t*>(v);
+  a.kc8 = k_cache;
+  a.vc8 = v_cache;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.k_stride = d.k_stride;
+  a.v_stride = d.v_stride;
+  return launch_walk<Append8>(a, d.head_dim, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status gqa_paged8_read(const gqa_paged_dims* dims, const uint8_t* k_cache, const uint8_t* v_cache,
+                                      const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                      const int32_t* q_start, const int32_t* kv_len, uint16_t* k, uint16_t* v,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  gqa_paged_dims d;
+  int st = check_paged8_dims(dims, &d);
+  if (st != MOE_OK) return (moe_status)st;
+  if (d.n_seqs == 0 || d.n_tokens == 0) return MOE_OK;
+  if ((st = check_pointers({block_table, q_start, kv_len}, {k, v, k_cache, v_cache, k_scale, v_scale, workspace})) != MOE_OK)
+    return (moe_status)st;
+  if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
+  int sms = 0;
+  if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
+  WalkArgs a;
+  fill(&a, d, block_table, q_start, kv_len, workspace);
+  a.k = k;
+  a.v = v;
+  a.kc8 = const_cast<uint8_t*>(k_cache);
+  a.vc8 = const_cast<uint8_t*>(v_cache);
+  a.ks = const_cast<float*>(k_scale);
+  a.vs = const_cast<float*>(v_scale);
+  a.k_stride = d.k_stride;
+  a.v_stride = d.v_stride;
+  return launch_walk<Read8>(a, d.head_dim, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+extern "C" moe_status gqa_paged8_attention(const gqa_paged_dims* dims, const uint16_t* q, const uint8_t* k_cache,
+                                           const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                                           const int32_t* block_table, const int32_t* q_start, const int32_t* kv_len,
+                                           uint16_t* o, void* workspace, size_t workspace_bytes, void* stream) {
+  gqa_paged_dims d;
+  int st = check_paged8_dims(dims, &d);
+  if (st != MOE_OK) return (moe_status)st;
+  if (d.n_seqs == 0 || d.n_tokens == 0) return MOE_OK;
+  if ((st = check_pointers({block_table, q_start, kv_len}, {q, k_cache, v_cache, k_scale, v_scale, o, workspace})) != MOE_OK)
+    return (moe_status)st;
+  if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
+  Paged8Args a;
+  fill(&a, d, block_table, q_start, kv_len, workspace);
+  a.q = q;
+  a.o = o;
+  a.kc8 = k_cache;
+  a.vc8 = v_cache;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(d.n_seqs, d.n_heads, (std::min(a.max_new, 1024) + kPlainWarps - 1) / kPlainWarps);
+  cfg.blockDim = dim3(kPlainWarps * 32);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (d.head_dim == 128)
+    e = a.fp16 ? cudaLaunchKernelEx(&cfg, attention8_kernel<128, true>, a) : cudaLaunchKernelEx(&cfg, attention8_kernel<128, false>, a);
+  else
+    e = a.fp16 ? cudaLaunchKernelEx(&cfg, attention8_kernel<64, true>, a) : cudaLaunchKernelEx(&cfg, attention8_kernel<64, false>, a);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
