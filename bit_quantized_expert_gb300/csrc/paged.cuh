@@ -256,6 +256,13 @@ __device__ __forceinline__ float2 unpack16(uint32_t x) {
   return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
 }
 
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
+}
+
 // Lets `kernel` use `bytes` of shared memory on the current device, once for each of the first 64 (bits of `ready`;
 // racing first calls set the same value).
 inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>* ready) {
@@ -304,6 +311,15 @@ bool encode_queries(CUtensorMap* m, const uint16_t* q, const gqa_paged_dims& d);
 // ------------------------------------------------------------------------------------------
 // The two forms and their joining launch
 // ------------------------------------------------------------------------------------------
+// Single tokens: what a CTA leaves of an item that it has in part, for each of the 8 rows of query heads D sums of values,
+// then the 8 maxima (base-2 units) and the 8 sums of numerators.
+struct DecodeSplit {
+  float* part;         // [ctas][2][8 * D + 16]
+  SplitRecord* rec;    // [ctas]
+};
+DecodeSplit paged_decode_split(int D, void* scratch, int ctas);
+cudaError_t launch_paged_decode_join(const PagedArgs& a, int D, const DecodeSplit& split, int ctas, cudaStream_t st);
+
 size_t paged_decode_scratch(int D, int ctas);      // bytes of partials and records
 size_t paged_chunk_scratch(int D, int ctas);
 cudaError_t launch_paged_chunk(const PagedMaps& maps, const PagedArgs& a, int D, void* scratch, int ctas, cudaStream_t st);

@@ -395,6 +395,12 @@ extern "C" moe_status gqa_paged8_attention(const gqa_paged_dims* dims, const uin
   a.vc8 = v_cache;
   a.ks = k_scale;
   a.vs = v_scale;
+  if (d.max_new == 1) {
+    int sms = 0;
+    if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
+    return launch_paged8_decode(d, a, static_cast<uint8_t*>(workspace) + kWsHeadBytes, std::min(sms, kPagedMaxCtas),
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;

@@ -55,11 +55,6 @@ struct Dec {
   static size_t smem(int B) { return 1024 + (size_t)kStages * kStageBytes + kJoinBytes + ((size_t)B + 1) * 4; }
 };
 
-struct DecodeSplit {
-  float* part;         // [ctas][2][kPartFloats]
-  SplitRecord* rec;    // [ctas]
-};
-
 template <bool FP16>
 __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
@@ -79,13 +74,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr)
-               : "memory");
-}
-
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
                : "r"(addr)
                : "memory");
@@ -498,8 +486,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Page
     }
     x /= L;
     y /= L;
-    if (!isfinite(x) || !isfinite(y)) raise_flag(a.err, kErrNonFinite);
-    *reinterpret_cast<uint32_t*>(a.o + rec.row * a.o_stride + (long long)(rec.g * a.G + row) * D + d) = pack16<FP16>(x, y);
+    const uint32_t w = pack16<FP16>(x, y);
+    const float2 back = unpack16<FP16>(w);   // (over an 8-bit cache a finite sum may be past fp16)
+    if (!isfinite(back.x) || !isfinite(back.y)) raise_flag(a.err, kErrNonFinite);
+    *reinterpret_cast<uint32_t*>(a.o + rec.row * a.o_stride + (long long)(rec.g * a.G + row) * D + d) = w;
   }
 }
 
@@ -519,11 +509,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedArgs& a, const DecodeSplit&
   cfg.attrs = at;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, decode_kernel<D, FP16>, maps, a, split);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(ctas, a.G);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<D, FP16>, a, split);
+  return e == cudaSuccess ? launch_paged_decode_join(a, D, split, ctas, st) : e;
 }
 
 }  // namespace
@@ -532,10 +518,32 @@ size_t paged_decode_scratch(int D, int ctas) {
   return (size_t)ctas * (2 * (kRows * D + 2 * kRows) * sizeof(float) + sizeof(SplitRecord));
 }
 
-cudaError_t launch_paged_decode(const PagedMaps& maps, const PagedArgs& a, int D, void* scratch, int ctas, cudaStream_t st) {
+DecodeSplit paged_decode_split(int D, void* scratch, int ctas) {
   DecodeSplit split;
   split.part = static_cast<float*>(scratch);
   split.rec = reinterpret_cast<SplitRecord*>(split.part + (size_t)ctas * 2 * (kRows * D + 2 * kRows));
+  return split;
+}
+
+cudaError_t launch_paged_decode_join(const PagedArgs& a, int D, const DecodeSplit& split, int ctas, cudaStream_t st) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, a.G);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (D == 128)
+    return a.fp16 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<128, true>, a, split)
+                  : cudaLaunchKernelEx(&cfg, decode_join_kernel<128, false>, a, split);
+  return a.fp16 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<64, true>, a, split)
+                : cudaLaunchKernelEx(&cfg, decode_join_kernel<64, false>, a, split);
+}
+
+cudaError_t launch_paged_decode(const PagedMaps& maps, const PagedArgs& a, int D, void* scratch, int ctas, cudaStream_t st) {
+  const DecodeSplit split = paged_decode_split(D, scratch, ctas);
   if (D == 128) return a.fp16 ? launch<128, true>(maps, a, split, ctas, st) : launch<128, false>(maps, a, split, ctas, st);
   return a.fp16 ? launch<64, true>(maps, a, split, ctas, st) : launch<64, false>(maps, a, split, ctas, st);
 }
