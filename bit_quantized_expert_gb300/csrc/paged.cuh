@@ -320,6 +320,14 @@ struct DecodeSplit {
 DecodeSplit paged_decode_split(int D, void* scratch, int ctas);
 cudaError_t launch_paged_decode_join(const PagedArgs& a, int D, const DecodeSplit& split, int ctas, cudaStream_t st);
 
+// Chunks: O of the 256 rows by four columns of all rows, then their maxima, then their sums.
+struct ChunkSplit {
+  float* part;         // [ctas][2][256 * (D + 2)]
+  SplitRecord* rec;    // [ctas]
+};
+ChunkSplit paged_chunk_split(int D, void* scratch, int ctas);
+cudaError_t launch_paged_chunk_join(const PagedArgs& a, int D, const ChunkSplit& split, int ctas, cudaStream_t st);
+
 size_t paged_decode_scratch(int D, int ctas);      // bytes of partials and records
 size_t paged_chunk_scratch(int D, int ctas);
 cudaError_t launch_paged_chunk(const PagedMaps& maps, const PagedArgs& a, int D, void* scratch, int ctas, cudaStream_t st);

@@ -213,62 +213,6 @@ __global__ void __launch_bounds__(kWalkThreads) read8_kernel(const WalkArgs a) {
   });
 }
 
-// A warp a row and head, position by position.
-constexpr int kPlainWarps = 8;
-template <int D, bool FP16>
-__global__ void __launch_bounds__(kPlainWarps * 32) attention8_kernel(const Paged8Args a) {
-  constexpr int E = D / 32;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int b = (int)blockIdx.x, h = (int)blockIdx.y, g = h / a.G, lane = threadIdx.x & 31;
-  bool bad = false, nonfinite = false;
-  const SeqRows s = load_seq(a, b, bad);
-  for (int i = (int)blockIdx.z * kPlainWarps + (threadIdx.x >> 5); i < s.n; i += (int)gridDim.z * kPlainWarps) {
-    const int p = s.p0 + i;
-    float q[E], o[E], m = kUnseen, l = 0.f;
-    for (int e = 0; e < E; ++e) {
-      const uint32_t w = a.q[(s.row0 + i) * a.q_stride + h * D + lane * E + e];
-      q[e] = unpack16<FP16>(w).x * a.qk_scale;
-      o[e] = 0.f;
-    }
-    for (int j = 0; j <= p; ++j) {
-      if (!paged_sees(a, p, j)) {
-        j = max(j, p - a.window);
-        continue;
-      }
-      const int page = a.table[(size_t)b * a.max_pages + (j >> a.page_shift)], off = j & ((1 << a.page_shift) - 1);
-      float k[E], v[E], x = 0.f;
-      for (int e = 0; e < E; ++e) k[e] = v[e] = 0.f;
-      if (page >= 0 && page < a.num_pages) {
-        const long long at = page * a.page_stride + g * a.head_stride + off * a.row_stride + lane * E;
-        const int si = scale_index(page, a.Hkv, g, a.page_shift, off);
-        float ks = a.ks[si], vs = a.vs[si];
-        if (!scale_ok(ks)) bad = true, ks = kLeastScale;
-        if (!scale_ok(vs)) bad = true, vs = kLeastScale;
-        for (int e = 0; e < E; ++e) {
-          k[e] = unpack16<true>(codes_to_half2(a.kc8[at + e])).x * ks;
-          v[e] = unpack16<true>(codes_to_half2(a.vc8[at + e])).x * vs;
-        }
-      } else {
-        bad = true;
-      }
-      for (int e = 0; e < E; ++e) x += q[e] * k[e];
-      for (int off2 = 16; off2 > 0; off2 >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, off2);
-      const float top = fmaxf(m, x), old = ex2(m - top), w = ex2(x - top);
-      m = top;
-      l = l * old + w;
-      for (int e = 0; e < E; ++e) o[e] = o[e] * old + w * v[e];
-    }
-    for (int e = 0; e < E; ++e) {
-      const float y = p < 0 ? 0.f : o[e] / l;
-      nonfinite |= !isfinite(y);
-      a.o[(s.row0 + i) * a.o_stride + h * D + lane * E + e] = (uint16_t)pack16<FP16>(y, 0.f);
-    }
-  }
-  if (bad) raise_flag(a.err, kErrBadPages);
-  if (nonfinite) raise_flag(a.err, kErrNonFinite);
-}
-
 // The dims rules of gqa_paged.h, and the caches' strides in bytes on 16-byte boundaries.
 int check_paged8_dims(const gqa_paged_dims* in, gqa_paged_dims* d) {
   const int st = check_paged_dims(in, d);
@@ -395,25 +339,9 @@ extern "C" moe_status gqa_paged8_attention(const gqa_paged_dims* dims, const uin
   a.vc8 = v_cache;
   a.ks = k_scale;
   a.vs = v_scale;
-  if (d.max_new == 1) {
-    int sms = 0;
-    if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
-    return launch_paged8_decode(d, a, static_cast<uint8_t*>(workspace) + kWsHeadBytes, std::min(sms, kPagedMaxCtas),
-                                static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-  }
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(d.n_seqs, d.n_heads, (std::min(a.max_new, 1024) + kPlainWarps - 1) / kPlainWarps);
-  cfg.blockDim = dim3(kPlainWarps * 32);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaError_t e;
-  if (d.head_dim == 128)
-    e = a.fp16 ? cudaLaunchKernelEx(&cfg, attention8_kernel<128, true>, a) : cudaLaunchKernelEx(&cfg, attention8_kernel<128, false>, a);
-  else
-    e = a.fp16 ? cudaLaunchKernelEx(&cfg, attention8_kernel<64, true>, a) : cudaLaunchKernelEx(&cfg, attention8_kernel<64, false>, a);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  int sms = 0;
+  if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
+  const auto launch = d.max_new == 1 ? launch_paged8_decode : launch_paged8_chunk;
+  return launch(d, a, static_cast<uint8_t*>(workspace) + kWsHeadBytes, std::min(sms, kPagedMaxCtas),
+                static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -46,5 +46,6 @@ __device__ __forceinline__ uint32_t to_codes4(float x0, float x1, float x2, floa
 }
 
 cudaError_t launch_paged8_decode(const gqa_paged_dims& d, const Paged8Args& a, void* scratch, int ctas, cudaStream_t st);
+cudaError_t launch_paged8_chunk(const gqa_paged_dims& d, const Paged8Args& a, void* scratch, int ctas, cudaStream_t st);
 
 }  // namespace moe

@@ -1,0 +1,814 @@
+// Attention of chunks of new tokens over the paged cache held in 8 bits (contract in include/gqa_paged8.h), on the
+// fifth-generation tensor cores.
+//
+// Rows, row tiles, items, the split of the work, tensor memory and the order of the products are those of the 16-bit
+// form (paged_chunk.cu).  What differs:
+//
+//   * Operands.  The tensor cores take e4m3 beside e4m3 alone, and queries and numerators need more bits than
+//     that, so codes become fp16, exactly, on their way into shared memory: two warps (10 and 11) load them from
+//     global memory into registers, one tile of keys or of values ahead, convert and store them in the operands' swizzle.
+//     A tile of the softmax takes ~2,800 cycles, its conversion about half of that, beside it.
+//   * Scales.  Warp 8 reads the tile's sixteen and leaves, in a ring of four, each block's key scale, the logarithm
+//     of its value scale over the largest that the segment has met, and the inverse of that ratio.  A score's exponent is
+//     score * (key scale * row scale) - reference + logarithm, one fma as without scales; numerators come out in the
+//     scale of the products with V (O is in units of the largest value scale), and the row's sum takes each
+//     block's sum times the inverse.
+//   * Queries.  bf16 ones are scaled by a power of two a row so that fp16 holds them: by the softmax threads, a row each, in
+//     shared memory before the item's first product.
+//   * NaN codes of masked tiles' values are taken out as they are converted.
+#include <cmath>
+#include <cstring>
+
+#include "paged8.cuh"
+#include "paged_chunk.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kConvertWarps = 2;
+constexpr int kFirstConvert = 10;
+// Registers a thread: 168 at launch; 2 * 200 + 104 = 3 * 168 after the split.
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+// Base-2 units by which the numerators' reference may lag behind the row's maximum, and by which it stands
+// below the maximum that sets it: fp16's range from 2^15 down.
+constexpr float kLazy = 6.f, kLift = 9.f;
+// Base-2 units from which on a row's reference is taken off its scaled scores apart (far_tiles8).
+constexpr float kFar = 65536.f;
+constexpr int kInfos = 4;
+
+template <int D>
+struct Chunk8 {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBoxBytes = kTN * 128;                  // 128 rows of 64 dims
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;        // a row tile of q, a tile of keys or of values
+  // Ring: a segment of n tiles takes n + 1 stages, the i-th with the values of its tile i - 1 and the keys of tile i.
+  static constexpr int kStages = 2;
+  static constexpr int kStageBytes = 2 * kTileBytes;           // keys, then values
+  static constexpr int kPartFloats = kItemRows * (D + 2);
+  static size_t smem(int B) {
+    return 1024 + (size_t)(2 + 2 * kStages) * kTileBytes + kSoftmaxWarps * kOutBytes + ((size_t)B + 1) * 4;
+  }
+};
+
+// Of the eight blocks of a tile: key scales, log2 of value scales over `v_ref`, and the inverses of those ratios.
+struct TileScales {
+  float k[8], v_log[8], v_inv[8];
+  float v_ref, pad[3];
+};
+
+// 0xFF in each byte of w that is a NaN code.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  const uint32_t bit = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // (a carry stays within its byte)
+  return (bit >> 7) * 0xFFu;
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// NaN for the dims d0 .. d0 + 15 in which a position that the row sees, in this segment's masked tiles, has a NaN code.
+__device__ __noinline__ uint32_t nan_dims(const Paged8Args& a, const int32_t* table, TileRange r, int i0, int n, int p_lo,
+                                          int p_hi, int p, int g, int d0) {
+  uint32_t dims = 0;
+  for (int i = i0; i < i0 + n; ++i) {
+    const int j0 = r.tile(i) * kTN;
+    if (tile_open<kTN>(a, j0, p_lo, p_hi)) continue;
+    for (int j = j0; j < j0 + kTN; ++j) {
+      if (!paged_sees(a, p, j)) continue;
+      const int page = table[j >> a.page_shift];
+      if (page < 0 || page >= a.num_pages) continue;
+      const uint4 c = __ldcg(reinterpret_cast<const uint4*>(a.vc8 + page * a.page_stride + g * a.head_stride +
+                                                            (j & ((1 << a.page_shift) - 1)) * a.row_stride + d0));
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      for (int e = 0; e < 16; ++e)
+        if ((w[e / 4] >> (8 * (e % 4)) & 0x7Fu) == 0x7Fu) dims |= 1u << e;
+    }
+  }
+  return dims;
+}
+
+// Softmax of tiles i .. n - 1 of a segment (the first one's scores are there, masked) for a warp with a row beyond kFar:
+// scaled scores are rounded before the reference is taken off, 32 at a time.  done < 0: a wait timed out.
+struct FarRow {
+  float m, l, v_ref;
+  int done, infos;
+};
+template <int D>
+__device__ __noinline__ FarRow far_tiles8(const PagedArgs& a, Item x, int i0, int i, int n, int p, uint32_t tS, uint32_t tO,
+                                          uint32_t sfull, int done, uint32_t pfull, uint32_t info0, int infos,
+                                          const TileScales* scales, float q_scale, volatile int* abort_s, FarRow row) {
+  float m = row.m, l = row.l, v_ref = row.v_ref;
+  for (bool waited = true; i < n; ++i, waited = false) {
+    if (!waited) {
+      const int j0 = x.r.tile(i0 + i) * kTN;
+      if (!mbar_wait_warp(sfull, done & 1, abort_s, a.err) ||
+          !mbar_wait_warp(info0 + 8u * (infos & 3), (infos >> 2) & 1, abort_s, a.err))
+        return FarRow{m, l, v_ref, -1, infos};
+      ++done;
+      ++infos;
+      tc_fence_after();
+      if (!tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) mask_scores(a, tS, p, j0);
+    }
+    const volatile TileScales* ts = scales + ((infos - 1) & 3);
+    float mx = -INFINITY, by = 1.f, sum = 0.f;
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(tS + c, v);
+      const float k0 = ts->k[c / 16] * q_scale, k1 = ts->k[c / 16 + 1] * q_scale;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]) * (e < 16 ? k0 : k1));
+    }
+    if (mx > m && (m == -INFINITY || mx - m > kLazy)) {
+      by = ex2(m - mx);   // 0 if nothing was seen before
+      m = mx;
+      l *= by;
+    }
+    by *= v_ref / ts->v_ref;
+    v_ref = ts->v_ref;
+    const float ref = m == -INFINITY ? 0.f : m;
+    __syncwarp();
+    if (i > 0) rescale<D>(tO, by);
+    // (numerators of 32 scores take the place of the 16 before them, which have been read)
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      uint32_t v[32], pk[16];
+      tmem_ld32(tS + c, v);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int blk = c / 16 + half;
+        const float k = ts->k[blk] * q_scale, up = kLift + ts->v_log[blk];
+        float s = 0.f;
+#pragma unroll
+        for (int e = 16 * half; e < 16 * half + 16; e += 2) {
+          const float p0 = ex2((__fmul_rn(__uint_as_float(v[e]), k) - ref) + up);
+          const float p1 = ex2((__fmul_rn(__uint_as_float(v[e + 1]), k) - ref) + up);
+          s += p0 + p1;
+          pk[e / 2] = pack16<true>(p0, p1);
+        }
+        sum += s * ts->v_inv[blk];
+      }
+      tmem_st16(tS + c / 2, pk);
+      if (c == 32 || c == 96) {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(pfull + 8u * (c / 64));
+        __syncwarp();
+      }
+    }
+    l += sum;
+  }
+  return FarRow{m, l, v_ref, done, infos};
+}
+
+template <int D, bool FP16>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk8_kernel(const __grid_constant__ CUtensorMap q_map, const Paged8Args a, const ChunkSplit split) {
+  using C = Chunk8<D>;
+  extern __shared__ uint8_t sm_raw[];
+  // barriers: stages (full, empty), q empty, per row tile q full, q converted, S full, P full (its first and its second
+  // half), O full, O empty; scales (a slot each)
+  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 1 + 14 + kInfos];
+  __shared__ __align__(16) TileScales scales_s[kInfos];
+  __shared__ uint32_t warp_s[kThreads / 32];
+  __shared__ Share share_s;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_s;
+  __shared__ int bad_s[4];   // segment + 1 whose values had NaN codes that a row sees
+  const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
+  const uint32_t sQ = base, sKV = base + 2 * C::kTileBytes;
+  const uint32_t sOut = sKV + C::kStages * C::kStageBytes;
+  uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (sOut - raw) + kSoftmaxWarps * kOutBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto FULL = [&](int s) { return bar0 + 8u * s; };
+  auto EMPTY = [&](int s) { return bar0 + 8u * (C::kStages + s); };
+  constexpr int kB = 2 * C::kStages;
+  const uint32_t QEMPTY = bar0 + 8u * kB;
+  auto QFULL = [&](int t) { return bar0 + 8u * (kB + 1 + t); };
+  auto QREADY = [&](int t) { return bar0 + 8u * (kB + 3 + t); };
+  auto SFULL = [&](int t) { return bar0 + 8u * (kB + 5 + t); };
+  auto PFULL = [&](int t, int part) { return bar0 + 8u * (kB + 7 + 2 * t + part); };
+  auto OFULL = [&](int t) { return bar0 + 8u * (kB + 11 + t); };
+  auto OEMPTY = [&](int t) { return bar0 + 8u * (kB + 13 + t); };
+  auto INFO = [&](int s) { return bar0 + 8u * (kB + 15 + s); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = (int)blockIdx.x;
+  const int tpt = 128 / a.G, tokens = 2 * tpt;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(FULL(s), kConvertWarps + 1);
+      mbar_init(EMPTY(s), 1);
+    }
+    mbar_init(QEMPTY, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(QFULL(t), 1);
+      mbar_init(SFULL(t), 1);
+      mbar_init(PFULL(t, 0), 4);
+      mbar_init(PFULL(t, 1), 4);
+      mbar_init(OFULL(t), 1);
+      mbar_init(OEMPTY(t), 4);
+      mbar_init(QREADY(t), 4);
+    }
+    for (int s = 0; s < kInfos; ++s) mbar_init(INFO(s), 1);
+    abort_s = 0;
+    for (int i = 0; i < 4; ++i) bad_s[i] = 0;
+    share_s.lo = share_s.hi = 0;
+    mbar_fence_init();
+    prefetch_tmap(&q_map);
+  }
+  if (warp == kSoftmaxWarps + 1) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  bool bad = false;
+  find_share(a, tokens, pre_s, warp_s, &share_s, bad);
+  if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
+  if (tid == 0) split.rec[cta].until = split.rec[cta].first = -1;
+  // Lanes part ways in the schedule (and below, wherever a lane's own data decides).  Every such place ends in
+  // __syncwarp before the warp's next collective instruction.
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  // Walks the segments of the share: body(b, s, g, item, i0, n, u) for tiles i0 .. i0 + n - 1 of an item,
+  // the first of them unit u; stops when the body returns false.
+  auto walk = [&](auto&& body) {
+    uint32_t u = share_s.lo, at = share_s.at;
+    const uint32_t hi = share_s.hi;
+    int b = share_s.b, qt = share_s.qt;
+    while (u < hi) {
+      const SeqRows s = load_seq(a, b, bad);
+      for (; u < hi && qt * tokens < s.n; ++qt) {
+        const Item x = item_of(a, s, qt, tokens);
+        const uint32_t units = (uint32_t)x.r.count + kItemUnits;
+        for (int g = 0; g < a.Hkv && u < hi; ++g, at += units) {
+          if (at + units <= u) continue;
+          const int i0 = max((int)(u - at) - kItemUnits, 0), i1 = (int)min(hi - at, units) - kItemUnits;
+          if (!body(b, s, g, x, i0, i1 - i0, u)) return;
+          u = min(hi, at + units);
+        }
+      }
+      qt = 0;
+      ++b;
+    }
+  };
+  // Whether a row at one of the positions p_lo .. p_hi sees some position of the block of 16 at j.
+  auto block_needed = [&](int j, int p_lo, int p_hi) {
+    return j <= p_hi && (a.window == 0 || j + 15 > p_lo - a.window || j < a.sinks);
+  };
+
+  if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kSoftmaxWarps) {
+      // ---- queries, and scales: lane 16 t + 8 kv + block of pairs of tiles, page numbers two pairs ahead, scales one
+      const int lt = lane >> 4, kv = (lane >> 3) & 1, blk = lane & 7;
+      const float* scales = kv ? a.vs : a.ks;
+      uint32_t at = 0, items = 0, tiles = 0;
+      bad = false;
+      walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
+        const bool two = x.n > tpt;
+        if (items > 0 && !mbar_wait_warp(QEMPTY, (items - 1) & 1, &abort_s, a.err)) return false;
+        ++items;
+        if (lane == 0) {   // the queries, once the segment before has done its last scores
+          const uint32_t bytes = (uint32_t)(64 * 2 * a.G * tpt);
+          for (int t = 0; t < (two ? 2 : 1); ++t) {
+            mbar_arrive_expect_tx(QFULL(t), bytes * C::kBoxes);
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+              tma_load_3d(sQ + t * C::kTileBytes + bx * C::kBoxBytes, &q_map, QFULL(t), bx * 64, g * a.G, s.row0 + x.t0 + t * tpt);
+          }
+        }
+        __syncwarp();
+        const int32_t* row = a.table + (size_t)b * a.max_pages;
+        auto block_at = [&](int i) {   // the block's first position in the pair of tiles from i on, -1 if no row sees it
+          const int t = i0 + i + lt;
+          if (i + lt >= n || t >= x.r.count) return -1;
+          const int j = x.r.tile(t) * kTN + blk * 16;
+          return block_needed(j, x.p_lo, x.p_hi) ? j : -1;
+        };
+        auto page_of = [&](int i) {
+          const int j = block_at(i);
+          return j < 0 ? -1 : row[j >> a.page_shift];
+        };
+        auto scale_of = [&](int i, int page) {
+          const int j = block_at(i);
+          if (j < 0 || page < 0 || page >= a.num_pages) return kLeastScale;   // (a bad page: the converters say so)
+          return scales[scale_index(page, a.Hkv, g, a.page_shift, j & ((1 << a.page_shift) - 1))];
+        };
+        int page = page_of(0);
+        float ahead = scale_of(0, page), now = 0.f, top = 0.f, v_ref = kLeastScale;
+        page = page_of(2);
+        for (int i = 0; i < n; ++i, ++at, ++tiles) {
+          if ((i & 1) == 0) {
+            now = ahead;
+            if (!scale_ok(now)) {
+              bad = true;
+              now = kLeastScale;
+            }
+            ahead = scale_of(i + 2, page);
+            page = page_of(i + 4);
+            __syncwarp();
+            top = now;
+#pragma unroll
+            for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+          }
+          __syncwarp();
+          v_ref = fmaxf(v_ref, __shfl_sync(0xFFFFFFFFu, top, (i & 1) * 16 + 8));
+          // (The slot's scales of four tiles ago are not needed once the ring stage of this tile's keys is free: then
+          // the products of two tiles ago and of all before are done, and with them their softmax.)
+          if (at >= C::kStages && !mbar_wait_warp(EMPTY(at & 1), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
+          TileScales* to = scales_s + (tiles & 3);
+          if (lt == (i & 1)) {
+            if (kv == 0) {
+              to->k[blk] = now;
+            } else {
+              to->v_log[blk] = log2f(now / v_ref);
+              to->v_inv[blk] = v_ref / now;
+              if (blk == 0) to->v_ref = v_ref;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(INFO(tiles & 3));
+            mbar_arrive(FULL(at & 1));
+          }
+          __syncwarp();
+        }
+        // (The last tile's values have a stage of their own.  This warp's word belongs to every stage, so that no stage
+        // can be used up, and its barriers come round to the same parity, before this warp has seen it free.)
+        if (at >= C::kStages && !mbar_wait_warp(EMPTY(at & 1), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
+        if (lane == 0) mbar_arrive(FULL(at & 1));
+        __syncwarp();
+        ++at;
+        return true;
+      });
+      if (bad) raise_flag(a.err, kErrBadPages);
+    } else if (warp == kSoftmaxWarps + 1) {
+      // ---- tensor-core instructions.  The whole warp takes every step, one elected lane issues (by predicate), and
+      // row tile and ring stage are constants of the unrolled code.
+      const uint32_t go = elect_one() ? 1u : 0u;
+      constexpr uint32_t id_s = (1u << 4) | ((kTN >> 3) << 17) | ((128u >> 4) << 24);
+      constexpr uint32_t id_o = (1u << 4) | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
+      constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
+      const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV + C::kTileBytes, C::kBoxBytes);
+      uint32_t at = 0, items = 0, seconds = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
+      auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait_warp(bar, phase & 1, &abort_s, a.err); };
+      // S_t = Q_t K^T with the keys of stage ST
+      auto scores = [&](auto t_c, auto st_c) {
+        constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
+#pragma unroll
+        for (int box = 0; box < C::kBoxes; ++box)
+          tc_mma4_ss(go, t * 128, dq + (t * kTileUnits + box * kBoxUnits), dk + (ST * 2 * kTileUnits + box * kBoxUnits), id_s,
+                     box != 0);
+        tc_commit_if(go, SFULL(t));
+      };
+      // O_t (+)= P_t V, P in two halves, with the values of stage ST; then the next tile's scores
+      auto turn = [&](auto t_c, auto st_c, uint32_t done, bool first, bool more) {
+        constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
+        const uint64_t v = dv + ST * 2 * kTileUnits;
+        if (!wait(PFULL(t, 0), done)) return false;
+        tc_fence_after();
+        tc_mma4_ts(go, kTmemO + t * 128, t * 128, v, id_o, !first);
+        if (!wait(PFULL(t, 1), done)) return false;
+        tc_fence_after();
+        tc_mma4_ts(go, kTmemO + t * 128, t * 128 + 32, v + (8192u >> 4), id_o, 1u);
+        if (more) scores(t_c, st_c);
+        else tc_commit_if(go, OFULL(t));
+        return true;
+      };
+      using Zero = std::integral_constant<int, 0>;
+      using One = std::integral_constant<int, 1>;
+      // body(stage as a constant) for the stage of a tile
+      static_assert(C::kStages == 2, "a tile's stage is its parity");
+      auto at_stage = [&](uint32_t tile, auto&& body) { return tile & 1 ? body(One{}) : body(Zero{}); };
+      walk([&](int, const SeqRows&, int, const Item& x, int, int n_any, uint32_t) {
+        const int n = __shfl_sync(0xFFFFFFFFu, n_any, 0);
+        const bool two = __shfl_sync(0xFFFFFFFFu, (int)(x.n > tpt), 0) != 0;
+        if (!wait(FP16 ? QFULL(0) : QREADY(0), items++)) return false;
+        if (two && !wait(FP16 ? QFULL(1) : QREADY(1), seconds++)) return false;
+        if (!at_stage(at, [&](auto st_c) {
+              constexpr int ST = decltype(st_c)::value;
+              if (!wait(FULL(ST), at >> 1)) return false;
+              tc_fence_after();
+              scores(Zero{}, st_c);
+              if (two) scores(One{}, st_c);
+              tc_commit_if(go, EMPTY(ST));
+              if (n == 1) tc_commit_if(go, QEMPTY);
+              return true;
+            }))
+          return false;
+        ++at;
+        for (int i = 0; i < n; ++i, ++at) {
+          const bool more = i + 1 < n;
+          if (!at_stage(at, [&](auto st_c) {   // the tile's values, the next one's keys
+                constexpr int ST = decltype(st_c)::value;
+                if (!wait(FULL(ST), at >> 1)) return false;
+                // (the second row tile's result too, where this item has none: bad_s is a short ring)
+                if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
+                if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
+                if (!turn(Zero{}, st_c, done0++, i == 0, more)) return false;
+                if (two) {
+                  if (!turn(One{}, st_c, done1++, i == 0, more)) return false;
+                }
+                tc_commit_if(go, EMPTY(ST));
+                if (i + 2 == n) tc_commit_if(go, QEMPTY);
+                return true;
+              }))
+            return false;
+        }
+        ++outs0;
+        outs1 += two;
+        return true;
+      });
+    } else {
+      // ---- codes into operands: a warp has 64 of the tile's positions, 16 bytes of a row a lane, kRows rows at a
+      // time.  While one tile of keys or values is converted, the next is loaded into the same registers.
+      constexpr int kChunks = D / 16, kRows = 32 / kChunks, kPieces = 64 / kRows, kPerBlock = 16 / kRows;
+      const int w = warp - kFirstConvert, q = lane % kChunks, rr = lane / kChunks;
+      const long long step = kRows * a.row_stride;
+      // where a lane's 16 dims go: the box, and the two 16-byte chunks in it, the odd one first in lanes whose partner
+      // of the same bank would otherwise be in the other box (128 dims)
+      const int swap = D == 128 ? q >> 2 : 0;
+      uint32_t at = 0;
+      int seg = 0;
+      uint4 raw4[kPieces];
+      bad = false;
+      walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
+        const int32_t* row = a.table + (size_t)b * a.max_pages;
+        const long long lane_off = g * a.head_stride + rr * a.row_stride + q * 16;
+        // Page numbers of the blocks of four tiles, one a lane, read four tiles ahead; a block that no row needs, or
+        // whose page is bad, is taken as zeros.
+        int pg = 0, ahead = 0;
+        bool need = false;
+        auto read_ahead = [&](int i) {
+          const int t = i0 + i + (lane >> 3);
+          const int j = i + (lane >> 3) < n && t < x.r.count ? x.r.tile(t) * kTN + (lane & 7) * 16 : -1;
+          need = j >= 0 && block_needed(j, x.p_lo, x.p_hi) && (j >> a.page_shift) < a.max_pages;
+          if (need) ahead = row[j >> a.page_shift];
+          __syncwarp();
+        };
+        auto next_pages = [&](int i) {
+          const bool ok = ahead >= 0 && ahead < a.num_pages;
+          pg = need && ok ? ahead : -1;
+          bad |= need && !ok;
+          read_ahead(i + 4);
+        };
+        // Piece k of tile i, of `cache`.
+        auto load = [&](const uint8_t* cache, int i, int k) {
+          const int blk = w * 4 + k / kPerBlock;
+          const int page = __shfl_sync(0xFFFFFFFFu, pg, (i & 3) * 8 + blk);
+          raw4[k] = make_uint4(0, 0, 0, 0);
+          if (page >= 0)
+            raw4[k] = __ldcg(reinterpret_cast<const uint4*>(
+                cache + page * a.page_stride + ((blk * 16) & ((1 << a.page_shift) - 1)) * a.row_stride + (k % kPerBlock) * step +
+                lane_off));
+        };
+        // The tile in registers into the operand at `to`, and behind it tile `next` of `cache` into its place; closed: NaN
+        // codes are taken out (any: some were, of positions from j on that a row sees).
+        auto convert = [&](uint32_t to, const uint8_t* cache, int next, bool more, bool closed, int j, bool* any) {
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k) {
+            const int r = w * 64 + k * kRows + rr;
+            uint32_t c[4] = {raw4[k].x, raw4[k].y, raw4[k].z, raw4[k].w};
+            if (closed) {
+              uint32_t found = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t nan = nan_codes(c[e]);
+                found |= nan;
+                c[e] &= ~nan;
+              }
+              const int at_j = j + r;
+              *any |= found != 0 && at_j <= x.p_hi && (a.window == 0 || at_j > x.p_lo - a.window || at_j < a.sinks);
+            }
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) codes_to_half4(c[e], h[2 * e], h[2 * e + 1]);
+            if (more) load(cache, next, k);
+            const uint32_t line = to + (q >> 2) * C::kBoxBytes + r * 128;
+            const uint32_t c0 = ((2 * q) & 7) ^ (r & 7), c1 = c0 ^ 1u;
+            if (swap) {
+              st_shared16(line + (c1 << 4), h[4], h[5], h[6], h[7]);
+              st_shared16(line + (c0 << 4), h[0], h[1], h[2], h[3]);
+            } else {
+              st_shared16(line + (c0 << 4), h[0], h[1], h[2], h[3]);
+              st_shared16(line + (c1 << 4), h[4], h[5], h[6], h[7]);
+            }
+          }
+        };
+        read_ahead(0);
+        next_pages(0);
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) load(a.kc8, 0, k);
+        for (int i = 0; i <= n; ++i, ++at) {
+          const uint32_t st = at & 1, stage = sKV + st * C::kStageBytes;
+          if (at >= C::kStages && !mbar_wait_warp(EMPTY(st), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
+          bool any = false;
+          if (i > 0) {
+            if (i < n && (i & 3) == 0) next_pages(i);
+            const int j0 = x.r.tile(i0 + i - 1) * kTN;
+            convert(stage + C::kTileBytes, a.kc8, i, i < n, !tile_open<kTN>(a, j0, x.p_lo, x.p_hi), j0, &any);
+            if (any) bad_s[seg & 3] = seg + 1;
+          }
+          if (i < n) convert(stage, a.vc8, i, true, false, 0, &any);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(FULL(st));
+          __syncwarp();
+        }
+        ++seg;
+        return true;
+      });
+      if (bad) raise_flag(a.err, kErrBadPages);
+    }
+  } else {
+    // ---- softmax: row `r` of row tile `t`
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G, head = r - tok * a.G;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = t * 128 + lanes, tO = kTmemO + t * 128 + lanes;
+    int seg = 0, done = 0, outs = 0, infos = 0;   // segments, own tiles, items and all tiles so far
+    walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t u) {
+      const int nt = x.n > tpt ? 2 : 1;
+      if (t >= nt) {
+        ++seg;
+        infos += n;
+        return true;
+      }
+      const bool live = tok < tpt && t * tpt + tok < x.n;
+      const int p = live ? x.p_lo + t * tpt + tok : -1;      // a row that is no token sees nothing
+      float q_scale = a.qk_scale;
+      if (!FP16) {
+        // bf16 times the power of two that brings the row's largest to 2^14 .. 2^15: exact down to 2^-24, and at that within
+        // 2^-40 of the largest
+        if (!mbar_wait_warp(QFULL(t), outs & 1, &abort_s, a.err)) return false;
+        const uint32_t line = sQ + t * C::kTileBytes + r * 128;
+        uint32_t w[D / 2];
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e)
+          ld_shared4(line + (e >> 3) * C::kBoxBytes + (((e & 7) ^ (r & 7)) << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < D / 2; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
+        const int E = (int)(top >> 7), e2 = E == 0 || E == 255 ? 0 : min(max(E - 141, -60), 60);
+        const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+        q_scale *= __uint_as_float((uint32_t)(127 + e2) << 23);
+#pragma unroll
+        for (int e = 0; e < D / 2; ++e) {
+          const float2 f = unpack16<false>(w[e]);
+          w[e] = pack16<true>(f.x * down, f.y * down);
+        }
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e)
+          st_shared16(line + (e >> 3) * C::kBoxBytes + (((e & 7) ^ (r & 7)) << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(QREADY(t));
+        __syncwarp();
+      }
+      float m = -INFINITY, negm = 0.f, l = 0.f, v_ref = kLeastScale;   // negm = kLift - m (0 while nothing is seen)
+      for (int i = 0; i < n; ++i) {
+        const int j0 = x.r.tile(i0 + i) * kTN;
+        const bool open = tile_open<kTN>(a, j0, x.p_lo, x.p_hi);
+        if (!mbar_wait_warp(SFULL(t), done & 1, &abort_s, a.err)) return false;
+        // (After the scores: their stage had the scales' word, so that this phase is the slot's latest.  A row tile that
+        // skips items may come to the slot several phases early.)
+        if (!mbar_wait_warp(INFO(infos & 3), (infos >> 2) & 1, &abort_s, a.err)) return false;
+        const TileScales* ts = scales_s + (infos & 3);
+        ++infos;
+        ++done;
+        tc_fence_after();
+        if (!open) mask_scores(a, tS, p, j0);
+        uint32_t sr[128];
+        tmem_ld128(tS, sr);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          float mx0 = fmaxf(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), mx1 = fmaxf(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+#pragma unroll
+          for (int e = 4; e < 16; e += 4) {
+            mx0 = max3(mx0, __uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1]));
+            mx1 = max3(mx1, __uint_as_float(sr[c + e + 2]), __uint_as_float(sr[c + e + 3]));
+          }
+          mx = fmaxf(mx, fmaxf(mx0, mx1) * (ts->k[c / 16] * q_scale));
+        }
+        // The reference moves if the new maximum is well above it (or is the first).
+        const bool move = mx > m && (m == -INFINITY || mx - m > kLazy);
+        const float v_new = ts->v_ref;
+        if (__any_sync(0xFFFFFFFFu, move || v_new != v_ref)) {
+          if (__any_sync(0xFFFFFFFFu, move && p >= 0 && fabsf(mx) > kFar)) {   // the tiles from here on in another way
+            const FarRow row = far_tiles8<D>(a, x, i0, i, n, p, tS, tO, SFULL(t), done, PFULL(t, 0), INFO(0), infos, scales_s,
+                                             q_scale, &abort_s, FarRow{m, l, v_ref, 0, 0});
+            if (row.done < 0) return false;
+            m = row.m;
+            l = row.l;
+            v_ref = row.v_ref;
+            done = row.done;
+            infos = row.infos;
+            negm = kLift - m;
+            break;
+          }
+          float by = v_ref / v_new;
+          v_ref = v_new;
+          if (move) {
+            const float alpha = m == -INFINITY ? 0.f : ex2(m - mx);
+            m = mx;
+            negm = kLift - mx;
+            l *= alpha;
+            by *= alpha;
+          }
+          __syncwarp();
+          if (i > 0) rescale<D>(tO, by);
+        }
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int blk = c / 16 + half;
+            const float k = ts->k[blk] * q_scale, up = negm + ts->v_log[blk];
+            const uint64_t scale2 = pair2(k, k), up2 = pair2(up, up);
+            uint64_t sum0 = 0, sum1 = 0;   // two fp32 sums each
+#pragma unroll
+            for (int e = 16 * half; e < 16 * half + 16; e += 4) {
+              const float2 x0 = unpair2(fma2(pair2(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])), scale2, up2));
+              const float2 x1 = unpair2(fma2(pair2(__uint_as_float(sr[c + e + 2]), __uint_as_float(sr[c + e + 3])), scale2, up2));
+              const float p0 = ex2(x0.x), p1 = ex2(x0.y), p2 = ex2(x1.x), p3 = ex2(x1.y);
+              sum0 = add2(sum0, pair2(p0, p1));
+              sum1 = add2(sum1, pair2(p2, p3));
+              pk[e / 2] = pack16<true>(p0, p1);
+              pk[e / 2 + 1] = pack16<true>(p2, p3);
+            }
+            const float2 s01 = unpair2(add2(sum0, sum1));
+            l = fmaf(s01.x + s01.y, ts->v_inv[blk], l);
+          }
+          tmem_st16(tS + c / 2, pk);
+          if (c == 32 || c == 96) {   // half of P is there: its part of the product can start
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(PFULL(t, c / 64));
+            __syncwarp();
+          }
+        }
+      }
+      // ---- the item's result, or this share's part of it
+      const int my_seg = seg++;
+      if (!mbar_wait_warp(OFULL(t), outs & 1, &abort_s, a.err)) return false;
+      ++outs;
+      tc_fence_after();
+      const bool whole = i0 == 0 && n == x.r.count;
+      if (*(volatile int*)&bad_s[my_seg & 3] == my_seg + 1) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t v[16];
+          tmem_ld16_wait(tO + c, v);
+          const uint32_t nan =
+              live ? nan_dims(a, a.table + (size_t)b * a.max_pages, x.r, i0, n, x.p_lo, x.p_hi, p, g, c) : 0u;
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = nan & (1u << e) ? 0x7FC00000u : v[e];
+          tmem_st16(tO + c, v);
+          tmem_wait_st();
+        }
+      }
+      __syncwarp();
+      // (O of a row that sees nothing is 0: its tiles are masked.)
+      const float inv = whole ? (p < 0 ? 0.f : v_ref / l) : v_ref;
+      // Rows of the result are stored by four lanes each: lane 4 i + j stores bytes 16 j of rows i, i + 8, ...
+      unsigned long long to[4];
+      {
+        const unsigned long long orow =
+            live ? reinterpret_cast<unsigned long long>(a.o + (long long)(s.row0 + x.t0 + t * tpt + tok) * a.o_stride +
+                                                        (long long)(g * a.G + head) * D)
+                 : 0ull;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          to[k] = __shfl_sync(0xFFFFFFFFu, orow, k * 8 + (lane >> 2));
+          if (to[k] != 0) to[k] += (lane & 3) * 16;
+        }
+      }
+      float* part = split.part + ((size_t)cta * 2 + (i0 == 0 ? 1 : 0)) * C::kPartFloats + 4 * (t * 128 + r);
+      const uint32_t out = sOut + warp * kOutBytes;
+      const uint64_t inv2 = pair2(inv, inv);
+      uint32_t not_finite = 0;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tO + c, v);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {   // pairs 2 e, 2 e + 2 become words e, e + 1
+            const uint64_t f0 = mul2(pair2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), inv2);
+            const uint64_t f1 = mul2(pair2(__uint_as_float(v[2 * e + 2]), __uint_as_float(v[2 * e + 3])), inv2);
+            const float2 y0 = unpair2(f0), y1 = unpair2(f1);
+            v[e] = pack16<FP16>(y0.x, y0.y);
+            v[e + 1] = pack16<FP16>(y1.x, y1.y);
+            not_finite |= non_finite_bits<FP16>(v[e]) | non_finite_bits<FP16>(v[e + 1]);
+          }
+          // 64 bytes a row through shared memory (16-byte pieces XOR-ed against bank conflicts), so that a store
+          // touches 8 rows, not 32.
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            st_shared16(out + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          __syncwarp();
+          uint4 w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = k * 8 + (lane >> 2);
+            ld_shared4(out + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), w[k].x, w[k].y, w[k].z, w[k].w);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (to[k] != 0) *reinterpret_cast<uint4*>(to[k] + 2 * c) = w[k];
+        } else if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + (c + e) * kItemRows) =
+                make_float4(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv, __uint_as_float(v[e + 2]) * inv,
+                            __uint_as_float(v[e + 3]) * inv);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(OEMPTY(t));
+      if (live && (not_finite & kSigns)) raise_flag(a.err, kErrNonFinite);
+      if (!whole) {
+        if (live) {
+          float* stats = part + D * kItemRows - 3 * (t * 128 + r);
+          stats[0] = m == -INFINITY ? kUnseen : -negm;
+          stats[kItemRows] = l;
+        }
+        if (i0 + n < x.r.count && tid == 0) {   // the item goes on: who begins it, and who ends it
+          const uint32_t first = i0 == 0 ? u : u - kItemUnits - i0, end = first + x.r.count + kItemUnits;
+          const uint32_t total = share_s.total;
+          const int ctas = share_s.ctas;
+          auto cut_at = [&](int c) { return snap(share_start(total, c, ctas), first, end, kItemUnits, share_s.slack); };
+          int c = share_of(i0 == 0 ? end - 1 : first, total, ctas);
+          if (i0 == 0) {
+            while (c > cta + 1 && cut_at(c) >= end) --c;
+            split.rec[cta] = SplitRecord{s.row0 + x.t0, g, x.n, x.p_lo, c, cta};
+          } else {
+            while (c + 1 < cta && cut_at(c + 1) <= first) ++c;
+            split.rec[cta].first = c;
+          }
+        }
+      }
+      __syncwarp();
+      return true;
+    });
+  }
+  // After a timeout, copies and products still in flight finish before the CTA gives up its memory.
+  if (tid == 0 && *(volatile int*)&abort_s) {
+    const long long c0 = clock64();
+    while (clock64() - c0 < 4000000ll) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftmaxWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_slot, 512);
+  }
+}
+
+template <int D, bool FP16>
+cudaError_t launch(const CUtensorMap& q_map, const Paged8Args& a, const ChunkSplit& split, int ctas, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(chunk8_kernel<D, FP16>), (int)Chunk8<D>::smem(kPagedMaxSeqs), &ready);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Chunk8<D>::smem(a.B);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, chunk8_kernel<D, FP16>, q_map, a, split);
+  return e == cudaSuccess ? launch_paged_chunk_join(a, D, split, ctas, st) : e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged8_chunk(const gqa_paged_dims& d, const Paged8Args& a, void* scratch, int ctas, cudaStream_t st) {
+  CUtensorMap q_map;
+  std::memset(&q_map, 0, sizeof(q_map));
+  if (!encode_queries(&q_map, a.q, d)) return cudaErrorInvalidValue;
+  const int D = d.head_dim;
+  const ChunkSplit split = paged_chunk_split(D, scratch, ctas);
+  if (D == 128) return a.fp16 ? launch<128, true>(q_map, a, split, ctas, st) : launch<128, false>(q_map, a, split, ctas, st);
+  return a.fp16 ? launch<64, true>(q_map, a, split, ctas, st) : launch<64, false>(q_map, a, split, ctas, st);
+}
+
+}  // namespace moe
