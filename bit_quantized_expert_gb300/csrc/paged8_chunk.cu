@@ -45,9 +45,10 @@ struct Chunk8 {
   static constexpr int kStages = 2;
   static constexpr int kStageBytes = 2 * kTileBytes;           // keys, then values
   static constexpr int kPartFloats = kItemRows * (D + 2);
-  static size_t smem(int B) {
-    return 1024 + (size_t)(2 + 2 * kStages) * kTileBytes + kSoftmaxWarps * kOutBytes + ((size_t)B + 1) * 4;
-  }
+  static constexpr int kRawBytes = kTN * D;                    // codes on their way, a tile of keys or of values
+  // (The schedule's sums lie where the ring will be.)
+  static constexpr int kSmem = 1024 + (2 + 2 * kStages) * kTileBytes + kSoftmaxWarps * kOutBytes + kRawBytes;
+  static_assert((kPagedMaxSeqs + 1) * 4 <= kStages * kStageBytes, "sums fit");
 };
 
 // Of the eight blocks of a tile: key scales, log2 of value scales over `v_ref`, and the inverses of those ratios.
@@ -64,6 +65,11 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// 16 bytes of global memory, or zeros, into shared memory, asynchronously.
+__device__ __forceinline__ void cp_async_16_if(bool go, uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(go ? 16 : 0) : "memory");
 }
 
 // NaN for the dims d0 .. d0 + 15 in which a position that the row sees, in this segment's masked tiles, has a NaN code.
@@ -180,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t sQ = base, sKV = base + 2 * C::kTileBytes;
   const uint32_t sOut = sKV + C::kStages * C::kStageBytes;
-  uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (sOut - raw) + kSoftmaxWarps * kOutBytes);
+  const uint32_t sRaw = sOut + kSoftmaxWarps * kOutBytes;
+  uint32_t* pre_s = reinterpret_cast<uint32_t*>(sm_raw + (sKV - raw));
   const uint32_t bar0 = smem_u32(bars);
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (C::kStages + s); };
@@ -427,17 +434,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       });
     } else {
-      // ---- codes into operands: a warp has 64 of the tile's positions, 16 bytes of a row a lane, kRows rows at a
-      // time.  While one tile of keys or values is converted, the next is loaded into the same registers.
+      // ---- codes into operands: a warp has 64 of the tile's positions, 16 bytes of a row a lane, kRows rows (a piece) at a
+      // time.  Pieces come by asynchronous copies into shared memory, each lane's own 16 bytes by itself, so that nothing but
+      // its own count of copies stands between them and their use: while one tile of keys or values is converted, the
+      // next one's pieces take its places.  (Held in registers they are 64 a lane, too many beside the rest: the
+      // compiler stored some as they arrived, and 2048 tokens at 32768 took 1,130 us.)
       constexpr int kChunks = D / 16, kRows = 32 / kChunks, kPieces = 64 / kRows, kPerBlock = 16 / kRows;
-      const int w = warp - kFirstConvert, q = lane % kChunks, rr = lane / kChunks;
+      const int w = warp - kFirstConvert;
+      // A lane's 16 dims q and its row of a piece: eight lanes in a row have two rows of one box of 64 dims, so that the
+      // chunks that they store lie in different banks.
+      const int q = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3, rr = D == 128 ? (lane >> 2) & 3 : lane >> 2;
       const long long step = kRows * a.row_stride;
-      // where a lane's 16 dims go: the box, and the two 16-byte chunks in it, the odd one first in lanes whose partner
-      // of the same bank would otherwise be in the other box (128 dims)
-      const int swap = D == 128 ? q >> 2 : 0;
+      const uint32_t line = (q >> 2) * C::kBoxBytes + (w * 64 + rr) * 128, chunk = ((2 * q) & 7) ^ (rr & 7);
       uint32_t at = 0;
       int seg = 0;
-      uint4 raw4[kPieces];
+      const uint32_t mine = sRaw + w * (kPieces * 512) + lane * 16;
       bad = false;
       walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
         const int32_t* row = a.table + (size_t)b * a.max_pages;
@@ -459,64 +470,75 @@ __global__ void __launch_bounds__(kThreads, 1)
           bad |= need && !ok;
           read_ahead(i + 4);
         };
-        // Piece k of tile i, of `cache`.
-        auto load = [&](const uint8_t* cache, int i, int k) {
-          const int blk = w * 4 + k / kPerBlock;
-          const int page = __shfl_sync(0xFFFFFFFFu, pg, (i & 3) * 8 + blk);
-          raw4[k] = make_uint4(0, 0, 0, 0);
-          if (page >= 0)
-            raw4[k] = __ldcg(reinterpret_cast<const uint4*>(
-                cache + page * a.page_stride + ((blk * 16) & ((1 << a.page_shift) - 1)) * a.row_stride + (k % kPerBlock) * step +
-                lane_off));
+        // The pieces of block blk of tile i of `cache`, one a call, to its places in the ring.
+        const uint8_t* from = a.kc8;
+        int page = -1;
+        auto block_of = [&](const uint8_t* cache, int i, int blk, bool more) {
+          page = __shfl_sync(0xFFFFFFFFu, pg, (i & 3) * 8 + w * 4 + blk);
+          if (!more) page = -1;
+          from = page < 0 ? cache
+                          : cache + page * a.page_stride + (((w * 4 + blk) * 16) & ((1 << a.page_shift) - 1)) * a.row_stride + lane_off;
         };
-        // The tile in registers into the operand at `to`, and behind it tile `next` of `cache` into its place; closed: NaN
-        // codes are taken out (any: some were, of positions from j on that a row sees).
-        auto convert = [&](uint32_t to, const uint8_t* cache, int next, bool more, bool closed, int j, bool* any) {
-#pragma unroll
-          for (int k = 0; k < kPieces; ++k) {
-            const int r = w * 64 + k * kRows + rr;
-            uint32_t c[4] = {raw4[k].x, raw4[k].y, raw4[k].z, raw4[k].w};
-            if (closed) {
-              uint32_t found = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t nan = nan_codes(c[e]);
-                found |= nan;
-                c[e] &= ~nan;
-              }
-              const int at_j = j + r;
-              *any |= found != 0 && at_j <= x.p_hi && (a.window == 0 || at_j > x.p_lo - a.window || at_j < a.sinks);
-            }
-            uint32_t h[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) codes_to_half4(c[e], h[2 * e], h[2 * e + 1]);
-            if (more) load(cache, next, k);
-            const uint32_t line = to + (q >> 2) * C::kBoxBytes + r * 128;
-            const uint32_t c0 = ((2 * q) & 7) ^ (r & 7), c1 = c0 ^ 1u;
-            if (swap) {
-              st_shared16(line + (c1 << 4), h[4], h[5], h[6], h[7]);
-              st_shared16(line + (c0 << 4), h[0], h[1], h[2], h[3]);
-            } else {
-              st_shared16(line + (c0 << 4), h[0], h[1], h[2], h[3]);
-              st_shared16(line + (c1 << 4), h[4], h[5], h[6], h[7]);
-            }
-          }
+        auto load = [&](uint32_t to) {
+          cp_async_16_if(page >= 0, to, from);
+          cp_async_commit();
+          from += page < 0 ? 0 : step;
         };
         read_ahead(0);
         next_pages(0);
+#pragma unroll 1
+        for (int blk = 0; blk < 4; ++blk) {
+          block_of(a.kc8, 0, blk, true);
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) load(a.kc8, 0, k);
+          for (int k = 0; k < kPerBlock; ++k) load(mine + (blk * kPerBlock + k) * 512);
+        }
         for (int i = 0; i <= n; ++i, ++at) {
           const uint32_t st = at & 1, stage = sKV + st * C::kStageBytes;
           if (at >= C::kStages && !mbar_wait_warp(EMPTY(st), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
-          bool any = false;
-          if (i > 0) {
-            if (i < n && (i & 3) == 0) next_pages(i);
-            const int j0 = x.r.tile(i0 + i - 1) * kTN;
-            convert(stage + C::kTileBytes, a.kc8, i, i < n, !tile_open<kTN>(a, j0, x.p_lo, x.p_hi), j0, &any);
-            if (any) bad_s[seg & 3] = seg + 1;
+          if (i > 0 && i < n && (i & 3) == 0) next_pages(i);
+          const int j0 = i > 0 ? x.r.tile(i0 + i - 1) * kTN : 0;
+          if (i > 0 && !tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) {
+            // The values of a masked tile: NaN codes are taken out where they lie.
+            cp_async_wait<0>();
+#pragma unroll 1
+            for (int k = 0; k < kPieces; ++k) {
+              uint32_t c[4], nan[4];
+              ld_shared4(mine + k * 512, c[0], c[1], c[2], c[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) nan[e] = nan_codes(c[e]);
+              if ((nan[0] | nan[1] | nan[2] | nan[3]) != 0) {
+                st_shared16(mine + k * 512, c[0] & ~nan[0], c[1] & ~nan[1], c[2] & ~nan[2], c[3] & ~nan[3]);
+                const int j = j0 + w * 64 + k * kRows + rr;
+                if (j <= x.p_hi && (a.window == 0 || j > x.p_lo - a.window || j < a.sinks)) bad_s[seg & 3] = seg + 1;
+              }
+            }
+            __syncwarp();
           }
-          if (i < n) convert(stage, a.vc8, i, true, false, 0, &any);
+          // The values of tile i - 1, then the keys of tile i, one code for both (twice as many instructions would be
+          // fetched anew each time), a block a turn; behind them come the keys of tile i and its values.
+#pragma unroll 1
+          for (int kv = i > 0 ? 1 : 0; kv >= (i < n ? 0 : 1); --kv) {
+            uint32_t to = stage + kv * C::kTileBytes + line + (chunk << 4), in = mine;
+#pragma unroll 1
+            for (int blk = 0; blk < 4; ++blk) {
+              block_of(kv ? a.kc8 : a.vc8, i, blk, i < n);
+#pragma unroll
+              for (int k = 0; k < kPerBlock; ++k) {
+                uint32_t c[4], h[8];
+                cp_async_wait<kPieces - 1>();   // the oldest of as many
+                ld_shared4(in, c[0], c[1], c[2], c[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) codes_to_half4(c[e], h[2 * e], h[2 * e + 1]);
+                load(in);
+                // rows 4 and 8 apart differ by one bit of the chunk in the swizzle, and not at all
+                const uint32_t at1 = kRows == 4 && k % 2 == 1 ? to ^ 64u : to;
+                st_shared16(at1, h[0], h[1], h[2], h[3]);
+                st_shared16(at1 ^ 16u, h[4], h[5], h[6], h[7]);
+                to += kRows * 128;
+                in += 512;
+              }
+            }
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(FULL(st));
@@ -783,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool FP16>
 cudaError_t launch(const CUtensorMap& q_map, const Paged8Args& a, const ChunkSplit& split, int ctas, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(chunk8_kernel<D, FP16>), (int)Chunk8<D>::smem(kPagedMaxSeqs), &ready);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(chunk8_kernel<D, FP16>), Chunk8<D>::kSmem, &ready);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -791,7 +813,7 @@ cudaError_t launch(const CUtensorMap& q_map, const Paged8Args& a, const ChunkSpl
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Chunk8<D>::smem(a.B);
+  cfg.dynamicSmemBytes = Chunk8<D>::kSmem;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
