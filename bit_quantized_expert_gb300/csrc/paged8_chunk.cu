@@ -521,22 +521,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t to = stage + kv * C::kTileBytes + line + (chunk << 4), in = mine;
 #pragma unroll 1
             for (int blk = 0; blk < 4; ++blk) {
+              uint32_t c[kPerBlock][4];
+              cp_async_wait<kPieces - kPerBlock>();   // the oldest block
+#pragma unroll
+              for (int k = 0; k < kPerBlock; ++k) ld_shared4(in + k * 512, c[k][0], c[k][1], c[k][2], c[k][3]);
               block_of(kv ? a.kc8 : a.vc8, i, blk, i < n);
+              uint32_t h[kPerBlock][8];
+#pragma unroll
+              for (int k = 0; k < kPerBlock; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) codes_to_half4(c[k][e], h[k][2 * e], h[k][2 * e + 1]);
 #pragma unroll
               for (int k = 0; k < kPerBlock; ++k) {
-                uint32_t c[4], h[8];
-                cp_async_wait<kPieces - 1>();   // the oldest of as many
-                ld_shared4(in, c[0], c[1], c[2], c[3]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) codes_to_half4(c[e], h[2 * e], h[2 * e + 1]);
-                load(in);
                 // rows 4 and 8 apart differ by one bit of the chunk in the swizzle, and not at all
-                const uint32_t at1 = kRows == 4 && k % 2 == 1 ? to ^ 64u : to;
-                st_shared16(at1, h[0], h[1], h[2], h[3]);
-                st_shared16(at1 ^ 16u, h[4], h[5], h[6], h[7]);
-                to += kRows * 128;
-                in += 512;
+                const uint32_t at1 = (kRows == 4 && k % 2 == 1 ? to ^ 64u : to) + k * kRows * 128;
+                st_shared16(at1, h[k][0], h[k][1], h[k][2], h[k][3]);
+                st_shared16(at1 ^ 16u, h[k][4], h[k][5], h[k][6], h[k][7]);
+                load(in + k * 512);
               }
+              to += 16 * 128;
+              in += kPerBlock * 512;
             }
           }
           fence_proxy_async_smem();
