@@ -25,10 +25,11 @@
 namespace moe {
 namespace {
 
-constexpr int kConvertWarps = 2;
-constexpr int kFirstConvert = 10;
-// Registers a thread: 168 at launch; 2 * 200 + 104 = 3 * 168 after the split.
-constexpr int kRegsSoftmax = 200, kRegsOther = 104;
+constexpr int kThreads = 512;               // two softmax warpgroups, one for queries, scales and products, one for codes
+constexpr int kConvertWarps = 4;
+constexpr int kFirstConvert = 12;
+// Registers a thread: 128 at launch; 2 * 192 + 64 + 64 = 4 * 128 after the split.
+constexpr int kRegsSoftmax = 192, kRegsOther = 64;
 // Base-2 units by which the numerators' reference may lag behind the row's maximum, and by which it stands
 // below the maximum that sets it: fp16's range from 2^15 down.
 constexpr float kLazy = 6.f, kLift = 9.f;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   bool bad = false;
-  find_share(a, tokens, pre_s, warp_s, &share_s, bad);
+  find_share<kThreads>(a, tokens, pre_s, warp_s, &share_s, bad);
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
   if (tid == 0) split.rec[cta].until = split.rec[cta].first = -1;
   // Lanes part ways in the schedule (and below, wherever a lane's own data decides).  Every such place ends in
@@ -433,19 +434,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         outs1 += two;
         return true;
       });
-    } else {
-      // ---- codes into operands: a warp has 64 of the tile's positions, 16 bytes of a row a lane, kRows rows (a piece) at a
+    } else if (warp >= kFirstConvert) {
+      // ---- codes into operands: a warp has 32 of the tile's positions, 16 bytes of a row a lane, kRows rows (a piece) at a
       // time.  Pieces come by asynchronous copies into shared memory, each lane's own 16 bytes by itself, so that nothing but
       // its own count of copies stands between them and their use: while one tile of keys or values is converted, the
       // next one's pieces take its places.  (Held in registers they are 64 a lane, too many beside the rest: the
       // compiler stored some as they arrived, and 2048 tokens at 32768 took 1,130 us.)
-      constexpr int kChunks = D / 16, kRows = 32 / kChunks, kPieces = 64 / kRows, kPerBlock = 16 / kRows;
+      constexpr int kPositions = kTN / kConvertWarps, kBlocks = kPositions / 16, kChunks = D / 16, kRows = 32 / kChunks, kPieces = kPositions / kRows, kPerBlock = 16 / kRows;
       const int w = warp - kFirstConvert;
       // A lane's 16 dims q and its row of a piece: eight lanes in a row have two rows of one box of 64 dims, so that the
       // chunks that they store lie in different banks.
       const int q = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3, rr = D == 128 ? (lane >> 2) & 3 : lane >> 2;
       const long long step = kRows * a.row_stride;
-      const uint32_t line = (q >> 2) * C::kBoxBytes + (w * 64 + rr) * 128, chunk = ((2 * q) & 7) ^ (rr & 7);
+      const uint32_t line = (q >> 2) * C::kBoxBytes + (w * kPositions + rr) * 128, chunk = ((2 * q) & 7) ^ (rr & 7);
       uint32_t at = 0;
       int seg = 0;
       const uint32_t mine = sRaw + w * (kPieces * 512) + lane * 16;
@@ -474,10 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* from = a.kc8;
         int page = -1;
         auto block_of = [&](const uint8_t* cache, int i, int blk, bool more) {
-          page = __shfl_sync(0xFFFFFFFFu, pg, (i & 3) * 8 + w * 4 + blk);
+          page = __shfl_sync(0xFFFFFFFFu, pg, (i & 3) * 8 + w * kBlocks + blk);
           if (!more) page = -1;
           from = page < 0 ? cache
-                          : cache + page * a.page_stride + (((w * 4 + blk) * 16) & ((1 << a.page_shift) - 1)) * a.row_stride + lane_off;
+                          : cache + page * a.page_stride + (((w * kBlocks + blk) * 16) & ((1 << a.page_shift) - 1)) * a.row_stride + lane_off;
         };
         auto load = [&](uint32_t to) {
           cp_async_16_if(page >= 0, to, from);
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         read_ahead(0);
         next_pages(0);
 #pragma unroll 1
-        for (int blk = 0; blk < 4; ++blk) {
+        for (int blk = 0; blk < kBlocks; ++blk) {
           block_of(a.kc8, 0, blk, true);
 #pragma unroll
           for (int k = 0; k < kPerBlock; ++k) load(mine + (blk * kPerBlock + k) * 512);
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 4; ++e) nan[e] = nan_codes(c[e]);
               if ((nan[0] | nan[1] | nan[2] | nan[3]) != 0) {
                 st_shared16(mine + k * 512, c[0] & ~nan[0], c[1] & ~nan[1], c[2] & ~nan[2], c[3] & ~nan[3]);
-                const int j = j0 + w * 64 + k * kRows + rr;
+                const int j = j0 + w * kPositions + k * kRows + rr;
                 if (j <= x.p_hi && (a.window == 0 || j > x.p_lo - a.window || j < a.sinks)) bad_s[seg & 3] = seg + 1;
               }
             }
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kv = i > 0 ? 1 : 0; kv >= (i < n ? 0 : 1); --kv) {
             uint32_t to = stage + kv * C::kTileBytes + line + (chunk << 4), in = mine;
 #pragma unroll 1
-            for (int blk = 0; blk < 4; ++blk) {
+            for (int blk = 0; blk < kBlocks; ++blk) {
               uint32_t c[kPerBlock][4];
               cp_async_wait<kPieces - kPerBlock>();   // the oldest block
 #pragma unroll

@@ -34,6 +34,7 @@
 namespace moe {
 namespace {
 
+constexpr int kThreads = 384;               // two softmax warpgroups, one for copies and products
 constexpr int kScanWarps = 2;
 // Registers a thread: 168 at launch; 2 * 200 + 104 = 3 * 168 after the split.
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   bool bad = false;
-  find_share(a, tokens, pre_s, warp_s, &share_s, bad);
+  find_share<kThreads>(a, tokens, pre_s, warp_s, &share_s, bad);
   if (bad && cta == 0) raise_flag(a.err, kErrBadPages);
   if (tid == 0) split.rec[cta].until = split.rec[cta].first = -1;
   // Lanes part ways in the schedule (and below, wherever a lane's own data decides).  Every such place ends in

@@ -10,7 +10,6 @@ namespace moe {
 namespace {
 
 constexpr int kTN = 128;                    // positions per cache tile
-constexpr int kThreads = 384;               // two softmax warpgroups, one for copies and products
 constexpr int kSoftmaxWarps = 8;
 constexpr int kItemRows = 256;              // two row tiles
 constexpr uint32_t kTmemO = 256;            // columns: S0 0, S1 128, O0 256, O1 384 (all 512 are allocated: base 0)
@@ -45,18 +44,19 @@ struct Share {
 // Finds this CTA's share, by the block together: row blocks per sequence are scanned into pre_s[0 .. B], then
 // their costs (units times heads), a run of consecutive row blocks a thread; the threads whose runs hold the
 // two cuts walk theirs once more.  Leaves the share empty if there is nothing to do, or (bad) 2^32 units or more.
+template <int NT>
 __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint32_t* pre_s, uint32_t* warp_s,
                                            Share* share_s, bool& bad) {
   const int tid = threadIdx.x, cta = (int)blockIdx.x;
   bool over;
-  const uint32_t blocks = scan_sequences<kThreads>(a.B, pre_s, warp_s, &over, [&](int b) {
+  const uint32_t blocks = scan_sequences<NT>(a.B, pre_s, warp_s, &over, [&](int b) {
     return (uint32_t)(load_seq(a, b, bad).n + tokens - 1) / (uint32_t)tokens;
   });
   if (over) {
     bad = true;
     return;
   }
-  const uint32_t per = (blocks + kThreads - 1) / kThreads;
+  const uint32_t per = (blocks + NT - 1) / NT;
   const uint32_t i0 = min(tid * per, blocks), i1 = min(i0 + per, blocks);
   // body(b, qt, units of an item) for the row blocks i0 .. i1 - 1
   auto run = [&](auto&& body) {
@@ -82,7 +82,7 @@ __device__ __forceinline__ void find_share(const PagedArgs& a, int tokens, uint3
     units_last = units;
   });
   uint32_t total;
-  uint32_t at = exclusive_scan<kThreads>(mine, warp_s, &total, &over);
+  uint32_t at = exclusive_scan<NT>(mine, warp_s, &total, &over);
   if (over) bad = true;
   if (over || total == 0) return;
   const int ctas = (int)min(gridDim.x, total);   // no more shares than units
