@@ -131,12 +131,8 @@ __global__ void __launch_bounds__(kWalkThreads) append8_kernel(const WalkArgs a)
     // top = 1.m * 2^(E - 127) <= 448 * 2^e = 1.75 * 2^(8 + e) from e = E - 135 on, or one more where 1.m > 1.75
     const int e = min(max((int)(top >> 23) - 135 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0), -60), 60);
     const float s = fmaxf(__uint_as_float((uint32_t)(e + 127) << 23), was);
-    const bool power = (__float_as_uint(s) & 0x7FFFFFu) == 0;
-    const float inv = 1.f / s, ratio = was / s;
-    auto code = [&](float v) {
-      const float y = power ? v * inv : v / s;
-      return fabsf(v) <= 448.f * kMostScale ? y : __uint_as_float(0x7FC00000u);
-    };
+    const float inv = 1.f / s, ratio = was / s;   // exact
+    auto code = [&](float v) { return fabsf(v) <= 448.f * kMostScale ? v * inv : __uint_as_float(0x7FC00000u); };
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
       const int o = r0 + i * kStep;

@@ -16,7 +16,10 @@ struct Paged8Args : PagedArgs {
   const float *ks, *vs;       // [num_pages, Hkv, page_size / 16]
 };
 
-__device__ __forceinline__ bool scale_ok(float s) { return s >= kLeastScale && s <= kMostScale; }   // (NaN: no)
+// A power of two in the scales' range.
+__device__ __forceinline__ bool scale_ok(float s) {
+  return s >= kLeastScale && s <= kMostScale && (__float_as_uint(s) & 0x7FFFFFu) == 0;
+}
 
 // Index of the scale of the block at offset `off` of a page.  Fits: num_pages * page_size * Hkv < 2^31.
 __device__ __forceinline__ int scale_index(int page, int Hkv, int g, int page_shift, int off) {

@@ -5,17 +5,16 @@
 // form (paged_chunk.cu).  What differs:
 //
 //   * Operands.  The tensor cores take e4m3 beside e4m3 alone, and queries and numerators need more bits than
-//     that, so codes become fp16, exactly, on their way into shared memory: two warps (10 and 11) load them from
-//     global memory into registers, one tile of keys or of values ahead, convert and store them in the operands' swizzle.
-//     A tile of the softmax takes ~2,800 cycles, its conversion about half of that, beside it.
-//   * Scales.  Warp 8 reads the tile's sixteen and leaves, in a ring of four, each block's key scale, the logarithm
-//     of its value scale over the largest that the segment has met, and the inverse of that ratio.  A score's exponent is
-//     score * (key scale * row scale) - reference + logarithm, one fma as without scales; numerators come out in the
-//     scale of the products with V (O is in units of the largest value scale), and the row's sum takes each
-//     block's sum times the inverse.
+//     that, so codes become fp16 on their way into shared memory: four warps (12 to 15) bring them there by asynchronous
+//     copies, one tile of keys or of values ahead, convert them and store them in the operands' swizzle.
+//   * Scales.  The same warps read the tile's sixteen, four tiles ahead, and multiply a block's codes by its scale over a
+//     reference: for keys the tile's largest scale, for values the largest that the segment has met.  These are
+//     powers of two, so that nothing is rounded but what is 2^-15 of the reference's scale and less, and then by 2^-25 of it
+//     at most.  The softmax then sees one factor a tile, and O is in units of the values' reference.  (Each block's
+//     factors in the softmax, which has no time to spare, kept such blocks exact too: 521 us in place of 466.)
 //   * Queries.  bf16 ones are scaled by a power of two a row so that fp16 holds them: by the softmax threads, a row each, in
 //     shared memory before the item's first product.
-//   * NaN codes of masked tiles' values are taken out as they are converted.
+//   * NaN codes of masked tiles' values are taken out before they are converted.
 #include <cmath>
 #include <cstring>
 
@@ -28,14 +27,15 @@ namespace {
 constexpr int kThreads = 512;               // two softmax warpgroups, one for queries, scales and products, one for codes
 constexpr int kConvertWarps = 4;
 constexpr int kFirstConvert = 12;
-// Registers a thread: 128 at launch; 2 * 192 + 64 + 64 = 4 * 128 after the split.
-constexpr int kRegsSoftmax = 192, kRegsOther = 64;
+// Registers a thread: 128 at launch; 2 * 184 + 64 + 80 = 4 * 128 after the split.
+constexpr int kRegsSoftmax = 184, kRegsIssue = 64, kRegsConvert = 80;
+static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "no more than at launch");
 // Base-2 units by which the numerators' reference may lag behind the row's maximum, and by which it stands
 // below the maximum that sets it: fp16's range from 2^15 down.
 constexpr float kLazy = 6.f, kLift = 9.f;
 // Base-2 units from which on a row's reference is taken off its scaled scores apart (far_tiles8).
 constexpr float kFar = 65536.f;
-constexpr int kInfos = 4;
+constexpr int kInfos = 4;                   // slots for tiles' scales, a power of two
 
 template <int D>
 struct Chunk8 {
@@ -52,10 +52,9 @@ struct Chunk8 {
   static_assert((kPagedMaxSeqs + 1) * 4 <= kStages * kStageBytes, "sums fit");
 };
 
-// Of the eight blocks of a tile: key scales, log2 of value scales over `v_ref`, and the inverses of those ratios.
+// The references of a tile's scales.
 struct TileScales {
-  float k[8], v_log[8], v_inv[8];
-  float v_ref, pad[3];
+  float k_ref, v_ref;
 };
 
 // 0xFF in each byte of w that is a NaN code.
@@ -71,6 +70,12 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y,
 // 16 bytes of global memory, or zeros, into shared memory, asynchronously.
 __device__ __forceinline__ void cp_async_16_if(bool go, uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(go ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 // NaN for the dims d0 .. d0 + 15 in which a position that the row sees, in this segment's masked tiles, has a NaN code.
@@ -98,42 +103,42 @@ __device__ __noinline__ uint32_t nan_dims(const Paged8Args& a, const int32_t* ta
 // scaled scores are rounded before the reference is taken off, 32 at a time.  done < 0: a wait timed out.
 struct FarRow {
   float m, l, v_ref;
-  int done, infos;
+  int done, tiles;
 };
 template <int D>
-__device__ __noinline__ FarRow far_tiles8(const PagedArgs& a, Item x, int i0, int i, int n, int p, uint32_t tS, uint32_t tO,
-                                          uint32_t sfull, int done, uint32_t pfull, uint32_t info0, int infos,
-                                          const TileScales* scales, float q_scale, volatile int* abort_s, FarRow row) {
+__device__ __noinline__ FarRow far_tiles8(const Paged8Args& a, Item x, int i0, int i, int n, int p, uint32_t tS, uint32_t tO,
+                                          uint32_t sfull, uint32_t pfull, const TileScales* scales, float q_scale,
+                                          volatile int* abort_s, FarRow row) {
   float m = row.m, l = row.l, v_ref = row.v_ref;
+  int done = row.done, tiles = row.tiles;
   for (bool waited = true; i < n; ++i, waited = false) {
     if (!waited) {
       const int j0 = x.r.tile(i0 + i) * kTN;
-      if (!mbar_wait_warp(sfull, done & 1, abort_s, a.err) ||
-          !mbar_wait_warp(info0 + 8u * (infos & 3), (infos >> 2) & 1, abort_s, a.err))
-        return FarRow{m, l, v_ref, -1, infos};
+      if (!mbar_wait_warp(sfull, done & 1, abort_s, a.err)) return FarRow{m, l, v_ref, -1, tiles};
       ++done;
-      ++infos;
+      ++tiles;
       tc_fence_after();
       if (!tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) mask_scores(a, tS, p, j0);
     }
-    const volatile TileScales* ts = scales + ((infos - 1) & 3);
+    const volatile TileScales* ts = scales + ((tiles - 1) & (kInfos - 1));
+    const float k = ts->k_ref * q_scale, v_new = ts->v_ref;
     float mx = -INFINITY, by = 1.f, sum = 0.f;
     __syncwarp();
 #pragma unroll 1
     for (int c = 0; c < 128; c += 32) {
       uint32_t v[32];
       tmem_ld32(tS + c, v);
-      const float k0 = ts->k[c / 16] * q_scale, k1 = ts->k[c / 16 + 1] * q_scale;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]) * (e < 16 ? k0 : k1));
+      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
     }
+    mx *= k;
     if (mx > m && (m == -INFINITY || mx - m > kLazy)) {
       by = ex2(m - mx);   // 0 if nothing was seen before
       m = mx;
       l *= by;
     }
-    by *= v_ref / ts->v_ref;
-    v_ref = ts->v_ref;
+    by *= v_ref / v_new;
+    v_ref = v_new;
     const float ref = m == -INFINITY ? 0.f : m;
     __syncwarp();
     if (i > 0) rescale<D>(tO, by);
@@ -143,18 +148,11 @@ __device__ __noinline__ FarRow far_tiles8(const PagedArgs& a, Item x, int i0, in
       uint32_t v[32], pk[16];
       tmem_ld32(tS + c, v);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int blk = c / 16 + half;
-        const float k = ts->k[blk] * q_scale, up = kLift + ts->v_log[blk];
-        float s = 0.f;
-#pragma unroll
-        for (int e = 16 * half; e < 16 * half + 16; e += 2) {
-          const float p0 = ex2((__fmul_rn(__uint_as_float(v[e]), k) - ref) + up);
-          const float p1 = ex2((__fmul_rn(__uint_as_float(v[e + 1]), k) - ref) + up);
-          s += p0 + p1;
-          pk[e / 2] = pack16<true>(p0, p1);
-        }
-        sum += s * ts->v_inv[blk];
+      for (int e = 0; e < 32; e += 2) {
+        const float p0 = ex2((__fmul_rn(__uint_as_float(v[e]), k) - ref) + kLift);
+        const float p1 = ex2((__fmul_rn(__uint_as_float(v[e + 1]), k) - ref) + kLift);
+        sum += p0 + p1;
+        pk[e / 2] = pack16<true>(p0, p1);
       }
       tmem_st16(tS + c / 2, pk);
       if (c == 32 || c == 96) {
@@ -167,7 +165,7 @@ __device__ __noinline__ FarRow far_tiles8(const PagedArgs& a, Item x, int i0, in
     }
     l += sum;
   }
-  return FarRow{m, l, v_ref, done, infos};
+  return FarRow{m, l, v_ref, done, tiles};
 }
 
 template <int D, bool FP16>
@@ -176,8 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Chunk8<D>;
   extern __shared__ uint8_t sm_raw[];
   // barriers: stages (full, empty), q empty, per row tile q full, q converted, S full, P full (its first and its second
-  // half), O full, O empty; scales (a slot each)
-  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 1 + 14 + kInfos];
+  // half), O full, O empty
+  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 1 + 14];
   __shared__ __align__(16) TileScales scales_s[kInfos];
   __shared__ uint32_t warp_s[kThreads / 32];
   __shared__ Share share_s;
@@ -200,14 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto PFULL = [&](int t, int part) { return bar0 + 8u * (kB + 7 + 2 * t + part); };
   auto OFULL = [&](int t) { return bar0 + 8u * (kB + 11 + t); };
   auto OEMPTY = [&](int t) { return bar0 + 8u * (kB + 13 + t); };
-  auto INFO = [&](int s) { return bar0 + 8u * (kB + 15 + s); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = (int)blockIdx.x;
   const int tpt = 128 / a.G, tokens = 2 * tpt;
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(FULL(s), kConvertWarps + 1);
+      mbar_init(FULL(s), kConvertWarps);
       mbar_init(EMPTY(s), 1);
     }
     mbar_init(QEMPTY, 1);
@@ -220,7 +217,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(OEMPTY(t), 4);
       mbar_init(QREADY(t), 4);
     }
-    for (int s = 0; s < kInfos; ++s) mbar_init(INFO(s), 1);
     abort_s = 0;
     for (int i = 0; i < 4; ++i) bad_s[i] = 0;
     share_s.lo = share_s.hi = 0;
@@ -272,91 +268,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     return j <= p_hi && (a.window == 0 || j + 15 > p_lo - a.window || j < a.sinks);
   };
 
-  if (warp >= kSoftmaxWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  if (warp >= kSoftmaxWarps && warp < kFirstConvert) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == kSoftmaxWarps) {
-      // ---- queries, and scales: lane 16 t + 8 kv + block of pairs of tiles, page numbers two pairs ahead, scales one
-      const int lt = lane >> 4, kv = (lane >> 3) & 1, blk = lane & 7;
-      const float* scales = kv ? a.vs : a.ks;
-      uint32_t at = 0, items = 0, tiles = 0;
-      bad = false;
-      walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
-        const bool two = x.n > tpt;
+      // ---- queries, once the segment before has done its last scores
+      uint32_t items = 0;
+      walk([&](int, const SeqRows& s, int g, const Item& x, int, int, uint32_t) {
         if (items > 0 && !mbar_wait_warp(QEMPTY, (items - 1) & 1, &abort_s, a.err)) return false;
         ++items;
-        if (lane == 0) {   // the queries, once the segment before has done its last scores
+        if (lane == 0) {
           const uint32_t bytes = (uint32_t)(64 * 2 * a.G * tpt);
-          for (int t = 0; t < (two ? 2 : 1); ++t) {
+          for (int t = 0; t < (x.n > tpt ? 2 : 1); ++t) {
             mbar_arrive_expect_tx(QFULL(t), bytes * C::kBoxes);
             for (int bx = 0; bx < C::kBoxes; ++bx)
               tma_load_3d(sQ + t * C::kTileBytes + bx * C::kBoxBytes, &q_map, QFULL(t), bx * 64, g * a.G, s.row0 + x.t0 + t * tpt);
           }
         }
         __syncwarp();
-        const int32_t* row = a.table + (size_t)b * a.max_pages;
-        auto block_at = [&](int i) {   // the block's first position in the pair of tiles from i on, -1 if no row sees it
-          const int t = i0 + i + lt;
-          if (i + lt >= n || t >= x.r.count) return -1;
-          const int j = x.r.tile(t) * kTN + blk * 16;
-          return block_needed(j, x.p_lo, x.p_hi) ? j : -1;
-        };
-        auto page_of = [&](int i) {
-          const int j = block_at(i);
-          return j < 0 ? -1 : row[j >> a.page_shift];
-        };
-        auto scale_of = [&](int i, int page) {
-          const int j = block_at(i);
-          if (j < 0 || page < 0 || page >= a.num_pages) return kLeastScale;   // (a bad page: the converters say so)
-          return scales[scale_index(page, a.Hkv, g, a.page_shift, j & ((1 << a.page_shift) - 1))];
-        };
-        int page = page_of(0);
-        float ahead = scale_of(0, page), now = 0.f, top = 0.f, v_ref = kLeastScale;
-        page = page_of(2);
-        for (int i = 0; i < n; ++i, ++at, ++tiles) {
-          if ((i & 1) == 0) {
-            now = ahead;
-            if (!scale_ok(now)) {
-              bad = true;
-              now = kLeastScale;
-            }
-            ahead = scale_of(i + 2, page);
-            page = page_of(i + 4);
-            __syncwarp();
-            top = now;
-#pragma unroll
-            for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-          }
-          __syncwarp();
-          v_ref = fmaxf(v_ref, __shfl_sync(0xFFFFFFFFu, top, (i & 1) * 16 + 8));
-          // (The slot's scales of four tiles ago are not needed once the ring stage of this tile's keys is free: then
-          // the products of two tiles ago and of all before are done, and with them their softmax.)
-          if (at >= C::kStages && !mbar_wait_warp(EMPTY(at & 1), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
-          TileScales* to = scales_s + (tiles & 3);
-          if (lt == (i & 1)) {
-            if (kv == 0) {
-              to->k[blk] = now;
-            } else {
-              to->v_log[blk] = log2f(now / v_ref);
-              to->v_inv[blk] = v_ref / now;
-              if (blk == 0) to->v_ref = v_ref;
-            }
-          }
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(INFO(tiles & 3));
-            mbar_arrive(FULL(at & 1));
-          }
-          __syncwarp();
-        }
-        // (The last tile's values have a stage of their own.  This warp's word belongs to every stage, so that no stage
-        // can be used up, and its barriers come round to the same parity, before this warp has seen it free.)
-        if (at >= C::kStages && !mbar_wait_warp(EMPTY(at & 1), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
-        if (lane == 0) mbar_arrive(FULL(at & 1));
-        __syncwarp();
-        ++at;
         return true;
       });
-      if (bad) raise_flag(a.err, kErrBadPages);
     } else if (warp == kSoftmaxWarps + 1) {
       // ---- tensor-core instructions.  The whole warp takes every step, one elected lane issues (by predicate), and
       // row tile and ring stage are constants of the unrolled code.
@@ -434,7 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         outs1 += two;
         return true;
       });
-    } else if (warp >= kFirstConvert) {
+    }
+  } else if (warp >= kFirstConvert) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    {
       // ---- codes into operands: a warp has 32 of the tile's positions, 16 bytes of a row a lane, kRows rows (a piece) at a
       // time.  Pieces come by asynchronous copies into shared memory, each lane's own 16 bytes by itself, so that nothing but
       // its own count of copies stands between them and their use: while one tile of keys or values is converted, the
@@ -447,29 +380,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int q = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3, rr = D == 128 ? (lane >> 2) & 3 : lane >> 2;
       const long long step = kRows * a.row_stride;
       const uint32_t line = (q >> 2) * C::kBoxBytes + (w * kPositions + rr) * 128, chunk = ((2 * q) & 7) ^ (rr & 7);
-      uint32_t at = 0;
+      uint32_t at = 0, tiles = 0;
       int seg = 0;
       const uint32_t mine = sRaw + w * (kPieces * 512) + lane * 16;
       bad = false;
       walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
         const int32_t* row = a.table + (size_t)b * a.max_pages;
         const long long lane_off = g * a.head_stride + rr * a.row_stride + q * 16;
-        // Page numbers of the blocks of four tiles, one a lane, read four tiles ahead; a block that no row needs, or
-        // whose page is bad, is taken as zeros.
-        int pg = 0, ahead = 0;
-        bool need = false;
-        auto read_ahead = [&](int i) {
+        // Blocks of four tiles, one a lane: page numbers, read four tiles ahead, and scales, read two ahead.  A block that no
+        // row needs, or whose page is bad, is taken as zeros under the least scale.
+        const int my_off = ((lane & 7) * 16) & ((1 << a.page_shift) - 1);
+        int pg = -1, pg_ahead = 0;
+        float ks_ahead = 0.f, vs_ahead = 0.f, k_by = 1.f, v_by = 1.f, k_ref = 1.f, v_ref = kLeastScale, v_last = kLeastScale;
+        auto read_pages = [&](int i) {
           const int t = i0 + i + (lane >> 3);
           const int j = i + (lane >> 3) < n && t < x.r.count ? x.r.tile(t) * kTN + (lane & 7) * 16 : -1;
-          need = j >= 0 && block_needed(j, x.p_lo, x.p_hi) && (j >> a.page_shift) < a.max_pages;
-          if (need) ahead = row[j >> a.page_shift];
+          const bool need = j >= 0 && block_needed(j, x.p_lo, x.p_hi) && (j >> a.page_shift) < a.max_pages;
+          pg_ahead = need ? row[j >> a.page_shift] : -1;
+          if (need && (pg_ahead < 0 || pg_ahead >= a.num_pages)) {
+            bad = true;
+            pg_ahead = -1;
+          }
           __syncwarp();
         };
-        auto next_pages = [&](int i) {
-          const bool ok = ahead >= 0 && ahead < a.num_pages;
-          pg = need && ok ? ahead : -1;
-          bad |= need && !ok;
-          read_ahead(i + 4);
+        auto read_scales = [&]() {
+          const int at = scale_index(max(pg_ahead, 0), a.Hkv, g, a.page_shift, my_off);
+          ks_ahead = vs_ahead = kLeastScale;
+          if (pg_ahead >= 0) {
+            ks_ahead = a.ks[at];
+            vs_ahead = a.vs[at];
+          }
+          __syncwarp();
+        };
+        auto next_four = [&](int i) {
+          pg = pg_ahead;
+          bool ok = scale_ok(ks_ahead) && scale_ok(vs_ahead);
+          const float ks = scale_ok(ks_ahead) ? ks_ahead : kLeastScale, vs = scale_ok(vs_ahead) ? vs_ahead : kLeastScale;
+          bad |= !ok;
+          __syncwarp();
+          k_ref = ks;
+          float top = vs;
+#pragma unroll
+          for (int off = 1; off < 8; off <<= 1) {
+            k_ref = fmaxf(k_ref, __shfl_xor_sync(0xFFFFFFFFu, k_ref, off));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+          }
+          v_ref = v_last;   // of this lane's tile: the largest so far
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const float x = __shfl_sync(0xFFFFFFFFu, top, 8 * t);
+            v_last = fmaxf(v_last, x);
+            if (t <= lane >> 3) v_ref = fmaxf(v_ref, x);
+          }
+          k_by = ks / k_ref;
+          v_by = vs / v_ref;
+          read_pages(i + 4);
         };
         // The pieces of block blk of tile i of `cache`, one a call, to its places in the ring.
         const uint8_t* from = a.kc8;
@@ -485,8 +450,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           cp_async_commit();
           from += page < 0 ? 0 : step;
         };
-        read_ahead(0);
-        next_pages(0);
+        read_pages(0);
+        read_scales();
+        next_four(0);
 #pragma unroll 1
         for (int blk = 0; blk < kBlocks; ++blk) {
           block_of(a.kc8, 0, blk, true);
@@ -496,7 +462,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i <= n; ++i, ++at) {
           const uint32_t st = at & 1, stage = sKV + st * C::kStageBytes;
           if (at >= C::kStages && !mbar_wait_warp(EMPTY(st), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
-          if (i > 0 && i < n && (i & 3) == 0) next_pages(i);
+          // (the values are tile i - 1's: their factors before those of the next four tiles)
+          float v_now[kBlocks];
+#pragma unroll
+          for (int blk = 0; blk < kBlocks; ++blk)
+            v_now[blk] = __shfl_sync(0xFFFFFFFFu, v_by, ((i - 1) & 3) * 8 + w * kBlocks + blk);
+          if (i > 0 && i < n) {
+            if ((i & 3) == 0) next_four(i);
+            if ((i & 3) == 2) read_scales();
+          }
           const int j0 = i > 0 ? x.r.tile(i0 + i - 1) * kTN : 0;
           if (i > 0 && !tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) {
             // The values of a masked tile: NaN codes are taken out where they lie.
@@ -527,11 +501,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < kPerBlock; ++k) ld_shared4(in + k * 512, c[k][0], c[k][1], c[k][2], c[k][3]);
               block_of(kv ? a.kc8 : a.vc8, i, blk, i < n);
+              const float k_now = __shfl_sync(0xFFFFFFFFu, k_by, (i & 3) * 8 + w * kBlocks + blk);
+              float by = kv ? (blk == 0 ? v_now[0] : v_now[kBlocks - 1]) : k_now;
+              static_assert(kBlocks <= 2, "v_now");
               uint32_t h[kPerBlock][8];
 #pragma unroll
               for (int k = 0; k < kPerBlock; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) codes_to_half4(c[k][e], h[k][2 * e], h[k][2 * e + 1]);
+              if (by < 0x1p-24f) {   // no fp16 number: in two steps, the first exact
+                by *= 0x1p12f;
+#pragma unroll
+                for (int k = 0; k < kPerBlock; ++k)
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) h[k][e] = mul_half2(h[k][e], 0x0C000C00u);   // 2^-12
+              }
+              const uint32_t by2 = pack16<true>(by, by);
+#pragma unroll
+              for (int k = 0; k < kPerBlock; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) h[k][e] = mul_half2(h[k][e], by2);
 #pragma unroll
               for (int k = 0; k < kPerBlock; ++k) {
                 // rows 4 and 8 apart differ by one bit of the chunk in the swizzle, and not at all
@@ -544,6 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               in += kPerBlock * 512;
             }
           }
+          // The tile's references, for its softmax: their slot was last used four tiles ago, whose softmax was done before this
+          // stage was free.  What follows from this warp's word (the scores, their barrier) tells the softmax of them.
+          if (i < n && w == 0 && lane == (i & 3) * 8) scales_s[tiles & (kInfos - 1)] = TileScales{k_ref, v_ref};
+          tiles += i < n;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(FULL(st));
@@ -560,12 +553,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, r = (warp & 3) * 32 + lane, tok = r / a.G, head = r - tok * a.G;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = t * 128 + lanes, tO = kTmemO + t * 128 + lanes;
-    int seg = 0, done = 0, outs = 0, infos = 0;   // segments, own tiles, items and all tiles so far
+    int seg = 0, done = 0, outs = 0, tiles = 0;   // segments, own tiles, items and all tiles so far
     walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t u) {
       const int nt = x.n > tpt ? 2 : 1;
       if (t >= nt) {
         ++seg;
-        infos += n;
+        tiles += n;
         return true;
       }
       const bool live = tok < tpt && t * tpt + tok < x.n;
@@ -604,40 +597,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j0 = x.r.tile(i0 + i) * kTN;
         const bool open = tile_open<kTN>(a, j0, x.p_lo, x.p_hi);
         if (!mbar_wait_warp(SFULL(t), done & 1, &abort_s, a.err)) return false;
-        // (After the scores: their stage had the scales' word, so that this phase is the slot's latest.  A row tile that
-        // skips items may come to the slot several phases early.)
-        if (!mbar_wait_warp(INFO(infos & 3), (infos >> 2) & 1, &abort_s, a.err)) return false;
-        const TileScales* ts = scales_s + (infos & 3);
-        ++infos;
         ++done;
         tc_fence_after();
+        const volatile TileScales* ts = scales_s + (tiles & (kInfos - 1));
+        ++tiles;
         if (!open) mask_scores(a, tS, p, j0);
         uint32_t sr[128];
         tmem_ld128(tS, sr);
-        float mx = -INFINITY;
+        const float k = ts->k_ref * q_scale, v_new = ts->v_ref;
+        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          float mx0 = fmaxf(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), mx1 = fmaxf(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
-#pragma unroll
-          for (int e = 4; e < 16; e += 4) {
-            mx0 = max3(mx0, __uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1]));
-            mx1 = max3(mx1, __uint_as_float(sr[c + e + 2]), __uint_as_float(sr[c + e + 3]));
-          }
-          mx = fmaxf(mx, fmaxf(mx0, mx1) * (ts->k[c / 16] * q_scale));
+        for (int c = 0; c < 128; c += 8) {
+          mx0 = max3(mx0, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+          mx1 = max3(mx1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+          mx2 = max3(mx2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
+          mx3 = max3(mx3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
         }
+        const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * k;
         // The reference moves if the new maximum is well above it (or is the first).
         const bool move = mx > m && (m == -INFINITY || mx - m > kLazy);
-        const float v_new = ts->v_ref;
         if (__any_sync(0xFFFFFFFFu, move || v_new != v_ref)) {
           if (__any_sync(0xFFFFFFFFu, move && p >= 0 && fabsf(mx) > kFar)) {   // the tiles from here on in another way
-            const FarRow row = far_tiles8<D>(a, x, i0, i, n, p, tS, tO, SFULL(t), done, PFULL(t, 0), INFO(0), infos, scales_s,
-                                             q_scale, &abort_s, FarRow{m, l, v_ref, 0, 0});
+            const FarRow row = far_tiles8<D>(a, x, i0, i, n, p, tS, tO, SFULL(t), PFULL(t, 0), scales_s, q_scale, &abort_s,
+                                             FarRow{m, l, v_ref, done, tiles});
             if (row.done < 0) return false;
             m = row.m;
             l = row.l;
             v_ref = row.v_ref;
             done = row.done;
-            infos = row.infos;
+            tiles = row.tiles;
             negm = kLift - m;
             break;
           }
@@ -653,27 +641,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (i > 0) rescale<D>(tO, by);
         }
+        const uint64_t scale2 = pair2(k, k), negm2 = pair2(negm, negm);
+        uint64_t sum0 = 0, sum1 = 0;   // two fp32 sums each
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           uint32_t pk[16];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int blk = c / 16 + half;
-            const float k = ts->k[blk] * q_scale, up = negm + ts->v_log[blk];
-            const uint64_t scale2 = pair2(k, k), up2 = pair2(up, up);
-            uint64_t sum0 = 0, sum1 = 0;   // two fp32 sums each
-#pragma unroll
-            for (int e = 16 * half; e < 16 * half + 16; e += 4) {
-              const float2 x0 = unpair2(fma2(pair2(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])), scale2, up2));
-              const float2 x1 = unpair2(fma2(pair2(__uint_as_float(sr[c + e + 2]), __uint_as_float(sr[c + e + 3])), scale2, up2));
-              const float p0 = ex2(x0.x), p1 = ex2(x0.y), p2 = ex2(x1.x), p3 = ex2(x1.y);
-              sum0 = add2(sum0, pair2(p0, p1));
-              sum1 = add2(sum1, pair2(p2, p3));
-              pk[e / 2] = pack16<true>(p0, p1);
-              pk[e / 2 + 1] = pack16<true>(p2, p3);
-            }
-            const float2 s01 = unpair2(add2(sum0, sum1));
-            l = fmaf(s01.x + s01.y, ts->v_inv[blk], l);
+          for (int e = 0; e < 32; e += 4) {
+            const float2 x0 = unpair2(fma2(pair2(__uint_as_float(sr[c + e]), __uint_as_float(sr[c + e + 1])), scale2, negm2));
+            const float2 x1 = unpair2(fma2(pair2(__uint_as_float(sr[c + e + 2]), __uint_as_float(sr[c + e + 3])), scale2, negm2));
+            const float p0 = ex2(x0.x), p1 = ex2(x0.y), p2 = ex2(x1.x), p3 = ex2(x1.y);
+            sum0 = add2(sum0, pair2(p0, p1));
+            sum1 = add2(sum1, pair2(p2, p3));
+            pk[e / 2] = pack16<true>(p0, p1);
+            pk[e / 2 + 1] = pack16<true>(p2, p3);
           }
           tmem_st16(tS + c / 2, pk);
           if (c == 32 || c == 96) {   // half of P is there: its part of the product can start
@@ -684,6 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
         }
+        const float2 s0 = unpair2(sum0), s1 = unpair2(sum1);
+        l += (s0.x + s0.y) + (s1.x + s1.y);
       }
       // ---- the item's result, or this share's part of it
       const int my_seg = seg++;

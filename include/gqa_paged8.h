@@ -13,8 +13,8 @@
  * of one key/value head:
  *     k_cache, v_cache  uint8 [num_pages, Hkv, page_size, D] with the strides of dims (elements are bytes here)
  *     k_scale, v_scale  fp32 [num_pages, Hkv, page_size / 16], packed
- * gqa_paged8_append writes scales that are powers of two.  The other calls take any scale from 2^-60 to 2^60; one
- * outside, of a block that a row needs, counts as 2^-60 and sets bit 16.
+ * A scale is a power of two from 2^-60 to 2^60, as gqa_paged8_append writes it.  Any other number in the place of a
+ * scale that a call needs counts as 2^-60 and sets bit 16.
  *
  * Rows.  In all three calls sequence b's rows are q_start[b] .. q_start[b+1] - 1 and stand for its positions
  * kv_len[b] - n .. kv_len[b] - 1, n = q_start[b+1] - q_start[b], as gqa_paged_plan writes them.
@@ -68,13 +68,16 @@ moe_status gqa_paged8_read(const gqa_paged_dims* dims, const uint8_t* k_cache, c
                            uint16_t* k, uint16_t* v, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Attention of the new tokens over the cache: gqa_paged_attention with K and V the products code * scale, exact.
- * Queries, whose type may hold numbers past the tensor cores' operand type, enter the products as fp16 multiples of
- * a power of two of each row and head, exact to 2^-40 of the row's largest (fp16 queries: exact); one past 2^75 counts as infinite.
- * The softmax's numerators are rounded to fp16 as gqa_paged_attention states for fp16, relative to a row's largest
- * numerator, times the scale of their block over the largest scale among those its segment of the cache has met (what falls
- * below fp16's range by that is less than 2^-33 (chunks) or 2^-39 (single tokens) of the largest value in the cache that
- * the row's tiles hold, for each such position).  Bit 8 is set for an output that is not finite: visible NaN codes, or
- * values past the dims' type.
+ * Products are fp16 on the tensor cores, with fp32 sums, and what enters them:
+ *   queries     fp16 as they are; bf16 times a power of two of each row and head, off by at most 2^-40 of the row's
+ *               largest number (one past 2^75 counts as infinite)
+ *   keys        single tokens: exact.  Chunks: off by at most 2^-33 of the largest key (rounded up to a power of two)
+ *               among the tile's 128 positions, and exact where the scales there are within 2^15 of one another
+ *   numerators  as gqa_paged_attention states for fp16 (single tokens: times their block's value scale over the
+ *               largest that the share has met, so 2^-39 of the largest value there in absolute terms)
+ *   values      single tokens: exact.  Chunks: off by at most 2^-33 of the largest value in the item's tiles up to there,
+ *               and exact where the scales there are within 2^15 of one another
+ * Bit 8 is set for an output that is not finite: visible NaN codes, or values past the dims' type.
  *   workspace  >= gqa_paged8_workspace_bytes(dims) */
 moe_status gqa_paged8_attention(const gqa_paged_dims* dims, const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
                                 const float* k_scale, const float* v_scale, const int32_t* block_table,

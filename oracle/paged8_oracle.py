@@ -53,6 +53,11 @@ def exponent(amax: float) -> int:
     return e
 
 
+def scale_ok(s: float) -> bool:
+    """A power of two from 2^LEAST to 2^MOST."""
+    return math.isfinite(s) and 2.0 ** LEAST <= s <= 2.0 ** MOST and math.frexp(s)[0] == 0.5
+
+
 def values(cache, scale, page_size) -> np.ndarray:
     """codes [P, H, S, D] and scales [P, H, S / 16] as float64 values."""
     s = np.asarray(scale, dtype=np.float64)
@@ -83,7 +88,7 @@ def append(k, v, table, q_start, kv_len, caches, scales, dtype):
                     s = 2.0 ** exponent(np.abs(x[good]).max(initial=0.0))
                     held = out_c[which][page, h, off:off + first - j0]
                     if first > j0:
-                        if not 2.0 ** LEAST <= was <= 2.0 ** MOST:
+                        if not scale_ok(was):
                             flags, was = flags | BAD, 2.0 ** LEAST
                         s = max(s, was)
                         if s != was:
