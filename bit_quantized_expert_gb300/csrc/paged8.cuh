@@ -48,6 +48,8 @@ __device__ __forceinline__ uint32_t to_codes4(float x0, float x1, float x2, floa
   return d;
 }
 
+// One cache as the tensor maps see it; boxes of `rows` positions of one page and head.
+bool encode_pages8(CUtensorMap* m, const uint8_t* cache, const gqa_paged_dims& d, int rows);
 cudaError_t launch_paged8_decode(const gqa_paged_dims& d, const Paged8Args& a, void* scratch, int ctas, cudaStream_t st);
 cudaError_t launch_paged8_chunk(const gqa_paged_dims& d, const Paged8Args& a, void* scratch, int ctas, cudaStream_t st);
 

@@ -25,6 +25,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 512;               // two softmax warpgroups, one for queries, scales and products, one for codes
+constexpr int kScanWarps = 2;
 constexpr int kConvertWarps = 4;
 constexpr int kFirstConvert = 12;
 // Registers a thread: 128 at launch; 2 * 184 + 64 + 80 = 4 * 128 after the split.
@@ -35,7 +36,7 @@ static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConvert <= 4 * 128, "no more 
 constexpr float kLazy = 6.f, kLift = 9.f;
 // Base-2 units from which on a row's reference is taken off its scaled scores apart (far_tiles8).
 constexpr float kFar = 65536.f;
-constexpr int kInfos = 4;                   // slots for tiles' scales, a power of two
+constexpr int kInfos = 8;                   // slots for tiles' scales, a power of two
 
 template <int D>
 struct Chunk8 {
@@ -52,32 +53,82 @@ struct Chunk8 {
   static_assert((kPagedMaxSeqs + 1) * 4 <= kStages * kStageBytes, "sums fit");
 };
 
-// The references of a tile's scales.
-struct TileScales {
-  float k_ref, v_ref;
-};
-
-// 0xFF in each byte of w that is a NaN code.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
-  const uint32_t bit = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // (a carry stays within its byte)
-  return (bit >> 7) * 0xFFu;
+// Waits for the phase of `parity`, the warp together; false: it gave up.  A look at a barrier that is not there yet takes ~3000
+// cycles (the hardware holds the thread until the phase completes, or so long), so this is about two seconds.  What a wait
+// that runs out needs is elsewhere (walk): with the clock and the abort word looked at here, as in mbar_wait, the
+// instructions of every wait are fetched beside the softmax's, and 2048 tokens at 32768 take 460 us in place of 404.
+constexpr int kTries = 1 << 20;
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+  int left = kTries;
+  bool ok;
+#pragma unroll 1
+  do {
+    ok = mbar_try_wait(bar, parity);
+  } while (!ok && --left > 0);
+  __syncwarp();
+  return __all_sync(0xFFFFFFFFu, ok);
 }
+
+// A tile's scales: the factors of its blocks as pairs of fp16 values, and the references that they are over.
+struct TileScales {
+  uint32_t k_by[8], v_by[8];
+  float k_ref, v_ref, pad[2];
+};
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// 16 bytes of global memory, or zeros, into shared memory, asynchronously.
-__device__ __forceinline__ void cp_async_16_if(bool go, uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(go ? 16 : 0) : "memory");
+// N times `bytes` (16, or none: zeros) of global memory, `step` apart, into shared memory, 512 bytes apart, asynchronously.
+// In one statement, so that every address has registers of its own: one that is stepped on waits until the copy before
+// has left its queue (which took 190 cycles a copy behind the stores).
+template <int N>
+__device__ __forceinline__ void cp_async_pieces(uint32_t dst, const uint8_t* src, long long step, int bytes) {
+  static_assert(N == 2 || N == 4, "pieces of a block");
+  if constexpr (N == 4)
+    asm volatile(
+        "cp.async.cg.shared.global [%0], [%1], 16, %5;\n\tcp.async.cg.shared.global [%0+512], [%2], 16, %5;\n\t"
+        "cp.async.cg.shared.global [%0+1024], [%3], 16, %5;\n\tcp.async.cg.shared.global [%0+1536], [%4], 16, %5;" ::"r"(dst),
+        "l"(src), "l"(src + step), "l"(src + 2 * step), "l"(src + 3 * step), "r"(bytes)
+        : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %3;\n\tcp.async.cg.shared.global [%0+512], [%2], 16, %3;" ::"r"(dst),
+                 "l"(src), "l"(src + step), "r"(bytes)
+                 : "memory");
 }
-
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
+// A power of two of at most 1 as the factor of a pair of fp16 values: 0 below 2^-24, the least that fp16 has.
+__device__ __forceinline__ uint32_t factor(float by) { return pack16<true>(by, by); }
+
+// This lane's codes of one block (16 bytes in each piece, 512 bytes apart at `in`) as fp16 values times `by` (factor) into the
+// operand at `out`.
+template <int D>
+__device__ __forceinline__ void convert_block(uint32_t in, uint32_t out, uint32_t by) {
+  constexpr int kRows = 512 / D, kPieces = 16 / kRows;
+  uint32_t c[kPieces][4], h[kPieces][8];
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) ld_shared4(in + k * 512, c[k][0], c[k][1], c[k][2], c[k][3]);
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) codes_to_half4(c[k][e], h[k][2 * e], h[k][2 * e + 1]);
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[k][e] = mul_half2(h[k][e], by);
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    // (rows 4 and 8 apart differ by one bit of the chunk in the swizzle, and not at all)
+    const uint32_t to = (D == 128 && k & 1 ? out ^ 64u : out) + k * kRows * 128;
+    st_shared16(to, h[k][0], h[k][1], h[k][2], h[k][3]);
+    st_shared16(to ^ 16u, h[k][4], h[k][5], h[k][6], h[k][7]);
+  }
+}
 // NaN for the dims d0 .. d0 + 15 in which a position that the row sees, in this segment's masked tiles, has a NaN code.
 __device__ __noinline__ uint32_t nan_dims(const Paged8Args& a, const int32_t* table, TileRange r, int i0, int n, int p_lo,
                                           int p_hi, int p, int g, int d0) {
@@ -108,13 +159,13 @@ struct FarRow {
 template <int D>
 __device__ __noinline__ FarRow far_tiles8(const Paged8Args& a, Item x, int i0, int i, int n, int p, uint32_t tS, uint32_t tO,
                                           uint32_t sfull, uint32_t pfull, const TileScales* scales, float q_scale,
-                                          volatile int* abort_s, FarRow row) {
+                                          FarRow row) {
   float m = row.m, l = row.l, v_ref = row.v_ref;
   int done = row.done, tiles = row.tiles;
   for (bool waited = true; i < n; ++i, waited = false) {
     if (!waited) {
       const int j0 = x.r.tile(i0 + i) * kTN;
-      if (!mbar_wait_warp(sfull, done & 1, abort_s, a.err)) return FarRow{m, l, v_ref, -1, tiles};
+      if (!wait_warp(sfull, done & 1)) return FarRow{m, l, v_ref, -1, tiles};
       ++done;
       ++tiles;
       tc_fence_after();
@@ -174,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Chunk8<D>;
   extern __shared__ uint8_t sm_raw[];
   // barriers: stages (full, empty), q empty, per row tile q full, q converted, S full, P full (its first and its second
-  // half), O full, O empty
-  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 1 + 14];
+  // half), O full, O empty; scales (full, empty, a slot each); values clean (a stage each)
+  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 1 + 14 + 2 * kInfos + C::kStages];
   __shared__ __align__(16) TileScales scales_s[kInfos];
   __shared__ uint32_t warp_s[kThreads / 32];
   __shared__ Share share_s;
@@ -198,6 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto PFULL = [&](int t, int part) { return bar0 + 8u * (kB + 7 + 2 * t + part); };
   auto OFULL = [&](int t) { return bar0 + 8u * (kB + 11 + t); };
   auto OEMPTY = [&](int t) { return bar0 + 8u * (kB + 13 + t); };
+  auto INFO = [&](int s) { return bar0 + 8u * (kB + 15 + s); };
+  auto INFOEMPTY = [&](int s) { return bar0 + 8u * (kB + 15 + kInfos + s); };
+  auto CLEAN = [&](int s) { return bar0 + 8u * (kB + 15 + 2 * kInfos + s); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = (int)blockIdx.x;
   const int tpt = 128 / a.G, tokens = 2 * tpt;
@@ -205,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(FULL(s), kConvertWarps);
-      mbar_init(EMPTY(s), 1);
+      mbar_init(EMPTY(s), 1 + kScanWarps);
+      mbar_init(CLEAN(s), kScanWarps);
     }
     mbar_init(QEMPTY, 1);
     for (int t = 0; t < 2; ++t) {
@@ -216,6 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(OFULL(t), 1);
       mbar_init(OEMPTY(t), 4);
       mbar_init(QREADY(t), 4);
+    }
+    for (int s = 0; s < kInfos; ++s) {
+      mbar_init(INFO(s), 1);
+      mbar_init(INFOEMPTY(s), kConvertWarps);
     }
     abort_s = 0;
     for (int i = 0; i < 4; ++i) bad_s[i] = 0;
@@ -242,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
 
   // Walks the segments of the share: body(b, s, g, item, i0, n, u) for tiles i0 .. i0 + n - 1 of an item,
-  // the first of them unit u; stops when the body returns false.
+  // the first of them unit u; stops when the body returns false.  (The others' waits then run out as well.)
   auto walk = [&](auto&& body) {
     uint32_t u = share_s.lo, at = share_s.at;
     const uint32_t hi = share_s.hi;
@@ -255,7 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; g < a.Hkv && u < hi; ++g, at += units) {
           if (at + units <= u) continue;
           const int i0 = max((int)(u - at) - kItemUnits, 0), i1 = (int)min(hi - at, units) - kItemUnits;
-          if (!body(b, s, g, x, i0, i1 - i0, u)) return;
+          if (!body(b, s, g, x, i0, i1 - i0, u)) {   // a wait gave up
+            abort_s = 1;
+            return;
+          }
           u = min(hi, at + units);
         }
       }
@@ -263,28 +325,87 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++b;
     }
   };
-  // Whether a row at one of the positions p_lo .. p_hi sees some position of the block of 16 at j.
-  auto block_needed = [&](int j, int p_lo, int p_hi) {
-    return j <= p_hi && (a.window == 0 || j + 15 > p_lo - a.window || j < a.sinks);
+  // The page of block lane & 7 of tile i + lane / 8 of a segment, as the table has it (looked at by page_or_none, later,
+  // so that nothing waits here), and -1 in the place of one whose block no row needs.
+  auto read_page = [&](const int32_t* row, const Item& x, int i0, int n, int i, bool* need) {
+    const int t = i0 + i + (lane >> 3);
+    const int j = i + (lane >> 3) < n && t < x.r.count ? x.r.tile(t) * kTN + (lane & 7) * 16 : -1;
+    *need = j >= 0 && j <= x.p_hi && (a.window == 0 || j + 15 > x.p_lo - a.window || j < a.sinks);
+    int page = -1;
+    if (*need) page = row[j >> a.page_shift];
+    __syncwarp();
+    return page;
+  };
+  auto page_or_none = [&](int page, bool need) {
+    const bool ok = page >= 0 && page < a.num_pages;
+    bad |= need && !ok;
+    return ok ? page : -1;
   };
 
   if (warp >= kSoftmaxWarps && warp < kFirstConvert) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == kSoftmaxWarps) {
-      // ---- queries, once the segment before has done its last scores
-      uint32_t items = 0;
-      walk([&](int, const SeqRows& s, int g, const Item& x, int, int, uint32_t) {
-        if (items > 0 && !mbar_wait_warp(QEMPTY, (items - 1) & 1, &abort_s, a.err)) return false;
-        ++items;
-        if (lane == 0) {
-          const uint32_t bytes = (uint32_t)(64 * 2 * a.G * tpt);
-          for (int t = 0; t < (x.n > tpt ? 2 : 1); ++t) {
-            mbar_arrive_expect_tx(QFULL(t), bytes * C::kBoxes);
-            for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_3d(sQ + t * C::kTileBytes + bx * C::kBoxBytes, &q_map, QFULL(t), bx * 64, g * a.G, s.row0 + x.t0 + t * tpt);
+    if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 2) {
+      // ---- queries (warp 8), once the segment before has done its last scores; and values of masked tiles (both warps, two
+      // positions a thread): NaN ones are taken out of the operand.  In the conversion itself, where all tiles come by, that
+      // code took a quarter of its time without being run (2048 tokens at 32768: 522 in place of 407 us).
+      // These warps see every stage, and a stage is free only with their word, so that they keep step with the ring.
+      // Their word that a tile is done goes to its stage's own barrier: a stage is filled again only after both of them and
+      // the product have left it.
+      const int w = warp == kSoftmaxWarps ? 0 : 1;
+      uint32_t at = 0, items = 0;
+      int seg = 0;
+      walk([&](int, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
+        if (w == 0) {
+          if (items > 0 && !wait_warp(QEMPTY, (items - 1) & 1)) return false;
+          ++items;
+          if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(64 * 2 * a.G * tpt);
+            for (int t = 0; t < (x.n > tpt ? 2 : 1); ++t) {
+              mbar_arrive_expect_tx(QFULL(t), bytes * C::kBoxes);
+              for (int bx = 0; bx < C::kBoxes; ++bx)
+                tma_load_3d(sQ + t * C::kTileBytes + bx * C::kBoxBytes, &q_map, QFULL(t), bx * 64, g * a.G, s.row0 + x.t0 + t * tpt);
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
+        for (int i = 0; i <= n; ++i, ++at) {
+          const uint32_t st = at & 1;
+          if (!wait_warp(FULL(st), (at >> 1) & 1)) return false;
+          const int j0 = i > 0 ? x.r.tile(i0 + i - 1) * kTN : 0;
+          if (i > 0 && !tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) {
+#pragma unroll 1
+            for (int r = w * 32 + lane; r < kTN; r += kScanWarps * 32) {
+              const uint32_t row = sKV + st * C::kStageBytes + C::kTileBytes + r * 128;
+              uint32_t any = 0;
+#pragma unroll 8
+              for (int c = 0; c < 8 * C::kBoxes; ++c) {   // of 16 bytes; lanes start at different ones
+                uint32_t w0, w1, w2, w3;
+                ld_shared4(row + (c >> 3) * C::kBoxBytes + (((c + lane) & 7) << 4), w0, w1, w2, w3);
+                any |= non_finite_bits<true>(w0) | non_finite_bits<true>(w1) | non_finite_bits<true>(w2) | non_finite_bits<true>(w3);
+              }
+              if (any & kSigns) {
+#pragma unroll 1
+                for (int c = 0; c < 8 * C::kBoxes; ++c) {
+                  const uint32_t to = row + (c >> 3) * C::kBoxBytes + ((c & 7) << 4);
+                  uint32_t v[4];
+                  ld_shared4(to, v[0], v[1], v[2], v[3]);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) v[e] &= ~(((non_finite_bits<true>(v[e]) & kSigns) >> 15) * 0xFFFFu);
+                  st_shared16(to, v[0], v[1], v[2], v[3]);
+                }
+                const int j = j0 + r;
+                if (j <= x.p_hi && (a.window == 0 || j > x.p_lo - a.window || j < a.sinks)) bad_s[seg & 3] = seg + 1;
+                fence_proxy_async_smem();
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(CLEAN(st));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(EMPTY(st));
+          __syncwarp();
+        }
+        ++seg;
         return true;
       });
     } else if (warp == kSoftmaxWarps + 1) {
@@ -295,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_o = (1u << 4) | (1u << 16) | (((uint32_t)D >> 3) << 17) | ((128u >> 4) << 24);
       constexpr uint32_t kTileUnits = C::kTileBytes >> 4, kBoxUnits = C::kBoxBytes >> 4;   // descriptors count 16 bytes
       const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(sKV), dv = desc_values(sKV + C::kTileBytes, C::kBoxBytes);
-      uint32_t at = 0, items = 0, seconds = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
-      auto wait = [&](uint32_t bar, uint32_t phase) { return mbar_wait_warp(bar, phase & 1, &abort_s, a.err); };
+      uint32_t at = 0, items = 0, cleans[2] = {0, 0}, seconds = 0, done0 = 0, done1 = 0, outs0 = 0, outs1 = 0;
+      auto wait = [&](uint32_t bar, uint32_t phase) { return wait_warp(bar, phase & 1); };
       // S_t = Q_t K^T with the keys of stage ST
       auto scores = [&](auto t_c, auto st_c) {
         constexpr int t = decltype(t_c)::value, ST = decltype(st_c)::value;
@@ -325,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // body(stage as a constant) for the stage of a tile
       static_assert(C::kStages == 2, "a tile's stage is its parity");
       auto at_stage = [&](uint32_t tile, auto&& body) { return tile & 1 ? body(One{}) : body(Zero{}); };
-      walk([&](int, const SeqRows&, int, const Item& x, int, int n_any, uint32_t) {
+      walk([&](int, const SeqRows&, int, const Item& x, int i0, int n_any, uint32_t) {
         const int n = __shfl_sync(0xFFFFFFFFu, n_any, 0);
         const bool two = __shfl_sync(0xFFFFFFFFu, (int)(x.n > tpt), 0) != 0;
         if (!wait(FP16 ? QFULL(0) : QREADY(0), items++)) return false;
@@ -343,10 +464,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           return false;
         ++at;
         for (int i = 0; i < n; ++i, ++at) {
-          const bool more = i + 1 < n;
+          const bool more = i + 1 < n, closed = !tile_open<kTN>(a, x.r.tile(i0 + i) * kTN, x.p_lo, x.p_hi);
           if (!at_stage(at, [&](auto st_c) {   // the tile's values, the next one's keys
                 constexpr int ST = decltype(st_c)::value;
                 if (!wait(FULL(ST), at >> 1)) return false;
+                if (closed && !wait(CLEAN(ST), cleans[ST]++)) return false;
                 // (the second row tile's result too, where this item has none: bad_s is a short ring)
                 if (i == 0 && outs0 > 0 && !wait(OEMPTY(0), outs0 - 1)) return false;
                 if (i == 0 && outs1 > 0 && !wait(OEMPTY(1), outs1 - 1)) return false;
@@ -364,189 +486,151 @@ __global__ void __launch_bounds__(kThreads, 1)
         outs1 += two;
         return true;
       });
-    }
-  } else if (warp >= kFirstConvert) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
-    {
-      // ---- codes into operands: a warp has 32 of the tile's positions, 16 bytes of a row a lane, kRows rows (a piece) at a
-      // time.  Pieces come by asynchronous copies into shared memory, each lane's own 16 bytes by itself, so that nothing but
-      // its own count of copies stands between them and their use: while one tile of keys or values is converted, the
-      // next one's pieces take its places.  (Held in registers they are 64 a lane, too many beside the rest: the
-      // compiler stored some as they arrived, and 2048 tokens at 32768 took 1,130 us.)
-      constexpr int kPositions = kTN / kConvertWarps, kBlocks = kPositions / 16, kChunks = D / 16, kRows = 32 / kChunks, kPieces = kPositions / kRows, kPerBlock = 16 / kRows;
-      const int w = warp - kFirstConvert;
-      // A lane's 16 dims q and its row of a piece: eight lanes in a row have two rows of one box of 64 dims, so that the
-      // chunks that they store lie in different banks.
-      const int q = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3, rr = D == 128 ? (lane >> 2) & 3 : lane >> 2;
-      const long long step = kRows * a.row_stride;
-      const uint32_t line = (q >> 2) * C::kBoxBytes + (w * kPositions + rr) * 128, chunk = ((2 * q) & 7) ^ (rr & 7);
-      uint32_t at = 0, tiles = 0;
-      int seg = 0;
-      const uint32_t mine = sRaw + w * (kPieces * 512) + lane * 16;
+    } else {
+      // ---- scales of blocks, four tiles at a time, read two tiles ahead.  A block that no row needs, or whose
+      // page is bad, has the least scale.
+      uint32_t tiles = 0;
       bad = false;
-      walk([&](int b, const SeqRows& s, int g, const Item& x, int i0, int n, uint32_t) {
+      walk([&](int b, const SeqRows&, int g, const Item& x, int i0, int n, uint32_t) {
         const int32_t* row = a.table + (size_t)b * a.max_pages;
-        const long long lane_off = g * a.head_stride + rr * a.row_stride + q * 16;
-        // Blocks of four tiles, one a lane: page numbers, read four tiles ahead, and scales, read two ahead.  A block that no
-        // row needs, or whose page is bad, is taken as zeros under the least scale.
-        const int my_off = ((lane & 7) * 16) & ((1 << a.page_shift) - 1);
-        int pg = -1, pg_ahead = 0;
-        float ks_ahead = 0.f, vs_ahead = 0.f, k_by = 1.f, v_by = 1.f, k_ref = 1.f, v_ref = kLeastScale, v_last = kLeastScale;
-        auto read_pages = [&](int i) {
-          const int t = i0 + i + (lane >> 3);
-          const int j = i + (lane >> 3) < n && t < x.r.count ? x.r.tile(t) * kTN + (lane & 7) * 16 : -1;
-          const bool need = j >= 0 && block_needed(j, x.p_lo, x.p_hi) && (j >> a.page_shift) < a.max_pages;
-          pg_ahead = need ? row[j >> a.page_shift] : -1;
-          if (need && (pg_ahead < 0 || pg_ahead >= a.num_pages)) {
-            bad = true;
-            pg_ahead = -1;
-          }
-          __syncwarp();
-        };
+        const int my_off = ((lane & 7) * 16) & ((1 << a.page_shift) - 1);   // of the block in its page
+        bool need;
+        int pg_ahead = read_page(row, x, i0, n, 0, &need);
+        float ks_ahead = kLeastScale, vs_ahead = kLeastScale, k_ref = 1.f, v_ref = kLeastScale, v_last = kLeastScale;
+        uint32_t k_by = 0u, v_by = 0u;
         auto read_scales = [&]() {
-          const int at = scale_index(max(pg_ahead, 0), a.Hkv, g, a.page_shift, my_off);
+          const int page = page_or_none(pg_ahead, need), index = scale_index(max(page, 0), a.Hkv, g, a.page_shift, my_off);
           ks_ahead = vs_ahead = kLeastScale;
-          if (pg_ahead >= 0) {
-            ks_ahead = a.ks[at];
-            vs_ahead = a.vs[at];
+          if (page >= 0) {
+            ks_ahead = a.ks[index];
+            vs_ahead = a.vs[index];
           }
           __syncwarp();
         };
-        auto next_four = [&](int i) {
-          pg = pg_ahead;
-          bool ok = scale_ok(ks_ahead) && scale_ok(vs_ahead);
-          const float ks = scale_ok(ks_ahead) ? ks_ahead : kLeastScale, vs = scale_ok(vs_ahead) ? vs_ahead : kLeastScale;
-          bad |= !ok;
-          __syncwarp();
-          k_ref = ks;
-          float top = vs;
-#pragma unroll
-          for (int off = 1; off < 8; off <<= 1) {
-            k_ref = fmaxf(k_ref, __shfl_xor_sync(0xFFFFFFFFu, k_ref, off));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
-          }
-          v_ref = v_last;   // of this lane's tile: the largest so far
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const float x = __shfl_sync(0xFFFFFFFFu, top, 8 * t);
-            v_last = fmaxf(v_last, x);
-            if (t <= lane >> 3) v_ref = fmaxf(v_ref, x);
-          }
-          k_by = ks / k_ref;
-          v_by = vs / v_ref;
-          read_pages(i + 4);
-        };
-        // The pieces of block blk of tile i of `cache`, one a call, to its places in the ring.
-        const uint8_t* from = a.kc8;
-        int page = -1;
-        auto block_of = [&](const uint8_t* cache, int i, int blk, bool more) {
-          page = __shfl_sync(0xFFFFFFFFu, pg, (i & 3) * 8 + w * kBlocks + blk);
-          if (!more) page = -1;
-          from = page < 0 ? cache
-                          : cache + page * a.page_stride + (((w * kBlocks + blk) * 16) & ((1 << a.page_shift) - 1)) * a.row_stride + lane_off;
-        };
-        auto load = [&](uint32_t to) {
-          cp_async_16_if(page >= 0, to, from);
-          cp_async_commit();
-          from += page < 0 ? 0 : step;
-        };
-        read_pages(0);
         read_scales();
-        next_four(0);
-#pragma unroll 1
-        for (int blk = 0; blk < kBlocks; ++blk) {
-          block_of(a.kc8, 0, blk, true);
-#pragma unroll
-          for (int k = 0; k < kPerBlock; ++k) load(mine + (blk * kPerBlock + k) * 512);
-        }
-        for (int i = 0; i <= n; ++i, ++at) {
-          const uint32_t st = at & 1, stage = sKV + st * C::kStageBytes;
-          if (at >= C::kStages && !mbar_wait_warp(EMPTY(st), (at / C::kStages - 1) & 1, &abort_s, a.err)) return false;
-          // (the values are tile i - 1's: their factors before those of the next four tiles)
-          float v_now[kBlocks];
-#pragma unroll
-          for (int blk = 0; blk < kBlocks; ++blk)
-            v_now[blk] = __shfl_sync(0xFFFFFFFFu, v_by, ((i - 1) & 3) * 8 + w * kBlocks + blk);
-          if (i > 0 && i < n) {
-            if ((i & 3) == 0) next_four(i);
-            if ((i & 3) == 2) read_scales();
-          }
-          const int j0 = i > 0 ? x.r.tile(i0 + i - 1) * kTN : 0;
-          if (i > 0 && !tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) {
-            // The values of a masked tile: NaN codes are taken out where they lie.
-            cp_async_wait<0>();
-#pragma unroll 1
-            for (int k = 0; k < kPieces; ++k) {
-              uint32_t c[4], nan[4];
-              ld_shared4(mine + k * 512, c[0], c[1], c[2], c[3]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) nan[e] = nan_codes(c[e]);
-              if ((nan[0] | nan[1] | nan[2] | nan[3]) != 0) {
-                st_shared16(mine + k * 512, c[0] & ~nan[0], c[1] & ~nan[1], c[2] & ~nan[2], c[3] & ~nan[3]);
-                const int j = j0 + w * kPositions + k * kRows + rr;
-                if (j <= x.p_hi && (a.window == 0 || j > x.p_lo - a.window || j < a.sinks)) bad_s[seg & 3] = seg + 1;
-              }
-            }
+        for (int i = 0; i < n; ++i, ++tiles) {
+          if ((i & 3) == 0) {
+            const float ks = scale_ok(ks_ahead) ? ks_ahead : kLeastScale, vs = scale_ok(vs_ahead) ? vs_ahead : kLeastScale;
+            bad |= !scale_ok(ks_ahead) || !scale_ok(vs_ahead);
             __syncwarp();
+            k_ref = ks;
+            float top = vs;
+#pragma unroll
+            for (int off = 1; off < 8; off <<= 1) {
+              k_ref = fmaxf(k_ref, __shfl_xor_sync(0xFFFFFFFFu, k_ref, off));
+              top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+            }
+            v_ref = v_last;   // of this lane's tile: the largest so far
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const float y = __shfl_sync(0xFFFFFFFFu, top, 8 * t);
+              v_last = fmaxf(v_last, y);
+              if (t <= lane >> 3) v_ref = fmaxf(v_ref, y);
+            }
+            k_by = factor(ks / k_ref);
+            v_by = factor(vs / v_ref);
+            pg_ahead = read_page(row, x, i0, n, i + 4, &need);
           }
-          // The values of tile i - 1, then the keys of tile i, one code for both (twice as many instructions would be
-          // fetched anew each time), a block a turn; behind them come the keys of tile i and its values.
-#pragma unroll 1
-          for (int kv = i > 0 ? 1 : 0; kv >= (i < n ? 0 : 1); --kv) {
-            uint32_t to = stage + kv * C::kTileBytes + line + (chunk << 4), in = mine;
-#pragma unroll 1
-            for (int blk = 0; blk < kBlocks; ++blk) {
-              uint32_t c[kPerBlock][4];
-              cp_async_wait<kPieces - kPerBlock>();   // the oldest block
-#pragma unroll
-              for (int k = 0; k < kPerBlock; ++k) ld_shared4(in + k * 512, c[k][0], c[k][1], c[k][2], c[k][3]);
-              block_of(kv ? a.kc8 : a.vc8, i, blk, i < n);
-              const float k_now = __shfl_sync(0xFFFFFFFFu, k_by, (i & 3) * 8 + w * kBlocks + blk);
-              float by = kv ? (blk == 0 ? v_now[0] : v_now[kBlocks - 1]) : k_now;
-              static_assert(kBlocks <= 2, "v_now");
-              uint32_t h[kPerBlock][8];
-#pragma unroll
-              for (int k = 0; k < kPerBlock; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) codes_to_half4(c[k][e], h[k][2 * e], h[k][2 * e + 1]);
-              if (by < 0x1p-24f) {   // no fp16 number: in two steps, the first exact
-                by *= 0x1p12f;
-#pragma unroll
-                for (int k = 0; k < kPerBlock; ++k)
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) h[k][e] = mul_half2(h[k][e], 0x0C000C00u);   // 2^-12
-              }
-              const uint32_t by2 = pack16<true>(by, by);
-#pragma unroll
-              for (int k = 0; k < kPerBlock; ++k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[k][e] = mul_half2(h[k][e], by2);
-#pragma unroll
-              for (int k = 0; k < kPerBlock; ++k) {
-                // rows 4 and 8 apart differ by one bit of the chunk in the swizzle, and not at all
-                const uint32_t at1 = (kRows == 4 && k % 2 == 1 ? to ^ 64u : to) + k * kRows * 128;
-                st_shared16(at1, h[k][0], h[k][1], h[k][2], h[k][3]);
-                st_shared16(at1 ^ 16u, h[k][4], h[k][5], h[k][6], h[k][7]);
-                load(in + k * 512);
-              }
-              to += 16 * 128;
-              in += kPerBlock * 512;
+          if ((i & 3) == 2) read_scales();
+          // The slot was last used eight tiles ago.  Once the values of four tiles ago have been converted, the products of six
+          // tiles ago are done, and with them the softmax of those before, which had its references from there.
+          if (tiles >= 4 && !wait_warp(INFOEMPTY((tiles - 4) & (kInfos - 1)), ((tiles - 4) / kInfos) & 1))
+            return false;
+          TileScales* to = scales_s + (tiles & (kInfos - 1));
+          if (lane >> 3 == (i & 3)) {
+            to->k_by[lane & 7] = k_by;
+            to->v_by[lane & 7] = v_by;
+            if ((lane & 7) == 0) {
+              to->k_ref = k_ref;
+              to->v_ref = v_ref;
             }
           }
-          // The tile's references, for its softmax: their slot was last used four tiles ago, whose softmax was done before this
-          // stage was free.  What follows from this warp's word (the scores, their barrier) tells the softmax of them.
-          if (i < n && w == 0 && lane == (i & 3) * 8) scales_s[tiles & (kInfos - 1)] = TileScales{k_ref, v_ref};
-          tiles += i < n;
-          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(FULL(st));
+          if (lane == 0) mbar_arrive(INFO(tiles & (kInfos - 1)));
           __syncwarp();
         }
-        ++seg;
         return true;
       });
       if (bad) raise_flag(a.err, kErrBadPages);
     }
+  } else if (warp >= kFirstConvert) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
+    // ---- codes into operands: a warp has 32 of the tile's positions, two blocks; a lane has 16 bytes of a row, and the
+    // warp kRows rows (a piece) at a time.
+    constexpr int kRows = 512 / D, kPerBlock = 16 / kRows;
+    const int w = warp - kFirstConvert;
+    // A lane's dims 16 q .. and its row of a piece; eight lanes in a row have two rows of one box of 64 dims, so that what
+    // they store lies in different banks.  Pieces come by asynchronous copies, each lane's own 16 bytes by itself, so that
+    // nothing but its own count of copies stands between them and their use.
+    const int q = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3, rr = D == 128 ? (lane >> 2) & 3 : lane >> 2;
+    const uint32_t mine = sRaw + w * 32 * D + lane * 16;
+    const uint32_t line = (q >> 2) * C::kBoxBytes + (w * 32 + rr) * 128 + ((((2 * q) & 7) ^ rr) << 4);
+    const long long step = kRows * a.row_stride;
+    const uint32_t infos = smem_u32(&scales_s[0].k_by[w * 2]);
+    uint32_t at = 0, tiles = 0;
+    int seg = 0;
+    bad = false;
+    walk([&](int b, const SeqRows&, int g, const Item& x, int i0, int n, uint32_t) {
+      const int32_t* row = a.table + (size_t)b * a.max_pages;
+      // Page numbers of the blocks of four tiles, one a lane, read four tiles ahead (-1: taken as zeros).
+      bool need;
+      int pg_ahead = read_page(row, x, i0, n, 0, &need), pg = -1;
+      auto next_four = [&](int i) {
+        pg = page_or_none(pg_ahead, need);
+        pg_ahead = read_page(row, x, i0, n, i + 4, &need);
+      };
+      next_four(0);
+      const long long lane_off = g * a.head_stride + rr * a.row_stride + q * 16;
+      // Block blk of tile i of a cache on its way to its place, which this lane has read: one group of copies.
+      auto fetch = [&](const uint8_t* cache, int i, int blk) {
+        const int page = __shfl_sync(0xFFFFFFFFu, pg, (i & 3) * 8 + w * 2 + blk);
+        const bool go = i < n && page >= 0;
+        cp_async_pieces<kPerBlock>(
+            mine + blk * kPerBlock * 512,
+            go ? cache + page * a.page_stride + ((w * 32 + blk * 16) & ((1 << a.page_shift) - 1)) * a.row_stride + lane_off : cache,
+            go ? step : 0, go ? 16 : 0);
+        cp_async_commit();
+      };
+#pragma unroll 1
+      for (int blk = 0; blk < 2; ++blk) fetch(a.kc8, 0, blk);
+      for (int i = 0; i <= n; ++i, ++at) {
+        const uint32_t st = at & 1;
+        if (i < n && !wait_warp(INFO(tiles & (kInfos - 1)), (tiles / kInfos) & 1)) return false;
+        if (at >= C::kStages && !wait_warp(EMPTY(st), (at / C::kStages - 1) & 1)) return false;
+        if (i > 0 && (i & 3) == 0) next_four(i);
+        // The values of tile i - 1, then the keys of tile i, by the same instructions (what is unrolled is fetched anew
+        // each time, beside the softmax's instructions, and that takes longer than it does), a block a turn; behind
+        // them come the keys of tile i and its values.
+#pragma unroll 1
+        for (int kv = i > 0 ? 1 : 0; kv >= (i < n ? 0 : 1); --kv) {
+          uint32_t to = sKV + st * C::kStageBytes + kv * C::kTileBytes + line, in = mine;
+          uint32_t by0, by1;
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                       : "=r"(by0), "=r"(by1)
+                       : "r"(infos + ((tiles - kv) & (kInfos - 1)) * (uint32_t)sizeof(TileScales) + kv * 32)
+                       : "memory");
+#pragma unroll 1
+          for (int blk = 0; blk < 2; ++blk) {
+            cp_async_wait<1>();   // the older of two blocks
+            convert_block<D>(in, to, blk == 0 ? by0 : by1);
+            fetch(kv ? a.kc8 : a.vc8, i, blk);
+            to += 16 * 128;
+            in += kPerBlock * 512;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(FULL(st));
+          if (i > 0) mbar_arrive(INFOEMPTY((tiles - 1) & (kInfos - 1)));
+        }
+        tiles += i < n;
+        __syncwarp();
+      }
+      ++seg;
+      return true;
+    });
+    if (bad) raise_flag(a.err, kErrBadPages);
   } else {
     // ---- softmax: row `r` of row tile `t`
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -567,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!FP16) {
         // bf16 times the power of two that brings the row's largest to 2^14 .. 2^15: exact down to 2^-24, and at that within
         // 2^-40 of the largest
-        if (!mbar_wait_warp(QFULL(t), outs & 1, &abort_s, a.err)) return false;
+        if (!wait_warp(QFULL(t), outs & 1)) return false;
         const uint32_t line = sQ + t * C::kTileBytes + r * 128;
         uint32_t w[D / 2];
 #pragma unroll
@@ -596,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n; ++i) {
         const int j0 = x.r.tile(i0 + i) * kTN;
         const bool open = tile_open<kTN>(a, j0, x.p_lo, x.p_hi);
-        if (!mbar_wait_warp(SFULL(t), done & 1, &abort_s, a.err)) return false;
+        if (!wait_warp(SFULL(t), done & 1)) return false;
         ++done;
         tc_fence_after();
         const volatile TileScales* ts = scales_s + (tiles & (kInfos - 1));
@@ -618,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool move = mx > m && (m == -INFINITY || mx - m > kLazy);
         if (__any_sync(0xFFFFFFFFu, move || v_new != v_ref)) {
           if (__any_sync(0xFFFFFFFFu, move && p >= 0 && fabsf(mx) > kFar)) {   // the tiles from here on in another way
-            const FarRow row = far_tiles8<D>(a, x, i0, i, n, p, tS, tO, SFULL(t), PFULL(t, 0), scales_s, q_scale, &abort_s,
+            const FarRow row = far_tiles8<D>(a, x, i0, i, n, p, tS, tO, SFULL(t), PFULL(t, 0), scales_s, q_scale,
                                              FarRow{m, l, v_ref, done, tiles});
             if (row.done < 0) return false;
             m = row.m;
@@ -670,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- the item's result, or this share's part of it
       const int my_seg = seg++;
-      if (!mbar_wait_warp(OFULL(t), outs & 1, &abort_s, a.err)) return false;
+      if (!wait_warp(OFULL(t), outs & 1)) return false;
       ++outs;
       tc_fence_after();
       const bool whole = i0 == 0 && n == x.r.count;
@@ -775,15 +859,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     });
   }
-  // After a timeout, copies and products still in flight finish before the CTA gives up its memory.
-  if (tid == 0 && *(volatile int*)&abort_s) {
-    const long long c0 = clock64();
-    while (clock64() - c0 < 4000000ll) {
-    }
-  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  // After a timeout, copies and products still in flight finish before the CTA gives up its memory.
+  if (warp == kSoftmaxWarps + 1 && *(volatile int*)&abort_s) {
+    if (lane == 0) raise_flag(a.err, kErrWaitTimeout);
+    const long long c0 = clock64();
+    while (clock64() - c0 < 4000000ll) {
+    }
+    __syncwarp();
+  }
   if (warp == kSoftmaxWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem_slot, 512);

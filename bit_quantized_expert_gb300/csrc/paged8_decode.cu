@@ -522,20 +522,6 @@ cudaError_t launch(const PagedMaps& maps, const Paged8Args& a, const DecodeSplit
 
 }  // namespace
 
-// One cache as the tensor maps see it; boxes of `rows` positions of one page and head.
-static bool encode_pages8(CUtensorMap* m, const uint8_t* cache, const gqa_paged_dims& d, int rows) {
-  EncodeTiledFn f = encode_fn();
-  if (f == nullptr) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.page_size, (cuuint64_t)d.n_kv_heads,
-                              (cuuint64_t)d.num_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)d.row_stride, (cuuint64_t)d.head_stride, (cuuint64_t)d.page_stride};
-  const cuuint32_t box[4] = {(cuuint32_t)d.head_dim, (cuuint32_t)(rows < d.page_size ? rows : d.page_size), 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(cache), dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, d.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t launch_paged8_decode(const gqa_paged_dims& d, const Paged8Args& a, void* scratch, int ctas, cudaStream_t st) {
   PagedMaps maps;
   std::memset(&maps, 0, sizeof(maps));

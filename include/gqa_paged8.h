@@ -71,12 +71,12 @@ moe_status gqa_paged8_read(const gqa_paged_dims* dims, const uint8_t* k_cache, c
  * Products are fp16 on the tensor cores, with fp32 sums, and what enters them:
  *   queries     fp16 as they are; bf16 times a power of two of each row and head, off by at most 2^-40 of the row's
  *               largest number (one past 2^75 counts as infinite)
- *   keys        single tokens: exact.  Chunks: off by at most 2^-33 of the largest key (rounded up to a power of two)
- *               among the tile's 128 positions, and exact where the scales there are within 2^15 of one another
+ *   keys        single tokens: exact.  Chunks: exact where their block's scale is within 2^15 of the largest one among
+ *               the tile's 128 positions; off by at most 2^-25 of that scale down to 2^24 below it, and then taken as 0
  *   numerators  as gqa_paged_attention states for fp16 (single tokens: times their block's value scale over the
  *               largest that the share has met, so 2^-39 of the largest value there in absolute terms)
- *   values      single tokens: exact.  Chunks: off by at most 2^-33 of the largest value in the item's tiles up to there,
- *               and exact where the scales there are within 2^15 of one another
+ *   values      single tokens: exact.  Chunks: the same, beside the largest scale in the tiles that the row block has
+ *               met (so never off by more than 2^-24 of the largest value there)
  * Bit 8 is set for an output that is not finite: visible NaN codes, or values past the dims' type.
  *   workspace  >= gqa_paged8_workspace_bytes(dims) */
 moe_status gqa_paged8_attention(const gqa_paged_dims* dims, const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
