@@ -52,7 +52,7 @@ struct Dec8 {
 
 __device__ __forceinline__ void mma_half(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -334,21 +334,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int st = (it + i) % C::kStages;
       if (mbar_wait_warp(smem_u32(&full[st]), ((it + i) / C::kStages) & 1, &abort_s, a.err)) {
         const uint32_t sk = base + st * C::kStageBytes, sv = sk + C::kTileBytes;
+        // (four independent products beside one another: one alone waits ~30 cycles for the one before it)
         float sc[4][4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+        for (int t = 0; t < 4; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
 #pragma unroll
-          for (int s = 0; s < D / 64; ++s) {
-            const uint4 w = ld_shared16(sk + C::at(half + 8 * t + r, c * (D / 64) + s));
-            const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+        for (int s = 0; s < D / 64; ++s) {
+          uint32_t w[4][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+          for (int t = 0; t < 4; ++t) {
+            const uint4 v = ld_shared16(sk + C::at(half + 8 * t + r, c * (D / 64) + s));
+            w[t][0] = v.x, w[t][1] = v.y, w[t][2] = v.z, w[t][3] = v.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
               uint32_t b0, b1;
-              codes_to_half4(w4[e], b0, b1);
+              codes_to_half4(w[t][e], b0, b1);
               mma_half(sc[t], qa[8 * s + 2 * e], 0u, qa[8 * s + 2 * e + 1], 0u, b0, b1);
             }
-          }
         }
         const float2 ks = *reinterpret_cast<const float2*>(&scale_s[st][half >> 4]);
         const float2 vs = *reinterpret_cast<const float2*>(&scale_s[st][4 + (half >> 4)]);
