@@ -318,7 +318,7 @@ struct DecodeSplit {
   SplitRecord* rec;    // [ctas]
 };
 DecodeSplit paged_decode_split(int D, void* scratch, int ctas);
-cudaError_t launch_paged_decode_join(const PagedArgs& a, int D, const DecodeSplit& split, int ctas, cudaStream_t st);
+cudaError_t launch_paged_decode_join(const PagedArgs& a, int D, const DecodeSplit& split, int ctas, bool wide, cudaStream_t st);
 
 // Chunks: O of the 256 rows by four columns of all rows, then their maxima, then their sums.
 struct ChunkSplit {

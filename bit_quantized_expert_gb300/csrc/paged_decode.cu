@@ -23,6 +23,7 @@
 // 33.6 MB, 14.0 us (10.5 with its cache in L2); 64 sequences with heads of 64, 69.5 MB, 18.2 us.  tcgen05
 // would not help: eight heads fill an eighth of its 64-row tiles, and bytes bound the rest.
 #include <cmath>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -414,10 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of one split item (blockIdx.x: the CTA that began it) for one query head (blockIdx.y).
 // Warp w takes parts w, w + 4, ...; the four warps are then joined in order.
+// A warp has BATCH of its parts in flight at once, or FEW where no warp has more (0: never looked at).  Here 8.  Over an 8-bit
+// cache, whose items take half as long, 10 and 2: one sequence's 76 parts a head come in two round trips, and an item of few
+// parts does not go through the sums of many (32768 positions 12.95 -> 12.55 us, windows 14.1 -> 13.9; with 20 in flight,
+// whose registers leave room for half as many blocks, 64 ragged take 22.7 in place of 21.9).
 constexpr int kJoinWarps = 4;
-constexpr int kJoinBatch = 8;
 
-template <int D, bool FP16>
+template <int D, bool FP16, int BATCH, int FEW>
 __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const PagedArgs a, const DecodeSplit split) {
   using C = Dec<D>;
   constexpr int E = D / 32;
@@ -433,10 +437,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Page
   float m = kUnseen, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int i0 = warp; i0 < parts; i0 += kJoinWarps * kJoinBatch) {
-    float mb[kJoinBatch], lb[kJoinBatch], ob[kJoinBatch][E];
+  auto turn = [&](auto batch_c, int i0) {
+    constexpr int N = decltype(batch_c)::value;
+    float mb[N], lb[N], ob[N][E];
 #pragma unroll
-    for (int i = 0; i < kJoinBatch; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int c = i0 + i * kJoinWarps;
       mb[i] = kUnseen;
       lb[i] = 0.f;
@@ -452,19 +457,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Page
     }
     float mx = m;
 #pragma unroll
-    for (int i = 0; i < kJoinBatch; ++i) mx = fmaxf(mx, mb[i]);
+    for (int i = 0; i < N; ++i) mx = fmaxf(mx, mb[i]);
     const float sc = exp2f(m - mx);
     l *= sc;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= sc;
 #pragma unroll
-    for (int i = 0; i < kJoinBatch; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float w = exp2f(mb[i] - mx);
       l += lb[i] * w;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] += ob[i][e] * w;
     }
     m = mx;
+  };
+  if (FEW > 0 && parts <= kJoinWarps * FEW) {
+    if (warp < parts) turn(std::integral_constant<int, FEW == 0 ? 1 : FEW>{}, warp);
+  } else {
+#pragma unroll 1
+    for (int i0 = warp; i0 < parts; i0 += kJoinWarps * BATCH) turn(std::integral_constant<int, BATCH>{}, i0);
   }
   if (lane == 0) {
     mw_s[warp] = m;
@@ -509,7 +520,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedArgs& a, const DecodeSplit&
   cfg.attrs = at;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, decode_kernel<D, FP16>, maps, a, split);
-  return e == cudaSuccess ? launch_paged_decode_join(a, D, split, ctas, st) : e;
+  return e == cudaSuccess ? launch_paged_decode_join(a, D, split, ctas, false, st) : e;
 }
 
 }  // namespace
@@ -525,7 +536,9 @@ DecodeSplit paged_decode_split(int D, void* scratch, int ctas) {
   return split;
 }
 
-cudaError_t launch_paged_decode_join(const PagedArgs& a, int D, const DecodeSplit& split, int ctas, cudaStream_t st) {
+namespace {
+template <int BATCH, int FEW>
+cudaError_t launch_join(const PagedArgs& a, int D, const DecodeSplit& split, int ctas, cudaStream_t st) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -536,10 +549,17 @@ cudaError_t launch_paged_decode_join(const PagedArgs& a, int D, const DecodeSpli
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (D == 128)
-    return a.fp16 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<128, true>, a, split)
-                  : cudaLaunchKernelEx(&cfg, decode_join_kernel<128, false>, a, split);
-  return a.fp16 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<64, true>, a, split)
-                : cudaLaunchKernelEx(&cfg, decode_join_kernel<64, false>, a, split);
+    return a.fp16 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<128, true, BATCH, FEW>, a, split)
+                  : cudaLaunchKernelEx(&cfg, decode_join_kernel<128, false, BATCH, FEW>, a, split);
+  return a.fp16 ? cudaLaunchKernelEx(&cfg, decode_join_kernel<64, true, BATCH, FEW>, a, split)
+                : cudaLaunchKernelEx(&cfg, decode_join_kernel<64, false, BATCH, FEW>, a, split);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode_join(const PagedArgs& a, int D, const DecodeSplit& split, int ctas, bool wide, cudaStream_t st) {
+  return wide ? launch_join<10, 2>(a, D, split, ctas, st)
+              : launch_join<8, 0>(a, D, split, ctas, st);
 }
 
 cudaError_t launch_paged_decode(const PagedMaps& maps, const PagedArgs& a, int D, void* scratch, int ctas, cudaStream_t st) {
