@@ -46,7 +46,7 @@ struct Unit {
 template <bool FROM_ZERO, class Body>
 __device__ __forceinline__ void walk_blocks(const WalkArgs& a, uint32_t* pre_s, uint32_t* warp_s, Body&& body) {
   bool bad = false, over;
-  const uint32_t total = scan_sequences<kWalkThreads>(a.B, pre_s, warp_s, &over, [&](int b) {
+  const uint32_t total = scan_sequences8<kWalkThreads>(a.B, pre_s, warp_s, &over, [&](int b) {
     return (unsigned long long)blocks_of(load_seq(a, b, bad), FROM_ZERO).n * a.Hkv;
   });
   if (over) bad = true;   // (cannot be: T * Hq and B * Hkv are below 2^31)
@@ -78,7 +78,7 @@ __device__ __forceinline__ void walk_blocks(const WalkArgs& a, uint32_t* pre_s, 
 
 // A lane has 8 dims (16 bytes of a row, 8 codes) of every (256 / D)-th row.
 template <int D, bool FP16>
-__global__ void __launch_bounds__(kWalkThreads) append8_kernel(const WalkArgs a) {
+__global__ void __launch_bounds__(kWalkThreads, 3) append8_kernel(const WalkArgs a) {
   constexpr int kLanes = D / 8, kStep = 32 / kLanes, kTurns = 16 / kStep;
   extern __shared__ uint32_t pre_s[];
   __shared__ uint32_t warp_s[kWalkThreads / 32];
@@ -94,19 +94,15 @@ __global__ void __launch_bounds__(kWalkThreads) append8_kernel(const WalkArgs a)
     if (u.page < 0) return;
     uint8_t* to = dst + u.page * a.page_stride + u.g * a.head_stride + (u.off + r0) * a.row_stride + dim;
     float* scale = scales + scale_index(u.page, a.Hkv, u.g, a.page_shift, u.off);
-    // Everything that is needed, in flight together: new rows, and what the block holds before them.
+    // The new rows, all in flight together.  (What the block holds before them is read only where the scale grows.)
     uint4 x[kTurns];
-    uint2 old[kTurns];
     float was = u.o0 > 0 ? *scale : kLeastScale;
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
       const int o = r0 + i * kStep;
       x[i] = make_uint4(0, 0, 0, 0);
-      old[i] = make_uint2(0, 0);
       if (o >= u.o0 && o < u.o1)
         x[i] = __ldcg(reinterpret_cast<const uint4*>(src + (long long)(u.row0 + o) * stride + u.g * D + dim));
-      else if (o < u.o0)
-        old[i] = __ldcg(reinterpret_cast<const uint2*>(to + (long long)i * kStep * a.row_stride));
     }
     if (!scale_ok(was)) {
       raise_flag(a.err, kErrBadPages);
@@ -136,22 +132,31 @@ __global__ void __launch_bounds__(kWalkThreads) append8_kernel(const WalkArgs a)
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
       const int o = r0 + i * kStep;
-      if (o >= u.o1 || (o < u.o0 && ratio == 1.f)) continue;
-      uint2 c;
-      if (o >= u.o0) {
-        const float2 f0 = unpack16<FP16>(x[i].x), f1 = unpack16<FP16>(x[i].y), f2 = unpack16<FP16>(x[i].z),
-                     f3 = unpack16<FP16>(x[i].w);
-        c.x = to_codes4(code(f0.x), code(f0.y), code(f1.x), code(f1.y));
-        c.y = to_codes4(code(f2.x), code(f2.y), code(f3.x), code(f3.y));
-      } else {
+      if (o < u.o0 || o >= u.o1) continue;
+      const float2 f0 = unpack16<FP16>(x[i].x), f1 = unpack16<FP16>(x[i].y), f2 = unpack16<FP16>(x[i].z),
+                   f3 = unpack16<FP16>(x[i].w);
+      *reinterpret_cast<uint2*>(to + (long long)i * kStep * a.row_stride) =
+          make_uint2(to_codes4(code(f0.x), code(f0.y), code(f1.x), code(f1.y)),
+                     to_codes4(code(f2.x), code(f2.y), code(f3.x), code(f3.y)));
+    }
+    if (u.o0 > 0 && ratio != 1.f) {   // codes in the scale before, to codes in the new one
+      uint2 old[kTurns];
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        old[i] = make_uint2(0, 0);
+        if (r0 + i * kStep < u.o0) old[i] = __ldcg(reinterpret_cast<const uint2*>(to + (long long)i * kStep * a.row_stride));
+      }
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        if (r0 + i * kStep >= u.o0) continue;
         uint32_t h[4];
         codes_to_half4(old[i].x, h[0], h[1]);
         codes_to_half4(old[i].y, h[2], h[3]);
         const float2 f0 = unpack16<true>(h[0]), f1 = unpack16<true>(h[1]), f2 = unpack16<true>(h[2]), f3 = unpack16<true>(h[3]);
-        c.x = to_codes4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
-        c.y = to_codes4(f2.x * ratio, f2.y * ratio, f3.x * ratio, f3.y * ratio);
+        *reinterpret_cast<uint2*>(to + (long long)i * kStep * a.row_stride) =
+            make_uint2(to_codes4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio),
+                       to_codes4(f2.x * ratio, f2.y * ratio, f3.x * ratio, f3.y * ratio));
       }
-      *reinterpret_cast<uint2*>(to + (long long)i * kStep * a.row_stride) = c;
     }
     if (lane == 0) *scale = s;
     if (lost) raise_flag(a.err, kErrNonFinite);

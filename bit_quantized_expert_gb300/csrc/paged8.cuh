@@ -48,6 +48,32 @@ __device__ __forceinline__ uint32_t to_codes4(float x0, float x1, float x2, floa
   return d;
 }
 
+// scan_sequences for the block, or for up to 32 sequences by every warp for itself, one a lane, without a barrier (all write
+// the same sums): 0.15 to 0.2 us of a call.
+template <int NT, class Cost>
+__device__ __forceinline__ uint32_t scan_sequences8(int B, uint32_t* pre_s, uint32_t* warp_s, bool* over, Cost cost) {
+  if (B > 32) return scan_sequences<NT>(B, pre_s, warp_s, over, cost);
+  const int lane = threadIdx.x & 31;
+  const unsigned long long mine = lane < B ? cost(lane) : 0;
+  uint32_t sum = (uint32_t)mine;
+  bool carry = mine >> 32 != 0;
+  __syncwarp();
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sum, off);
+    if (lane >= off) {
+      sum += x;
+      carry |= sum < x;
+    }
+  }
+  if (lane < B) pre_s[lane + 1] = sum;
+  if (lane == 0) pre_s[0] = 0;
+  sum = __shfl_sync(0xFFFFFFFFu, sum, 31);
+  *over = __any_sync(0xFFFFFFFFu, carry);
+  __syncwarp();
+  return sum;
+}
+
 // One cache as the tensor maps see it; boxes of `rows` positions of one page and head.
 bool encode_pages8(CUtensorMap* m, const uint8_t* cache, const gqa_paged_dims& d, int rows);
 cudaError_t launch_paged8_decode(const gqa_paged_dims& d, const Paged8Args& a, void* scratch, int ctas, cudaStream_t st);

@@ -101,29 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return s.n == 0 ? 0ull : (unsigned long long)(visible_tiles<kTN>(a, s.p0, s.p0).count + kItemUnits) * a.Hkv;
   };
   bool over;
-  uint32_t total;
-  if (a.B <= 32) {
-    // Every warp for itself, one sequence a lane: no barrier.  (All write the same sums.)
-    const unsigned long long mine = lane < a.B ? cost(lane) : 0;
-    uint32_t sum = (uint32_t)mine;
-    bool carry = mine >> 32 != 0;
-    __syncwarp();
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sum, off);
-      if (lane >= off) {
-        sum += x;
-        carry |= sum < x;
-      }
-    }
-    if (lane < a.B) pre_s[lane + 1] = sum;
-    if (lane == 0) pre_s[0] = 0;
-    total = __shfl_sync(0xFFFFFFFFu, sum, 31);
-    over = __any_sync(0xFFFFFFFFu, carry);
-    __syncwarp();
-  } else {
-    total = scan_sequences<kThreads>(a.B, pre_s, warp_s, &over, cost);
-  }
+  uint32_t total = scan_sequences8<kThreads>(a.B, pre_s, warp_s, &over, cost);
   if (over) {   // refused: nothing is computed
     bad = true;
     total = 0;

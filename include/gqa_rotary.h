@@ -74,8 +74,8 @@ typedef struct gqa_rotary_dims {
 /*   q, k              [T, heads, head_dim] with their token strides, 16-byte aligned
  *   positions         int32 [T], any numbers (negative ones turn the other way)
  *   turns             [rot_dim / 2], as gqa_rotary_table writes them (16-byte aligned)
- *   n_rows            int32 [1] or NULL: rows at or past it are neither read nor written (q_start + n_seqs of a plan);
- *                     NULL: all T
+ *   n_rows            int32 [1] or NULL: rows at or past it are not written, and what they hold has no effect (q_start +
+ *                     n_seqs of a plan); NULL: all T
  *   q_out, k_out      [T, heads, head_dim]; may be q and k themselves with the same strides.  An output may not
  *                     overlap an input or the other output in any other way
  * Sums are fp32, rounded once to the 16-bit type.  Device pointers, streams and statuses as in gqa_paged.h; no
