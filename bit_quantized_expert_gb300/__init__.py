@@ -537,43 +537,91 @@ def _paged8_caches(k, v, ks, vs, pd: GqaPagedDims, dev: int):
     return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr()
 
 
+# What the calls on an 8-bit cache compare their tensors with, by the dims' bytes: made once for each set of dims, since
+# reading the fields of the structure takes as long as the comparisons.
+_wants8 = {}
+
+
+class _Want8:
+    def __init__(self, pd: GqaPagedDims):
+        P, H, S, D, T, B = pd.num_pages, pd.n_kv_heads, pd.page_size, pd.head_dim, pd.n_tokens, pd.n_seqs
+        self.B, self.types, self.table = B, _paged_types[pd.dtype], (B, pd.max_pages)
+        self.q, self.kv = (T, pd.n_heads, D), (T, H, D)
+        self.q_st, self.o_st = ((s or pd.n_heads * D, D, 1) for s in (pd.q_stride, pd.o_stride))
+        self.k_st, self.v_st = ((s or H * D, D, 1) for s in (pd.k_stride, pd.v_stride))
+        self.cache, self.scale = (P, H, S, D), (P, H, S // 16)
+        self.cache_st = (pd.page_stride or H * S * D, pd.head_stride or S * D, pd.row_stride or D, 1)
+
+
+def _want8(pd: GqaPagedDims) -> _Want8:
+    if len(_wants8) > 1000:
+        _wants8.clear()
+    w = _wants8[bytes(pd)] = _Want8(pd)
+    return w
+
+
+def _rows8(t, shape, strides, types, dev: int, pd: GqaPagedDims, stride: str, name: str) -> int:
+    """Pointer of a [rows, heads, D] tensor: at once where its shape and strides are those of the dims, else by _paged_rows,
+    which knows which strides do not count, and refuses."""
+    if t.shape == shape and t.stride() == strides and t.dtype in types and t.get_device() == dev:
+        return t.data_ptr()
+    return _paged_rows(t, *shape, getattr(pd, stride), pd.dtype, dev, name)
+
+
+def _caches8(k, v, ks, vs, w: _Want8, dev: int, pd: GqaPagedDims):
+    """_paged8_caches, at once where shapes and strides are those of the dims."""
+    if (k.shape == w.cache and k.stride() == w.cache_st and k.dtype in _byte_types and k.get_device() == dev
+            and v.shape == w.cache and v.stride() == w.cache_st and v.dtype in _byte_types and v.get_device() == dev
+            and ks.shape == w.scale and ks.dtype is _float32 and ks.get_device() == dev and ks.is_contiguous()
+            and vs.shape == w.scale and vs.dtype is _float32 and vs.get_device() == dev and vs.is_contiguous()):
+        return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr()
+    return _paged8_caches(k, v, ks, vs, pd, dev)
+
+
+def _tables8(block_table, q_start, kv_len, w: _Want8, dev: int, pd: GqaPagedDims):
+    if (block_table.shape == w.table and block_table.dtype is _int32 and block_table.get_device() == dev
+            and block_table.is_contiguous()):
+        table = block_table.data_ptr()
+    else:
+        table = _paged_table(block_table, w.B, pd.max_pages, dev)
+    return table, _paged_ints(q_start, w.B + 1, dev, "q_start"), _paged_ints(kv_len, w.B, dev, "kv_len")
+
+
 def gqa_paged8_append(pd: GqaPagedDims, k, v, block_table, q_start, kv_len, k_cache, v_cache, k_scale, v_scale, workspace,
                       stream=None):
     """k, v [T, Hkv, D] of pd's type, quantised (e4m3 codes, one scale for 16 positions of a head) into the positions
     that q_start and kv_len give their rows, the last ones of each sequence.  The caches are 8-bit
     [num_pages, Hkv, page_size, D], the scales fp32 [num_pages, Hkv, page_size / 16] (include/gqa_paged8.h)."""
-    dev, T, H, D, B, dt = _paged_device(), pd.n_tokens, pd.n_kv_heads, pd.head_dim, pd.n_seqs, pd.dtype
-    kc, vc, ks, vs = _paged8_caches(k_cache, v_cache, k_scale, v_scale, pd, dev)
+    dev = _paged_device()
+    w = _wants8.get(bytes(pd)) or _want8(pd)
     _check(load_library().gqa_paged8_append(
-        ctypes.byref(pd), _paged_rows(k, T, H, D, pd.k_stride, dt, dev, "k"), _paged_rows(v, T, H, D, pd.v_stride, dt, dev, "v"),
-        _paged_table(block_table, B, pd.max_pages, dev), _paged_ints(q_start, B + 1, dev, "q_start"),
-        _paged_ints(kv_len, B, dev, "kv_len"), kc, vc, ks, vs, _paged_workspace(workspace, dev), workspace.nbytes,
+        ctypes.byref(pd), _rows8(k, w.kv, w.k_st, w.types, dev, pd, "k_stride", "k"),
+        _rows8(v, w.kv, w.v_st, w.types, dev, pd, "v_stride", "v"), *_tables8(block_table, q_start, kv_len, w, dev, pd),
+        *_caches8(k_cache, v_cache, k_scale, v_scale, w, dev, pd), _paged_workspace(workspace, dev), workspace.nbytes,
         _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged8_append")
 
 
 def gqa_paged8_read(pd: GqaPagedDims, k_cache, v_cache, k_scale, v_scale, block_table, q_start, kv_len, k, v, workspace,
                     stream=None):
     """The cached keys and values of each sequence's last rows, in pd's type, into k and v [T, Hkv, D]."""
-    dev, T, H, D, B, dt = _paged_device(), pd.n_tokens, pd.n_kv_heads, pd.head_dim, pd.n_seqs, pd.dtype
-    kc, vc, ks, vs = _paged8_caches(k_cache, v_cache, k_scale, v_scale, pd, dev)
+    dev = _paged_device()
+    w = _wants8.get(bytes(pd)) or _want8(pd)
     _check(load_library().gqa_paged8_read(
-        ctypes.byref(pd), kc, vc, ks, vs, _paged_table(block_table, B, pd.max_pages, dev),
-        _paged_ints(q_start, B + 1, dev, "q_start"), _paged_ints(kv_len, B, dev, "kv_len"),
-        _paged_rows(k, T, H, D, pd.k_stride, dt, dev, "k"), _paged_rows(v, T, H, D, pd.v_stride, dt, dev, "v"),
-        _paged_workspace(workspace, dev), workspace.nbytes,
+        ctypes.byref(pd), *_caches8(k_cache, v_cache, k_scale, v_scale, w, dev, pd),
+        *_tables8(block_table, q_start, kv_len, w, dev, pd), _rows8(k, w.kv, w.k_st, w.types, dev, pd, "k_stride", "k"),
+        _rows8(v, w.kv, w.v_st, w.types, dev, pd, "v_stride", "v"), _paged_workspace(workspace, dev), workspace.nbytes,
         _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged8_read")
 
 
 def gqa_paged8_attention(pd: GqaPagedDims, q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, kv_len, o, workspace,
                          stream=None):
     """gqa_paged_attention over an 8-bit cache.  q, o [T, Hq, D] of pd's type."""
-    dev, T, H, D, B, dt = _paged_device(), pd.n_tokens, pd.n_heads, pd.head_dim, pd.n_seqs, pd.dtype
-    kc, vc, ks, vs = _paged8_caches(k_cache, v_cache, k_scale, v_scale, pd, dev)
+    dev = _paged_device()
+    w = _wants8.get(bytes(pd)) or _want8(pd)
     _check(load_library().gqa_paged8_attention(
-        ctypes.byref(pd), _paged_rows(q, T, H, D, pd.q_stride, dt, dev, "q"), kc, vc, ks, vs,
-        _paged_table(block_table, B, pd.max_pages, dev), _paged_ints(q_start, B + 1, dev, "q_start"),
-        _paged_ints(kv_len, B, dev, "kv_len"), _paged_rows(o, T, H, D, pd.o_stride, dt, dev, "o"),
-        _paged_workspace(workspace, dev), workspace.nbytes,
+        ctypes.byref(pd), _rows8(q, w.q, w.q_st, w.types, dev, pd, "q_stride", "q"),
+        *_caches8(k_cache, v_cache, k_scale, v_scale, w, dev, pd), *_tables8(block_table, q_start, kv_len, w, dev, pd),
+        _rows8(o, w.q, w.o_st, w.types, dev, pd, "o_stride", "o"), _paged_workspace(workspace, dev), workspace.nbytes,
         _raw_stream(dev) if stream is None else _stream(stream)), "gqa_paged8_attention")
 
 
@@ -607,22 +655,47 @@ def gqa_rotary_table(rot_dim, base=10000.0, scaling="none", factor=1.0, original
     return torch.tensor([x - 2**64 if x >= 2**63 else x for x in turns], dtype=torch.int64).to(device)
 
 
+_wants_rotary = {}
+
+
+class _WantRotary:
+    def __init__(self, rd: GqaRotaryDims):
+        T, D = rd.n_tokens, rd.head_dim
+        self.T, self.D, self.dtype, self.pairs, self.types = T, D, rd.dtype, rd.rot_dim // 2, _paged_types[rd.dtype]
+        self.rows = [(h, (T, h, D), (s or h * D, D, 1), s) for h, s in (
+            (rd.n_heads, rd.q_stride), (rd.n_kv_heads, rd.k_stride), (rd.n_heads, rd.q_out_stride),
+            (rd.n_kv_heads, rd.k_out_stride))]
+
+
+def _want_rotary(rd: GqaRotaryDims) -> _WantRotary:
+    if len(_wants_rotary) > 1000:
+        _wants_rotary.clear()
+    w = _wants_rotary[bytes(rd)] = _WantRotary(rd)
+    return w
+
+
+def _rotary_rows(t, i: int, w: _WantRotary, dev: int, name: str):
+    heads, shape, strides, stride = w.rows[i]
+    if heads == 0:
+        return None
+    if t.shape == shape and t.stride() == strides and t.dtype in w.types and t.get_device() == dev:
+        return t.data_ptr()
+    return _paged_rows(t, *shape, stride, w.dtype, dev, name)
+
+
 def gqa_rotary(rd: GqaRotaryDims, q, k, positions, table, q_out, k_out, n_rows=None, stream=None):
     """The pairs of q [T, Hq, D] and k [T, Hkv, D] turned by their rows' positions (int32 [T]) into q_out and k_out, which
     may be q and k.  table: gqa_rotary_table's.  n_rows: an int32 tensor whose first entry is the number of rows in use
     (q_start[B:] of a plan), or None.  A tensor without heads is None."""
-    dev, T, D, dt = _paged_device(), rd.n_tokens, rd.head_dim, rd.dtype
-
-    def rows(x, heads, stride, name):
-        return None if heads == 0 else _paged_rows(x, T, heads, D, stride, dt, dev, name)
-    if table.get_device() != dev or table.dtype is not _int64 or table.numel() != rd.rot_dim // 2 or not table.is_contiguous():
-        raise ValueError(f"table: expected a contiguous int64 tensor of {rd.rot_dim // 2} entries on device {dev}")
+    dev = _paged_device()
+    w = _wants_rotary.get(bytes(rd)) or _want_rotary(rd)
+    if table.get_device() != dev or table.dtype is not _int64 or table.numel() != w.pairs or not table.is_contiguous():
+        raise ValueError(f"table: expected a contiguous int64 tensor of {w.pairs} entries on device {dev}")
     _check(load_library().gqa_rotary(
-        ctypes.byref(rd), rows(q, rd.n_heads, rd.q_stride, "q"), rows(k, rd.n_kv_heads, rd.k_stride, "k"),
-        _paged_ints(positions, T, dev, "positions"), table.data_ptr(),
-        None if n_rows is None else _paged_ints(n_rows, 1, dev, "n_rows"), rows(q_out, rd.n_heads, rd.q_out_stride, "q_out"),
-        rows(k_out, rd.n_kv_heads, rd.k_out_stride, "k_out"), _raw_stream(dev) if stream is None else _stream(stream)),
-        "gqa_rotary")
+        ctypes.byref(rd), _rotary_rows(q, 0, w, dev, "q"), _rotary_rows(k, 1, w, dev, "k"),
+        _paged_ints(positions, w.T, dev, "positions"), table.data_ptr(),
+        None if n_rows is None else _paged_ints(n_rows, 1, dev, "n_rows"), _rotary_rows(q_out, 2, w, dev, "q_out"),
+        _rotary_rows(k_out, 3, w, dev, "k_out"), _raw_stream(dev) if stream is None else _stream(stream)), "gqa_rotary")
 
 
 def gdn_dims(T, H, d_k=128, d_v=128) -> GdnDims:
