@@ -295,6 +295,7 @@ extern "C" moe_status gqa_paged8_append(const gqa_paged_dims* dims, const uint16
   if ((st = check_pointers({block_table, q_start, kv_len}, {k, v, k_cache, v_cache, k_scale, v_scale, workspace})) != MOE_OK)
     return (moe_status)st;
   if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
+  if (k_cache == v_cache || k_scale == v_scale) return MOE_ERR_INVALID_ARG;   // (both would be written)
   int sms = 0;
   if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
   WalkArgs a;
@@ -321,6 +322,7 @@ extern "C" moe_status gqa_paged8_read(const gqa_paged_dims* dims, const uint8_t*
   if ((st = check_pointers({block_table, q_start, kv_len}, {k, v, k_cache, v_cache, k_scale, v_scale, workspace})) != MOE_OK)
     return (moe_status)st;
   if (workspace_bytes < gqa_paged_workspace_bytes(dims)) return MOE_ERR_WORKSPACE;
+  if (k == v) return MOE_ERR_INVALID_ARG;   // (both would be written)
   int sms = 0;
   if (device_sms(&sms) != MOE_OK) return MOE_ERR_CUDA;
   WalkArgs a;

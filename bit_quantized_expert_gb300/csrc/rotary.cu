@@ -239,7 +239,8 @@ extern "C" moe_status gqa_rotary(const gqa_rotary_dims* dims, const uint16_t* q,
       (d.dtype != GQA_PAGED_BF16 && d.dtype != GQA_PAGED_FP16) || !std::isfinite(d.amplitude))
     return MOE_ERR_INVALID_ARG;
   const long long heads = (long long)d.n_heads + d.n_kv_heads, lim = 1ll << 31;
-  if (d.head_dim % 8 != 0 || d.head_dim > 2 * kRotMaxPairs || heads * d.head_dim >= lim || d.n_tokens * heads >= lim)
+  if (d.head_dim % 8 != 0 || d.head_dim > 2 * kRotMaxPairs || heads * d.head_dim > (1 << 26) ||
+      d.n_tokens * heads >= lim)
     return MOE_ERR_UNSUPPORTED;
   const long long qw = (long long)d.n_heads * d.head_dim, kw = (long long)d.n_kv_heads * d.head_dim;
   int64_t* strides[4] = {&d.q_stride, &d.q_out_stride, &d.k_stride, &d.k_out_stride};
@@ -293,8 +294,8 @@ extern "C" moe_status gqa_rotary(const gqa_rotary_dims* dims, const uint16_t* q,
   const bool half = d.pairs == GQA_ROTARY_HALF;
   const int V = half ? (a.pairs % 8 == 0 ? 8 : a.pairs % 4 == 0 ? 4 : a.pairs % 2 == 0 ? 2 : 1) : 8;
   a.turned = half ? a.pairs / V : (d.rot_dim + 7) / 8;
+  // (units of a CTA: at most 2^29, so that its counters stay within 32 bits)
   a.units = a.turned + (copy ? (half ? (d.head_dim - d.rot_dim) / V : d.head_dim / 8 - a.turned) : 0);
-  if ((long long)a.heads * a.units * kRotMaxTokens >= lim) return MOE_ERR_UNSUPPORTED;
   // Tokens of a CTA: one while there are few, then as many as fill its turns best.
   const int per = a.heads * a.units, turn = kRotThreads * kRotBatch;
   a.tokens = 1;

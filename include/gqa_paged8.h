@@ -61,8 +61,8 @@ moe_status gqa_paged8_append(const gqa_paged_dims* dims, const uint16_t* k, cons
  *   k, v         [T, Hkv, D] of the dims' type with their token strides: code * scale, rounded once (fp16: values
  *                past 65504 become 65504); zeros in rows before position 0 and of a page number out of range (which
  *                sets bit 16)
- * window, sinks and max_new play no part but for max_new's check.  Rows of no sequence are left as they were.  One
- * launch. */
+ * window, sinks and max_new play no part but for max_new's check.  Rows of no sequence are left as they were.  k and v
+ * have no element in common (one address for both is refused).  One launch. */
 moe_status gqa_paged8_read(const gqa_paged_dims* dims, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
                            const float* v_scale, const int32_t* block_table, const int32_t* q_start, const int32_t* kv_len,
                            uint16_t* k, uint16_t* v, void* workspace, size_t workspace_bytes, void* stream);

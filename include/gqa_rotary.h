@@ -56,7 +56,8 @@ typedef struct gqa_rotary_scaling {
 moe_status gqa_rotary_table(const gqa_rotary_scaling* scaling, uint64_t* turns);
 
 /* Shapes.  Strides are in elements, from one token to the next; 0 stands for the packed value.
- *   n_heads, n_kv_heads   heads of q and of k; one of them may be 0 (its pointers are then not used)
+ *   n_heads, n_kv_heads   heads of q and of k; one of them may be 0 (its pointers are then not used); (n_heads +
+ *                n_kv_heads) * head_dim <= 2^26
  *   head_dim     a multiple of 8, at most 256
  *   rot_dim      even, 2 .. head_dim
  *   n_tokens     T, rows of q, k and positions; T * (n_heads + n_kv_heads) < 2^31

@@ -653,6 +653,31 @@ def test_repeats_bit_by_bit_and_on_two_streams(new):
         assert torch.equal(x.dev["o"], y) and x.flags() == 0
 
 
+def test_graphs_that_share_a_workspace():
+    """Single tokens and chunks, each in a graph of its own, one workspace: replayed in turn on one stream."""
+    batches = [Batch8([(3000, 1), (70, 1)], seed=33), Batch8([(2000, 90), (500, 30)], seed=34)]
+    for x in batches:
+        x.upload()
+    ws = max((x.dev["ws"] for x in batches), key=torch.numel)
+    graphs, first = [], []
+    for x in batches:
+        x.dev["ws"] = ws
+        x.attend()
+        torch.cuda.synchronize()
+        first.append(x.dev["o"].clone())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            x.attend()
+    for _ in range(4):
+        for x in batches:
+            x.dev["o"].zero_()
+        for g in graphs:
+            g.replay()
+        for x, y in zip(batches, first):
+            assert torch.equal(x.dev["o"], y)
+    assert all(x.flags() == 0 for x in batches)
+
+
 @pytest.mark.parametrize("new", [1, 20])
 def test_caches_past_32_bit_offsets(new):
     """A cache whose pages lie more than 2^32 bytes apart."""

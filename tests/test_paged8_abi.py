@@ -69,6 +69,15 @@ def test_dims_accepted(lib, extra):
     assert n >= 256 and n >= lib.gqa_paged_workspace_bytes(ctypes.byref(d))     # it serves the plan as well
 
 
+def test_one_address_for_two_outputs(lib):
+    """What a call writes for keys and for values lies apart; where it only reads them, one cache may be both."""
+    d = moe.gqa_paged_dims(**GOOD)
+    apart = dict(kc=1 << 20, vc=1 << 21, ks=1 << 22, vs=1 << 23)
+    assert _call(lib, "append", d, **{**apart, "vc": apart["kc"]}) == INVALID
+    assert _call(lib, "append", d, **{**apart, "vs": apart["ks"]}) == INVALID
+    assert _call(lib, "read", d, **apart, k=1 << 24, v=1 << 24) == INVALID
+
+
 @pytest.mark.parametrize("name", list(ORDER))
 def test_nothing_to_do(lib, name):
     none = {p: None for p in ORDER[name]}
@@ -116,7 +125,8 @@ def _rotary(lib, d, **kw):
     (dict(n_heads=-1), INVALID), (dict(n_heads=0, n_kv_heads=0), INVALID), (dict(rot_dim=0), INVALID), (dict(rot_dim=7), INVALID),
     (dict(rot_dim=130), INVALID), (dict(n_tokens=-1), INVALID), (dict(head_dim=0), INVALID), (dict(amplitude=float("nan")), INVALID),
     (dict(amplitude=float("inf")), INVALID), (dict(head_dim=260, rot_dim=64), UNSUPPORTED), (dict(head_dim=100, rot_dim=64), UNSUPPORTED),
-    (dict(n_tokens=1 << 27), UNSUPPORTED), (dict(q_stride=2040), INVALID), (dict(q_stride=2052), MISALIGNED),
+    (dict(n_tokens=1 << 27), UNSUPPORTED), (dict(n_heads=(1 << 19) - 1), UNSUPPORTED), (dict(q_stride=2040), INVALID),
+    (dict(q_stride=2052), MISALIGNED),
     (dict(k_out_stride=100), INVALID), (dict(k_stride=1 << 39), UNSUPPORTED)])
 def test_rotary_dims_refused(lib, bad, status):
     assert _rotary(lib, moe.gqa_rotary_dims(**{**ROT, **bad})) == status
