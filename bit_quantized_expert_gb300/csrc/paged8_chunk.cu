@@ -4,17 +4,33 @@
 // Rows, row tiles, items, the split of the work, tensor memory and the order of the products are those of the 16-bit
 // form (paged_chunk.cu).  What differs:
 //
-//   * Operands.  The tensor cores take e4m3 beside e4m3 alone, and queries and numerators need more bits than
-//     that, so codes become fp16 on their way into shared memory: four warps (12 to 15) bring them there by asynchronous
-//     copies, one tile of keys or of values ahead, convert them and store them in the operands' swizzle.
-//   * Scales.  The same warps read the tile's sixteen, four tiles ahead, and multiply a block's codes by its scale over a
-//     reference: for keys the tile's largest scale, for values the largest that the segment has met.  These are
-//     powers of two, so that nothing is rounded but what is 2^-15 of the reference's scale and less, and then by 2^-25 of it
-//     at most.  The softmax then sees one factor a tile, and O is in units of the values' reference.  (Each block's
-//     factors in the softmax, which has no time to spare, kept such blocks exact too: 521 us in place of 466.)
+//   * Operands.  The tensor cores take e4m3 beside e4m3 alone, and queries and numerators need more bits than that, so codes
+//     become fp16 on their way into shared memory: four warps (12 to 15) bring them there by asynchronous copies, a tile of
+//     keys or of values ahead, convert them and store them in the operands' swizzle.
+//   * Scales and pages.  One warp (11) reads them, up to four tiles ahead, and leaves in a ring what the others need of a tile:
+//     where its blocks are, and each block's scale over a reference, by which its codes are multiplied as they are
+//     converted.  The reference is for keys the tile's largest scale, for values the largest that the segment has met.  Both
+//     are powers of two, so nothing is rounded but what is 2^-15 of the reference and less, and then by 2^-25 of it at
+//     most.  The softmax sees one factor a tile, and O is in units of the values' reference.
 //   * Queries.  bf16 ones are scaled by a power of two a row so that fp16 holds them: by the softmax threads, a row each, in
 //     shared memory before the item's first product.
-//   * NaN codes of masked tiles' values are taken out before they are converted.
+//   * Values of masked tiles.  NaN ones are taken out of the operand once it is there, by warps 8 and 10, so that 0 * NaN does
+//     not reach rows that do not see them; rows that do get their NaN back at the end.
+//   * Registers.  184 a thread for the softmax, 64 for the issuing warpgroup, 80 for the converting one.
+//
+// What bounds it: the chain of a row tile, softmax, P V, next scores, as in the 16-bit form, whose softmax here shares its
+// issue slots with the conversion (58 % of them are taken, the tensor pipe is active 58 % of the time, 75 % in the 16-bit
+// form).  Measured in a graph: 2048 tokens at 32768 positions (16 / 2 heads of 128, bf16) 381 us, 1.49 PFLOP/s, 78 % of the
+// dense rate (the 16-bit form of the same shape: 331); heads of 64 308; 34 sequences of single tokens and chunks (fp16)
+// 78.9; 16 prompts 21.4; 4096 tokens with a window of 1024 69.3; 512 tokens of one prompt 19.1.
+//
+// Steps at 2048 tokens: 522 with NaN codes taken out in the conversion itself; 505 with them in other warps; 466 with
+// codes multiplied by their scales as they are converted, not scores and numerators in the softmax (which has no time to
+// spare); 434 with one factor a tile; 404 with short waits; 391 with the scales in a warp of their own; 381 with the
+// pages there as well.  Not kept: codes brought by tensor map (1030 us by one warp, 620 by the converting ones), or
+// through registers (spills); unrolled conversion (25 % more: its instructions displace the softmax's); NaN codes looked for
+// in global memory ahead of the conversion (16 prompts 22.4: four loads' latency a tile, where every tile is masked); a
+// barrier of its own for a tile's places, so that its copies do not wait for its scales (16 prompts 21.0, 2048 tokens 389).
 #include <cmath>
 #include <cstring>
 
@@ -69,10 +85,15 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// A tile's scales: the factors of its blocks as pairs of fp16 values, and the references that they are over.
-struct TileScales {
+// What is known of a tile before its codes: the factors of its blocks as pairs of fp16 values, where the blocks start in the
+// caches (-1: taken as zeros), the references that the factors are over, and whether it is its segment's last tile, or
+// none (behind the share's last one).
+constexpr uint32_t kLastTile = 1u, kNoTile = 2u;
+struct __align__(16) TileInfo {
   uint32_t k_by[8], v_by[8];
-  float k_ref, v_ref, pad[2];
+  long long at[8];
+  float k_ref, v_ref;
+  uint32_t last, pad;
 };
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -158,7 +179,7 @@ struct FarRow {
 };
 template <int D>
 __device__ __noinline__ FarRow far_tiles8(const Paged8Args& a, Item x, int i0, int i, int n, int p, uint32_t tS, uint32_t tO,
-                                          uint32_t sfull, uint32_t pfull, const TileScales* scales, float q_scale,
+                                          uint32_t sfull, uint32_t pfull, const TileInfo* infos, float q_scale,
                                           FarRow row) {
   float m = row.m, l = row.l, v_ref = row.v_ref;
   int done = row.done, tiles = row.tiles;
@@ -171,7 +192,7 @@ __device__ __noinline__ FarRow far_tiles8(const Paged8Args& a, Item x, int i0, i
       tc_fence_after();
       if (!tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) mask_scores(a, tS, p, j0);
     }
-    const volatile TileScales* ts = scales + ((tiles - 1) & (kInfos - 1));
+    const volatile TileInfo* ts = infos + ((tiles - 1) & (kInfos - 1));
     const float k = ts->k_ref * q_scale, v_new = ts->v_ref;
     float mx = -INFINITY, by = 1.f, sum = 0.f;
     __syncwarp();
@@ -227,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // barriers: stages (full, empty), q empty, per row tile q full, q converted, S full, P full (its first and its second
   // half), O full, O empty; scales (full, empty, a slot each); values clean (a stage each)
   __shared__ __align__(8) uint64_t bars[2 * C::kStages + 1 + 14 + 2 * kInfos + C::kStages];
-  __shared__ __align__(16) TileScales scales_s[kInfos];
+  __shared__ __align__(16) TileInfo infos_s[kInfos];
   __shared__ uint32_t warp_s[kThreads / 32];
   __shared__ Share share_s;
   __shared__ uint32_t tmem_slot;
@@ -490,18 +511,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- scales of blocks, four tiles at a time, read two tiles ahead.  A block that no row needs, or whose
       // page is bad, has the least scale.
       uint32_t tiles = 0;
+      bool ended = true;
       bad = false;
+      // The slot was last used eight tiles ago.  Once the values of four tiles ago have been converted, the products of six
+      // tiles ago are done, and with them the softmax of those before, which had its references from there.
+      auto next_info = [&]() -> TileInfo* {
+        if (tiles >= 4 && !wait_warp(INFOEMPTY((tiles - 4) & (kInfos - 1)), ((tiles - 4) / kInfos) & 1)) {
+          ended = false;
+          return nullptr;
+        }
+        return infos_s + (tiles & (kInfos - 1));
+      };
       walk([&](int b, const SeqRows&, int g, const Item& x, int i0, int n, uint32_t) {
         const int32_t* row = a.table + (size_t)b * a.max_pages;
         const int my_off = ((lane & 7) * 16) & ((1 << a.page_shift) - 1);   // of the block in its page
         bool need;
         int pg_ahead = read_page(row, x, i0, n, 0, &need);
         float ks_ahead = kLeastScale, vs_ahead = kLeastScale, k_ref = 1.f, v_ref = kLeastScale, v_last = kLeastScale;
+        long long from_ahead = -1, from = -1;
         uint32_t k_by = 0u, v_by = 0u;
         auto read_scales = [&]() {
           const int page = page_or_none(pg_ahead, need), index = scale_index(max(page, 0), a.Hkv, g, a.page_shift, my_off);
           ks_ahead = vs_ahead = kLeastScale;
+          from_ahead = -1;
           if (page >= 0) {
+            from_ahead = page * a.page_stride + g * a.head_stride + my_off * a.row_stride;
             ks_ahead = a.ks[index];
             vs_ahead = a.vs[index];
           }
@@ -527,20 +561,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               v_last = fmaxf(v_last, y);
               if (t <= lane >> 3) v_ref = fmaxf(v_ref, y);
             }
+            from = from_ahead;
             k_by = factor(ks / k_ref);
             v_by = factor(vs / v_ref);
             pg_ahead = read_page(row, x, i0, n, i + 4, &need);
           }
           if ((i & 3) == 2) read_scales();
-          // The slot was last used eight tiles ago.  Once the values of four tiles ago have been converted, the products of six
-          // tiles ago are done, and with them the softmax of those before, which had its references from there.
-          if (tiles >= 4 && !wait_warp(INFOEMPTY((tiles - 4) & (kInfos - 1)), ((tiles - 4) / kInfos) & 1))
-            return false;
-          TileScales* to = scales_s + (tiles & (kInfos - 1));
+          TileInfo* to = next_info();
+          if (to == nullptr) return false;
           if (lane >> 3 == (i & 3)) {
             to->k_by[lane & 7] = k_by;
             to->v_by[lane & 7] = v_by;
+            to->at[lane & 7] = from;
             if ((lane & 7) == 0) {
+              to->last = i + 1 == n ? kLastTile : 0u;
               to->k_ref = k_ref;
               to->v_ref = v_ref;
             }
@@ -551,6 +585,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       });
+      if (ended) {
+        TileInfo* to = next_info();
+        if (to != nullptr) {
+          if (lane < 8) to->at[lane] = -1;
+          if (lane == 0) to->last = kNoTile;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(INFO(tiles & (kInfos - 1)));
+        } else {
+          abort_s = 1;
+        }
+      }
       if (bad) raise_flag(a.err, kErrBadPages);
     }
   } else if (warp >= kFirstConvert) {
@@ -565,72 +610,75 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3, rr = D == 128 ? (lane >> 2) & 3 : lane >> 2;
     const uint32_t mine = sRaw + w * 32 * D + lane * 16;
     const uint32_t line = (q >> 2) * C::kBoxBytes + (w * 32 + rr) * 128 + ((((2 * q) & 7) ^ rr) << 4);
-    const long long step = kRows * a.row_stride;
-    const uint32_t infos = smem_u32(&scales_s[0].k_by[w * 2]);
-    uint32_t at = 0, tiles = 0;
-    int seg = 0;
-    bad = false;
-    walk([&](int b, const SeqRows&, int g, const Item& x, int i0, int n, uint32_t) {
-      const int32_t* row = a.table + (size_t)b * a.max_pages;
-      // Page numbers of the blocks of four tiles, one a lane, read four tiles ahead (-1: taken as zeros).
-      bool need;
-      int pg_ahead = read_page(row, x, i0, n, 0, &need), pg = -1;
-      auto next_four = [&](int i) {
-        pg = page_or_none(pg_ahead, need);
-        pg_ahead = read_page(row, x, i0, n, i + 4, &need);
-      };
-      next_four(0);
-      const long long lane_off = g * a.head_stride + rr * a.row_stride + q * 16;
-      // Block blk of tile i of a cache on its way to its place, which this lane has read: one group of copies.
-      auto fetch = [&](const uint8_t* cache, int i, int blk) {
-        const int page = __shfl_sync(0xFFFFFFFFu, pg, (i & 3) * 8 + w * 2 + blk);
-        const bool go = i < n && page >= 0;
-        cp_async_pieces<kPerBlock>(
-            mine + blk * kPerBlock * 512,
-            go ? cache + page * a.page_stride + ((w * 32 + blk * 16) & ((1 << a.page_shift) - 1)) * a.row_stride + lane_off : cache,
-            go ? step : 0, go ? 16 : 0);
-        cp_async_commit();
-      };
+    const long long step = kRows * a.row_stride, lane_off = rr * a.row_stride + q * 16;
+    const uint32_t infos = smem_u32(infos_s);
+    long long from0 = -1, from1 = -1;   // this warp's two blocks of the tile whose copies go out
+    uint32_t last = kNoTile;            // of the tile that is converted
+    auto read_info = [&](uint32_t tile) {
+      const uint32_t info = infos + (tile & (kInfos - 1)) * (uint32_t)sizeof(TileInfo);
+      uint32_t word;
+      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(from0), "=l"(from1) : "r"(info + 64 + w * 16) : "memory");
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(word) : "r"(info + 136) : "memory");
+      return word;
+    };
+    // A block of a cache on its way to its place, which this lane has read: one group of copies.
+    auto fetch = [&](const uint8_t* cache, long long from, int blk) {
+      const bool go = from >= 0;
+      cp_async_pieces<kPerBlock>(mine + blk * kPerBlock * 512, go ? cache + from + lane_off : cache, go ? step : 0, go ? 16 : 0);
+      cp_async_commit();
+    };
+    // Keys and values of one tile after another, whatever segment it is of.  A stage has the values of a tile and the
+    // keys of the next one, or only one of them at a segment's ends.  By the same instructions, a block a turn (what is
+    // unrolled is fetched anew each time, beside the softmax's instructions, and that takes longer than it does); behind
+    // keys come the values of their tile, behind values the keys of the next.
+    uint32_t at = 0, tile = 0, kv = 0;
+    bool fresh = true, ok = wait_warp(INFO(0), 0);
+    if (ok) last = read_info(0);
 #pragma unroll 1
-      for (int blk = 0; blk < 2; ++blk) fetch(a.kc8, 0, blk);
-      for (int i = 0; i <= n; ++i, ++at) {
-        const uint32_t st = at & 1;
-        if (i < n && !wait_warp(INFO(tiles & (kInfos - 1)), (tiles / kInfos) & 1)) return false;
-        if (at >= C::kStages && !wait_warp(EMPTY(st), (at / C::kStages - 1) & 1)) return false;
-        if (i > 0 && (i & 3) == 0) next_four(i);
-        // The values of tile i - 1, then the keys of tile i, by the same instructions (what is unrolled is fetched anew
-        // each time, beside the softmax's instructions, and that takes longer than it does), a block a turn; behind
-        // them come the keys of tile i and its values.
-#pragma unroll 1
-        for (int kv = i > 0 ? 1 : 0; kv >= (i < n ? 0 : 1); --kv) {
-          uint32_t to = sKV + st * C::kStageBytes + kv * C::kTileBytes + line, in = mine;
-          uint32_t by0, by1;
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                       : "=r"(by0), "=r"(by1)
-                       : "r"(infos + ((tiles - kv) & (kInfos - 1)) * (uint32_t)sizeof(TileScales) + kv * 32)
-                       : "memory");
-#pragma unroll 1
-          for (int blk = 0; blk < 2; ++blk) {
-            cp_async_wait<1>();   // the older of two blocks
-            convert_block<D>(in, to, blk == 0 ? by0 : by1);
-            fetch(kv ? a.kc8 : a.vc8, i, blk);
-            to += 16 * 128;
-            in += kPerBlock * 512;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(FULL(st));
-          if (i > 0) mbar_arrive(INFOEMPTY((tiles - 1) & (kInfos - 1)));
-        }
-        tiles += i < n;
-        __syncwarp();
+    for (int blk = 0; blk < 2; ++blk) fetch(a.kc8, blk == 0 ? from0 : from1, blk);
+    while (last != kNoTile) {
+      const uint32_t st = at & 1;
+      if (fresh && at >= C::kStages && !wait_warp(EMPTY(st), (at / C::kStages - 1) & 1)) {
+        ok = false;
+        break;
       }
-      ++seg;
-      return true;
-    });
-    if (bad) raise_flag(a.err, kErrBadPages);
+      uint32_t to = sKV + st * C::kStageBytes + kv * C::kTileBytes + line, in = mine;
+      uint32_t by0, by1, next = last;
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                   : "=r"(by0), "=r"(by1)
+                   : "r"(infos + (tile & (kInfos - 1)) * (uint32_t)sizeof(TileInfo) + kv * 32 + w * 8)
+                   : "memory");
+      if (kv != 0) {
+        if (!wait_warp(INFO((tile + 1) & (kInfos - 1)), ((tile + 1) / kInfos) & 1)) {
+          ok = false;
+          break;
+        }
+        next = read_info(tile + 1);
+      }
+#pragma unroll 1
+      for (int blk = 0; blk < 2; ++blk) {
+        cp_async_wait<1>();   // the older of two blocks
+        convert_block<D>(in, to, blk == 0 ? by0 : by1);
+        fetch(kv != 0 ? a.kc8 : a.vc8, blk == 0 ? from0 : from1, blk);
+        to += 16 * 128;
+        in += kPerBlock * 512;
+      }
+      fresh = kv == 0 || last != 0u;
+      if (fresh) {
+        fence_proxy_async_smem();
+        ++at;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (fresh) mbar_arrive(FULL(st));
+        if (kv != 0) mbar_arrive(INFOEMPTY(tile & (kInfos - 1)));
+      }
+      __syncwarp();
+      tile += kv;
+      last = next;
+      kv ^= 1u;
+    }
+    if (!ok) abort_s = 1;
   } else {
     // ---- softmax: row `r` of row tile `t`
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -683,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_warp(SFULL(t), done & 1)) return false;
         ++done;
         tc_fence_after();
-        const volatile TileScales* ts = scales_s + (tiles & (kInfos - 1));
+        const volatile TileInfo* ts = infos_s + (tiles & (kInfos - 1));
         ++tiles;
         if (!open) mask_scores(a, tS, p, j0);
         uint32_t sr[128];
@@ -702,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool move = mx > m && (m == -INFINITY || mx - m > kLazy);
         if (__any_sync(0xFFFFFFFFu, move || v_new != v_ref)) {
           if (__any_sync(0xFFFFFFFFu, move && p >= 0 && fabsf(mx) > kFar)) {   // the tiles from here on in another way
-            const FarRow row = far_tiles8<D>(a, x, i0, i, n, p, tS, tO, SFULL(t), PFULL(t, 0), scales_s, q_scale,
+            const FarRow row = far_tiles8<D>(a, x, i0, i, n, p, tS, tO, SFULL(t), PFULL(t, 0), infos_s, q_scale,
                                              FarRow{m, l, v_ref, done, tiles});
             if (row.done < 0) return false;
             m = row.m;
