@@ -1,5 +1,6 @@
-"""Build the sm_103a library (MoE layer, decode attention, paged attention, DeltaNet scan) in-tree: one nvcc process per translation unit (in parallel),
-then one link step.  Output: bit_quantized_expert_gb300/libmoe_gb300.so.
+"""Build the sm_103a library (MoE layer, decode attention, paged attention in 16 and 8 bits, rotary positions, DeltaNet
+scan) in-tree: one nvcc process per translation unit (in parallel), then one link step.  Output:
+bit_quantized_expert_gb300/libmoe_gb300.so.
 
     python -m bit_quantized_expert_gb300.build [--force]
 """

@@ -7,6 +7,11 @@
 //                   have a block in common, so a scale and the codes under it change together.
 //   read8_kernel    the same walk, codes times scale into 16-bit rows.
 // Every CTA scans the sequences' block counts for itself, so that a warp finds its block by a search in shared memory.
+//
+// Measured in a graph (2 heads of 128).  Append: 64 single tokens 3.8 us, the latency of a launch and four dependent
+// loads (schedule, page, scale and rows, old codes where the scale grows); 8 prompts (14.6 MB) 8.0 us.
+// Read: 300 positions 2.4 us; 8 sequences of up to 32768 (37.8 MB) 9.1 us, 4.2 TB/s, 62 % of the copy rate.
+// Steps: 8 prompts 10.2 -> 8.0 with held codes read only where the scale grows.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
