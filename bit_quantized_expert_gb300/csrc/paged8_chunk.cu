@@ -19,7 +19,7 @@
 //   * Registers.  184 a thread for the softmax, 64 for the issuing warpgroup, 80 for the converting one.
 //
 // What bounds it: the chain of a row tile, softmax, P V, next scores, as in the 16-bit form, whose softmax here shares its
-// issue slots with the conversion (58 % of them are taken, the tensor pipe is active 58 % of the time, 75 % in the 16-bit
+// issue slots with the conversion (58 % of them are taken, the tensor pipe is active 64 % of the time, 75 % in the 16-bit
 // form).  Measured in a graph: 2048 tokens at 32768 positions (16 / 2 heads of 128, bf16) 381 us, 1.49 PFLOP/s, 78 % of the
 // dense rate (the 16-bit form of the same shape: 331); heads of 64 308; 34 sequences of single tokens and chunks (fp16)
 // 78.9; 16 prompts 21.4; 4096 tokens with a window of 1024 69.3; 512 tokens of one prompt 19.1.
