@@ -15,15 +15,20 @@
 //     value scale multiplies its numerators, relative to the largest that the warp has met (O is kept in units
 //     of that), so that all of fp16's range serves the numerators, rounded ones in rows 0..7 and their remainders
 //     in rows 8..15 of the operand.
+//   * the warps' results of a segment lie in one of two buffers; a warp joins them only when its tiles of the next segment
+//     are done, so that none waits for a slower one before the share's end.
 //
-// Measured in a graph, 16 / 2 heads of 128: one sequence of 32768 positions (fp16) 12.6 us, of which 2.5 are its bytes and the
-// rest is a chain: the schedule 1.4, the first tile's way 0.9, tiles 2.4, the join within a CTA 1.5, the second launch and
-// its join 4 to 4.5; 64 ragged ones (up to 32768, 69.6 MB) 21.9 us, 3.2 TB/s, 47 % of the copy rate; 32 of them with a window of
-// 4096 13.9; 64 ragged ones with heads of 64 18.3.  While tiles run, issue slots bound it: 42 % of them are taken over a whole
-// ragged call, and a warp waits for its products, conversions and shared loads in turn.
-// Steps: 32768 positions 13.8 -> 13.0 and 64 ragged ones 22.5 -> 21.7 with four independent products side by side (one waits ~30
-// cycles for the one before); 32768 positions 13.0 -> 12.6 with the schedule of up to 32 sequences without barriers and
-// joins of many parts in fewer round trips.  kItemUnits of 3, 5, 6 and 8 at 64 ragged ones: 23.5, 22.2, 22.5, 23.0 (4: 22.0).
+// Measured in a graph, 16 / 2 heads of 128: one sequence of 32768 positions (fp16) 12.2 us, of which 2.5 are its bytes and the
+// rest is a chain: the dependency wait 0.7, the schedule 1.4, the first tile's way 0.9, tiles 2.4, the join within a CTA 1.2,
+// the second launch and its join 4; 64 ragged ones (up to 32768, 69.6 MB) 21.7 us, 3.2 TB/s, 47 % of the copy rate (20.9 in
+// pages of 64); 32 of them with a window of 4096 13.2; 64 ragged ones with heads of 64 18.4 (16.6 in pages of 64).  While
+// tiles run, a warp's own chain bounds it (conversion, product, maximum, exponential, product): two warps a scheduler
+// fill 41 % of the issue slots.  Twelve consumer warps of 152 registers, three a scheduler, were slower (26.7), and so were
+// rings of 96 or 160 KB with one joining buffer (23.3).
+// Steps: 32768 positions 13.8 -> 13.0 and 64 ragged ones 22.5 -> 21.7 with four independent products side by side (one
+// waits ~30 cycles for the one before); 32768 positions 13.0 -> 12.5 with the schedule of up to 32 sequences without
+// barriers and joins of many parts in fewer round trips; windows 13.9 -> 13.2, 64 ragged in pages of 64 22.1 -> 20.9
+// without a barrier at a segment's end.  kItemUnits of 2, 3, 4, 5 at the latter: 25.1, 22.2, 20.9, 21.1.
 #include <cmath>
 #include <cstring>
 
@@ -71,17 +76,23 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
+
+// A segment whose warps' results lie in a joining buffer.
+struct Told {
+  int g, i0, n, count, p0, row0;
+  uint32_t first, end;
+};
 
 template <int D, bool FP16>
 __global__ void __launch_bounds__(kThreads, 1)
     decode8_kernel(const __grid_constant__ PagedMaps maps, const Paged8Args a, const DecodeSplit split) {
   using C = Dec8<D>;
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages];
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], told[2], joined[2];
   __shared__ __align__(16) float scale_s[C::kStages][8];      // of the stage's blocks: keys, values
   __shared__ __align__(16) float ml_s[2][kRows][2][kWarps];   // per buffer and row: the warps' max, then sum
   __shared__ uint32_t warp_s[kThreads / 32];
+  __shared__ Told told_s[2];
   __shared__ int abort_s;
   const uint32_t raw = smem_u32(sm_raw), base = (raw + 1023u) & ~1023u;
   float* join_s = reinterpret_cast<float*>(sm_raw + (base - raw) + C::kStages * C::kStageBytes);
@@ -93,6 +104,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&full[s]), kCopyWarps + 1);
       mbar_init(smem_u32(&empty[s]), kWarps / kGroups);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&told[i]), kWarps);
+      mbar_init(smem_u32(&joined[i]), kWarps);
     }
     abort_s = 0;
     mbar_fence_init();
@@ -331,7 +346,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  int it = 0, buf = 0;   // tiles of the share so far, joining buffer
+  // Joins the eight warps' results of the s-th segment in order.  Every warp comes here only when its tiles of the next
+  // segment are done, so that none waits for a slower one but behind the share's last segment.
+  auto join = [&](int s) {
+    const int buf = s & 1;
+    mbar_wait_warp(smem_u32(&told[buf]), (s >> 1) & 1, &abort_s, a.err);
+    const Told now = told_s[buf];
+    const bool whole = now.i0 == 0 && now.n == now.count;
+    float* part = split.part + ((size_t)cta * 2 + (now.i0 == 0 ? 1 : 0)) * C::kPartFloats;
+    for (int e = tid; e < a.G * (D / 4); e += kWarps * 32) {
+      const int row = e / (D / 4), dim = (e % (D / 4)) * 4;
+      float mw[kWarps], lw[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; w += 4) {
+        const float4 m4 = *reinterpret_cast<const float4*>(&ml_s[buf][row][0][w]);
+        const float4 l4 = *reinterpret_cast<const float4*>(&ml_s[buf][row][1][w]);
+        mw[w] = m4.x, mw[w + 1] = m4.y, mw[w + 2] = m4.z, mw[w + 3] = m4.w;
+        lw[w] = l4.x, lw[w + 1] = l4.y, lw[w + 2] = l4.z, lw[w + 3] = l4.w;
+      }
+      float M = mw[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, mw[w]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v =
+            *reinterpret_cast<const float4*>(join_s + buf * C::kJoinFloats + (w * kRows + row) * C::kOStride + dim);
+        const float sw = ex2(mw[w] - M);
+        acc.x += v.x * sw;
+        acc.y += v.y * sw;
+        acc.z += v.z * sw;
+        acc.w += v.w * sw;
+        L += lw[w] * sw;
+      }
+      if (whole) {
+        const float inv = now.p0 < 0 ? 0.f : 1.f / L;
+        const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        const uint2 w = make_uint2(pack16<FP16>(v.x, v.y), pack16<FP16>(v.z, v.w));
+        const float2 w0 = unpack16<FP16>(w.x), w1 = unpack16<FP16>(w.y);
+        if (!isfinite(w0.x) || !isfinite(w0.y) || !isfinite(w1.x) || !isfinite(w1.y)) raise_flag(a.err, kErrNonFinite);
+        *reinterpret_cast<uint2*>(a.o + now.row0 * a.o_stride + (long long)(now.g * a.G + row) * D + dim) = w;
+      } else {
+        *reinterpret_cast<float4*>(part + row * D + dim) = acc;
+        if (dim == 0) {
+          part[kRows * D + row] = M;
+          part[kRows * D + kRows + row] = L;
+        }
+      }
+    }
+    if (now.i0 == 0 && !whole && tid == 0) {
+      // the last CTA with a part: the one whose share holds the item's last unit
+      int c2 = share_of(now.end - 1, total, ctas);
+      while (c2 > cta + 1 && snap(share_start(total, c2, ctas), now.first, now.end, kItemUnits, kSlack) >= now.end) --c2;
+      split.rec[cta] = SplitRecord{now.row0, now.g, 1, now.p0, c2, cta};
+    }
+    __syncwarp();   // lanes part above; the next tiles' products are collective
+    if (lane == 0) mbar_arrive(smem_u32(&joined[buf]));
+    __syncwarp();
+  };
+
+  int it = 0, segs = 0;   // tiles and segments of the share so far
   Segment x = next_segment();
   load_queries(x);
   while (x.n > 0) {
@@ -443,7 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     it += x.n;
 
-    // ---- join the eight warps in order; the next segment's queries are on their way meanwhile
+    // ---- this warp's result, for the join (the buffer has been read, two segments ago); the next segment's queries are on
+    // their way meanwhile
+    const int buf = segs & 1;
+    if (segs >= 2) mbar_wait_warp(smem_u32(&joined[buf]), ((segs >> 1) - 1) & 1, &abort_s, a.err);
     l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 1);
     l_run += __shfl_xor_sync(0xFFFFFFFFu, l_run, 2);
     if (c == 0) {
@@ -457,63 +535,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       *reinterpret_cast<float4*>(ow + 16 * j) =
           make_float4((o[2 * j][0] + o[2 * j][2]) * unit, (o[2 * j + 1][0] + o[2 * j + 1][2]) * unit,
                       (o[2 * j][1] + o[2 * j][3]) * unit, (o[2 * j + 1][1] + o[2 * j + 1][3]) * unit);
-    const Segment now = x;
+    if (tid == 0) told_s[buf] = Told{x.g, x.i0, x.n, x.r.count, x.p0, x.row0, x.first, x.end};
     x = next_segment();
     load_queries(x);
     __syncwarp();
-    consumers_sync();
-    const bool whole = now.i0 == 0 && now.n == now.r.count;
-    float* part = split.part + ((size_t)cta * 2 + (now.i0 == 0 ? 1 : 0)) * C::kPartFloats;
-    for (int e = tid; e < a.G * (D / 4); e += kWarps * 32) {
-      const int row = e / (D / 4), dim = (e % (D / 4)) * 4;
-      float mw[kWarps], lw[kWarps];
-#pragma unroll
-      for (int w = 0; w < kWarps; w += 4) {
-        const float4 m4 = *reinterpret_cast<const float4*>(&ml_s[buf][row][0][w]);
-        const float4 l4 = *reinterpret_cast<const float4*>(&ml_s[buf][row][1][w]);
-        mw[w] = m4.x, mw[w + 1] = m4.y, mw[w + 2] = m4.z, mw[w + 3] = m4.w;
-        lw[w] = l4.x, lw[w + 1] = l4.y, lw[w + 2] = l4.z, lw[w + 3] = l4.w;
-      }
-      float M = mw[0];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, mw[w]);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float L = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 v =
-            *reinterpret_cast<const float4*>(join_s + buf * C::kJoinFloats + (w * kRows + row) * C::kOStride + dim);
-        const float sw = ex2(mw[w] - M);
-        acc.x += v.x * sw;
-        acc.y += v.y * sw;
-        acc.z += v.z * sw;
-        acc.w += v.w * sw;
-        L += lw[w] * sw;
-      }
-      if (whole) {
-        const float inv = now.p0 < 0 ? 0.f : 1.f / L;
-        const float4 v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        const uint2 w = make_uint2(pack16<FP16>(v.x, v.y), pack16<FP16>(v.z, v.w));
-        const float2 w0 = unpack16<FP16>(w.x), w1 = unpack16<FP16>(w.y);
-        if (!isfinite(w0.x) || !isfinite(w0.y) || !isfinite(w1.x) || !isfinite(w1.y)) raise_flag(a.err, kErrNonFinite);
-        *reinterpret_cast<uint2*>(a.o + now.row0 * a.o_stride + (long long)(now.g * a.G + row) * D + dim) = w;
-      } else {
-        *reinterpret_cast<float4*>(part + row * D + dim) = acc;
-        if (dim == 0) {
-          part[kRows * D + row] = M;
-          part[kRows * D + kRows + row] = L;
-        }
-      }
-    }
-    if (now.i0 == 0 && !whole && tid == 0) {
-      // the last CTA with a part: the one whose share holds the item's last unit
-      int c2 = share_of(now.end - 1, total, ctas);
-      while (c2 > cta + 1 && snap(share_start(total, c2, ctas), now.first, now.end, kItemUnits, kSlack) >= now.end) --c2;
-      split.rec[cta] = SplitRecord{now.row0, now.g, 1, now.p0, c2, cta};
-    }
-    __syncwarp();   // lanes part above; the next tiles' products are collective
-    buf ^= 1;
+    if (lane == 0) mbar_arrive(smem_u32(&told[buf]));
+    __syncwarp();
+    if (segs > 0) join(segs - 1);
+    ++segs;
   }
+  if (segs > 0) join(segs - 1);
 }
 
 template <int D, bool FP16>
