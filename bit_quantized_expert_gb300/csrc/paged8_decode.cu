@@ -23,7 +23,7 @@
 // the second launch and its join 4; 64 ragged ones (up to 32768, 69.6 MB) 21.7 us, 3.2 TB/s, 47 % of the copy rate (20.9 in
 // pages of 64); 32 of them with a window of 4096 13.2; 64 ragged ones with heads of 64 18.4 (16.6 in pages of 64).  While
 // tiles run, a warp's own chain bounds it (conversion, product, maximum, exponential, product): two warps a scheduler
-// fill 41 % of the issue slots.  Twelve consumer warps of 152 registers, three a scheduler, were slower (26.7), and so were
+// fill 43 % of the issue slots.  Twelve consumer warps of 152 registers, three a scheduler, were slower (26.7), and so were
 // rings of 96 or 160 KB with one joining buffer (23.3).
 // Steps: 32768 positions 13.8 -> 13.0 and 64 ragged ones 22.5 -> 21.7 with four independent products side by side (one
 // waits ~30 cycles for the one before); 32768 positions 13.0 -> 12.5 with the schedule of up to 32 sequences without
