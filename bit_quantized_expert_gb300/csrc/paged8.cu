@@ -8,10 +8,11 @@
 //   read8_kernel    the same walk, codes times scale into 16-bit rows.
 // Every CTA scans the sequences' block counts for itself, so that a warp finds its block by a search in shared memory.
 //
-// Measured in a graph (2 heads of 128).  Append: 64 single tokens 3.8 us, the latency of a launch and four dependent
-// loads (schedule, page, scale and rows, old codes where the scale grows); 8 prompts (14.6 MB) 8.0 us.
-// Read: 300 positions 2.4 us; 8 sequences of up to 32768 (37.8 MB) 9.1 us, 4.2 TB/s, 62 % of the copy rate.
-// Steps: 8 prompts 10.2 -> 8.0 with held codes read only where the scale grows.
+// Measured in a graph (2 heads of 128).  Append: 64 single tokens 3.4 us, the latency of a launch and four dependent
+// loads (schedule, page beside the rows, scale, old codes where the scale grows); 8 prompts (17.6 MB) 7.3 us.
+// Read: 300 positions 2.4 us; 8 sequences of up to 32768 (37.8 MB) 9.0 us, 4.2 TB/s, 62 % of the copy rate.
+// Steps at 8 prompts: 10.2; 8.0 with held codes read only where the scale grows; 7.7 with the rows on their way before the
+// page is known; 7.3 with CTAs of 128 threads.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -21,8 +22,13 @@
 namespace moe {
 namespace {
 
-constexpr int kWalkThreads = 256;
-constexpr int kWalkCtasPerSm = 4;
+// Threads of a CTA.  Few sequences: 128, as many CTAs as an SM holds (append of 64 tokens 3.4 us, 8 prompts 7.3; with 256 threads
+// 3.6 and 7.7).  Every CTA scans the sequences, so for many of them there are few and wide ones, in one wave (append of 1024
+// tokens of as many 7.8 us, of 4096 26.7; with 256 threads and four CTAs an SM 9.1 and 67; at 200 sequences narrow ones
+// still win, 3.9 against 4.5, at 400 wide ones, 4.7 against 5.9).
+constexpr int kNarrow = 128, kWide = 512;
+constexpr int kManySeqs = 256;
+constexpr int kNarrowThreads = 1024;   // of an SM, keys and values each, at most
 
 // Arguments of the append and of the read: `k`, `v` are rows of 16-bit values.
 struct WalkArgs : PagedArgs {
@@ -42,21 +48,21 @@ __device__ __forceinline__ Blocks blocks_of(const SeqRows& s, bool from_zero) {
   return Blocks{first, ((s.p0 + s.n - 1) >> kBlock8Shift) - first + 1};
 }
 
-// One block of one head: sequence, page (-1: none) and offsets o0 .. o1 - 1 that rows row0 .. have.
+// One block of one head: page number as the table has it, and offsets o0 .. o1 - 1 that rows row0 .. have.
 struct Unit {
   int g, page, off, row0, o0, o1;
 };
 
-// body(unit) for every block, a warp each; blockIdx.y: keys or values.
-template <bool FROM_ZERO, class Body>
+// body(unit, page) for every block, a warp each; page() gives the page's number, -1 for none; blockIdx.y: keys or values.
+template <int NT, bool FROM_ZERO, class Body>
 __device__ __forceinline__ void walk_blocks(const WalkArgs& a, uint32_t* pre_s, uint32_t* warp_s, Body&& body) {
   bool bad = false, over;
-  const uint32_t total = scan_sequences8<kWalkThreads>(a.B, pre_s, warp_s, &over, [&](int b) {
+  const uint32_t total = scan_sequences8<NT>(a.B, pre_s, warp_s, &over, [&](int b) {
     return (unsigned long long)blocks_of(load_seq(a, b, bad), FROM_ZERO).n * a.Hkv;
   });
   if (over) bad = true;   // (cannot be: T * Hq and B * Hkv are below 2^31)
-  const uint32_t warps = gridDim.x * (kWalkThreads / 32);
-  for (uint32_t u = blockIdx.x * (kWalkThreads / 32) + (threadIdx.x >> 5); !over && u < total; u += warps) {
+  const uint32_t warps = gridDim.x * (NT / 32);
+  for (uint32_t u = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); !over && u < total; u += warps) {
     const int b = find_sequence(pre_s, a.B, u);
     const SeqRows s = load_seq(a, b, bad);
     const uint32_t at = u - pre_s[b], block = at / a.Hkv;
@@ -66,27 +72,24 @@ __device__ __forceinline__ void walk_blocks(const WalkArgs& a, uint32_t* pre_s, 
     x.o0 = max((FROM_ZERO ? max(s.p0, 0) : s.p0) - j0, 0);
     x.o1 = min(s.p0 + s.n - j0, 1 << kBlock8Shift);
     x.row0 = s.row0 + (j0 - s.p0);   // the row that offset 0 would have
-    x.page = -1;
-    if (j0 >= 0) {
-      x.page = a.table[(size_t)b * a.max_pages + (j0 >> a.page_shift)];
-      if (x.page < 0 || x.page >= a.num_pages) {
-        bad = true;
-        x.page = -1;
-      }
-    }
+    x.page = j0 >= 0 ? a.table[(size_t)b * a.max_pages + (j0 >> a.page_shift)] : -1;
     x.off = j0 & ((1 << a.page_shift) - 1);
-    body(x);
+    body(x, [&]() {   // the number is looked at here, not before: what does not depend on it goes first
+      const bool ok = x.page >= 0 && x.page < a.num_pages;
+      bad |= !ok && j0 >= 0;
+      return ok ? x.page : -1;
+    });
     __syncwarp();
   }
   if (bad) raise_flag(a.err, kErrBadPages);
 }
 
 // A lane has 8 dims (16 bytes of a row, 8 codes) of every (256 / D)-th row.
-template <int D, bool FP16>
-__global__ void __launch_bounds__(kWalkThreads, 3) append8_kernel(const WalkArgs a) {
+template <int D, bool FP16, int NT>
+__global__ void __launch_bounds__(NT, NT == kNarrow ? 5 : 1) append8_kernel(const WalkArgs a) {
   constexpr int kLanes = D / 8, kStep = 32 / kLanes, kTurns = 16 / kStep;
   extern __shared__ uint32_t pre_s[];
-  __shared__ uint32_t warp_s[kWalkThreads / 32];
+  __shared__ uint32_t warp_s[NT / 32];
   pdl_wait();
   pdl_launch_dependents();
   const bool values = blockIdx.y != 0;
@@ -95,13 +98,10 @@ __global__ void __launch_bounds__(kWalkThreads, 3) append8_kernel(const WalkArgs
   float* scales = values ? a.vs : a.ks;
   const long long stride = values ? a.v_stride : a.k_stride;
   const int lane = threadIdx.x & 31, r0 = lane / kLanes, dim = (lane % kLanes) * 8;
-  walk_blocks<true>(a, pre_s, warp_s, [&](const Unit& u) {
-    if (u.page < 0) return;
-    uint8_t* to = dst + u.page * a.page_stride + u.g * a.head_stride + (u.off + r0) * a.row_stride + dim;
-    float* scale = scales + scale_index(u.page, a.Hkv, u.g, a.page_shift, u.off);
-    // The new rows, all in flight together.  (What the block holds before them is read only where the scale grows.)
+  walk_blocks<NT, true>(a, pre_s, warp_s, [&](const Unit& u, auto&& page_of) {
+    // The new rows, all in flight together, beside the page's number.  (What the block holds before them is read only where
+    // the scale grows.)
     uint4 x[kTurns];
-    float was = u.o0 > 0 ? *scale : kLeastScale;
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
       const int o = r0 + i * kStep;
@@ -109,6 +109,11 @@ __global__ void __launch_bounds__(kWalkThreads, 3) append8_kernel(const WalkArgs
       if (o >= u.o0 && o < u.o1)
         x[i] = __ldcg(reinterpret_cast<const uint4*>(src + (long long)(u.row0 + o) * stride + u.g * D + dim));
     }
+    const int page = page_of();
+    if (page < 0) return;
+    uint8_t* to = dst + page * a.page_stride + u.g * a.head_stride + (u.off + r0) * a.row_stride + dim;
+    float* scale = scales + scale_index(page, a.Hkv, u.g, a.page_shift, u.off);
+    float was = u.o0 > 0 ? *scale : kLeastScale;
     if (!scale_ok(was)) {
       raise_flag(a.err, kErrBadPages);
       was = kLeastScale;
@@ -168,11 +173,11 @@ __global__ void __launch_bounds__(kWalkThreads, 3) append8_kernel(const WalkArgs
   });
 }
 
-template <int D, bool FP16>
-__global__ void __launch_bounds__(kWalkThreads) read8_kernel(const WalkArgs a) {
+template <int D, bool FP16, int NT>
+__global__ void __launch_bounds__(NT) read8_kernel(const WalkArgs a) {
   constexpr int kLanes = D / 8, kStep = 32 / kLanes, kTurns = 16 / kStep;
   extern __shared__ uint32_t pre_s[];
-  __shared__ uint32_t warp_s[kWalkThreads / 32];
+  __shared__ uint32_t warp_s[NT / 32];
   pdl_wait();
   pdl_launch_dependents();
   const bool values = blockIdx.y != 0;
@@ -181,19 +186,20 @@ __global__ void __launch_bounds__(kWalkThreads) read8_kernel(const WalkArgs a) {
   const float* scales = values ? a.vs : a.ks;
   const long long stride = values ? a.v_stride : a.k_stride;
   const int lane = threadIdx.x & 31, r0 = lane / kLanes, dim = (lane % kLanes) * 8;
-  walk_blocks<false>(a, pre_s, warp_s, [&](const Unit& u) {
+  walk_blocks<NT, false>(a, pre_s, warp_s, [&](const Unit& u, auto&& page_of) {
+    const int page = page_of();
     uint2 x[kTurns];
     float s = 0.f;
-    if (u.page >= 0) s = scales[scale_index(u.page, a.Hkv, u.g, a.page_shift, u.off)];
-    const uint8_t* from = src + u.page * a.page_stride + u.g * a.head_stride + (u.off + r0) * a.row_stride + dim;
+    if (page >= 0) s = scales[scale_index(page, a.Hkv, u.g, a.page_shift, u.off)];
+    const uint8_t* from = src + page * a.page_stride + u.g * a.head_stride + (u.off + r0) * a.row_stride + dim;
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
       const int o = r0 + i * kStep;
       x[i] = make_uint2(0, 0);
-      if (u.page >= 0 && o >= u.o0 && o < u.o1)
+      if (page >= 0 && o >= u.o0 && o < u.o1)
         x[i] = __ldcg(reinterpret_cast<const uint2*>(from + (long long)i * kStep * a.row_stride));
     }
-    if (u.page >= 0 && !scale_ok(s)) {
+    if (page >= 0 && !scale_ok(s)) {
       raise_flag(a.err, kErrBadPages);
       s = kLeastScale;
     }
@@ -237,7 +243,7 @@ void fill(Args* a, const gqa_paged_dims& d, const int32_t* block_table, const in
   a->err = static_cast<uint32_t*>(workspace);
 }
 
-template <template <int, bool> class K>
+template <template <int, bool, int> class K, int NT>
 cudaError_t launch_walk(const WalkArgs& a, int D, int sms, cudaStream_t st) {
   // At most this many blocks: a sequence's rows touch two more than a sixteenth of them, and one each.
   const long long blocks = std::min((long long)a.T, (long long)a.T / 16 + 2ll * std::min(a.B, a.T)) * a.Hkv;
@@ -245,23 +251,30 @@ cudaError_t launch_walk(const WalkArgs& a, int D, int sms, cudaStream_t st) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min((blocks + kWalkThreads / 32 - 1) / (kWalkThreads / 32), (long long)sms * kWalkCtasPerSm), 2);
-  cfg.blockDim = dim3(kWalkThreads);
+  const int most = NT == kNarrow ? sms * (kNarrowThreads / NT) : K<64, false, NT>::wide_ctas(sms);
+  cfg.gridDim = dim3((unsigned)std::min((blocks + NT / 32 - 1) / (NT / 32), (long long)most), 2);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = ((size_t)a.B + 1) * 4;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (D == 128)
-    return a.fp16 ? cudaLaunchKernelEx(&cfg, K<128, true>::fn, a) : cudaLaunchKernelEx(&cfg, K<128, false>::fn, a);
-  return a.fp16 ? cudaLaunchKernelEx(&cfg, K<64, true>::fn, a) : cudaLaunchKernelEx(&cfg, K<64, false>::fn, a);
+    return a.fp16 ? cudaLaunchKernelEx(&cfg, K<128, true, NT>::fn, a) : cudaLaunchKernelEx(&cfg, K<128, false, NT>::fn, a);
+  return a.fp16 ? cudaLaunchKernelEx(&cfg, K<64, true, NT>::fn, a) : cudaLaunchKernelEx(&cfg, K<64, false, NT>::fn, a);
 }
-template <int D, bool FP16>
+template <template <int, bool, int> class K>
+cudaError_t launch_walk(const WalkArgs& a, int D, int sms, cudaStream_t st) {
+  return a.B <= kManySeqs ? launch_walk<K, kNarrow>(a, D, sms, st) : launch_walk<K, kWide>(a, D, sms, st);
+}
+template <int D, bool FP16, int NT>
 struct Append8 {
-  static constexpr auto fn = append8_kernel<D, FP16>;
+  static constexpr auto fn = append8_kernel<D, FP16, NT>;
+  static int wide_ctas(int sms) { return sms / 2; }
 };
-template <int D, bool FP16>
+template <int D, bool FP16, int NT>
 struct Read8 {
-  static constexpr auto fn = read8_kernel<D, FP16>;
+  static constexpr auto fn = read8_kernel<D, FP16, NT>;
+  static int wide_ctas(int sms) { return sms; }
 };
 
 }  // namespace

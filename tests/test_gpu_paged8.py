@@ -304,6 +304,15 @@ def test_read_long():
     _read_ok(Batch8([(0, 9000), (10, 0), (0, 1), (77, 4000)], Hq=2, Hkv=2, seed=3))
 
 
+@pytest.mark.parametrize("n", [32, 33, 256, 257, 2000])
+def test_append_and_read_sequences(n):
+    """On either side of the counts from which on sequences are scanned, and CTAs sized, in another way; blocks for several
+    turns of every warp at the last one."""
+    seqs = [(5 * i % 67, (i % 5) * (20 if i % 97 == 0 else 1)) for i in range(n)]
+    _appended(Batch8(seqs, Hq=4, Hkv=4, D=128, page=32, seed=n))
+    _read_ok(Batch8(seqs, Hq=4, Hkv=4, D=128, page=32, seed=n))
+
+
 def test_read_ends_of_the_types():
     """All codes under the largest and the smallest scales; fp16 ends at 65504."""
     for dtype, scales in (("bf16", [2.0 ** -60, 2.0 ** 60, 2.0]), ("fp16", [2.0 ** 8, 2.0 ** -20, 2.0 ** -60, 2.0 ** 7])):
