@@ -21,13 +21,13 @@
 // What bounds it: the chain of a row tile, softmax, P V, next scores, as in the 16-bit form, whose softmax here shares its
 // issue slots with the conversion (58 % of them are taken, the tensor pipe is active 64 % of the time, 75 % in the 16-bit
 // form).  Measured in a graph: 2048 tokens at 32768 positions (16 / 2 heads of 128, bf16) 381 us, 1.49 PFLOP/s, 78 % of the
-// dense rate (the 16-bit form of the same shape: 331); heads of 64 308; 34 sequences of single tokens and chunks (fp16)
+// dense rate (the 16-bit form of the same shape: 344); heads of 64 308; 34 sequences of single tokens and chunks (fp16)
 // 78.9; 16 prompts 21.4; 4096 tokens with a window of 1024 69.3; 512 tokens of one prompt 19.1.
 //
-// Steps at 2048 tokens: 522 with NaN codes taken out in the conversion itself; 505 with them in other warps; 466 with
-// codes multiplied by their scales as they are converted, not scores and numerators in the softmax (which has no time to
-// spare); 434 with one factor a tile; 404 with short waits; 391 with the scales in a warp of their own; 381 with the
-// pages there as well.  Not kept: codes brought by tensor map (1030 us by one warp, 620 by the converting ones), or
+// Steps at 2048 tokens: 1131 us with codes through registers; 607 by asynchronous copies; 536 a block's codes at once; 505 by
+// four warps of their own; 434 with scales that are powers of two and multiply the codes as they are converted, not scores
+// and numerators in the softmax; 391 with NaN codes taken out by two other warps, scales read by a third, and short
+// waits; 381 with the pages there as well.  Not kept: codes brought by tensor map (1030 us by one warp, 620 by the converting ones), or
 // through registers (spills); unrolled conversion (25 % more: its instructions displace the softmax's); NaN codes looked for
 // in global memory ahead of the conversion (16 prompts 22.4: four loads' latency a tile, where every tile is masked); a
 // barrier of its own for a tile's places, so that its copies do not wait for its scales (16 prompts 21.0, 2048 tokens 389).
