@@ -10,8 +10,13 @@
 //   * Scales and pages.  One warp (11) reads them, up to four tiles ahead, and leaves in a ring what the others need of a tile:
 //     where its blocks are, and each block's scale over a reference, by which its codes are multiplied as they are
 //     converted.  The reference is for keys the tile's largest scale, for values the largest that the segment has met.  Both
-//     are powers of two, so nothing is rounded but what is 2^-15 of the reference and less, and then by 2^-25 of it at
-//     most.  The softmax sees one factor a tile, and O is in units of the values' reference.
+//     are powers of two, and a code times 2^-15 or more is still an fp16 value, so nothing is rounded.  The softmax
+//     sees one factor a tile, and O is in units of the values' reference.
+//   * Wide tiles.  A reference may be a scale that only some of the rows see, and a factor below 2^-15 would take bits from what
+//     the others see.  Codes of a tile with such a factor, or behind values so far apart that O in fp32 might lose them,
+//     are left unscaled; the softmax goes on from there in a form of its own (far_tiles8), in which each
+//     block's key scale multiplies its scores, its value scale the numerators, relative to the largest that the row itself
+//     has seen, and O is in units of that.
 //   * Queries.  bf16 ones are scaled by a power of two a row so that fp16 holds them: by the softmax threads, a row each, in
 //     shared memory before the item's first product.
 //   * Values of masked tiles.  NaN ones are taken out of the operand once it is there, by warps 8 and 10, so that 0 * NaN does
@@ -53,6 +58,9 @@ constexpr float kLazy = 6.f, kLift = 9.f;
 // Base-2 units from which on a row's reference is taken off its scaled scores apart (far_tiles8).
 constexpr float kFar = 65536.f;
 constexpr int kInfos = 8;                   // slots for tiles' scales, a power of two
+// The least factor that takes no bits from a code (the least code is 2^-9, the least fp16 value 2^-24), and the least ratio of a
+// segment's value scales at which O moves to the larger unit without losing any (it has 2^9 and fp32's 2^-126).
+constexpr float kLeastFactor = 0x1p-15f, kLeastRatio = 0x1p-64f;
 
 template <int D>
 struct Chunk8 {
@@ -87,13 +95,15 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
 
 // What is known of a tile before its codes: the factors of its blocks as pairs of fp16 values, where the blocks start in the
 // caches (-1: taken as zeros), the references that the factors are over, and whether it is its segment's last tile, or
-// none (behind the share's last one).
+// none (behind the share's last one).  In a wide tile the factors are 1, v_ref is negative, and the blocks' scales count, as
+// their exponents of fp32.
 constexpr uint32_t kLastTile = 1u, kNoTile = 2u;
 struct __align__(16) TileInfo {
   uint32_t k_by[8], v_by[8];
   long long at[8];
   float k_ref, v_ref;
-  uint32_t last, pad;
+  uint32_t last;
+  uint16_t exps[8];   // keys' in the low byte, values' in the high one
 };
 
 __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -123,8 +133,10 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// A power of two of at most 1 as the factor of a pair of fp16 values: 0 below 2^-24, the least that fp16 has.
+// A power of two of at most 1 as the factor of a pair of fp16 values.
 __device__ __forceinline__ uint32_t factor(float by) { return pack16<true>(by, by); }
+// The power of two with this exponent of fp32.
+__device__ __forceinline__ float power(uint32_t exponent) { return __uint_as_float(exponent << 23); }
 
 // This lane's codes of one block (16 bytes in each piece, 512 bytes apart at `in`) as fp16 values times `by` (factor) into the
 // operand at `out`.
@@ -150,6 +162,12 @@ __device__ __forceinline__ void convert_block(uint32_t in, uint32_t out, uint32_
     st_shared16(to ^ 16u, h[k][4], h[k][5], h[k][6], h[k][7]);
   }
 }
+// The first eight words of v to 8 consecutive columns of this thread's row.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // NaN for the dims d0 .. d0 + 15 in which a position that the row sees, in this segment's masked tiles, has a NaN code.
 __device__ __noinline__ uint32_t nan_dims(const Paged8Args& a, const int32_t* table, TileRange r, int i0, int n, int p_lo,
                                           int p_hi, int p, int g, int d0) {
@@ -171,8 +189,9 @@ __device__ __noinline__ uint32_t nan_dims(const Paged8Args& a, const int32_t* ta
   return dims;
 }
 
-// Softmax of tiles i .. n - 1 of a segment (the first one's scores are there, masked) for a warp with a row beyond kFar:
-// scaled scores are rounded before the reference is taken off, 32 at a time.  done < 0: a wait timed out.
+// Softmax of tiles i .. n - 1 of a segment (the first one's scores are there, masked) for a warp with a row beyond kFar, or from a
+// wide tile on: scaled scores are rounded before the reference is taken off, a block at a time.  done < 0: a wait timed out.
+// (v_ref: the row's unit of O.)
 struct FarRow {
   float m, l, v_ref;
   int done, tiles;
@@ -193,17 +212,29 @@ __device__ __noinline__ FarRow far_tiles8(const Paged8Args& a, Item x, int i0, i
       if (!tile_open<kTN>(a, j0, x.p_lo, x.p_hi)) mask_scores(a, tS, p, j0);
     }
     const volatile TileInfo* ts = infos + ((tiles - 1) & (kInfos - 1));
-    const float k = ts->k_ref * q_scale, v_new = ts->v_ref;
+    const float k = ts->k_ref * q_scale, v_tile = ts->v_ref;
+    const bool wide = v_tile < 0.f;
+    float v_new = wide ? v_ref : v_tile;   // the unit of O: of a wide tile the largest scale that the row has seen
+    if (wide) {
+#pragma unroll 1
+      for (int blk = 0; blk < 8; ++blk) {
+        const int j = x.r.tile(i0 + i) * kTN + 16 * blk;
+        if (j <= p && (a.window == 0 || j + 15 > p - a.window || j < a.sinks)) v_new = fmaxf(v_new, power(ts->exps[blk] >> 8));
+      }
+    }
+    auto k_of = [&](int blk) { return wide ? power(ts->exps[blk] & 0xFFu) * q_scale : k; };
+    auto v_of = [&](int blk) { return wide ? power(ts->exps[blk] >> 8) / v_new : 1.f; };
     float mx = -INFINITY, by = 1.f, sum = 0.f;
     __syncwarp();
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      uint32_t v[32];
-      tmem_ld32(tS + c, v);
+    for (int blk = 0; blk < 8; ++blk) {
+      uint32_t v[16];
+      float top = -INFINITY;
+      tmem_ld16_wait(tS + 16 * blk, v);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, __uint_as_float(v[e]));
+      mx = fmaxf(mx, top * k_of(blk));
     }
-    mx *= k;
     if (mx > m && (m == -INFINITY || mx - m > kLazy)) {
       by = ex2(m - mx);   // 0 if nothing was seen before
       m = mx;
@@ -214,24 +245,25 @@ __device__ __noinline__ FarRow far_tiles8(const Paged8Args& a, Item x, int i0, i
     const float ref = m == -INFINITY ? 0.f : m;
     __syncwarp();
     if (i > 0) rescale<D>(tO, by);
-    // (numerators of 32 scores take the place of the 16 before them, which have been read)
+    // (numerators of a block take the place of scores that have been read)
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      uint32_t v[32], pk[16];
-      tmem_ld32(tS + c, v);
+    for (int blk = 0; blk < 8; ++blk) {
+      const float k_blk = k_of(blk), v_blk = v_of(blk);
+      uint32_t v[16];
+      tmem_ld16_wait(tS + 16 * blk, v);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        const float p0 = ex2((__fmul_rn(__uint_as_float(v[e]), k) - ref) + kLift);
-        const float p1 = ex2((__fmul_rn(__uint_as_float(v[e + 1]), k) - ref) + kLift);
+      for (int e = 0; e < 16; e += 2) {
+        const float p0 = ex2((__fmul_rn(__uint_as_float(v[e]), k_blk) - ref) + kLift);
+        const float p1 = ex2((__fmul_rn(__uint_as_float(v[e + 1]), k_blk) - ref) + kLift);
         sum += p0 + p1;
-        pk[e / 2] = pack16<true>(p0, p1);
+        v[e / 2] = pack16<true>(p0 * v_blk, p1 * v_blk);
       }
-      tmem_st16(tS + c / 2, pk);
-      if (c == 32 || c == 96) {
+      tmem_st8(tS + 8 * blk, v);
+      if ((blk & 3) == 3) {
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(pfull + 8u * (c / 64));
+        if ((threadIdx.x & 31) == 0) mbar_arrive(pfull + 8u * (blk / 4));
         __syncwarp();
       }
     }
@@ -528,8 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool need;
         int pg_ahead = read_page(row, x, i0, n, 0, &need);
         float ks_ahead = kLeastScale, vs_ahead = kLeastScale, k_ref = 1.f, v_ref = kLeastScale, v_last = kLeastScale;
+        float v_least = kMostScale;   // the segment's least value scale
         long long from_ahead = -1, from = -1;
-        uint32_t k_by = 0u, v_by = 0u;
+        uint32_t k_by = 0u, v_by = 0u, exps = 0u;
         auto read_scales = [&]() {
           const int page = page_or_none(pg_ahead, need), index = scale_index(max(page, 0), a.Hkv, g, a.page_shift, my_off);
           ks_ahead = vs_ahead = kLeastScale;
@@ -547,23 +580,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float ks = scale_ok(ks_ahead) ? ks_ahead : kLeastScale, vs = scale_ok(vs_ahead) ? vs_ahead : kLeastScale;
             bad |= !scale_ok(ks_ahead) || !scale_ok(vs_ahead);
             __syncwarp();
+            from = from_ahead;
             k_ref = ks;
-            float top = vs;
+            float top = vs, least = from >= 0 ? vs : kMostScale;
 #pragma unroll
             for (int off = 1; off < 8; off <<= 1) {
               k_ref = fmaxf(k_ref, __shfl_xor_sync(0xFFFFFFFFu, k_ref, off));
               top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+              least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, off));
             }
             v_ref = v_last;   // of this lane's tile: the largest so far
+            float v_low = v_least;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const float y = __shfl_sync(0xFFFFFFFFu, top, 8 * t);
+              const float y = __shfl_sync(0xFFFFFFFFu, top, 8 * t), z = __shfl_sync(0xFFFFFFFFu, least, 8 * t);
               v_last = fmaxf(v_last, y);
-              if (t <= lane >> 3) v_ref = fmaxf(v_ref, y);
+              v_least = fminf(v_least, z);
+              if (t <= lane >> 3) {
+                v_ref = fmaxf(v_ref, y);
+                v_low = fminf(v_low, z);
+              }
             }
-            from = from_ahead;
-            k_by = factor(ks / k_ref);
-            v_by = factor(vs / v_ref);
+            // (blocks that are taken as zeros lose nothing)
+            const bool lost = (from >= 0 && (ks < k_ref * kLeastFactor || vs < v_ref * kLeastFactor)) || v_low < v_ref * kLeastRatio;
+            const bool wide = (__ballot_sync(0xFFFFFFFFu, lost) >> (lane & 24) & 0xFFu) != 0u;
+            k_by = factor(wide ? 1.f : ks / k_ref);
+            v_by = factor(wide ? 1.f : vs / v_ref);
+            v_ref = wide ? -v_ref : v_ref;
+            exps = __float_as_uint(ks) >> 23 | __float_as_uint(vs) >> 23 << 8;
             pg_ahead = read_page(row, x, i0, n, i + 4, &need);
           }
           if ((i & 3) == 2) read_scales();
@@ -573,6 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             to->k_by[lane & 7] = k_by;
             to->v_by[lane & 7] = v_by;
             to->at[lane & 7] = from;
+            to->exps[lane & 7] = (uint16_t)exps;
             if ((lane & 7) == 0) {
               to->last = i + 1 == n ? kLastTile : 0u;
               to->k_ref = k_ref;
@@ -746,10 +791,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx3 = max3(mx3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
         }
         const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * k;
-        // The reference moves if the new maximum is well above it (or is the first).
+        // The reference moves if the new maximum is well above it (or is the first).  (A wide tile, whose v_ref is negative and
+        // whose scores are not what they seem here, comes by the same condition.)
         const bool move = mx > m && (m == -INFINITY || mx - m > kLazy);
         if (__any_sync(0xFFFFFFFFu, move || v_new != v_ref)) {
-          if (__any_sync(0xFFFFFFFFu, move && p >= 0 && fabsf(mx) > kFar)) {   // the tiles from here on in another way
+          if (__any_sync(0xFFFFFFFFu, v_new < 0.f || (move && p >= 0 && fabsf(mx) > kFar))) {   // from here on in another way
             const FarRow row = far_tiles8<D>(a, x, i0, i, n, p, tS, tO, SFULL(t), PFULL(t, 0), infos_s, q_scale,
                                              FarRow{m, l, v_ref, done, tiles});
             if (row.done < 0) return false;

@@ -71,12 +71,11 @@ moe_status gqa_paged8_read(const gqa_paged_dims* dims, const uint8_t* k_cache, c
  * Products are fp16 on the tensor cores, with fp32 sums, and what enters them:
  *   queries     fp16 as they are; bf16 times a power of two of each row and head, off by at most 2^-40 of the row's
  *               largest number (one past 2^75 counts as infinite)
- *   keys        single tokens: exact.  Chunks: exact where their block's scale is within 2^15 of the largest one among
- *               the tile's 128 positions; off by at most 2^-25 of that scale down to 2^24 below it, and then taken as 0
- *   numerators  as gqa_paged_attention states for fp16 (single tokens: times their block's value scale over the
- *               largest that the share has met, so 2^-39 of the largest value there in absolute terms)
- *   values      single tokens: exact.  Chunks: the same, beside the largest scale in the tiles that the row block has
- *               met (so never off by more than 2^-24 of the largest value there)
+ *   keys, values   exact
+ *   numerators  as gqa_paged_attention states for fp16.  In single tokens, and in chunks from 128 positions on whose scales
+ *               (those that some row of its block needs) differ by more than 2^15, or are that far below an earlier value
+ *               scale: times their block's value scale over the largest that the token has met, and so each off by
+ *               2^-40 (single tokens) or 2^-34 (chunks) of 448 times the largest value scale that the token sees
  * Bit 8 is set for an output that is not finite: visible NaN codes, or values past the dims' type.
  *   workspace  >= gqa_paged8_workspace_bytes(dims) */
 moe_status gqa_paged8_attention(const gqa_paged_dims* dims, const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
