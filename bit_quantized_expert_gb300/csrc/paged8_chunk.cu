@@ -742,8 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p = live ? x.p_lo + t * tpt + tok : -1;      // a row that is no token sees nothing
       float q_scale = a.qk_scale;
       if (!FP16) {
-        // bf16 times the power of two that brings the row's largest to 2^14 .. 2^15: exact down to 2^-24, and at that within
-        // 2^-40 of the largest
+        // bf16 times the power of two that brings the row's largest to 2^14 .. 2^15: exact down to 2^-24, and so within 2^-39 of the
+        // largest, or 2^-105.  (At most 2^80, so that a scale of the scores is never 0, which would undo a mask.)
         if (!wait_warp(QFULL(t), outs & 1)) return false;
         const uint32_t line = sQ + t * C::kTileBytes + r * 128;
         uint32_t w[D / 2];
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < D / 2; ++e) top = max(top, max(w[e] & 0x7FFFu, (w[e] >> 16) & 0x7FFFu));
-        const int E = (int)(top >> 7), e2 = E == 0 || E == 255 ? 0 : min(max(E - 141, -60), 60);
+        const int E = (int)(top >> 7), e2 = E == 255 ? 0 : min(max(E - 141, -80), 60);
         const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
         q_scale *= __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll

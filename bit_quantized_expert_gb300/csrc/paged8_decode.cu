@@ -329,14 +329,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto convert_queries = [&]() {
     q_scale = a.qk_scale;
     if (FP16) return;
-    // bf16 times the power of two that brings the row's largest to 2^14 .. 2^15: exact down to 2^-24, and at that within
-    // 2^-40 of the largest
+    // bf16 times the power of two that brings the row's largest to 2^14 .. 2^15: exact down to 2^-24, and so within 2^-39 of the
+    // largest, or 2^-105.
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < D / 8; ++e) top = max(top, max(qa[e] & 0x7FFFu, (qa[e] >> 16) & 0x7FFFu));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const int E = (int)(top >> 7), e2 = E == 0 || E == 255 ? 0 : min(max(E - 141, -60), 60);
+    const int E = (int)(top >> 7), e2 = E == 255 ? 0 : min(max(E - 141, -80), 60);
     const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
     q_scale *= __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll

@@ -69,8 +69,8 @@ moe_status gqa_paged8_read(const gqa_paged_dims* dims, const uint8_t* k_cache, c
 
 /* Attention of the new tokens over the cache: gqa_paged_attention with K and V the products code * scale, exact.
  * Products are fp16 on the tensor cores, with fp32 sums, and what enters them:
- *   queries     fp16 as they are; bf16 times a power of two of each row and head, off by at most 2^-40 of the row's
- *               largest number (one past 2^75 counts as infinite)
+ *   queries     fp16 as they are; bf16 times a power of two of each row and head, off by at most 2^-39 of the row's
+ *               largest number, or by 2^-105 if that is less than 2^-66 (one of 65520 * 2^60 or more counts as infinite)
  *   keys, values   exact
  *   numerators  as gqa_paged_attention states for fp16.  In single tokens, and in chunks from 128 positions on whose scales
  *               (those that some row of its block needs) differ by more than 2^15, or are that far below an earlier value

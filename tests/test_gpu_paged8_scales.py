@@ -157,3 +157,30 @@ def test_nan_in_a_block_of_far_larger_scale(which, span):
         rows = slice(b.q_start[seq] + max(pos - c, 0), b.q_start[seq + 1])
         ref[0][rows, :, slice(None) if which == 0 else 5] = np.nan
     check(b, ref=ref, want=8)
+
+
+@pytest.mark.parametrize("new", [1, 25])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_queries_beside_large_keys(new, D):
+    """bf16 queries down to the least number under the largest key scale: keys point to and away from the query in turn, their
+    values are 1 and -1, so that a result is the score's own size."""
+    for size in (2.0 ** -46 * (1 + 2.0 ** -7), 2.0 ** -70, 2.0 ** -80 * (1 + 2.0 ** -7), 2.0 ** -84 * 1.5, 2.0 ** -86, 2.0 ** -100, 2.0 ** -133):
+        b = Batch8([(64 - new, new)], Hq=4, Hkv=2, D=D, page=64, seed=90)
+        page = b.table[0, 0]
+        b.q[:] = bits(np.array(size), "bf16")
+        sign = np.where(np.arange(64) % 2 == 0, 1.0, -1.0)[None, :, None]
+        b.c[0][page], b.c[1][page] = Q.to_codes(448.0 * sign), Q.to_codes(sign)
+        b.s[0][page], b.s[1][page] = 2.0 ** 60 if size < 2.0 ** -60 else 2.0 ** 36, 1.0
+        check(b, f"size {size}")
+
+
+@pytest.mark.parametrize("new", [1, 25])
+@pytest.mark.parametrize("apart", [0, 30])
+def test_least_queries_and_least_key_scales(new, apart):
+    """Scores that are nothing beside 1: every visible value counts the same, what is masked does not count."""
+    b = Batch8([(300, new), (0, new)], Hq=4, Hkv=2, page=32, seed=91, window=100, sinks=3)
+    b.q[:] = bits(np.array(2.0 ** -126), "bf16")
+    for i, low in ((0, -60), (1, -20)):
+        b.s[i][:] = np.where(np.isnan(b.s[i]), np.nan, 2.0 ** low)
+        b.s[i][b.table[0, 9], :, 1] = 2.0 ** (low + apart)
+    check(b)
