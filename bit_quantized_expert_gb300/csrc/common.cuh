@@ -65,8 +65,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 
 // Wait for the phase of `parity` to complete.  Gives up (returns false) when the CTA-wide
 // abort word is set by another role, or after `limit` cycles, in which case it sets the abort
-// word and the timeout flag.  No wait in these kernels is unbounded: they all use
-// kWaitTimeoutCycles (mbar_wait); only the wait probe passes a shorter limit.
+// word and the timeout flag.  No wait in these kernels is unbounded: they use kWaitTimeoutCycles
+// (mbar_wait) or count their tries (mbar_wait_warp_tries); only the wait probe passes shorter limits.
 __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, volatile int* abort_s, uint32_t* err,
                                               long long limit) {
   if (mbar_try_wait(bar, parity)) return true;
@@ -100,6 +100,21 @@ __device__ __forceinline__ bool mbar_wait_warp_for(uint32_t bar, uint32_t parity
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_s,
                                                uint32_t* err) {
   return mbar_wait_warp_for(bar, parity, abort_s, err, kWaitTimeoutCycles);
+}
+
+// The same for a whole warp without clock and abort word: false after `tries` looks at the barrier.  A look that fails takes as
+// long as the hardware suspends the thread for, ~3000 cycles here and no more than that is promised of it, so a
+// million are about two seconds, and at the least (no suspension) some tens of milliseconds.
+constexpr int kWaitTries = 1 << 20;
+constexpr long long kTryCycles = 3000;
+__device__ __forceinline__ bool mbar_wait_warp_tries(uint32_t bar, uint32_t parity, int tries) {
+  bool ok;
+#pragma unroll 1
+  do {
+    ok = mbar_try_wait(bar, parity);
+  } while (!ok && --tries > 0);
+  __syncwarp();
+  return __all_sync(0xFFFFFFFFu, ok);
 }
 
 // ------------------------------------------------------------------------------------------

@@ -77,20 +77,12 @@ struct Chunk8 {
   static_assert((kPagedMaxSeqs + 1) * 4 <= kStages * kStageBytes, "sums fit");
 };
 
-// Waits for the phase of `parity`, the warp together; false: it gave up.  A look at a barrier that is not there yet takes ~3000
-// cycles (the hardware holds the thread until the phase completes, or so long), so this is about two seconds.  What a wait
-// that runs out needs is elsewhere (walk): with the clock and the abort word looked at here, as in mbar_wait, the
-// instructions of every wait are fetched beside the softmax's, and 2048 tokens at 32768 take 460 us in place of 404.
-constexpr int kTries = 1 << 20;
+// Waits for the phase of `parity`, the warp together; false: it gave up.  What a wait that runs out needs is elsewhere (walk):
+// with the clock and the abort word looked at here, as in mbar_wait, the instructions of every wait are fetched beside the
+// softmax's, and 2048 tokens at 32768 take 460 us in place of 404 (with a time limit given to the instruction itself 395 in
+// place of 384).
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-  int left = kTries;
-  bool ok;
-#pragma unroll 1
-  do {
-    ok = mbar_try_wait(bar, parity);
-  } while (!ok && --left > 0);
-  __syncwarp();
-  return __all_sync(0xFFFFFFFFu, ok);
+  return mbar_wait_warp_tries(bar, parity, kWaitTries);
 }
 
 // What is known of a tile before its codes: the factors of its blocks as pairs of fp16 values, where the blocks start in the

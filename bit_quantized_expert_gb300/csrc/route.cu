@@ -326,24 +326,32 @@ cudaError_t launch_topk(const RouteArgs& a, cudaStream_t st) {
 
 // The library's bounded waits, made to run out: thread 0 waits on an mbarrier that nothing
 // completes until `limit` cycles pass, gives up, sets the CTA's abort word and the timeout bit of
-// the error word; warp 1 then waits on the same barrier collectively and leaves through the abort
-// word at once, all lanes with the same outcome.  Nothing else is touched.
-__global__ void __launch_bounds__(64) wait_probe_kernel(uint32_t* err, long long limit) {
+// its error word; warp 1 then waits on the same barrier collectively and leaves through the abort
+// word at once, all lanes with the same outcome; warp 2 waits for as many tries as take about as
+// long.  The timeout bit of the caller's error word is set if all three gave up.  Nothing else is
+// touched.
+__global__ void __launch_bounds__(96) wait_probe_kernel(uint32_t* err, long long limit) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ int abort_s;
+  __shared__ uint32_t err_s;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bar), 1);
     abort_s = 0;
+    err_s = 0;
     mbar_fence_init();
   }
   __syncthreads();
-  if (threadIdx.x == 0) (void)mbar_wait_for(smem_u32(&bar), 0, &abort_s, err, limit);
+  bool met = false;
+  if (threadIdx.x == 0) met = mbar_wait_for(smem_u32(&bar), 0, &abort_s, &err_s, limit);
   __syncthreads();
-  if (threadIdx.x >= 32) (void)mbar_wait_warp_for(smem_u32(&bar), 0, &abort_s, err, limit);
+  if (threadIdx.x >= 64) met = mbar_wait_warp_tries(smem_u32(&bar), 0, (int)(limit / kTryCycles) + 1);
+  else if (threadIdx.x >= 32) met = mbar_wait_warp_for(smem_u32(&bar), 0, &abort_s, &err_s, limit);
+  const bool all = __syncthreads_or(met) == 0;
+  if (threadIdx.x == 0 && all) raise_flag(err, err_s & kErrWaitTimeout);
 }
 
 cudaError_t launch_wait_probe(uint32_t* err, long long limit, cudaStream_t st) {
-  wait_probe_kernel<<<1, 64, 0, st>>>(err, limit);
+  wait_probe_kernel<<<1, 96, 0, st>>>(err, limit);
   return cudaGetLastError();
 }
 

@@ -34,9 +34,10 @@ moe_status moe_decode_stream_probe(const moe_dims* dims, const int32_t* idx, con
                                    const moe_experts* shared, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Test aid for the library's bounded waits: one CTA waits on an mbarrier that nothing completes,
- * through the same wait every kernel of the library uses, but giving up after limit_cycles SM
- * cycles instead of the kernels' fixed limit (about two seconds).  The wait gives up, sets bit 1
- * (a bounded device wait timed out) of the workspace's error word, and the kernel returns; the
+ * through the same waits the kernels of the library use (by the clock, as a thread and as a warp, and by
+ * counted tries), but giving up after limit_cycles SM cycles, or tries that take about as long,
+ * instead of the kernels' fixed limits (about two seconds).  The waits give up, bit 1
+ * (a bounded device wait timed out) of the workspace's error word is set, and the kernel returns; the
  * context stays usable.  limit_cycles must lie in 1 .. 4e9 (MOE_ERR_INVALID_ARG otherwise); the
  * workspace must hold at least the error word (256 bytes, 16-byte aligned: MOE_ERR_WORKSPACE /
  * MOE_ERR_MISALIGNED otherwise).  Nothing is written except the error word. */
