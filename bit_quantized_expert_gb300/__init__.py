@@ -405,11 +405,16 @@ def alloc_gqa_paged_workspace(pd: GqaPagedDims, device="cuda"):
 _paged_types = _int32 = _int64 = _float32 = _byte_types = _device = _raw_stream = None
 
 
+class _Types(dict):
+    def __missing__(self, dtype):   # refused as the library does it
+        raise MoeError(1, f"dims of dtype {dtype}")
+
+
 def _load_paged_types():
     global _paged_types, _int32, _int64, _float32, _byte_types, _device, _raw_stream
     import torch
     bits = (torch.int16, torch.uint16)
-    _paged_types, _int32 = ((torch.bfloat16, *bits), (torch.float16, *bits)), torch.int32
+    _paged_types, _int32 = _Types({0: (torch.bfloat16, *bits), 1: (torch.float16, *bits)}), torch.int32
     _int64, _float32, _byte_types = torch.int64, torch.float32, (torch.uint8, torch.int8, torch.float8_e4m3fn)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
     _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # last: _paged_device looks at it

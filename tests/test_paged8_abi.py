@@ -203,3 +203,18 @@ def test_table_refusals_of_the_binding(lib):
             moe.gqa_rotary_table(rot, device="cpu")
     with pytest.raises(KeyError):
         moe.gqa_rotary_table(64, scaling="other", device="cpu")
+
+
+@pytest.mark.parametrize("dtype", [2, -1, 77])
+def test_binding_refuses_dims_of_no_type(dtype):
+    """As the library itself does, with the same error."""
+    import torch
+    moe._load_paged_types()
+    d, rd = moe.gqa_paged_dims(**GOOD), moe.gqa_rotary_dims(**ROT)
+    d.dtype = rd.dtype = dtype
+    rows, cache = torch.zeros(37, 16, 128, dtype=torch.bfloat16), torch.zeros(100, 2, 64, 128, dtype=torch.bfloat16)
+    for call in (lambda: moe._want8(d), lambda: moe._want_rotary(rd), lambda: moe._paged_caches(cache, cache, d, -1),
+                 lambda: moe._paged_rows(rows, 37, 16, 128, 0, dtype, -1, "q")):
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert "MOE_ERR_INVALID_ARG" in str(e.value)
