@@ -16,7 +16,7 @@
 //     the others see.  Codes of a tile with such a factor, or behind values so far apart that O in fp32 might lose them,
 //     are left unscaled; the softmax goes on from there in a form of its own (far_tiles8), in which each
 //     block's key scale multiplies its scores, its value scale the numerators, relative to the largest that the row itself
-//     has seen, and O is in units of that.
+//     sees, and O is in units of that.
 //   * Queries.  bf16 ones are scaled by a power of two a row so that fp16 holds them: by the softmax threads, a row each, in
 //     shared memory before the item's first product.
 //   * Values of masked tiles.  NaN ones are taken out of the operand once it is there, by warps 8 and 10, so that 0 * NaN does
@@ -25,14 +25,15 @@
 //
 // What bounds it: the chain of a row tile, softmax, P V, next scores, as in the 16-bit form, whose softmax here shares its
 // issue slots with the conversion (58 % of them are taken, the tensor pipe is active 64 % of the time, 75 % in the 16-bit
-// form).  Measured in a graph: 2048 tokens at 32768 positions (16 / 2 heads of 128, bf16) 381 us, 1.49 PFLOP/s, 78 % of the
-// dense rate (the 16-bit form of the same shape: 344); heads of 64 308; 34 sequences of single tokens and chunks (fp16)
-// 78.9; 16 prompts 21.4; 4096 tokens with a window of 1024 69.3; 512 tokens of one prompt 19.1.
+// form).  Measured in a graph: 2048 tokens at 32768 positions (16 / 2 heads of 128, bf16) 385 us, 1.47 PFLOP/s, 77 % of the
+// dense rate (the 16-bit form of the same shape: 344); heads of 64 313; 34 sequences of single tokens and chunks (fp16)
+// 80.2; 16 prompts 21.7; 4096 tokens with a window of 1024 69.8; 512 tokens of one prompt 19.3.  Where a wide tile is among the
+// first: 2048 tokens 810 us (keys) and 1041 (values), the 34 sequences 138 and 172.
 //
 // Steps at 2048 tokens: 1131 us with codes through registers; 607 by asynchronous copies; 536 a block's codes at once; 505 by
 // four warps of their own; 434 with scales that are powers of two and multiply the codes as they are converted, not scores
 // and numerators in the softmax; 391 with NaN codes taken out by two other warps, scales read by a third, and short
-// waits; 381 with the pages there as well.  Not kept: codes brought by tensor map (1030 us by one warp, 620 by the converting ones), or
+// waits; 381 with the pages there as well (385 since wide tiles have a form of their own).  Not kept: codes brought by tensor map (1030 us by one warp, 620 by the converting ones), or
 // through registers (spills); unrolled conversion (25 % more: its instructions displace the softmax's); NaN codes looked for
 // in global memory ahead of the conversion (16 prompts 22.4: four loads' latency a tile, where every tile is masked); a
 // barrier of its own for a tile's places, so that its copies do not wait for its scales (16 prompts 21.0, 2048 tokens 389).
@@ -181,6 +182,22 @@ __device__ __noinline__ uint32_t nan_dims(const Paged8Args& a, const int32_t* ta
   return dims;
 }
 
+// The least unit in which O of this thread's row, now in units of `unit`, stays below 2^60.  (What a row sees sets its unit in a
+// wide tile, and the tiles before may have had a larger one for other rows' sake.)
+template <int D>
+__device__ __forceinline__ float least_unit(uint32_t tO, float unit) {
+  float top = 0.f;
+  __syncwarp();
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t v[16];
+    tmem_ld16_wait(tO + c, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(__uint_as_float(v[e])));
+  }
+  const int down = min(max(60 + 126 - (int)(__float_as_uint(top) >> 23), 0), 120);   // top < 2^(exponent - 126)
+  return fmaxf(unit * power(127 - down), kLeastScale);
+}
 // Softmax of tiles i .. n - 1 of a segment (the first one's scores are there, masked) for a warp with a row beyond kFar, or from a
 // wide tile on: scaled scores are rounded before the reference is taken off, a block at a time.  done < 0: a wait timed out.
 // (v_ref: the row's unit of O.)
@@ -206,8 +223,9 @@ __device__ __noinline__ FarRow far_tiles8(const Paged8Args& a, Item x, int i0, i
     const volatile TileInfo* ts = infos + ((tiles - 1) & (kInfos - 1));
     const float k = ts->k_ref * q_scale, v_tile = ts->v_ref;
     const bool wide = v_tile < 0.f;
-    float v_new = wide ? v_ref : v_tile;   // the unit of O: of a wide tile the largest scale that the row has seen
+    float v_new = v_tile;   // the unit of O
     if (wide) {
+      v_new = i > 0 ? least_unit<D>(tO, v_ref) : kLeastScale;
 #pragma unroll 1
       for (int blk = 0; blk < 8; ++blk) {
         const int j = x.r.tile(i0 + i) * kTN + 16 * blk;

@@ -75,7 +75,8 @@ SPANS = (8, 14, 15, 16, 20, 24, 25, 31, 50, 66)
 # (sequences, arguments, the block whose scale is far above the others'): rows before it, or behind its window, do not
 # see it, others of their row block do
 HIDDEN = [([(0, 60)], {}, 2), ([(700, 25)], {}, 44), ([(300, 100)], dict(window=64), 15), ([(0, 33), (6000, 40)], {}, 376),
-          ([(100, 200)], dict(window=40, sinks=20), 12)]
+          ([(100, 200)], dict(window=40, sinks=20), 12), ([(2072, 20)], dict(window=30), 127),
+          ([(500, 20), (2070, 60)], dict(window=30, sinks=2), 128)]
 
 
 @pytest.mark.parametrize("case", range(len(HIDDEN)))
@@ -184,3 +185,33 @@ def test_least_queries_and_least_key_scales(new, apart):
         b.s[i][:] = np.where(np.isnan(b.s[i]), np.nan, 2.0 ** low)
         b.s[i][b.table[0, 9], :, 1] = 2.0 ** (low + apart)
     check(b)
+
+
+@pytest.mark.parametrize("new", [1, 45])
+def test_repeats_and_graphs(new):
+    """Blocks of far larger scale among others: the same bits every time, beside another batch, and from a graph."""
+    batches = []
+    for seed in (0, 1):
+        b = Batch8([(3000, new), (40, new), (0, new)], Hq=8, Hkv=2, seed=95 + seed)
+        r = np.random.default_rng(seed)
+        for i in range(2):
+            up = r.random(b.s[i].shape) < 0.02
+            b.s[i][up] *= 2.0 ** 25
+        b.upload()
+        b.attend()
+        batches.append(b)
+    first = [b.dev["o"].clone() for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, b in zip(streams, batches):
+            b.attend(stream=s)
+    torch.cuda.synchronize()
+    for b, want in zip(batches, first):
+        assert torch.equal(b.dev["o"], want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.attend()
+        b.dev["o"].zero_()
+        g.replay()
+        assert torch.equal(b.dev["o"], want) and b.flags() == 0
