@@ -23,9 +23,17 @@ namespace moe {
 namespace {
 
 // Threads of a CTA.  Few sequences: 128, as many CTAs as an SM holds (append of 64 tokens 3.4 us, 8 prompts 7.3; with 256 threads
-// 3.6 and 7.7).  Every CTA scans the sequences, so for many of them there are few and wide ones, in one wave (append of 1024
-// tokens of as many 7.8 us, of 4096 26.7; with 256 threads and four CTAs an SM 9.1 and 67; at 200 sequences narrow ones
-// still win, 3.9 against 4.5, at 400 wide ones, 4.7 against 5.9).
+// 3.6 and 7.7).  Every CTA scans the sequences, so for many of them there are few and wide ones, in one wave.  Narrow against
+// wide CTAs, in a graph, us:
+//                       append                                       read
+//   200 sequences       1 token 3.9 / 4.5, 500 39.2 / 42.0           up to 64 4.6 / 4.7, 500 27.1 / 29.6
+//   300                 1 token 4.1 / 4.7, 32 10.0 / 9.6, 500 57.0 / 59.5      1 3.2 / 3.2, 32 6.4 / 6.6, 500 39.7 / 43.0
+//   400                 1 token 5.9 / 4.7
+//   1000                100 49.2 / 45.0                              100 38.2 / 29.5
+//   1024                1 token 12.1 / 7.8                           up to 64 19.5 / 9.4
+//   4000                20 245 / 53                                  20 224 / 32
+//   4096                1 token 234 / 27
+// So the sides meet between 200 and 400 sequences, whatever their rows; between 257 and there the rule costs up to 14 %.
 constexpr int kNarrow = 128, kWide = 512;
 constexpr int kManySeqs = 256;
 constexpr int kNarrowThreads = 1024;   // of an SM, keys and values each, at most

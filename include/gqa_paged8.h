@@ -21,7 +21,8 @@
  *
  * Conventions, statuses, the limits of dims and the error word are those of gqa_paged.h, but: strides of the caches
  * are multiples of 16 bytes; the scales are 16-byte aligned; bit 8 is also set by gqa_paged8_append for an input that
- * is not finite (below).  Block-table entries, codes and scales of what no row needs are not read, or have no effect.
+ * is not finite (below).  Block-table entries, codes and scales of what no row needs are not read, or have no effect;
+ * and as there, what a row does not see has no effect on that row (but for last bits), whatever its scales.
  */
 #ifndef GQA_PAGED8_GB300_H_
 #define GQA_PAGED8_GB300_H_
