@@ -33,10 +33,11 @@
 // Steps at 2048 tokens: 1131 us with codes through registers; 607 by asynchronous copies; 536 a block's codes at once; 505 by
 // four warps of their own; 434 with scales that are powers of two and multiply the codes as they are converted, not scores
 // and numerators in the softmax; 391 with NaN codes taken out by two other warps, scales read by a third, and short
-// waits; 381 with the pages there as well (385 since wide tiles have a form of their own).  Not kept: codes brought by tensor map (1030 us by one warp, 620 by the converting ones), or
-// through registers (spills); unrolled conversion (25 % more: its instructions displace the softmax's); NaN codes looked for
-// in global memory ahead of the conversion (16 prompts 22.4: four loads' latency a tile, where every tile is masked); a
-// barrier of its own for a tile's places, so that its copies do not wait for its scales (16 prompts 21.0, 2048 tokens 389).
+// waits; 381 with the pages there as well (385 since wide tiles have a form of their own).  Not kept: codes brought by
+// tensor map (1030 us by one warp, 620 by the converting ones), or through registers (spills); unrolled conversion (25 %
+// more: its instructions displace the softmax's); NaN codes looked for in global memory ahead of the conversion (16
+// prompts 22.4: four loads' latency a tile, where every tile is masked); a barrier of its own for a tile's places, so that
+// its copies do not wait for its scales (16 prompts 21.0, 2048 tokens 389).
 #include <cmath>
 #include <cstring>
 

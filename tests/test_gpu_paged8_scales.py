@@ -165,7 +165,8 @@ def test_nan_in_a_block_of_far_larger_scale(which, span):
 def test_small_queries_beside_large_keys(new, D):
     """bf16 queries down to the least number under the largest key scale: keys point to and away from the query in turn, their
     values are 1 and -1, so that a result is the score's own size."""
-    for size in (2.0 ** -46 * (1 + 2.0 ** -7), 2.0 ** -70, 2.0 ** -80 * (1 + 2.0 ** -7), 2.0 ** -84 * 1.5, 2.0 ** -86, 2.0 ** -100, 2.0 ** -133):
+    for size in (2.0 ** -46 * (1 + 2.0 ** -7), 2.0 ** -70, 2.0 ** -80 * (1 + 2.0 ** -7), 2.0 ** -84 * 1.5, 2.0 ** -86, 2.0 ** -100,
+                 2.0 ** -133):
         b = Batch8([(64 - new, new)], Hq=4, Hkv=2, D=D, page=64, seed=90)
         page = b.table[0, 0]
         b.q[:] = bits(np.array(size), "bf16")
